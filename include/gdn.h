@@ -266,6 +266,87 @@ int gdn_conv_bwd(const void* x, const float* w, const float* bias, const int32_t
                  const float* dfinal_tail, float* dx, float* dw, float* dbias, float* dconv_init, void* workspace,
                  size_t ws_bytes, gdn_stream_t stream);
 
+/*
+ * Decayed linear attention: the layer without the delta rule's erase, with a constant decay for each
+ * head. Per document and value head h (key head h / (H_v / H_k)), lam = exp(log_decay[h]):
+ *     S_t = lam S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * packed, started and forked exactly as gdn_chunk_fwd (cu_seqlens, init_idx, initial_state; the final
+ * state of an empty document is its start state). All tensor pointers are device pointers:
+ *   q, k      : bf16 [T, H_k, 128];  v, out, dout : bf16 [T, H_v, 128]
+ *   log_decay : fp32 [H_v], expected <= 0 (0 = plain linear attention; below -10000 reads as -10000).
+ *               It is a constant of the model (retention- and slope-type layers do not learn it): the
+ *               backward returns no gradient for it.
+ *   strides   : host array or NULL. Elements from one token to the next of q, k, v (and dout in the
+ *               backward), for views into a fused projection; 0 or NULL = contiguous. A multiple of 8, at least
+ *               heads * 128; the heads of a token are contiguous. out and the gradients are contiguous.
+ *   initial_state : fp32 [n_init, H_v, 128, 128];  final_state, dfinal_state : fp32 [N, H_v, 128, 128]
+ * out, dq, dk [T, H_k, 128] (summed over each key head's value heads) and dv are bf16: the inputs'
+ * type, as a training step hands them on. The states and their gradients are fp32 and are formed
+ * with compensated products (relative error about 1e-6). gdn_la_bwd is the backward of
+ * sum(dout * out) + sum(dfinal_state * final_state); dinitial_state [n_init, H_v, 128, 128] sums over
+ * the documents that start from each entry, and a fork's gradient flows into the document it forked
+ * from. Every sum has a fixed order (deterministic).
+ * workspace: gdn_la_workspace_size(...) bytes, 256-byte aligned (has_init: init_idx is given); bad
+ * cu_seqlens / init_idx are reported in its status word (gdn_workspace_status). Ownership, stream
+ * and device rules as for gdn_chunk_fwd; nothing is allocated.
+ */
+size_t gdn_la_workspace_size(int N, int T, int H_k, int H_v, int has_init, int backward);
+int gdn_la_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* cu_seqlens, int N,
+               int T, int H_k, int H_v, int head_dim, const int64_t* strides, const int32_t* init_idx,
+               const float* initial_state, int n_init, float scale, void* out, float* final_state, void* workspace,
+               size_t ws_bytes, gdn_stream_t stream);
+int gdn_la_bwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* cu_seqlens, int N,
+               int T, int H_k, int H_v, int head_dim, const int64_t* strides, const int32_t* init_idx,
+               const float* initial_state, int n_init, float scale, const void* dout, const float* dfinal_state,
+               void* dq, void* dk, void* dv, float* dinitial_state, void* workspace, size_t ws_bytes,
+               gdn_stream_t stream);
+
+/* Element types and 8-bit outputs of the calls below. */
+enum gdn_dtype { GDN_DTYPE_BF16 = 0, GDN_DTYPE_FP16 = 1, GDN_DTYPE_FP32 = 2 };
+enum gdn_quant {
+  GDN_QUANT_NONE = 0,
+  GDN_QUANT_ROW = 1,  /* e4m3 with one fp32 scale a row */
+  GDN_QUANT_GROUP = 2 /* e4m3 with one fp32 scale for each 128 columns of a row */
+};
+
+/*
+ * One token per sequence of the decayed linear attention, in place on a pool of states:
+ *     S = state_pool[state_idx[b], h];  S = lam S + k v^T (stored back),  out = scale S^T q.
+ *   q, k : [B, H_k, 128];  v, out : [B, H_v, 128], all of `dtype` (bf16 or fp16);  strides : host array
+ *   of the elements from one sequence to the next of q, k, v, or NULL (as in gdn_la_fwd)
+ *   state_idx, state_pool, status : as in gdn_decode_step (an index out of range is skipped, its out
+ *   row zero, and reported)
+ * Nothing is allocated, everything runs on `stream`. B = 0 is a no-op.
+ */
+int gdn_la_decode_step(const void* q, const void* k, const void* v, const float* log_decay, int B, int H_k, int H_v,
+                       int head_dim, int dtype, const int64_t* strides, const int32_t* state_idx, float* state_pool,
+                       int n_pool, float scale, void* out, int32_t* status, gdn_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, per row of D (1 <= D <= 32768):
+ *     h = x + residual,  y = w h / sqrt(mean(h^2) + eps)
+ *   x, residual, residual_out (= h) : [T, D] of `dtype` (bf16, fp16 or fp32), contiguous; residual and
+ *   residual_out are both given or both NULL (then h = x); residual_out may be residual or x itself, y may
+ *   be x itself
+ *   w : [D] of `w_dtype`;  y : [T, D] of `dtype`, or e4m3 bytes with `quant`
+ *   scales : fp32 [T] (GDN_QUANT_ROW) or [T, ceil(D / 128)] (GDN_QUANT_GROUP), else NULL: y stands for
+ *   bytes * scale, scale = amax / 448 (1 where the row or group is all zero)
+ * The sums are fp32; h is rounded once, y is formed from the unrounded sum. T = 0 is a no-op.
+ */
+int gdn_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64_t T, int D, int dtype, int w_dtype,
+                    float eps, void* residual_out, void* y, int quant, float* scales, gdn_stream_t stream);
+
+/*
+ * Backward of the norm from the h that the forward left (x itself without a residual): with dy the
+ * gradient of y and dh that of h from elsewhere (NULL = none),
+ *     dx = rs w dy - h rs^3 mean(w dy h) + dh,   dw = sum over rows of dy h rs   (rs = (mean(h^2) + eps)^{-1/2})
+ * dx [T, D] of `dtype` is the gradient of x and of the residual alike, and may be dh or dy itself; dw is
+ * fp32 [D], summed in a fixed order. workspace: gdn_rmsnorm_workspace_size(T, D) bytes, 256-byte aligned.
+ */
+size_t gdn_rmsnorm_workspace_size(int64_t T, int D);
+int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D, int dtype,
+                    int w_dtype, float eps, void* dx, float* dw, void* workspace, size_t ws_bytes, gdn_stream_t stream);
+
 /* Copy the workspace's device status word to the host (synchronises `stream`) and return it:
  * GDN_OK or the first device-side error of the last call that used this workspace. */
 int gdn_workspace_status(const void* workspace, gdn_stream_t stream);

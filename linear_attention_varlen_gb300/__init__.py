@@ -29,7 +29,9 @@ CHUNK = 64
 EXPORTS = ("gdn_default_options", "gdn_fwd_workspace_size", "gdn_bwd_workspace_size", "gdn_chunk_fwd",
            "gdn_chunk_bwd", "gdn_workspace_status", "gdn_status_string", "gdn_plan_host", "gdn_chunk_fwd_noalloc",
            "gdn_noalloc_scratch_bytes", "gdn_noalloc_status", "gdn_fwd_check_args", "gdn_bwd_check_args",
-           "gdn_decode_step", "gdn_conv_workspace_size", "gdn_conv_fwd", "gdn_conv_bwd")
+           "gdn_decode_step", "gdn_conv_workspace_size", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_la_workspace_size",
+           "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode_step", "gdn_rmsnorm_fwd", "gdn_rmsnorm_workspace_size",
+           "gdn_rmsnorm_bwd")
 
 
 class GdnError(RuntimeError):
@@ -143,6 +145,21 @@ def load(path: Optional[str] = None):
         lib.gdn_conv_fwd.restype = I
         lib.gdn_conv_bwd.argtypes = [P, P, P, P, I, I, I, P, P, I, P, P, P, P, P, P, P, Z, P]
         lib.gdn_conv_bwd.restype = I
+        F, L = ctypes.c_float, ctypes.c_int64
+        lib.gdn_la_workspace_size.argtypes = [I, I, I, I, I, I]
+        lib.gdn_la_workspace_size.restype = Z
+        lib.gdn_la_fwd.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, P, I, F, P, P, P, Z, P]
+        lib.gdn_la_fwd.restype = I
+        lib.gdn_la_bwd.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, P, I, F, P, P, P, P, P, P, P, Z, P]
+        lib.gdn_la_bwd.restype = I
+        lib.gdn_la_decode_step.argtypes = [P, P, P, P, I, I, I, I, I, P, P, P, I, F, P, P, P]
+        lib.gdn_la_decode_step.restype = I
+        lib.gdn_rmsnorm_fwd.argtypes = [P, P, P, L, I, I, I, F, P, P, I, P, P]
+        lib.gdn_rmsnorm_fwd.restype = I
+        lib.gdn_rmsnorm_workspace_size.argtypes = [L, I]
+        lib.gdn_rmsnorm_workspace_size.restype = Z
+        lib.gdn_rmsnorm_bwd.argtypes = [P, P, P, P, L, I, I, I, F, P, P, P, Z, P]
+        lib.gdn_rmsnorm_bwd.restype = I
         if path is None:
             _lib = lib
         return lib
@@ -423,6 +440,232 @@ def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfi
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_conv_bwd")
     return dict(dx=dx, dw=dw, dbias=dbias, dconv_init=dci)
+
+
+# ----------------------------------------------------------------------------- decayed linear attention
+
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+QUANT = {"none": 0, None: 0, "row": 1, "group": 2}
+NORM_GROUP = 128  # columns to one scale of quant="group"
+
+
+def _dtype_code(t, name, allowed):
+    torch = _torch()
+    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name}: unsupported type {t.dtype}")
+    return code
+
+
+def _rows(t, name, dtype, shape):
+    """A tensor [tokens, heads, 128] whose tokens may be further apart than its heads need (a view into a
+    fused projection). Returns the elements between tokens, 0 when contiguous."""
+    torch = _torch()
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name}: expected a CUDA {dtype} tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    n, heads, d = shape
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d) or st[0] < heads * d or st[0] % 8 != 0:
+        raise ValueError(f"{name}: the heads of a token must be contiguous and tokens a multiple of 8 elements apart")
+    return st[0]
+
+
+def _strides(values):
+    return (ctypes.c_int64 * len(values))(*values) if any(values) else None
+
+
+def la_workspace_size(N: int, T: int, H_k: int, H_v: int, has_init: bool = False, backward: bool = False) -> int:
+    return int(load().gdn_la_workspace_size(N, T, H_k, H_v, 1 if has_init else 0, 1 if backward else 0))
+
+
+def _la_inputs(q, k, v, log_decay, cu_seqlens, init_idx, initial_state, dout=None):
+    torch = _torch()
+    T, Hk, D = q.shape
+    Hv = v.shape[1]
+    N = cu_seqlens.shape[0] - 1
+    strides = [_rows(q, "q", torch.bfloat16, (T, Hk, D)), _rows(k, "k", torch.bfloat16, (T, Hk, D)),
+               _rows(v, "v", torch.bfloat16, (T, Hv, D))]
+    if dout is not None:
+        strides.append(_rows(dout, "dout", torch.bfloat16, (T, Hv, D)))
+    _check(log_decay, "log_decay", torch.float32, (Hv,))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
+    n_init = 0
+    if initial_state is not None:
+        _check(initial_state, "initial_state", torch.float32)
+        if initial_state.dim() != 4 or tuple(initial_state.shape[1:]) != (Hv, D, D):
+            raise ValueError("initial_state: expected [n_init, Hv, 128, 128]")
+        n_init = initial_state.shape[0]
+    if init_idx is not None:
+        _check(init_idx, "init_idx", torch.int32, (N,))
+    return T, Hk, Hv, D, N, n_init, _strides(strides)
+
+
+def la_chunk_fwd(q, k, v, log_decay, cu_seqlens, init_idx=None, initial_state=None, scale: float = 1.0, out=None,
+                 final_state=None, workspace=None, stream=None):
+    """Decayed linear attention over a packed batch: S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale
+    S_t^T q_t. Shapes: q, k [T, Hk, 128] bf16; v [T, Hv, 128] bf16 (tokens may be strided); log_decay [Hv]
+    fp32; cu_seqlens, init_idx and initial_state as in chunk_fwd. Returns (out [T, Hv, 128] bf16,
+    final_state [N, Hv, 128, 128] fp32)."""
+    torch = _torch()
+    T, Hk, Hv, D, N, n_init, strides = _la_inputs(q, k, v, log_decay, cu_seqlens, init_idx, initial_state)
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, Hv, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check(out, "out", torch.bfloat16, (T, Hv, D))
+    if final_state is None:
+        final_state = torch.empty((N, Hv, D, D), dtype=torch.float32, device=dev)
+    else:
+        _check(final_state, "final_state", torch.float32, (N, Hv, D, D))
+    if workspace is None:
+        workspace = torch.empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None), dtype=torch.uint8, device=dev)
+    rc = load().gdn_la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), N, T, Hk, Hv, D, strides,
+                           _ptr(init_idx), _ptr(initial_state), n_init, float(scale), _ptr(out), _ptr(final_state),
+                           _ptr(workspace), workspace.numel(), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_la_fwd")
+    return out, final_state
+
+
+def la_chunk_bwd(q, k, v, log_decay, cu_seqlens, dout, dfinal_state=None, init_idx=None, initial_state=None,
+                 scale: float = 1.0, workspace=None, stream=None, grads=None):
+    """Backward of la_chunk_fwd. Returns dict of dq, dk, dv (bf16) and dinit (fp32; None without a pool).
+    `grads` may hold preallocated outputs under those keys."""
+    torch = _torch()
+    if dout is None:
+        raise ValueError("dout is required")
+    T, Hk, Hv, D, N, n_init, strides = _la_inputs(q, k, v, log_decay, cu_seqlens, init_idx, initial_state, dout)
+    if dfinal_state is not None:
+        _check(dfinal_state, "dfinal_state", torch.float32, (N, Hv, D, D))
+    dev = q.device
+    grads = grads or {}
+
+    def out_buf(key, shape, dtype):
+        t = grads.get(key)
+        return torch.empty(shape, dtype=dtype, device=dev) if t is None else _check(t, key, dtype, shape)
+    dq = out_buf("dq", (T, Hk, D), torch.bfloat16)
+    dk = out_buf("dk", (T, Hk, D), torch.bfloat16)
+    dv = out_buf("dv", (T, Hv, D), torch.bfloat16)
+    dinit = out_buf("dinit", (n_init, Hv, D, D), torch.float32) if n_init > 0 else None
+    if workspace is None:
+        workspace = torch.empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None, True), dtype=torch.uint8,
+                                device=dev)
+    rc = load().gdn_la_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), N, T, Hk, Hv, D, strides,
+                           _ptr(init_idx), _ptr(initial_state), n_init, float(scale), _ptr(dout), _ptr(dfinal_state),
+                           _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinit), _ptr(workspace), workspace.numel(),
+                           _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_la_bwd")
+    return dict(dq=dq, dk=dk, dv=dv, dinit=dinit)
+
+
+def la_decode_step(q, k, v, log_decay, state_pool, state_idx, scale: float = 1.0, out=None, status=None, stream=None):
+    """One token per sequence of the decayed linear attention, in place on the state pool. q, k [B, Hk, 128],
+    v [B, Hv, 128] bf16 or fp16 (sequences may be strided); log_decay [Hv] fp32; state_pool, state_idx and
+    status as in decode_step. Returns out [B, Hv, 128] of the inputs' type."""
+    torch = _torch()
+    B, Hk, D = q.shape
+    Hv = v.shape[1]
+    code = _dtype_code(q, "q", (DTYPE_BF16, DTYPE_FP16))
+    strides = _strides([_rows(q, "q", q.dtype, (B, Hk, D)), _rows(k, "k", q.dtype, (B, Hk, D)),
+                        _rows(v, "v", q.dtype, (B, Hv, D))])
+    _check(log_decay, "log_decay", torch.float32, (Hv,))
+    _check(state_idx, "state_idx", torch.int32, (B,))
+    _check(state_pool, "state_pool", torch.float32)
+    if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (Hv, D, D):
+        raise ValueError("state_pool: expected [n_pool, Hv, 128, 128]")
+    if status is not None:
+        _check(status, "status", torch.int32, (1,))
+    if out is None:
+        out = torch.empty((B, Hv, D), dtype=q.dtype, device=q.device)
+    else:
+        _check(out, "out", q.dtype, (B, Hv, D))
+    rc = load().gdn_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, Hk, Hv, D, code, strides,
+                                   _ptr(state_idx), _ptr(state_pool), state_pool.shape[0], float(scale), _ptr(out),
+                                   _ptr(status), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_la_decode_step")
+    return out
+
+
+# ----------------------------------------------------------------------------- root-mean-square norm
+
+
+def rmsnorm_fwd(x, w, residual=None, eps: float = 1e-6, quant=None, y=None, residual_out=None, scales=None,
+                stream=None):
+    """y = w h / sqrt(mean(h^2) + eps) with h = x + residual, per row of x [T, D] (bf16, fp16 or fp32; w [D] of
+    any of them). quant: None, "row" or "group" (y in float8_e4m3fn with fp32 scales [T, 1] or
+    [T, ceil(D / 128)]). Returns (y, h, scales); h is None without a residual, scales without quant.
+    residual_out may be `residual` itself (in place)."""
+    torch = _torch()
+    if quant not in QUANT:
+        raise ValueError('quant: expected None, "none", "row" or "group"')
+    code, q = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32)), QUANT[quant]
+    T, D = x.shape
+    _check(x, "x", x.dtype, (T, D))
+    wcode = _dtype_code(w, "w", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
+    _check(w, "w", w.dtype, (D,))
+    if residual is not None:
+        _check(residual, "residual", x.dtype, (T, D))
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        else:
+            _check(residual_out, "residual_out", x.dtype, (T, D))
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    ydt = torch.float8_e4m3fn if q else x.dtype
+    if y is None:
+        y = torch.empty((T, D), dtype=ydt, device=x.device)
+    else:
+        _check(y, "y", ydt, (T, D))
+    if q:
+        shape = (T, 1 if q == 1 else -(-D // NORM_GROUP))
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        else:
+            _check(scales, "scales", torch.float32, shape)
+    elif scales is not None:
+        raise ValueError("scales without quant")
+    rc = load().gdn_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(w), T, D, code, wcode, float(eps), _ptr(residual_out),
+                                _ptr(y), q, _ptr(scales), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_rmsnorm_fwd")
+    return y, residual_out, scales
+
+
+def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspace=None, stream=None):
+    """Backward of rmsnorm_fwd from the h it left (x without a residual), dy the gradient of y and dh that of h
+    from elsewhere. Returns (dx [T, D] of h's type: the gradient of x and of the residual, dw [D] fp32)."""
+    torch = _torch()
+    code = _dtype_code(h, "h", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
+    T, D = h.shape
+    _check(h, "h", h.dtype, (T, D))
+    _check(dy, "dy", h.dtype, (T, D))
+    wcode = _dtype_code(w, "w", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
+    _check(w, "w", w.dtype, (D,))
+    if dh is not None:
+        _check(dh, "dh", h.dtype, (T, D))
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _check(dx, "dx", h.dtype, (T, D))
+    if dw is None:
+        dw = torch.empty((D,), dtype=torch.float32, device=h.device)
+    else:
+        _check(dw, "dw", torch.float32, (D,))
+    if workspace is None:
+        workspace = torch.empty(int(load().gdn_rmsnorm_workspace_size(T, D)), dtype=torch.uint8, device=h.device)
+    rc = load().gdn_rmsnorm_bwd(_ptr(h), _ptr(w), _ptr(dy), _ptr(dh), T, D, code, wcode, float(eps), _ptr(dx), _ptr(dw),
+                                _ptr(workspace), workspace.numel(), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_rmsnorm_bwd")
+    return dx, dw
 
 
 def workspace_status(workspace, stream=None) -> int:
