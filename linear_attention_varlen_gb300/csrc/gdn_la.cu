@@ -40,7 +40,6 @@ namespace {
 
 using namespace bw;
 
-constexpr int kLaThreads = 256;
 constexpr float kLaLog2e = 1.44269504f;
 constexpr float kLaCut = -86.f;  // log2 of the smallest row factor
 constexpr uint32_t kTile = 32768;  // 128 x 128 bf16, two 64-column blocks
@@ -48,7 +47,7 @@ constexpr uint32_t kTile = 32768;  // 128 x 128 bf16, two 64-column blocks
 enum { kMapQ = 0, kMapK = 1, kMapV = 2, kMapDo = 3 };
 
 struct LaRole {
-  int mq, mk, mv;           // tensor maps of the role's query, key and value
+  int mq, mk, mv, mo;       // tensor maps of the role's query, key, value and output
   int div_q, div_k, div_v;  // value heads to one head of each
   int rev;                  // walks the document from its end
   int trans;                // its state is stored transposed
@@ -59,8 +58,9 @@ struct LaRole {
 };
 
 struct LaParams {
-  CUtensorMap map[4];
+  CUtensorMap map[4], map_out[3];
   LaRole role[3];
+  int n_roles;
   const float* log_decay;
   const float* start;   // pool of start states
   const float* dfinal;  // gradient of the final states, or null
@@ -69,6 +69,7 @@ struct LaParams {
   int32_t* seg0;
   int32_t* is_src;
   float *slot_f, *slot_r, *fin, *acc;
+  float *end_fwd, *end_rev;  // final states, start-state gradients of the documents; null = not wanted
   const int32_t* cu;
   const int32_t* init_idx;
   int N, T, Hv, n_init, seg_chunks, bwd;
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
         s.nseg = cnt;
         s.src_fwd = (k > 0 || fork) ? -2 : idx;
         s.src_rev = (k < cnt - 1 || src) ? -2 : -1;
-        s.need = ((k < cnt - 1 || src) ? 1 : 0) | ((k > 0 || fork) ? 2 : 0);
+        // a cut document's final state, and its start's gradient where one is wanted, come from the scan
+        s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0);
         p.segs[base + k] = s;
       }
     }
@@ -173,34 +175,57 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
     p.hd->status = kOk;
     p.hd->n_segs = s_base;
     p.hd->scan = s_scan;
+    p.hd->seg_chunks = p.seg_chunks;
   }
 }
 
 // ---------------------------------------------------------------------------------------- chunks
+//
+// One persistent CTA per SM walks items (segment, role, head), chunk by chunk. Warps:
+//   0-7   K/S: the weighted keys into tensor memory (32 tokens at a time, warps 0-3 and 4-7 in turn),
+//         then the state's update in registers and its bf16 copy, the queries' operand
+//   8-11  P/O: the map from Q K^T, in place in tensor memory, and the outputs
+//   then one warp each for the copies and for issuing the products.
+// Per chunk the products are QK^T, Q S, P V (two terms) and K~^T V (three terms), 128^3 each: 1792
+// cycles of the tensor pipe at its nominal rate, against about 3400 cycles of HBM traffic (80 KB) at
+// four value heads to a key head. The vector work (8 K/S warps and 4 P/O warps on the SM's four
+// schedulers) is of the same order, so everything overlaps: QK of the next chunk is issued as soon as
+// this chunk's P V is, and two chunks' tiles are in flight.
+//
+// Tensor memory: Q K^T and P (in place: 32 key tokens' fp32 columns become 16 columns of the first
+// bf16 term and 16 of the second), O, K~^T V, and two stages of three terms of 32 tokens' keys (the
+// states-only walk: two accumulators, four stages).
 
-struct LaSmem {
-  uint8_t q[kTile], k[kTile], v[kTile], s[kTile];
-  float w[kLaChunk];     // weights of the key rows
-  float col[kLaChunk];   // column factors of P''
-  float rowe[kLaChunk];  // log2 of the row factors
-  uint64_t bar_load, bar_mma;
-  uint32_t tmem;
-  int fail;
+constexpr uint32_t kColKV = 0, kColQK = 128, kColO = 256, kKtStage = 48;
+constexpr int kKsWarps = 8;
+// Shared memory is seven tiles of 32 KB. The role's walk keeps a ring of five (a chunk's K, Q, V in this
+// order: Q is done with first, after Q S, then K, then V), the state and the outputs on their way out;
+// the states-only walk a ring of seven (K, V).
+template <bool kOut>
+struct LaShape {
+  static constexpr uint32_t kSlots = kOut ? 5 : 7, kPerChunk = kOut ? 3 : 2, kTileV = kOut ? 2 : 1;
+  // the states-only walk has room for two accumulators and a stage for each quarter of a chunk's keys
+  static constexpr int kKv = kOut ? 1 : 2;
+  static constexpr uint32_t kColKt = kOut ? 384 : 256;
+  static constexpr int kTmaWarp = kOut ? 12 : 8, kKvWarp = kTmaWarp + 1, kOutWarp = kTmaWarp + 2;
+  static constexpr int kThreads = 32 * (kOut ? kOutWarp + 1 : kKvWarp + 1);
 };
 
-constexpr uint32_t kColQK = 0, kColO = 128, kColKV = 256, kColHi = 384, kColLo = 448;
+struct LaSmem {
+  uint8_t tiles[5 * kTile];
+  uint8_t s[kTile], o[kTile];  // the states-only walk's last two tiles
+  float col[kLaChunk];  // column factors of P''
+  uint64_t full[7], free_[7], kt_ready[4], kt_free[4], kv_full[2], kv_free[2];
+  uint64_t col_sync, drain[2];
+  uint64_t qk_full, p_ready[2], s_ready, qs_done, o_full, o_free;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(LaSmem) + 1024 <= 232448, "227 KB of shared memory");
 
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* m, int head, int tok, uint64_t* bar) {
   tma_load_3d(dst, m, 0, head, tok, bar);
   tma_load_3d(static_cast<uint8_t*>(dst) + kTile / 2, m, 64, head, tok, bar);
-}
-
-// D (+)= A B over K = 128, A and B in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, bool b_mn, uint32_t idesc) {
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-    umma_bf16(d, kmajor_step(a, kTile / 2, ks), b_mn ? mnmajor_step(b, ks) : kmajor_step(b, kTile / 2, ks), idesc,
-              ks > 0);
 }
 
 // exp(g x) for a whole number x of steps, the product's rounding error carried along
@@ -211,326 +236,735 @@ __device__ __forceinline__ float decay_pow(float g, float x) {
   return isfinite(lo) ? fmaf(e, lo, e) : e;
 }
 
-// Walks the chunks of one segment. kOut: the whole role (outputs and end state); otherwise only the
-// segment's end state from zero, for the scan.
+// Bounded wait of one role; false once any role of the CTA has given up.
+__device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, LaSmem& sm) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+    if (clock64() - t0 > kWaitBudget) {
+      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, LaSmem& sm) {
+  return __all_sync(0xffffffffu, la_wait(bar, parity, sm));
+}
+
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 16 columns: register 2i is row lane / 4, column 4i + lane % 4, register 2i + 1 row lane / 4 + 8
+__device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  return f2_fma(b, f2_pack(-1.f, -1.f), a);
+}
+// true in one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// the two bf16 of a word as fp32 (exact)
+__device__ __forceinline__ uint64_t f2_of_bf16x2(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t bf16x2_of(uint64_t v) { return pack_bf16x2(f2_lo(v), f2_hi(v)); }
+
+// Tile i (K 0; with outputs Q 1 and V 2, else V 1) of the CTA's x-th chunk in its ring.
 template <bool kOut>
-__global__ void __launch_bounds__(kLaThreads, 1) la_chunk_kernel(const __grid_constant__ LaParams p) {
+struct LaTile {
+  uint32_t slot, use;
+  __device__ __forceinline__ LaTile(uint32_t x, uint32_t i) {
+    const uint32_t t = LaShape<kOut>::kPerChunk * x + i;
+    slot = t % LaShape<kOut>::kSlots;
+    use = t / LaShape<kOut>::kSlots;
+  }
+  __device__ __forceinline__ uint8_t* at(LaSmem& sm) const { return sm.tiles + slot * kTile; }
+  __device__ __forceinline__ bool wait_full(LaSmem& sm) const { return la_wait(&sm.full[slot], use & 1, sm); }
+  __device__ __forceinline__ bool wait_full_all(LaSmem& sm) const { return la_wait_all(&sm.full[slot], use & 1, sm); }
+};
+
+struct LaItem;
+__device__ __forceinline__ bool la_writes_end(const LaParams& p, const LaItem& it);
+// One item of a CTA's walk and what its roles derive from it.
+struct LaItem {
+  LaSeg seg;
+  int sidx, h, nch;
+  int first;  // first chunk that the walk takes
+  int exact;  // chunks from this one on update the state with three terms
+  const LaRole* R;
+  __device__ __forceinline__ bool three(int c) const { return c >= exact; }
+};
+template <bool kOut>
+__device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaItem& it) {
+  it.h = i % p.Hv;
+  const int r = (i / p.Hv) % roles;
+  it.sidx = i / (p.Hv * roles);
+  it.R = &p.role[r];
+  it.seg = p.segs[it.sidx];
+  it.nch = (it.seg.ntok + kLaChunk - 1) / kLaChunk;
+  it.first = 0;
+  const float g = -fmaxf(p.log_decay[it.h], -1e4f) * kLaChunk;  // decay of a chunk
+  if (kOut) {
+    // Three terms where the state itself is an output (of an uncut document; the scan gives a cut one's)
+    // and this chunk's part of it is not below 2^-10 by then; else two, far below the rounding of the
+    // state's bf16 copy that the queries read.
+    it.exact = it.nch;
+    if (la_writes_end(p, it))
+      it.exact = it.nch - (g > 0.f ? (int)fminf(ceilf(7.f / g) + 1.f, (float)it.nch) : it.nch);
+  } else {
+    // chunks whose part is below e^-30 of those after them leave no trace in fp32
+    it.exact = 0;
+    if (g > 0.f) it.first = it.nch - (int)fminf(ceilf(30.f / g) + 1.f, (float)it.nch);
+  }
+  return kOut || ((it.seg.need >> it.R->rev) & 1);
+}
+// whether the walk's last state goes to the role's output: an uncut document's, unless the scan has it
+__device__ __forceinline__ bool la_writes_end(const LaParams& p, const LaItem& it) {
+  return it.R->last != nullptr && it.seg.nseg == 1 && !((it.seg.need >> it.R->rev) & 1);
+}
+// chunk c of the item in its walking order: first token and count (cut from the segment's first token)
+__device__ __forceinline__ int la_chunk_at(const LaItem& it, int c, int& n) {
+  const int ci = it.R->rev ? it.nch - 1 - c : c;
+  n = min(kLaChunk, it.seg.ntok - ci * kLaChunk);
+  return it.seg.tok0 + ci * kLaChunk;
+}
+
+// kOut: the whole role (outputs and end state); otherwise only each segment's end state from zero,
+// for the scan.
+template <bool kOut>
+__global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(const __grid_constant__ LaParams p) {
+  using Sh = LaShape<kOut>;
   extern __shared__ uint8_t raw[];
   LaSmem& sm = *reinterpret_cast<LaSmem*>(smem_align1024(raw));
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int quarter = wid & 3, ch = wid >> 2;  // tensor-memory lanes 32 quarter .. +31, columns 64 ch .. +63
-  const int row = 32 * quarter + lane;
+  const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (wid == Sh::kKvWarp) tmem_alloc(&sm.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < 7; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.free_[i], kOut ? 2 : 1);  // of both issuing warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.kv_free[i], kKsWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      if (i < 2) mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.kt_ready[i], 4);
+      mbar_init(&sm.kt_free[i], 1);
+    }
+    mbar_init(&sm.col_sync, 4);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
+    mbar_init(&sm.qk_full, 1);
+    mbar_init(&sm.qs_done, 1);
+    mbar_init(&sm.s_ready, kKsWarps);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_free, 4);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
   griddep_wait();
   griddep_launch_dependents();
-  const int sidx = blockIdx.x / p.Hv, h = blockIdx.x % p.Hv;
-  if (sidx >= p.hd->n_segs) return;
-  const LaRole& R = p.role[blockIdx.y];
-  const LaSeg seg = p.segs[sidx];
-  if (!kOut && !((seg.need >> R.rev) & 1)) return;
-  if (wid == 0) {
-    tmem_alloc(&sm.tmem, 512);
+  const int roles = p.n_roles;
+  const int n_items = p.hd->n_segs * roles * p.Hv;
+  uint32_t cc = 0;  // chunks this CTA has begun, over all its items
+  bool ok = true;
+  LaItem it;
+
+  if (wid < kKsWarps) {
+    // ------------------------------------------------------------------ keys and state
+    const int quarter = wid & 3, ch = wid >> 2;  // tensor-memory lanes 32 quarter .. +31, columns 64 ch .. +63
+    const int row = 32 * quarter + lane;
+    const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+    float S[64];
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      if (!la_item<kOut>(p, roles, i, it)) continue;
+      const LaRole& R = *it.R;
+      const float g = fmaxf(p.log_decay[it.h], -1e4f);
+      const float a = R.rev ? 0.f : 1.f;
+      const float* sp = nullptr;
+      if constexpr (kOut) {
+        const int src = R.rev ? it.seg.src_rev : it.seg.src_fwd;
+        if (src == -2)
+          sp = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.sidx * p.Hv + it.h) * kLaState;
+        else if (R.rev)
+          sp = p.dfinal ? p.dfinal + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState : nullptr;
+        else if (src >= 0)
+          sp = p.start + ((size_t)src * p.Hv + it.h) * kLaState;
+      }
+      if (!sp) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) S[j] = 0.f;
+      } else if (R.trans) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) S[j] = sp[(size_t)(64 * ch + j) * kDim + row];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + 64 * ch + j);
+          S[j] = x.x;
+          S[j + 1] = x.y;
+          S[j + 2] = x.z;
+          S[j + 3] = x.w;
+        }
+      }
+      // weights of this thread's 16 tokens, in pairs: two fp32, or (two terms) bf16 of the weight and of its rest
+      uint32_t w[16];
+      float lam_hi = 1.f, lam_lo = 0.f;
+      int n_conv = -1, n_state = -1;
+      bool w_three = false;
+      // the weighted keys of half q2 (0, 1) of chunk c (the x-th of the CTA): 32 tokens in three bf16 terms
+      auto convert = [&](int c, uint32_t x, int q2) {
+        int n;
+        la_chunk_at(it, c, n);
+        const LaTile<kOut> tk(x, 0);
+        const bool three = it.three(c);
+        if (q2 == 0) {
+          if (n != n_conv || three != w_three) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int t = 32 * (ch + 2 * (y >> 2)) + 8 * (y & 3) + 2 * (lane & 3);
+              float f[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int u = R.rev ? n - 1 - t - z : t + z;
+                f[z] = t + z < n ? R.s_in * decay_pow(g, (float)(n - u) - a) : 0.f;
+              }
+              w[2 * y] = three ? __float_as_uint(f[0]) : pack_bf16x2(f[0], f[1]);
+              const uint64_t r = f2_sub(f2_pack(f[0], f[1]), f2_of_bf16x2(pack_bf16x2(f[0], f[1])));
+              w[2 * y + 1] = three ? __float_as_uint(f[1]) : bf16x2_of(r);
+            }
+            n_conv = n;
+            w_three = three;
+          }
+          if (!tk.wait_full(sm)) return false;
+          // rows past the chunk belong to another document (or lie outside the tensor): nothing they
+          // hold may reach the products
+          if (n < kLaChunk && ch == 0) {
+            const LaTile<kOut> tv(x, Sh::kTileV);
+            if (!tv.wait_full(sm)) return false;
+            uint8_t* vt = tv.at(sm);
+            for (int e = tid; e < (kLaChunk - n) * 16; e += 128) {
+              const int r = n + e / 16, y = e % 16;
+              *reinterpret_cast<uint4*>(vt + (y >> 3) * (kTile / 2) + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        const uint32_t kb = smem_u32(tk.at(sm));
+        const int t0 = 32 * (ch + 2 * q2);
+        // this half's stage of tensor memory was last used two halves (kOut) or a chunk ago
+        const uint32_t use = kOut ? 2 * x + q2 : x;
+        const int slot = kOut ? ch : ch + 2 * q2;
+        if (use > 0 && !la_wait(&sm.kt_free[slot], (use - 1) & 1, sm)) return false;
+        tc_fence_after();
+        const uint32_t ta = tl + Sh::kColKt + kKtStage * slot;
+        // 16 lanes at a time: the loop stays rolled, since the roles' code together should stay in
+        // the instruction cache
+#pragma unroll 1
+        for (int hl = 0; hl < 2; ++hl) {
+          uint32_t k1[8], k2[8], k3[8];
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) {
+            const int tok = t0 + 16 * tt + ((lane >> 4) & 1) * 8 + (lane & 7);
+            const int dc = 4 * quarter + 2 * hl + ((lane >> 3) & 1);  // 16-byte column of the key's row
+            ldsm_x4_trans(kb + (dc >> 3) * (kTile / 2) + tok * 128 + (((dc ^ tok) & 7) << 4), &k3[4 * tt]);
+          }
+          if (n < kLaChunk) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int t = t0 + 8 * y + 2 * (lane & 3);
+              const uint32_t keep = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
+              k3[2 * y] &= keep;
+              k3[2 * y + 1] &= keep;
+            }
+          }
+          const uint32_t tb = ta + ((uint32_t)(16 * hl) << 16);
+          if (three) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int z = 2 * (y >> 1);
+              const uint64_t f = q2 ? f2_pack(__uint_as_float(w[8 + z]), __uint_as_float(w[9 + z]))
+                                    : f2_pack(__uint_as_float(w[z]), __uint_as_float(w[z + 1]));
+              const uint64_t v = f2_mul(f2_of_bf16x2(k3[y]), f);
+              k1[y] = bf16x2_of(v);
+              const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[y]));
+              k2[y] = bf16x2_of(r1);
+              k3[y] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[y])));
+            }
+            tmem_st16x128_x4(tb + 32, k3);
+          } else {
+            // with w = w1 + w2 in bf16: k w1 rounded, then its exact error (16 bits in all) plus k w2
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int z = 2 * (y >> 1);
+              const uint32_t w1 = q2 ? w[8 + z] : w[z], w2 = q2 ? w[9 + z] : w[z + 1];
+              k1[y] = bf2_mul(k3[y], w1);
+              k2[y] = bf2_fma(k3[y], w2, bf2_fma(k3[y], w1, k1[y] ^ 0x80008000u));
+            }
+          }
+          tmem_st16x128_x4(tb, k1);
+          tmem_st16x128_x4(tb + 16, k2);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.kt_ready[slot]);
+        return true;
+      };
+      // the state as the queries' operand: row = key dimension, 64 value columns to a block
+      auto publish = [&]() {
+        if constexpr (kOut) {
+          uint8_t* sb = sm.s + ch * (kTile / 2);
+#pragma unroll
+          for (int j = 0; j < 64; j += 8)
+            *reinterpret_cast<uint4*>(sb + sw128_off(row, j)) =
+                make_uint4(pack_bf16x2(S[j], S[j + 1]), pack_bf16x2(S[j + 2], S[j + 3]),
+                           pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_ready);
+        }
+      };
+      if (it.nch > 0) {
+        publish();
+        ok = convert(it.first, cc, 0);
+      }
+      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
+        if (!(ok = convert(c, cc, 1))) break;
+        // the next chunk's first half goes ahead of the state: the products can begin on it
+        if (c + 1 < it.nch && !(ok = convert(c + 1, cc + 1, 0))) break;
+        if (!(ok = la_wait(&sm.kv_full[cc % Sh::kKv], (cc / Sh::kKv) & 1, sm))) break;
+        tc_fence_after();
+        int n;
+        la_chunk_at(it, c, n);
+        if (n != n_state) {
+          const float hi = g * (float)n, lo = fmaf(g, (float)n, -hi);
+          lam_hi = expf(hi);
+          lam_lo = isfinite(lo) ? lam_hi * lo : 0.f;
+          n_state = n;
+        }
+        // S = lam^n S + this chunk's part
+        const uint64_t lh = f2_pack(lam_hi, lam_hi), ll = f2_pack(lam_lo, lam_lo);
+        const uint32_t kv = tl + kColKV + 128 * (cc % Sh::kKv) + 64 * ch;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float x[32];
+          tmem_ld32(kv + 32 * half, x);
+          tmem_ld_wait();
+          if (half == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.kv_free[cc % Sh::kKv]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint64_t s2 = f2_pack(S[32 * half + j], S[32 * half + j + 1]);
+            const uint64_t r = f2_fma(s2, lh, f2_fma(s2, ll, f2_pack(x[j], x[j + 1])));
+            S[32 * half + j] = f2_lo(r);
+            S[32 * half + j + 1] = f2_hi(r);
+          }
+        }
+        // the copy of the state that the queries of this chunk read may go
+        if constexpr (kOut)
+          if (!(ok = la_wait(&sm.qs_done, cc & 1, sm))) break;
+        if (c + 1 < it.nch) publish();
+      }
+      if (!ok) break;
+      float* dst = nullptr;
+      if (!kOut)
+        dst = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.sidx * p.Hv + it.h) * kLaState;
+      else if (la_writes_end(p, it))
+        dst = R.last + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState;
+      if (dst) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 4)
+          *reinterpret_cast<float4*>(dst + (size_t)row * kDim + 64 * ch + j) =
+              make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    }
+  } else if (kOut && wid < Sh::kTmaWarp) {
+    // ------------------------------------------------------------------ map and outputs
+    const int quarter = wid & 3, row = 32 * quarter + lane, t128 = tid - 32 * kKsWarps;
+    uint32_t col_phase = 0;
+    auto sync_col = [&]() {  // the four warps meet, with the limit of every other wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.col_sync);
+      const bool met = la_wait(&sm.col_sync, col_phase, sm);
+      col_phase ^= 1;
+      return met;
+    };
+    const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      if (!la_item<kOut>(p, roles, i, it)) continue;
+      const LaRole& R = *it.R;
+      const float g = fmaxf(p.log_decay[it.h], -1e4f), g2 = g * kLaLog2e;
+      const bool strong = g2 * kLaChunk < kLaCut;  // some row factor of a full chunk is below the cut
+      const float a = R.rev ? 0.f : 1.f;
+      int n_prev = -1, ut = 0;
+      float re = 0.f, of = 0.f;
+      for (int c = 0; c < it.nch; ++c, ++cc) {
+        int n;
+        const int tok = la_chunk_at(it, c, n);
+        if (n != n_prev) {
+          const int u = R.rev ? n - 1 - t128 : t128;
+          if (!(ok = sync_col())) break;  // the last chunk's readers of col
+          sm.col[t128] = t128 < n ? R.s_in * exp2f(-g2 * ((float)u + a)) : 0.f;
+          if (!(ok = sync_col())) break;
+          ut = R.rev ? n - 1 - row : row;
+          re = row < n ? fmaxf(g2 * ((float)ut + a), kLaCut) : 0.f;
+          of = R.s_out * exp2f(re);
+          n_prev = n;
+        }
+        if (!(ok = la_wait(&sm.qk_full, cc & 1, sm))) break;
+        tc_fence_after();
+        // P'': row = query token; 32 key tokens at a time, two bf16 terms over the fp32 columns read
+        const int j0 = R.rev ? quarter : 0, j1 = R.rev ? 3 : quarter;  // blocks that hold something
+        float x[32];
+        tmem_ld32(tl + kColQK + 32 * j0, x);
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {
+          uint32_t hi[16], lo[16];
+          if (jb < j0 || jb > j1) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0;
+          } else {
+            tmem_ld_wait();
+            if (strong) {
+              // whole numbers of steps, exact in fp32, before the decay multiplies them
+              const float base = (float)(R.rev ? ut - (n - 1) + 32 * jb : ut - 32 * jb), step = R.rev ? 1.f : -1.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] *= R.s_in * ex2(g2 * fmaxf(fmaf(step, (float)j, base), 0.f) - re);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&sm.col[32 * jb + j]);
+                const uint64_t v0 = f2_mul(f2_pack(x[j], x[j + 1]), f2_pack(f.x, f.y));
+                const uint64_t v1 = f2_mul(f2_pack(x[j + 2], x[j + 3]), f2_pack(f.z, f.w));
+                x[j] = f2_lo(v0);
+                x[j + 1] = f2_hi(v0);
+                x[j + 2] = f2_lo(v1);
+                x[j + 3] = f2_hi(v1);
+              }
+            }
+            if (jb == quarter) {  // the diagonal block
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = (R.rev ? j >= lane : j <= lane) ? x[j] : 0.f;
+            }
+            if (n < kLaChunk) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = 32 * jb + j < n ? x[j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint64_t v = f2_pack(x[2 * j], x[2 * j + 1]);
+              hi[j] = bf16x2_of(v);
+              lo[j] = bf16x2_of(f2_sub(v, f2_of_bf16x2(hi[j])));
+            }
+            if (jb < j1) tmem_ld32(tl + kColQK + 32 * (jb + 1), x);
+          }
+          tmem_st16(tl + kColQK + 32 * jb, hi);
+          tmem_st16(tl + kColQK + 32 * jb + 16, lo);
+          if (jb & 1) {  // two blocks at a time: each hand-over costs a store's latency
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_ready[jb >> 1]);
+          }
+        }
+        if (!(ok = la_wait(&sm.o_full, cc & 1, sm))) break;
+        tc_fence_after();
+        // A warp's 32 rows leave through its own 8 KB of shared memory (two blocks of 64 columns, as the
+        // tensor map stores them); rows of a ragged end, and partial sums, go from registers.
+        const bool whole = 32 * quarter + 32 <= n && !R.out_f32;
+        uint8_t* stage = sm.o + quarter * (kTile / 4);
+        const size_t at = ((size_t)(tok + row) * p.Hv + it.h) * kDim;
+        tmem_ld32(tl + kColO, x);
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {
+          tmem_ld_wait();
+          if (jb == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_free);
+          }
+          if (R.out_f32) {
+            if (row < n) {
+              float* o = static_cast<float*>(R.out) + at + 32 * jb;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(o + j) = make_float4(x[j] * of, x[j + 1] * of, x[j + 2] * of, x[j + 3] * of);
+            }
+            if (jb < 3) tmem_ld32(tl + kColO + 32 * (jb + 1), x);
+          } else {
+            uint32_t b[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) b[j] = pack_bf16x2(x[2 * j] * of, x[2 * j + 1] * of);
+            if (jb < 3) tmem_ld32(tl + kColO + 32 * (jb + 1), x);
+            if (whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(stage + (jb >> 1) * (kTile / 8) + sw128_off(lane, 32 * (jb & 1) + 8 * j)) =
+                    make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+            } else if (row < n) {
+              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(R.out) + at + 32 * jb;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+            }
+          }
+        }
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.map_out[R.mo], stage, 0, it.h, tok + 32 * quarter);
+            tma_store_3d(&p.map_out[R.mo], stage + kTile / 8, 64, it.h, tok + 32 * quarter);
+            bulk_commit_group();
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  } else if (wid == Sh::kTmaWarp) {
+    // ------------------------------------------------------------------ copies
     if (lane == 0) {
-      mbar_init(&sm.bar_load, 1);
-      mbar_init(&sm.bar_mma, 1);
-      fence_mbar_init();
+      uint32_t loaded = 0;
+      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+        if (!la_item<kOut>(p, roles, i, it)) continue;
+        const LaRole& R = *it.R;
+        const int hq = it.h / R.div_q, hk = it.h / R.div_k, hv = it.h / R.div_v;
+        for (int c = it.first; c < it.nch; ++c, ++cc) {
+          int n;
+          const int tok = la_chunk_at(it, c, n);
+#pragma unroll
+          for (uint32_t x = 0; x < Sh::kPerChunk; ++x) {
+            const LaTile<kOut> t(cc, x);
+            if (t.use > 0 && !(ok = la_wait(&sm.free_[t.slot], (t.use - 1) & 1, sm))) break;
+            mbar_arrive_expect_tx(&sm.full[t.slot], kTile);
+            const bool key = x == 0, val = x == Sh::kTileV;
+            load_tile(t.at(sm), &p.map[key ? R.mk : val ? R.mv : R.mq], key ? hk : val ? hv : hq, tok, &sm.full[t.slot]);
+            ++loaded;
+          }
+          if (!ok) break;
+        }
+      }
+      // copies still in flight land before the shared memory goes
+      if (!ok)
+        for (uint32_t x = loaded < Sh::kSlots ? 0 : loaded - Sh::kSlots; x < loaded; ++x)
+          mbar_wait(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1, kWaitBudget);
+    }
+  } else if (wid == Sh::kKvWarp) {
+    // ------------------------------------------------------------------ products of the state
+    // One elected lane issues: elect.sync keeps the branch and the descriptors uniform. With a test of
+    // the lane number each product took 57 cycles to issue (its operands move to uniform registers
+    // one by one), close to the 64 cycles it takes to run; elected it takes under 32. For the same reason
+    // the trip counts and the outcomes of the waits are made uniform (shuffles and votes).
+    const uint32_t id_mn = idesc_bf16(128, 128, 0, 1);
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      if (!la_item<kOut>(p, roles, i, it)) continue;
+      const int first = __shfl_sync(0xffffffffu, it.first, 0), nch = __shfl_sync(0xffffffffu, it.nch, 0);
+      const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
+      for (int c = first; ok && c < nch; ++c, ++cc) {
+        const uint32_t kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
+        const LaTile<kOut> tk(cc, 0), tv(cc, Sh::kTileV);
+        const uint64_t dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
+        const bool three = c >= exact;
+        if (!(ok = tv.wait_full_all(sm) && (kvu == 0 || la_wait_all(&sm.kv_free[kvb], (kvu - 1) & 1, sm)))) break;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
+          const int slot = kOut ? q & 1 : q;
+          if (!(ok = la_wait_all(&sm.kt_ready[slot], kOut ? q >> 1 : cc & 1, sm))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ka = tm + Sh::kColKt + kKtStage * slot;
+            const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              umma_bf16_ts(tkv, ka + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, x & 1), id_mn, x > 0 ? 1u : (uint32_t)q);
+            if (three) {
+              umma_bf16_ts(tkv, ka + 32, mnmajor_step(dvq, 0), id_mn, 1);
+              umma_bf16_ts(tkv, ka + 40, mnmajor_step(dvq, 1), id_mn, 1);
+            }
+            umma_commit(&sm.kt_free[slot]);
+            if (q == 3) {
+              umma_commit(&sm.kv_full[kvb]);
+              umma_commit(&sm.free_[tk.slot]);
+              umma_commit(&sm.free_[tv.slot]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  } else if (kOut && wid == Sh::kOutWarp) {
+    // ------------------------------------------------------------------ products of the outputs
+    const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_mn = idesc_bf16(128, 128, 0, 1);
+    const uint64_t ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      if (!la_item<kOut>(p, roles, i, it)) continue;
+      const int nch = __shfl_sync(0xffffffffu, it.nch, 0);
+      for (int c = 0; ok && c < nch; ++c, ++cc) {
+        const uint32_t par = cc & 1;
+        const LaTile<kOut> tk(cc, 0), tq(cc, 1), tv(cc, Sh::kTileV);
+        const uint64_t dk = kmajor_desc(smem_u32(tk.at(sm)), kTile / 2, 0), dq = kmajor_desc(smem_u32(tq.at(sm)), kTile / 2, 0),
+                       dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
+        if (!(ok = tk.wait_full_all(sm) && tq.wait_full_all(sm))) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16(tm + kColQK, kmajor_step(dq, kTile / 2, ks), kmajor_step(dk, kTile / 2, ks), id_qk, ks > 0);
+          umma_commit(&sm.qk_full);
+          umma_commit(&sm.free_[tk.slot]);
+        }
+        __syncwarp();
+        // the outputs of the chunk before have been read, and this chunk's state is in place
+        if (!(ok = la_wait_all(&sm.s_ready, par, sm) && (cc == 0 || la_wait_all(&sm.o_free, (cc - 1) & 1, sm)))) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16(tm + kColO, kmajor_step(dq, kTile / 2, ks), mnmajor_step(ds, ks), id_mn, ks > 0);
+          umma_commit(&sm.qs_done);
+          umma_commit(&sm.free_[tq.slot]);
+          umma_commit(&sm.free_[tq.slot]);  // for both of its counts
+        }
+        __syncwarp();
+        if (!(ok = tv.wait_full_all(sm))) break;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {  // P V for 32 key tokens
+          if (!(j & 1) && !(ok = la_wait_all(&sm.p_ready[j >> 1], par, sm))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dvj = dv + (uint64_t)j * (4096u >> 4);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              umma_bf16_ts(tm + kColO, tm + kColQK + 32 * j + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvj, x & 1), id_mn, 1);
+            if (j == 3) {
+              umma_commit(&sm.o_full);
+              umma_commit(&sm.free_[tv.slot]);
+            }
+          }
+          __syncwarp();
+        }
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = sm.tmem;
-  const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
-
-  const float g = fmaxf(p.log_decay[h], -1e4f), g2 = g * kLaLog2e;
-  const bool strong = g2 * kLaChunk < kLaCut;  // some row factor of a full chunk is below the cut
-  const float a = R.rev ? 0.f : 1.f;
-  const int hq = h / R.div_q, hk = h / R.div_k, hv = h / R.div_v;
-
-  // the state: row `row`, columns 64 ch .. +63
-  float S[64];
-  const int src = R.rev ? seg.src_rev : seg.src_fwd;
-  const float* sp = nullptr;
-  if constexpr (kOut) {
-    if (src == -2)
-      sp = (R.rev ? p.slot_r : p.slot_f) + ((size_t)sidx * p.Hv + h) * kLaState;
-    else if (R.rev)
-      sp = p.dfinal ? p.dfinal + ((size_t)seg.doc * p.Hv + h) * kLaState : nullptr;
-    else if (src >= 0)
-      sp = p.start + ((size_t)src * p.Hv + h) * kLaState;
-  }
-  if (!sp) {
-#pragma unroll
-    for (int j = 0; j < 64; ++j) S[j] = 0.f;
-  } else if (R.trans) {
-#pragma unroll
-    for (int j = 0; j < 64; ++j) S[j] = sp[(size_t)(64 * ch + j) * kDim + row];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + 64 * ch + j);
-      S[j] = x.x;
-      S[j + 1] = x.y;
-      S[j + 2] = x.z;
-      S[j + 3] = x.w;
-    }
-  }
-
-  const uint32_t idesc_qk = idesc_bf16(128, 128, 0, 0), idesc_mn = idesc_bf16(128, 128, 0, 1);
-  const uint64_t dq = kmajor_desc(smem_u32(sm.q), kTile / 2, 0), dk = kmajor_desc(smem_u32(sm.k), kTile / 2, 0);
-  const uint64_t dv = mnmajor_desc(smem_u32(sm.v), kTile / 2, 0), ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
-
-  const int nch = (seg.ntok + kLaChunk - 1) / kLaChunk;
-  uint32_t ph_load = 0, ph_mma = 0;
-  bool ok = true;
-  for (int c = 0; c < nch; ++c) {
-    // chunks are cut from the segment's first token in both directions
-    const int ci = R.rev ? nch - 1 - c : c;
-    const int tok = seg.tok0 + ci * kLaChunk;
-    const int n = min(kLaChunk, seg.ntok - ci * kLaChunk);
-    if (tid == 0) {
-      mbar_arrive_expect_tx(&sm.bar_load, (kOut ? 3 : 2) * kTile);
-      if constexpr (kOut) load_tile(sm.q, &p.map[R.mq], hq, tok, &sm.bar_load);
-      load_tile(sm.k, &p.map[R.mk], hk, tok, &sm.bar_load);
-      load_tile(sm.v, &p.map[R.mv], hv, tok, &sm.bar_load);
-    }
-    if (tid < kLaChunk) {
-      const int u = R.rev ? n - 1 - tid : tid;
-      const bool in = tid < n;
-      sm.w[tid] = in ? R.s_in * decay_pow(g, (float)(n - u) - a) : 0.f;
-      if constexpr (kOut) {
-        sm.col[tid] = in ? R.s_in * exp2f(-g2 * ((float)u + a)) : 0.f;
-        sm.rowe[tid] = in ? fmaxf(g2 * ((float)u + a), kLaCut) : 0.f;
+  if (sm.abort) {
+    // Products still in flight: everything issued reads shared memory that no copy writes any more; a last
+    // commit of each issuing warp, waited for with a limit, orders them before the tensor memory goes.
+    if (wid == Sh::kKvWarp || (kOut && wid == Sh::kOutWarp)) {
+      if (elect_one()) {
+        umma_commit(&sm.drain[wid - Sh::kKvWarp]);
+        mbar_wait(&sm.drain[wid - Sh::kKvWarp], 0, kWaitBudget);
+        la_status(p.hd, kErrTimeout);
       }
+      __syncwarp();
     }
-    const float lam_hi = expf(g * (float)n);
-    if (!wait_all(&sm.bar_load, ph_load)) {
-      ok = false;
-      break;
-    }
-    ph_load ^= 1;
-    // rows past the chunk belong to another document (or lie outside the tensor): zero them, so
-    // that nothing they hold reaches the products
-    if (n < kLaChunk) {
-      for (int i = tid; i < (kLaChunk - n) * 16; i += kLaThreads) {
-        const int r = n + i / 16, x = i % 16;
-        *reinterpret_cast<uint4*>(sm.v + (x >> 3) * (kTile / 2) + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
-    }
-    // weighted keys, transposed (lane = key dimension), as hi + lo bf16
-    {
-      const uint8_t* kb = sm.k + (row >> 6) * (kTile / 2);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = 64 * ch + 32 * half + 2 * j;
-          const float w0 = sm.w[t], w1 = sm.w[t + 1];
-          float x0 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(kb + sw128_off(t, row & 63)));
-          float x1 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(kb + sw128_off(t + 1, row & 63)));
-          x0 = t < n ? x0 * w0 : 0.f;
-          x1 = t + 1 < n ? x1 * w1 : 0.f;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-          hi[j] = *reinterpret_cast<const uint32_t*>(&b);
-          lo[j] = pack_bf16x2(x0 - __low2float(b), x1 - __high2float(b));
-        }
-        tmem_st16(tl + kColHi + 32 * ch + 16 * half, hi);
-        tmem_st16(tl + kColLo + 32 * ch + 16 * half, lo);
-      }
-      tmem_st_wait();
-    }
-    if constexpr (kOut) {
-      // the state as the queries' operand: row = key dimension, 64 value columns to a block
-      uint8_t* sb = sm.s + ch * (kTile / 2);
-#pragma unroll
-      for (int j = 0; j < 64; j += 8)
-        *reinterpret_cast<uint4*>(sb + sw128_off(row, j)) =
-            make_uint4(pack_bf16x2(S[j], S[j + 1]), pack_bf16x2(S[j + 2], S[j + 3]), pack_bf16x2(S[j + 4], S[j + 5]),
-                       pack_bf16x2(S[j + 6], S[j + 7]));
-    }
-    sync_generic_to_async();
-    if (tid == 0) {
-      if constexpr (kOut) {
-        mma_ss(tm + kColQK, dq, dk, false, idesc_qk);
-        mma_ss(tm + kColO, dq, ds, true, idesc_mn);
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        umma_bf16_ts(tm + kColKV, tm + (i < 8 ? kColHi : kColLo) + 8 * (i & 7), mnmajor_step(dv, i & 7), idesc_mn, i > 0);
-      umma_commit(&sm.bar_mma);
-    }
-    if (!wait_all(&sm.bar_mma, ph_mma)) {
-      ok = false;
-      break;
-    }
-    ph_mma ^= 1;
-    tc_fence_after();
-    if constexpr (kOut) {
-      // P'': row = query token, columns = key tokens; bf16 over the fp32 columns this warp has read
-      const int ut = R.rev ? n - 1 - row : row;
-      const float re = sm.rowe[row];
-      float x[64];
-      tmem_ld32(tl + kColQK + 64 * ch, x);
-      tmem_ld32(tl + kColQK + 64 * ch + 32, x + 32);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 64; ++j) {
-        const int s = 64 * ch + j;
-        const int us = R.rev ? n - 1 - s : s;
-        const float f = strong ? R.s_in * exp2f(g2 * (float)(ut - us) - re) : sm.col[s];
-        x[j] = (us <= ut && s < n) ? x[j] * f : 0.f;
-      }
-      // hi + lo, 32 columns each: a row may have a single term of weight, whose rounding nothing averages
-      uint32_t hi[32], lo[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-        hi[j] = *reinterpret_cast<const uint32_t*>(&b);
-        lo[j] = pack_bf16x2(x[2 * j] - __low2float(b), x[2 * j + 1] - __high2float(b));
-      }
-      tmem_st16(tl + kColQK + 64 * ch, hi);
-      tmem_st16(tl + kColQK + 64 * ch + 16, hi + 16);
-      tmem_st16(tl + kColQK + 64 * ch + 32, lo);
-      tmem_st16(tl + kColQK + 64 * ch + 48, lo + 16);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int ks = i & 7;
-          umma_bf16_ts(tm + kColO, tm + kColQK + 64 * (ks >> 2) + 32 * (i >> 3) + 8 * (ks & 3), mnmajor_step(dv, ks),
-                       idesc_mn, 1);
-        }
-        umma_commit(&sm.bar_mma);
-      }
-    }
-    // S = lam^n S + this chunk's part
-    {
-      const float hi = g * (float)n, lo = fmaf(g, (float)n, -hi);
-      const float lam_lo = isfinite(lo) ? lam_hi * lo : 0.f;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[32];
-        tmem_ld32(tl + kColKV + 64 * ch + 32 * half, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) S[32 * half + j] = fmaf(S[32 * half + j], lam_hi, fmaf(S[32 * half + j], lam_lo, x[j]));
-      }
-    }
-    if constexpr (kOut) {
-      if (!wait_all(&sm.bar_mma, ph_mma)) {
-        ok = false;
-        break;
-      }
-      ph_mma ^= 1;
-      tc_fence_after();
-      float x[64];
-      tmem_ld32(tl + kColO + 64 * ch, x);
-      tmem_ld32(tl + kColO + 64 * ch + 32, x + 32);
-      tmem_ld_wait();
-      const float f = R.s_out * exp2f(sm.rowe[row]);
-      if (row < n) {
-        const size_t at = ((size_t)(tok + row) * p.Hv + h) * kDim + 64 * ch;
-        if (R.out_f32) {
-          float* o = static_cast<float*>(R.out) + at;
-#pragma unroll
-          for (int j = 0; j < 64; j += 4)
-            *reinterpret_cast<float4*>(o + j) = make_float4(x[j] * f, x[j + 1] * f, x[j + 2] * f, x[j + 3] * f);
-        } else {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(R.out) + at;
-#pragma unroll
-          for (int j = 0; j < 64; j += 8)
-            *reinterpret_cast<uint4*>(o + j) =
-                make_uint4(pack_bf16x2(x[j] * f, x[j + 1] * f), pack_bf16x2(x[j + 2] * f, x[j + 3] * f),
-                           pack_bf16x2(x[j + 4] * f, x[j + 5] * f), pack_bf16x2(x[j + 6] * f, x[j + 7] * f));
-        }
-      }
-    }
-    tc_fence_before();
     __syncthreads();
   }
-  if (!ok) {
-    if (tid == 0) la_status(p.hd, kErrTimeout);
-  } else {
-    float* dst = nullptr;
-    if (!kOut)
-      dst = (R.rev ? p.slot_r : p.slot_f) + ((size_t)sidx * p.Hv + h) * kLaState;
-    else if (R.last && (R.rev ? seg.k == 0 : seg.k == seg.nseg - 1))
-      dst = R.last + ((size_t)seg.doc * p.Hv + h) * kLaState;
-    if (dst) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 4)
-        *reinterpret_cast<float4*>(dst + (size_t)row * kDim + 64 * ch + j) =
-            make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-    }
-  }
-  __syncthreads();
-  if (wid == 0) tmem_dealloc(tm, 512);
+  if (wid == Sh::kKvWarp) tmem_dealloc(tm, 512);
 }
 
 // ---------------------------------------------------------------------------------------- scan
 
 // Start states of the segments from their end states from zero, in place: one thread per head and
-// four elements walks the documents in order (blockIdx.y = 1: the state gradients, from the end).
+// four elements walks the documents in order (blockIdx.y = 1: the state gradients, from the end). The
+// slots of a document do not depend on one another, so eight are read ahead of the recurrence.
 __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ LaParams p) {
   griddep_wait();
   griddep_launch_dependents();
   if (!p.hd->scan) return;
   const int h = blockIdx.x / 16, e = ((blockIdx.x % 16) * 256 + threadIdx.x) * 4;
   const float g = fmaxf(p.log_decay[h], -1e4f);
-  auto at = [&](float* base, int i) { return reinterpret_cast<float4*>(base + ((size_t)i * p.Hv + h) * kLaState + e); };
-  auto cat = [&](const float* base, int i) {
-    return *reinterpret_cast<const float4*>(base + ((size_t)i * p.Hv + h) * kLaState + e);
-  };
-  auto step = [&](float4& S, int n, const float4& b) {
-    const float l = decay_pow(g, (float)n);
-    S = make_float4(fmaf(S.x, l, b.x), fmaf(S.y, l, b.y), fmaf(S.z, l, b.z), fmaf(S.w, l, b.w));
-  };
+  const bool rev = blockIdx.y != 0;
+  const int seg_tok = p.hd->seg_chunks * kLaChunk;
+  const size_t per = (size_t)p.Hv * kLaState;
+  const size_t off = (size_t)h * kLaState + e;
+  auto at = [&](float* base, int i) { return reinterpret_cast<float4*>(base + i * per + off); };
+  auto cat = [&](const float* base, int i) { return *reinterpret_cast<const float4*>(base + i * per + off); };
+  auto add = [](const float4& a, const float4& b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); };
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (blockIdx.y == 0) {
-    for (int d = 0; d < p.N; ++d) {
-      const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
-      const int idx = p.init_idx ? p.init_idx[d] : -1;
-      const bool fork = idx >= 0 && idx >= p.n_init, src = p.is_src[d] != 0;
-      if (s1 - s0 == 1 && !fork && !src) continue;
-      float4 S = fork ? *at(p.fin, idx - p.n_init) : idx >= 0 ? cat(p.start, idx) : zero;
-      for (int s = s0; s < s1; ++s) {
-        const int need = p.segs[s].need, n = p.segs[s].ntok;
-        float4* slot = at(p.slot_f, s);
-        const float4 b = (need & 1) ? *slot : zero;
-        *slot = S;
-        step(S, n, b);
-      }
-      if (src) *at(p.fin, d) = S;
+  const float l_full = decay_pow(g, (float)seg_tok);
+  float* slots = rev ? p.slot_r : p.slot_f;
+  if (rev && p.init_idx)
+    for (int d = 0; d < p.N; ++d)
+      if (p.is_src[d]) *at(p.acc, d) = zero;
+  for (int i = 0; i < p.N; ++i) {
+    const int d = rev ? p.N - 1 - i : i;
+    const int s0 = p.seg0[d], cnt = p.seg0[d + 1] - s0;
+    const int idx = p.init_idx ? p.init_idx[d] : -1;
+    const bool fork = idx >= 0 && idx >= p.n_init, src = p.is_src[d] != 0;
+    if (cnt == 1 && !fork && !src) continue;
+    const int len = p.cu[d + 1] - p.cu[d];
+    const float l_last = cnt > 1 ? decay_pow(g, (float)(len - (cnt - 1) * seg_tok)) : decay_pow(g, (float)len);
+    float4 S;
+    if (rev) {
+      S = p.dfinal ? cat(p.dfinal, d) : zero;
+      if (src) S = add(S, *at(p.acc, d));
+    } else {
+      S = fork ? *at(p.fin, idx - p.n_init) : idx >= 0 ? cat(p.start, idx) : zero;
     }
-  } else {
-    if (p.init_idx)
-      for (int d = 0; d < p.N; ++d)
-        if (p.is_src[d]) *at(p.acc, d) = zero;
-    for (int d = p.N - 1; d >= 0; --d) {
-      const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
-      const int idx = p.init_idx ? p.init_idx[d] : -1;
-      const bool fork = idx >= 0 && idx >= p.n_init, src = p.is_src[d] != 0;
-      if (s1 - s0 == 1 && !fork && !src) continue;
-      float4 X = p.dfinal ? cat(p.dfinal, d) : zero;
-      if (src) {
-        const float4 b = *at(p.acc, d);
-        X = make_float4(X.x + b.x, X.y + b.y, X.z + b.z, X.w + b.w);
+    for (int k0 = 0; k0 < cnt; k0 += 8) {
+      float4 b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j;  // in the walk's order; the last one's end state may not have been asked for
+        const bool need = k < cnt && (k < cnt - 1 || (rev ? fork || (cnt > 1 && p.end_rev) : src || cnt > 1));
+        b[j] = need ? *at(slots, rev ? s0 + cnt - 1 - k : s0 + k) : zero;
       }
-      for (int s = s1 - 1; s >= s0; --s) {
-        const int need = p.segs[s].need, n = p.segs[s].ntok;
-        float4* slot = at(p.slot_r, s);
-        const float4 b = (need & 2) ? *slot : zero;
-        *slot = X;
-        step(X, n, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j;
+        if (k >= cnt) break;
+        const int q = rev ? cnt - 1 - k : k;
+        *at(slots, s0 + q) = S;
+        const float l = q == cnt - 1 ? l_last : l_full;
+        S = make_float4(fmaf(S.x, l, b[j].x), fmaf(S.y, l, b[j].y), fmaf(S.z, l, b[j].z), fmaf(S.w, l, b[j].w));
       }
-      if (fork) {
-        float4* acc = at(p.acc, idx - p.n_init);
-        const float4 b = *acc;
-        *acc = make_float4(X.x + b.x, X.y + b.y, X.z + b.z, X.w + b.w);
-      }
+    }
+    if (rev) {
+      if (fork) *at(p.acc, idx - p.n_init) = add(*at(p.acc, idx - p.n_init), S);
+      if (p.end_rev) *at(p.end_rev, d) = S;
+    } else {
+      if (src) *at(p.fin, d) = S;
+      if (p.end_fwd) *at(p.end_fwd, d) = S;
     }
   }
 }
@@ -599,7 +1033,7 @@ int sm_count(int dev) {
 
 bool la_sizes_ok(int N, int T, int H_k, int H_v) {
   return N >= 1 && T >= 0 && H_k >= 1 && H_v >= 1 && H_v % H_k == 0 && (int64_t)T * H_v * kDim <= ((int64_t)1 << 40) &&
-         ((int64_t)N + T / kLaChunk) * H_v < (int64_t)INT32_MAX && H_v <= 4096;
+         ((int64_t)N + T / kLaChunk) * H_v < ((int64_t)1 << 29) && H_v <= 4096;
 }
 
 struct LaCall {
@@ -687,23 +1121,31 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   return GDN_OK;
 }
 
-void la_launch_chunks(const LaParams& p, const LaLayout& L, bool out, int roles, cudaStream_t s) {
-  const dim3 grid((unsigned)(L.smax * p.Hv), roles);
+// 32 rows of one head, as a warp's outputs are staged
+bool la_out_map(CUtensorMap* m, void* out, int T, int Hv) {
+  return make_tmap_bf16_3d(m, out, kDim, Hv, T, kDim * 2, (uint64_t)Hv * kDim * 2, 64, 1, 32);
+}
+
+void la_launch_chunks(LaParams& p, const LaLayout& L, bool out, int roles, int sms, cudaStream_t s) {
+  p.n_roles = roles;
+  const int64_t items = L.smax * p.Hv * roles;
+  const dim3 grid((unsigned)(items < sms ? items : sms));
   const size_t smem = sizeof(LaSmem) + 1024;
   if (out)
-    launch_early(la_chunk_kernel<true>, grid, kLaThreads, smem, s, p);
+    launch_early(la_chunk_kernel<true>, grid, LaShape<true>::kThreads, smem, s, p);
   else
-    launch_early(la_chunk_kernel<false>, grid, kLaThreads, smem, s, p);
+    launch_early(la_chunk_kernel<false>, grid, LaShape<false>::kThreads, smem, s, p);
 }
 
 // Plan, and, where documents are cut or may fork, the segments' start states.
-void la_launch_starts(const LaParams& p, const LaLayout& L, const LaRole& fwd, const LaRole* rev, cudaStream_t s) {
+void la_launch_starts(const LaParams& p, const LaLayout& L, const LaRole& fwd, const LaRole* rev, int sms,
+                      cudaStream_t s) {
   launch_early(la_plan_kernel, dim3(1), kLaPlanThreads, 0, s, p);
   if (!L.seg_chunks && !p.init_idx) return;
   LaParams a = p;
   a.role[0] = fwd;
   if (rev) a.role[1] = *rev;
-  la_launch_chunks(a, L, false, rev ? 2 : 1, s);
+  la_launch_chunks(a, L, false, rev ? 2 : 1, sms, s);
   launch_early(la_scan_kernel, dim3(16 * p.Hv, rev ? 2 : 1), 256, 0, s, a);
 }
 
@@ -735,10 +1177,12 @@ extern "C" int gdn_la_fwd(const void* q, const void* k, const void* v, const flo
   if (rc != GDN_OK) return rc;
   cudaStream_t s = (cudaStream_t)stream;
   const int G = H_v / H_k;
-  const LaRole fwd{kMapQ, kMapK, kMapV, G, G, 1, 0, 0, 1.f, scale, out, 0, final_state};
-  la_launch_starts(p, L, fwd, nullptr, s);
+  const LaRole fwd{kMapQ, kMapK, kMapV, 0, G, G, 1, 0, 0, 1.f, scale, out, 0, final_state};
+  if (T > 0 && !la_out_map(&p.map_out[0], out, T, H_v)) return GDN_ERR_CUDA;
+  p.end_fwd = final_state;
+  la_launch_starts(p, L, fwd, nullptr, sms, s);
   p.role[0] = fwd;
-  la_launch_chunks(p, L, true, 1, s);
+  la_launch_chunks(p, L, true, 1, sms, s);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -766,15 +1210,19 @@ extern "C" int gdn_la_bwd(const void* q, const void* k, const void* v, const flo
   float* part_q = G > 1 ? reinterpret_cast<float*>(ws + L.part_q) : nullptr;
   float* part_k = G > 1 ? reinterpret_cast<float*>(ws + L.part_k) : nullptr;
   float* dstart = n_init > 0 && init_idx ? reinterpret_cast<float*>(ws + L.dstart) : nullptr;
-  const LaRole fwd{kMapQ, kMapK, kMapV, G, G, 1, 0, 0, 1.f, scale, nullptr, 0, nullptr};
-  const LaRole rdq{kMapDo, kMapV, kMapK, 1, 1, G, 0, 1, 1.f, scale, G > 1 ? (void*)part_q : dq, G > 1, nullptr};
-  const LaRole rdv{kMapK, kMapQ, kMapDo, G, G, 1, 1, 0, scale, 1.f, dv, 0, dstart};
-  const LaRole rdk{kMapV, kMapDo, kMapQ, 1, 1, G, 1, 1, scale, 1.f, G > 1 ? (void*)part_k : dk, G > 1, nullptr};
-  la_launch_starts(p, L, fwd, &rdv, s);
+  const LaRole fwd{kMapQ, kMapK, kMapV, 0, G, G, 1, 0, 0, 1.f, scale, nullptr, 0, nullptr};
+  const LaRole rdq{kMapDo, kMapV, kMapK, 0, 1, 1, G, 0, 1, 1.f, scale, G > 1 ? (void*)part_q : dq, G > 1, nullptr};
+  const LaRole rdv{kMapK, kMapQ, kMapDo, 1, G, G, 1, 1, 0, scale, 1.f, dv, 0, dstart};
+  const LaRole rdk{kMapV, kMapDo, kMapQ, 2, 1, 1, G, 1, 1, scale, 1.f, G > 1 ? (void*)part_k : dk, G > 1, nullptr};
+  if (T > 0 && (!la_out_map(&p.map_out[1], dv, T, H_v) ||
+                (G == 1 && (!la_out_map(&p.map_out[0], dq, T, H_v) || !la_out_map(&p.map_out[2], dk, T, H_v)))))
+    return GDN_ERR_CUDA;
+  p.end_rev = dstart;
+  la_launch_starts(p, L, fwd, &rdv, sms, s);
   p.role[0] = rdq;
   p.role[1] = rdv;
   p.role[2] = rdk;
-  la_launch_chunks(p, L, true, 3, s);
+  la_launch_chunks(p, L, true, 3, sms, s);
   if (G > 1 && T > 0) {
     const LaGroupParams gp{part_q, part_k, static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),
                            (int64_t)T * H_k * 32, G};

@@ -27,7 +27,8 @@ struct LaHeader {
   int32_t status;
   int32_t n_segs;
   int32_t scan;          // some document needs the scan over its segments (or a fork)
-  int32_t pad[61];
+  int32_t seg_chunks;    // longest segment (0 = documents are not cut)
+  int32_t pad[60];
 };
 static_assert(sizeof(LaHeader) == 256, "header is 256 bytes");
 
