@@ -16,9 +16,10 @@
 //
 // Precision. The products' operands are bf16. The state is held in fp32 registers, and its update
 // uses the weighted keys as a sum of two bf16 terms (relative error about 2^-17 an element), because
-// the states are fp32 outputs. The map P is a sum of two bf16 terms too: a row may hold a single one
-// of weight (the first tokens, a strong decay), and its rounding would double that of the output. The
-// state that the queries read is rounded to bf16 once: each output averages 128 of those roundings.
+// the states are fp32 outputs. The map P is a sum of two bf16 terms near its diagonal (in the 32 x 32
+// blocks on it): a row may hold a single entry of weight there (the first tokens, a strong decay), and
+// its rounding would double that of the output. The rest of P, and the state that the queries read, are
+// rounded to bf16 once: an output averages many of those roundings.
 //
 // Row factors leave the products: the output is r_t (S^T q_t + sum_s P''_ts v_s) with r_t =
 // max(lam^{u+a}, 2^-86) and P'' = P / r_t, so the query enters the state product as it was loaded.
@@ -182,22 +183,23 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 // ---------------------------------------------------------------------------------------- chunks
 //
 // One persistent CTA per SM walks items (segment, role, head), chunk by chunk. Warps:
-//   0-7   K/S: the weighted keys into tensor memory (32 tokens at a time, warps 0-3 and 4-7 in turn),
-//         then the state's update in registers and its bf16 copy, the queries' operand
-//   8-11  P/O: the map from Q K^T, in place in tensor memory, and the outputs
-//   then one warp each for the copies and for issuing the products.
+//   S (8): the state's update in registers, and its bf16 copy, the queries' operand
+//   K (8): the weighted keys into tensor memory, 32 tokens and 32 dimensions a warp at a time
+//   P/O (8): the map from Q K^T, in place in tensor memory, and the outputs
+//   then a warp for the copies and one that issues the products.
 // Per chunk the products are QK^T, Q S, P V (two terms) and K~^T V (three terms), 128^3 each: 1792
 // cycles of the tensor pipe at its nominal rate, against about 3400 cycles of HBM traffic (80 KB) at
 // four value heads to a key head. The vector work (8 K/S warps and 4 P/O warps on the SM's four
 // schedulers) is of the same order, so everything overlaps: QK of the next chunk is issued as soon as
 // this chunk's P V is, and two chunks' tiles are in flight.
 //
-// Tensor memory: Q K^T and P (in place: 32 key tokens' fp32 columns become 16 columns of the first
-// bf16 term and 16 of the second), O, K~^T V, and two stages of three terms of 32 tokens' keys (the
-// states-only walk: two accumulators, four stages).
+// Tensor memory: Q K^T and P (in place: 16 key tokens' fp32 columns become 8 columns of the first
+// bf16 term and 8 of the second), O, K~^T V, and the weighted keys (four stages of 32 tokens in
+// two terms, or two in three; the states-only walk: two accumulators, four stages in three).
 
-constexpr uint32_t kColKV = 0, kColQK = 128, kColO = 256, kKtStage = 48;
-constexpr int kKsWarps = 8;
+constexpr uint32_t kColKV = 0, kColQK = 128, kColO = 256;
+constexpr int kSWarps = 8, kKWarps = 8, kPoWarps = 8;
+
 // Shared memory is seven tiles of 32 KB. The role's walk keeps a ring of five (a chunk's K, Q, V in this
 // order: Q is done with first, after Q S, then K, then V), the state and the outputs on their way out;
 // the states-only walk a ring of seven (K, V).
@@ -207,21 +209,27 @@ struct LaShape {
   // the states-only walk has room for two accumulators and a stage for each quarter of a chunk's keys
   static constexpr int kKv = kOut ? 1 : 2;
   static constexpr uint32_t kColKt = kOut ? 384 : 256;
-  static constexpr int kTmaWarp = kOut ? 12 : 8, kKvWarp = kTmaWarp + 1, kOutWarp = kTmaWarp + 2;
-  static constexpr int kThreads = 32 * (kOut ? kOutWarp + 1 : kKvWarp + 1);
+  static constexpr int kPo0 = kSWarps + kKWarps, kTmaWarp = kPo0 + (kOut ? kPoWarps : 0), kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (kTmaWarp + 4);  // whole warpgroups, so that registers can move
+  // registers of a thread at launch, and what the warpgroups of each role make of them
+  static constexpr int kRegs = kOut ? 72 : 96, kRegsS = kOut ? 104 : 120, kRegsK = kOut ? 56 : 88, kRegsPo = 72,
+                       kRegsRest = kOut ? 40 : 64;
+  static_assert(2 * kRegsS + 2 * kRegsK + (kOut ? 2 * kRegsPo : 0) + kRegsRest == kThreads / 128 * kRegs,
+                "the split is of what the block was launched with");
 };
 
 struct LaSmem {
   uint8_t tiles[5 * kTile];
   uint8_t s[kTile], o[kTile];  // the states-only walk's last two tiles
-  float col[kLaChunk];  // column factors of P''
+  uint4 w[2][kLaChunk / 2];  // weights of the keys, of a full chunk and of the item's last
+  float col[kLaChunk];       // column factors of P''
   uint64_t full[7], free_[7], kt_ready[4], kt_free[4], kv_full[2], kv_free[2];
-  uint64_t col_sync, drain[2];
+  uint64_t w_sync, col_sync, drain;
   uint64_t qk_full, p_ready[2], s_ready, qs_done, o_full, o_free;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(LaSmem) + 1024 <= 232448, "227 KB of shared memory");
+static_assert(sizeof(LaSmem) <= 232448, "227 KB of shared memory");
 
 __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* m, int head, int tok, uint64_t* bar) {
   tma_load_3d(dst, m, 0, head, tok, bar);
@@ -260,6 +268,14 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
+// tmem_ld32 and its wait as one statement: nothing, not even a spill, can touch the registers in between
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
 // 16 lanes x 16 columns: register 2i is row lane / 4, column 4i + lane % 4, register 2i + 1 row lane / 4 + 8
 __device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -268,6 +284,13 @@ __device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t*
 }
 __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
   return f2_fma(b, f2_pack(-1.f, -1.f), a);
+}
+template <int kTo, int kFrom>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (kTo > kFrom)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTo));
+  else if constexpr (kTo < kFrom)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTo));
 }
 // true in one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
@@ -295,6 +318,12 @@ __device__ __forceinline__ uint64_t f2_of_bf16x2(uint32_t w) {
   return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 __device__ __forceinline__ uint32_t bf16x2_of(uint64_t v) { return pack_bf16x2(f2_lo(v), f2_hi(v)); }
+
+// Columns of the weighted keys of quarter q. With outputs: four stages of two terms, or two of three.
+template <bool kOut>
+__device__ __forceinline__ uint32_t la_kt_col(int q, bool three) {
+  return kOut ? (three ? 48u * (q & 1) : 32u * q) : 48u * q;
+}
 
 // Tile i (K 0; with outputs Q 1 and V 2, else V 1) of the CTA's x-th chunk in its ring.
 template <bool kOut>
@@ -361,32 +390,36 @@ __device__ __forceinline__ int la_chunk_at(const LaItem& it, int c, int& n) {
 template <bool kOut>
 __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(const __grid_constant__ LaParams p) {
   using Sh = LaShape<kOut>;
-  extern __shared__ uint8_t raw[];
-  LaSmem& sm = *reinterpret_cast<LaSmem*>(smem_align1024(raw));
+  extern __shared__ __align__(1024) uint8_t raw[];
+  if ((smem_u32(raw) & 1023u) != 0) {  // the swizzled tiles need it; no room is left to round up
+    if (threadIdx.x == 0) la_status(p.hd, kErrCuda);
+    return;
+  }
+  LaSmem& sm = *reinterpret_cast<LaSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  if (wid == Sh::kKvWarp) tmem_alloc(&sm.tmem, 512);
+  if (wid == Sh::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < 7; ++i) {
       mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.free_[i], kOut ? 2 : 1);  // of both issuing warps
+      mbar_init(&sm.free_[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.kv_full[i], 1);
-      mbar_init(&sm.kv_free[i], kKsWarps);
+      mbar_init(&sm.kv_free[i], kSWarps);
     }
     for (int i = 0; i < 4; ++i) {
       if (i < 2) mbar_init(&sm.p_ready[i], 4);
       mbar_init(&sm.kt_ready[i], 4);
       mbar_init(&sm.kt_free[i], 1);
     }
-    mbar_init(&sm.col_sync, 4);
-    mbar_init(&sm.drain[0], 1);
-    mbar_init(&sm.drain[1], 1);
+    mbar_init(&sm.w_sync, kKWarps);
+    mbar_init(&sm.col_sync, kPoWarps);
+    mbar_init(&sm.drain, 1);
     mbar_init(&sm.qk_full, 1);
     mbar_init(&sm.qs_done, 1);
-    mbar_init(&sm.s_ready, kKsWarps);
+    mbar_init(&sm.s_ready, kSWarps);
     mbar_init(&sm.o_full, 1);
-    mbar_init(&sm.o_free, 4);
+    mbar_init(&sm.o_free, kPoWarps);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -402,17 +435,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   bool ok = true;
   LaItem it;
 
-  if (wid < kKsWarps) {
-    // ------------------------------------------------------------------ keys and state
+  if (wid < kSWarps) {
+    // ------------------------------------------------------------------ state
+    set_regs<Sh::kRegsS, Sh::kRegs>();
     const int quarter = wid & 3, ch = wid >> 2;  // tensor-memory lanes 32 quarter .. +31, columns 64 ch .. +63
+    constexpr int kCols = 64;
     const int row = 32 * quarter + lane;
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
-    float S[64];
+    float S[kCols];
     for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       if (!la_item<kOut>(p, roles, i, it)) continue;
       const LaRole& R = *it.R;
       const float g = fmaxf(p.log_decay[it.h], -1e4f);
-      const float a = R.rev ? 0.f : 1.f;
       const float* sp = nullptr;
       if constexpr (kOut) {
         const int src = R.rev ? it.seg.src_rev : it.seg.src_fwd;
@@ -425,130 +459,28 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       }
       if (!sp) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = 0.f;
+        for (int j = 0; j < kCols; ++j) S[j] = 0.f;
       } else if (R.trans) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = sp[(size_t)(64 * ch + j) * kDim + row];
+        for (int j = 0; j < kCols; ++j) S[j] = sp[(size_t)(kCols * ch + j) * kDim + row];
       } else {
 #pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + 64 * ch + j);
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + kCols * ch + j);
           S[j] = x.x;
           S[j + 1] = x.y;
           S[j + 2] = x.z;
           S[j + 3] = x.w;
         }
       }
-      // weights of this thread's 16 tokens, in pairs: two fp32, or (two terms) bf16 of the weight and of its rest
-      uint32_t w[16];
       float lam_hi = 1.f, lam_lo = 0.f;
-      int n_conv = -1, n_state = -1;
-      bool w_three = false;
-      // the weighted keys of half q2 (0, 1) of chunk c (the x-th of the CTA): 32 tokens in three bf16 terms
-      auto convert = [&](int c, uint32_t x, int q2) {
-        int n;
-        la_chunk_at(it, c, n);
-        const LaTile<kOut> tk(x, 0);
-        const bool three = it.three(c);
-        if (q2 == 0) {
-          if (n != n_conv || three != w_three) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int t = 32 * (ch + 2 * (y >> 2)) + 8 * (y & 3) + 2 * (lane & 3);
-              float f[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int u = R.rev ? n - 1 - t - z : t + z;
-                f[z] = t + z < n ? R.s_in * decay_pow(g, (float)(n - u) - a) : 0.f;
-              }
-              w[2 * y] = three ? __float_as_uint(f[0]) : pack_bf16x2(f[0], f[1]);
-              const uint64_t r = f2_sub(f2_pack(f[0], f[1]), f2_of_bf16x2(pack_bf16x2(f[0], f[1])));
-              w[2 * y + 1] = three ? __float_as_uint(f[1]) : bf16x2_of(r);
-            }
-            n_conv = n;
-            w_three = three;
-          }
-          if (!tk.wait_full(sm)) return false;
-          // rows past the chunk belong to another document (or lie outside the tensor): nothing they
-          // hold may reach the products
-          if (n < kLaChunk && ch == 0) {
-            const LaTile<kOut> tv(x, Sh::kTileV);
-            if (!tv.wait_full(sm)) return false;
-            uint8_t* vt = tv.at(sm);
-            for (int e = tid; e < (kLaChunk - n) * 16; e += 128) {
-              const int r = n + e / 16, y = e % 16;
-              *reinterpret_cast<uint4*>(vt + (y >> 3) * (kTile / 2) + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-        }
-        const uint32_t kb = smem_u32(tk.at(sm));
-        const int t0 = 32 * (ch + 2 * q2);
-        // this half's stage of tensor memory was last used two halves (kOut) or a chunk ago
-        const uint32_t use = kOut ? 2 * x + q2 : x;
-        const int slot = kOut ? ch : ch + 2 * q2;
-        if (use > 0 && !la_wait(&sm.kt_free[slot], (use - 1) & 1, sm)) return false;
-        tc_fence_after();
-        const uint32_t ta = tl + Sh::kColKt + kKtStage * slot;
-        // 16 lanes at a time: the loop stays rolled, since the roles' code together should stay in
-        // the instruction cache
-#pragma unroll 1
-        for (int hl = 0; hl < 2; ++hl) {
-          uint32_t k1[8], k2[8], k3[8];
-#pragma unroll
-          for (int tt = 0; tt < 2; ++tt) {
-            const int tok = t0 + 16 * tt + ((lane >> 4) & 1) * 8 + (lane & 7);
-            const int dc = 4 * quarter + 2 * hl + ((lane >> 3) & 1);  // 16-byte column of the key's row
-            ldsm_x4_trans(kb + (dc >> 3) * (kTile / 2) + tok * 128 + (((dc ^ tok) & 7) << 4), &k3[4 * tt]);
-          }
-          if (n < kLaChunk) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int t = t0 + 8 * y + 2 * (lane & 3);
-              const uint32_t keep = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
-              k3[2 * y] &= keep;
-              k3[2 * y + 1] &= keep;
-            }
-          }
-          const uint32_t tb = ta + ((uint32_t)(16 * hl) << 16);
-          if (three) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int z = 2 * (y >> 1);
-              const uint64_t f = q2 ? f2_pack(__uint_as_float(w[8 + z]), __uint_as_float(w[9 + z]))
-                                    : f2_pack(__uint_as_float(w[z]), __uint_as_float(w[z + 1]));
-              const uint64_t v = f2_mul(f2_of_bf16x2(k3[y]), f);
-              k1[y] = bf16x2_of(v);
-              const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[y]));
-              k2[y] = bf16x2_of(r1);
-              k3[y] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[y])));
-            }
-            tmem_st16x128_x4(tb + 32, k3);
-          } else {
-            // with w = w1 + w2 in bf16: k w1 rounded, then its exact error (16 bits in all) plus k w2
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int z = 2 * (y >> 1);
-              const uint32_t w1 = q2 ? w[8 + z] : w[z], w2 = q2 ? w[9 + z] : w[z + 1];
-              k1[y] = bf2_mul(k3[y], w1);
-              k2[y] = bf2_fma(k3[y], w2, bf2_fma(k3[y], w1, k1[y] ^ 0x80008000u));
-            }
-          }
-          tmem_st16x128_x4(tb, k1);
-          tmem_st16x128_x4(tb + 16, k2);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.kt_ready[slot]);
-        return true;
-      };
+      int n_state = -1;
       // the state as the queries' operand: row = key dimension, 64 value columns to a block
       auto publish = [&]() {
         if constexpr (kOut) {
           uint8_t* sb = sm.s + ch * (kTile / 2);
 #pragma unroll
-          for (int j = 0; j < 64; j += 8)
+          for (int j = 0; j < kCols; j += 8)
             *reinterpret_cast<uint4*>(sb + sw128_off(row, j)) =
                 make_uint4(pack_bf16x2(S[j], S[j + 1]), pack_bf16x2(S[j + 2], S[j + 3]),
                            pack_bf16x2(S[j + 4], S[j + 5]), pack_bf16x2(S[j + 6], S[j + 7]));
@@ -557,14 +489,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           if (lane == 0) mbar_arrive(&sm.s_ready);
         }
       };
-      if (it.nch > 0) {
-        publish();
-        ok = convert(it.first, cc, 0);
-      }
-      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
-        if (!(ok = convert(c, cc, 1))) break;
-        // the next chunk's first half goes ahead of the state: the products can begin on it
-        if (c + 1 < it.nch && !(ok = convert(c + 1, cc + 1, 0))) break;
+      if (it.nch > 0) publish();
+      for (int c = it.first; c < it.nch; ++c, ++cc) {
         if (!(ok = la_wait(&sm.kv_full[cc % Sh::kKv], (cc / Sh::kKv) & 1, sm))) break;
         tc_fence_after();
         int n;
@@ -577,23 +503,21 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         }
         // S = lam^n S + this chunk's part
         const uint64_t lh = f2_pack(lam_hi, lam_hi), ll = f2_pack(lam_lo, lam_lo);
-        const uint32_t kv = tl + kColKV + 128 * (cc % Sh::kKv) + 64 * ch;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int y = 0; y < kCols; y += 32) {
           float x[32];
-          tmem_ld32(kv + 32 * half, x);
-          tmem_ld_wait();
-          if (half == 1) {
+          tmem_ld32_wait(tl + kColKV + 128 * (cc % Sh::kKv) + kCols * ch + y, x);
+          if (y + 32 == kCols) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.kv_free[cc % Sh::kKv]);
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const uint64_t s2 = f2_pack(S[32 * half + j], S[32 * half + j + 1]);
+            const uint64_t s2 = f2_pack(S[y + j], S[y + j + 1]);
             const uint64_t r = f2_fma(s2, lh, f2_fma(s2, ll, f2_pack(x[j], x[j + 1])));
-            S[32 * half + j] = f2_lo(r);
-            S[32 * half + j + 1] = f2_hi(r);
+            S[y + j] = f2_lo(r);
+            S[y + j + 1] = f2_hi(r);
           }
         }
         // the copy of the state that the queries of this chunk read may go
@@ -609,16 +533,148 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         dst = R.last + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState;
       if (dst) {
 #pragma unroll
-        for (int j = 0; j < 64; j += 4)
-          *reinterpret_cast<float4*>(dst + (size_t)row * kDim + 64 * ch + j) =
+        for (int j = 0; j < kCols; j += 4)
+          *reinterpret_cast<float4*>(dst + (size_t)row * kDim + kCols * ch + j) =
               make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+      }
+    }
+  } else if (wid < Sh::kPo0) {
+    // ------------------------------------------------------------------ keys
+    set_regs<Sh::kRegsK, Sh::kRegs>();
+    const int quarter = wid & 3, ch = (wid - kSWarps) >> 2;  // dimensions 32 quarter .. +31, tokens 32 ch and 64 on
+    const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+    uint32_t w_phase = 0;
+    auto sync_w = [&]() {  // these warps meet, with the limit of every other wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.w_sync);
+      const bool met = la_wait(&sm.w_sync, w_phase, sm);
+      w_phase ^= 1;
+      return met;
+    };
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      if (!la_item<kOut>(p, roles, i, it)) continue;
+      const LaRole& R = *it.R;
+      const float g = fmaxf(p.log_decay[it.h], -1e4f);
+      const float a = R.rev ? 0.f : 1.f;
+      // The weights, for full chunks and for the last one: in pairs of tokens, as fp32, and as bf16 of the
+      // weight and of its rest.
+      if (!(ok = sync_w())) break;  // every warp is done with the last item's
+      if (const int e = tid - 32 * kSWarps; e < kLaChunk) {
+        const int t = e & 63, n = e < 64 ? kLaChunk : it.seg.ntok - (it.nch - 1) * kLaChunk;
+        float f[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int tok = 2 * t + z, u = R.rev ? n - 1 - tok : tok;
+          f[z] = tok < n ? R.s_in * decay_pow(g, (float)(n - u) - a) : 0.f;
+        }
+        const uint32_t w1 = pack_bf16x2(f[0], f[1]);
+        const uint64_t r = f2_sub(f2_pack(f[0], f[1]), f2_of_bf16x2(w1));
+        sm.w[e >> 6][t] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), w1, bf16x2_of(r));
+      }
+      if (!(ok = sync_w())) break;
+      // The weighted keys of chunk c (the x-th of the CTA) in two or three bf16 terms, 32 tokens and 32
+      // dimensions a warp: quarter ch + 2 half of the tokens.
+      auto convert = [&](int c, uint32_t x, int half) {
+        int n;
+        la_chunk_at(it, c, n);
+        const LaTile<kOut> tk(x, 0);
+        const bool three = it.three(c);
+        const int q = ch + 2 * half, t0 = 32 * q;
+        if (!tk.wait_full(sm)) return false;
+        // rows past the chunk belong to another document (or lie outside the tensor): nothing they
+        // hold may reach the products
+        if (half == 0 && ch == 0 && n < kLaChunk) {
+          const LaTile<kOut> tv(x, Sh::kTileV);
+          if (!tv.wait_full(sm)) return false;
+          uint8_t* vt = tv.at(sm);
+          for (int e = tid - 32 * kSWarps; e < (kLaChunk - n) * 16; e += 128) {
+            const int r = n + e / 16, y = e % 16;
+            *reinterpret_cast<uint4*>(vt + (y >> 3) * (kTile / 2) + r * 128 + (y & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        // The stage's last reader. Without outputs each quarter has its own stage. With them the chunk's keys
+        // follow the whole of the chunk before (two terms and three are laid out differently), and in three
+        // terms the later half takes the earlier one's place. (Each of these barriers is waited for once in
+        // every one of its phases, so that its parity cannot be mistaken.)
+        if (!kOut || half == 0) {
+          if (x > 0 && !la_wait(&sm.kt_free[kOut ? 3 : q], (x - 1) & 1, sm)) return false;
+        } else if (three && !la_wait(&sm.kt_free[ch], x & 1, sm)) {
+          return false;
+        }
+        tc_fence_after();
+        const uint32_t ta = tl + Sh::kColKt + la_kt_col<kOut>(q, three);
+        const uint4* w = &sm.w[n < kLaChunk][t0 / 2 + (lane & 3)];
+        // this lane's row of the four 8 x 8 blocks that a load takes: 8 tokens (lane bit 4), 8 dimensions (bit 3)
+        const int tok = t0 + ((lane >> 4) & 1) * 8 + (lane & 7), d8 = 4 * quarter + ((lane >> 3) & 1);
+        const uint32_t kr = smem_u32(tk.at(sm)) + (d8 >> 3) * (kTile / 2) + tok * 128;
+        // 16 dimensions (lanes) at a time: the loop stays rolled and the two halves share it, since the
+        // roles' code together should stay in the instruction cache
+#pragma unroll 1
+        for (int hl = 0; hl < 2; ++hl) {
+          uint32_t k1[8], k2[8], k3[8];
+          const uint32_t ka = kr + ((((d8 + 2 * hl) ^ tok) & 7) << 4);
+          ldsm_x4_trans(ka, &k3[0]);
+          ldsm_x4_trans(ka + 16 * 128, &k3[4]);
+          if (n < kLaChunk) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int t = t0 + 8 * y + 2 * (lane & 3);
+              const uint32_t keep = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
+              k3[2 * y] &= keep;
+              k3[2 * y + 1] &= keep;
+            }
+          }
+          const uint32_t tb = ta + ((uint32_t)(16 * hl) << 16);
+          if (three) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4 wy = w[4 * y];
+              const uint64_t f = f2_pack(__uint_as_float(wy.x), __uint_as_float(wy.y));
+#pragma unroll
+              for (int z = 2 * y; z < 2 * y + 2; ++z) {
+                const uint64_t v = f2_mul(f2_of_bf16x2(k3[z]), f);
+                k1[z] = bf16x2_of(v);
+                const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[z]));
+                k2[z] = bf16x2_of(r1);
+                k3[z] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[z])));
+              }
+            }
+            tmem_st16x128_x4(tb + 32, k3);
+          } else if (kOut) {
+            // with w = w1 + w2 in bf16: k w1 rounded, then its exact error (16 bits in all) plus k w2
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4 wy = w[4 * y];
+#pragma unroll
+              for (int z = 2 * y; z < 2 * y + 2; ++z) {
+                k1[z] = bf2_mul(k3[z], wy.z);
+                k2[z] = bf2_fma(k3[z], wy.w, bf2_fma(k3[z], wy.z, k1[z] ^ 0x80008000u));
+              }
+            }
+          }
+          tmem_st16x128_x4(tb, k1);
+          tmem_st16x128_x4(tb + 16, k2);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.kt_ready[q]);
+        return true;
+      };
+      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half)
+          if (!(ok = convert(c, cc, half))) break;
       }
     }
   } else if (kOut && wid < Sh::kTmaWarp) {
     // ------------------------------------------------------------------ map and outputs
-    const int quarter = wid & 3, row = 32 * quarter + lane, t128 = tid - 32 * kKsWarps;
+    set_regs<Sh::kRegsPo, Sh::kRegs>();
+    const int quarter = wid & 3, half = (wid - Sh::kPo0) >> 2;  // query rows 32 quarter .. +31, columns 64 half .. +63
+    const int row = 32 * quarter + lane, ct = tid - 32 * Sh::kPo0;
     uint32_t col_phase = 0;
-    auto sync_col = [&]() {  // the four warps meet, with the limit of every other wait
+    auto sync_col = [&]() {  // the eight warps meet, with the limit of every other wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.col_sync);
       const bool met = la_wait(&sm.col_sync, col_phase, sm);
@@ -629,19 +685,19 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       if (!la_item<kOut>(p, roles, i, it)) continue;
       const LaRole& R = *it.R;
-      const float g = fmaxf(p.log_decay[it.h], -1e4f), g2 = g * kLaLog2e;
+      const float g2 = fmaxf(p.log_decay[it.h], -1e4f) * kLaLog2e;
       const bool strong = g2 * kLaChunk < kLaCut;  // some row factor of a full chunk is below the cut
       const float a = R.rev ? 0.f : 1.f;
       int n_prev = -1, ut = 0;
       float re = 0.f, of = 0.f;
+      if (!(ok = sync_col())) break;  // every warp is done with the last item's
+      if (ct < kLaChunk) sm.col[ct] = R.s_in * exp2f(-g2 * ((float)(R.rev ? kLaChunk - 1 - ct : ct) + a));
+      if (!(ok = sync_col())) break;
+      const uint32_t diag = R.rev ? 0xffffffffu << lane : (2u << lane) - 1u;  // the diagonal block's columns of this row
       for (int c = 0; c < it.nch; ++c, ++cc) {
         int n;
         const int tok = la_chunk_at(it, c, n);
         if (n != n_prev) {
-          const int u = R.rev ? n - 1 - t128 : t128;
-          if (!(ok = sync_col())) break;  // the last chunk's readers of col
-          sm.col[t128] = t128 < n ? R.s_in * exp2f(-g2 * ((float)u + a)) : 0.f;
-          if (!(ok = sync_col())) break;
           ut = R.rev ? n - 1 - row : row;
           re = row < n ? fmaxf(g2 * ((float)ut + a), kLaCut) : 0.f;
           of = R.s_out * exp2f(re);
@@ -649,19 +705,20 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         }
         if (!(ok = la_wait(&sm.qk_full, cc & 1, sm))) break;
         tc_fence_after();
-        // P'': row = query token; 32 key tokens at a time, two bf16 terms over the fp32 columns read
-        const int j0 = R.rev ? quarter : 0, j1 = R.rev ? 3 : quarter;  // blocks that hold something
+        // P'': row = query token; 16 key tokens' fp32 columns become 8 columns of each bf16 term
         float x[32];
-        tmem_ld32(tl + kColQK + 32 * j0, x);
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
-          uint32_t hi[16], lo[16];
-          if (jb < j0 || jb > j1) {
+        for (int jb = 2 * half; jb < 2 * half + 2; ++jb) {
+          const uint32_t tq = tl + kColQK + 32 * jb;
+          if (R.rev ? jb < quarter : jb > quarter) {
+            uint32_t z[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0;
+            for (int j = 0; j < 16; ++j) z[j] = 0;
+            tmem_st16(tq, z);
+            tmem_st16(tq + 16, z);
           } else {
-            tmem_ld_wait();
-            if (strong) {
+            tmem_ld32_wait(tq, x);
+            if (strong || (R.rev && n < kLaChunk)) {
               // whole numbers of steps, exact in fp32, before the decay multiplies them
               const float base = (float)(R.rev ? ut - (n - 1) + 32 * jb : ut - 32 * jb), step = R.rev ? 1.f : -1.f;
 #pragma unroll
@@ -678,88 +735,113 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
                 x[j + 3] = f2_hi(v1);
               }
             }
-            if (jb == quarter) {  // the diagonal block
+            if (jb == quarter) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = (R.rev ? j >= lane : j <= lane) ? x[j] : 0.f;
+              for (int j = 0; j < 32; ++j)
+                if (!(diag & (1u << j))) x[j] = 0.f;
             }
             if (n < kLaChunk) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) x[j] = 32 * jb + j < n ? x[j] : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint64_t v = f2_pack(x[2 * j], x[2 * j + 1]);
-              hi[j] = bf16x2_of(v);
-              lo[j] = bf16x2_of(f2_sub(v, f2_of_bf16x2(hi[j])));
+            for (int k16 = 0; k16 < 2; ++k16) {
+              uint32_t t[16];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                t[j] = pack_bf16x2(x[16 * k16 + 2 * j], x[16 * k16 + 2 * j + 1]);
+                t[8 + j] = 0;
+              }
+              if (jb == quarter) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  t[8 + j] = bf16x2_of(f2_sub(f2_pack(x[16 * k16 + 2 * j], x[16 * k16 + 2 * j + 1]), f2_of_bf16x2(t[j])));
+              }
+              tmem_st16(tq + 16 * k16, t);
             }
-            if (jb < j1) tmem_ld32(tl + kColQK + 32 * (jb + 1), x);
-          }
-          tmem_st16(tl + kColQK + 32 * jb, hi);
-          tmem_st16(tl + kColQK + 32 * jb + 16, lo);
-          if (jb & 1) {  // two blocks at a time: each hand-over costs a store's latency
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_ready[jb >> 1]);
           }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[half]);
+        // The outputs leave through 4 KB of shared memory of the warp's own, as the tensor maps store them
+        // (32 rows of 64 bf16, or of 32 fp32 partial sums at a time); rows of a ragged end go from registers.
+        const bool whole = 32 * quarter + 32 <= n;
+        uint8_t* stage = sm.o + (wid - Sh::kPo0) * (kTile / 8);
+        const size_t at = ((size_t)(tok + row) * p.Hv + it.h) * kDim + 64 * half;
+        if (lane == 0) bulk_wait_read_all();
         if (!(ok = la_wait(&sm.o_full, cc & 1, sm))) break;
         tc_fence_after();
-        // A warp's 32 rows leave through its own 8 KB of shared memory (two blocks of 64 columns, as the
-        // tensor map stores them); rows of a ragged end, and partial sums, go from registers.
-        const bool whole = 32 * quarter + 32 <= n && !R.out_f32;
-        uint8_t* stage = sm.o + quarter * (kTile / 4);
-        const size_t at = ((size_t)(tok + row) * p.Hv + it.h) * kDim;
-        tmem_ld32(tl + kColO, x);
-        if (lane == 0) bulk_wait_read_all();
         __syncwarp();
+        const uint64_t of2 = f2_pack(of, of);
 #pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {
-          tmem_ld_wait();
-          if (jb == 3) {
+        for (int jb = 0; jb < 2; ++jb) {
+          tmem_ld32_wait(tl + kColO + 64 * half + 32 * jb, x);
+          if (jb == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_free);
           }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const uint64_t v = f2_mul(f2_pack(x[j], x[j + 1]), of2);
+            x[j] = f2_lo(v);
+            x[j + 1] = f2_hi(v);
+          }
           if (R.out_f32) {
-            if (row < n) {
+            if (jb == 1) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+            if (whole) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(stage + sw128_off(lane, 8 * j)) =
+                    make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&p.map_out[R.mo], stage, 64 * half + 32 * jb, it.h, tok + 32 * quarter);
+                bulk_commit_group();
+              }
+            } else if (row < n) {
               float* o = static_cast<float*>(R.out) + at + 32 * jb;
 #pragma unroll
               for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<float4*>(o + j) = make_float4(x[j] * of, x[j + 1] * of, x[j + 2] * of, x[j + 3] * of);
+                *reinterpret_cast<float4*>(o + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
             }
-            if (jb < 3) tmem_ld32(tl + kColO + 32 * (jb + 1), x);
           } else {
-            uint32_t b[16];
+            uint4 b[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) b[j] = pack_bf16x2(x[2 * j] * of, x[2 * j + 1] * of);
-            if (jb < 3) tmem_ld32(tl + kColO + 32 * (jb + 1), x);
+            for (int j = 0; j < 4; ++j)
+              b[j] = make_uint4(pack_bf16x2(x[8 * j], x[8 * j + 1]), pack_bf16x2(x[8 * j + 2], x[8 * j + 3]),
+                                pack_bf16x2(x[8 * j + 4], x[8 * j + 5]), pack_bf16x2(x[8 * j + 6], x[8 * j + 7]));
             if (whole) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(stage + (jb >> 1) * (kTile / 8) + sw128_off(lane, 32 * (jb & 1) + 8 * j)) =
-                    make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+              for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage + sw128_off(lane, 32 * jb + 8 * j)) = b[j];
             } else if (row < n) {
               __nv_bfloat16* o = static_cast<__nv_bfloat16*>(R.out) + at + 32 * jb;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]);
+              for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 8 * j) = b[j];
             }
           }
         }
-        if (whole) {
+        if (whole && !R.out_f32) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&p.map_out[R.mo], stage, 0, it.h, tok + 32 * quarter);
-            tma_store_3d(&p.map_out[R.mo], stage + kTile / 8, 64, it.h, tok + 32 * quarter);
+            tma_store_3d(&p.map_out[R.mo], stage, 64 * half, it.h, tok + 32 * quarter);
             bulk_commit_group();
           }
         }
       }
     }
     if (lane == 0) bulk_wait_all();
-  } else if (wid == Sh::kTmaWarp) {
+  } else {
+    set_regs<Sh::kRegsRest, Sh::kRegs>();
+  }
+  if (wid == Sh::kTmaWarp) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
       uint32_t loaded = 0;
@@ -787,98 +869,104 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         for (uint32_t x = loaded < Sh::kSlots ? 0 : loaded - Sh::kSlots; x < loaded; ++x)
           mbar_wait(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1, kWaitBudget);
     }
-  } else if (wid == Sh::kKvWarp) {
-    // ------------------------------------------------------------------ products of the state
+  } else if (wid == Sh::kMmaWarp) {
+    // ------------------------------------------------------------------ products
     // One elected lane issues: elect.sync keeps the branch and the descriptors uniform. With a test of
     // the lane number each product took 57 cycles to issue (its operands move to uniform registers
     // one by one), close to the 64 cycles it takes to run; elected it takes under 32. For the same reason
     // the trip counts and the outcomes of the waits are made uniform (shuffles and votes).
-    const uint32_t id_mn = idesc_bf16(128, 128, 0, 1);
+    // A chunk's order is Q K^T, Q S, the state's product, P V: the two in the middle run while the map is made.
+    const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_mn = idesc_bf16(128, 128, 0, 1);
+    const uint64_t ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
     for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
       if (!la_item<kOut>(p, roles, i, it)) continue;
       const int first = __shfl_sync(0xffffffffu, it.first, 0), nch = __shfl_sync(0xffffffffu, it.nch, 0);
       const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
       for (int c = first; ok && c < nch; ++c, ++cc) {
-        const uint32_t kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
-        const LaTile<kOut> tk(cc, 0), tv(cc, Sh::kTileV);
+        const uint32_t par = cc & 1, kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
+        const LaTile<kOut> tk(cc, 0), tq(cc, 1), tv(cc, Sh::kTileV);
         const uint64_t dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
+        if constexpr (kOut) {
+          const uint64_t dk = kmajor_desc(smem_u32(tk.at(sm)), kTile / 2, 0), dq = kmajor_desc(smem_u32(tq.at(sm)), kTile / 2, 0);
+          if (!(ok = tk.wait_full_all(sm) && tq.wait_full_all(sm))) break;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16(tm + kColQK, kmajor_step(dq, kTile / 2, ks), kmajor_step(dk, kTile / 2, ks), id_qk, ks > 0);
+            umma_commit(&sm.qk_full);
+          }
+          __syncwarp();
+          // this chunk's state is in place, and the outputs of the chunk before have been read
+          if (!(ok = la_wait_all(&sm.s_ready, par, sm) && (cc == 0 || la_wait_all(&sm.o_free, (cc - 1) & 1, sm)))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16(tm + kColO, kmajor_step(dq, kTile / 2, ks), mnmajor_step(ds, ks), id_mn, ks > 0);
+            umma_commit(&sm.qs_done);
+            umma_commit(&sm.free_[tq.slot]);
+          }
+          __syncwarp();
+        }
         const bool three = c >= exact;
         if (!(ok = tv.wait_full_all(sm) && (kvu == 0 || la_wait_all(&sm.kv_free[kvb], (kvu - 1) & 1, sm)))) break;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
-          const int slot = kOut ? q & 1 : q;
-          if (!(ok = la_wait_all(&sm.kt_ready[slot], kOut ? q >> 1 : cc & 1, sm))) break;
+        // Products go out in groups as large as their operands allow: the pipe drains while this warp waits.
+        if (kOut && !three) {
+          if (!(ok = la_wait_all(&sm.kt_ready[0], par, sm) && la_wait_all(&sm.kt_ready[1], par, sm) &&
+                     la_wait_all(&sm.kt_ready[2], par, sm) && la_wait_all(&sm.kt_ready[3], par, sm)))
+            break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t ka = tm + Sh::kColKt + kKtStage * slot;
-            const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
+            const uint32_t ka = tm + Sh::kColKt;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              umma_bf16_ts(tkv, ka + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, x & 1), id_mn, x > 0 ? 1u : (uint32_t)q);
-            if (three) {
-              umma_bf16_ts(tkv, ka + 32, mnmajor_step(dvq, 0), id_mn, 1);
-              umma_bf16_ts(tkv, ka + 40, mnmajor_step(dvq, 1), id_mn, 1);
-            }
-            umma_commit(&sm.kt_free[slot]);
-            if (q == 3) {
-              umma_commit(&sm.kv_full[kvb]);
-              umma_commit(&sm.free_[tk.slot]);
-              umma_commit(&sm.free_[tv.slot]);
-            }
+            for (int x = 0; x < 16; ++x)  // two terms of eight steps of 16 tokens
+              umma_bf16_ts(tkv, ka + la_kt_col<kOut>(x >> 2, false) + 16 * ((x >> 1) & 1) + 8 * (x & 1),
+                           mnmajor_step(dv, 2 * (x >> 2) + (x & 1)), id_mn, x > 0);
+            umma_commit(&sm.kv_full[kvb]);
+            umma_commit(&sm.free_[tk.slot]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) umma_commit(&sm.kt_free[q]);
           }
           __syncwarp();
-        }
-      }
-    }
-  } else if (kOut && wid == Sh::kOutWarp) {
-    // ------------------------------------------------------------------ products of the outputs
-    const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_mn = idesc_bf16(128, 128, 0, 1);
-    const uint64_t ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      if (!la_item<kOut>(p, roles, i, it)) continue;
-      const int nch = __shfl_sync(0xffffffffu, it.nch, 0);
-      for (int c = 0; ok && c < nch; ++c, ++cc) {
-        const uint32_t par = cc & 1;
-        const LaTile<kOut> tk(cc, 0), tq(cc, 1), tv(cc, Sh::kTileV);
-        const uint64_t dk = kmajor_desc(smem_u32(tk.at(sm)), kTile / 2, 0), dq = kmajor_desc(smem_u32(tq.at(sm)), kTile / 2, 0),
-                       dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
-        if (!(ok = tk.wait_full_all(sm) && tq.wait_full_all(sm))) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_bf16(tm + kColQK, kmajor_step(dq, kTile / 2, ks), kmajor_step(dk, kTile / 2, ks), id_qk, ks > 0);
-          umma_commit(&sm.qk_full);
-          umma_commit(&sm.free_[tk.slot]);
-        }
-        __syncwarp();
-        // the outputs of the chunk before have been read, and this chunk's state is in place
-        if (!(ok = la_wait_all(&sm.s_ready, par, sm) && (cc == 0 || la_wait_all(&sm.o_free, (cc - 1) & 1, sm)))) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_bf16(tm + kColO, kmajor_step(dq, kTile / 2, ks), mnmajor_step(ds, ks), id_mn, ks > 0);
-          umma_commit(&sm.qs_done);
-          umma_commit(&sm.free_[tq.slot]);
-          umma_commit(&sm.free_[tq.slot]);  // for both of its counts
-        }
-        __syncwarp();
-        if (!(ok = tv.wait_full_all(sm))) break;
+        } else {
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {  // P V for 32 key tokens
-          if (!(j & 1) && !(ok = la_wait_all(&sm.p_ready[j >> 1], par, sm))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t dvj = dv + (uint64_t)j * (4096u >> 4);
+          for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
+            if (!(ok = la_wait_all(&sm.kt_ready[q], par, sm))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t ka = tm + Sh::kColKt + la_kt_col<kOut>(q, true);
+              const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              umma_bf16_ts(tm + kColO, tm + kColQK + 32 * j + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvj, x & 1), id_mn, 1);
-            if (j == 3) {
-              umma_commit(&sm.o_full);
-              umma_commit(&sm.free_[tv.slot]);
+              for (int x = 0; x < 6; ++x)
+                umma_bf16_ts(tkv, ka + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, x & 1), id_mn, x > 0 ? 1u : (uint32_t)q);
+              umma_commit(&sm.kt_free[q]);
+              if (q == 3) {
+                umma_commit(&sm.kv_full[kvb]);
+                umma_commit(&sm.free_[tk.slot]);
+                if (!kOut) umma_commit(&sm.free_[tv.slot]);
+              }
             }
+            __syncwarp();
           }
-          __syncwarp();
+        }
+        if (!ok) break;
+        if constexpr (kOut) {
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {  // P V for 64 key tokens
+            if (!(ok = la_wait_all(&sm.p_ready[j], par, sm))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dvj = dv + (uint64_t)j * (8192u >> 4);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)  // two terms of four steps
+                umma_bf16_ts(tm + kColO, tm + kColQK + 64 * j + 16 * (x & 3) + 8 * (x >> 2), mnmajor_step(dvj, x & 3), id_mn, 1);
+              if (j == 1) {
+                umma_commit(&sm.o_full);
+                umma_commit(&sm.free_[tv.slot]);
+              }
+            }
+            __syncwarp();
+          }
         }
       }
     }
@@ -888,18 +976,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   tc_fence_after();
   if (sm.abort) {
     // Products still in flight: everything issued reads shared memory that no copy writes any more; a last
-    // commit of each issuing warp, waited for with a limit, orders them before the tensor memory goes.
-    if (wid == Sh::kKvWarp || (kOut && wid == Sh::kOutWarp)) {
+    // commit, waited for with a limit, orders them before the tensor memory goes.
+    if (wid == Sh::kMmaWarp) {
       if (elect_one()) {
-        umma_commit(&sm.drain[wid - Sh::kKvWarp]);
-        mbar_wait(&sm.drain[wid - Sh::kKvWarp], 0, kWaitBudget);
+        umma_commit(&sm.drain);
+        mbar_wait(&sm.drain, 0, kWaitBudget);
         la_status(p.hd, kErrTimeout);
       }
       __syncwarp();
     }
     __syncthreads();
   }
-  if (wid == Sh::kKvWarp) tmem_dealloc(tm, 512);
+  if (wid == Sh::kMmaWarp) tmem_dealloc(tm, 512);
 }
 
 // ---------------------------------------------------------------------------------------- scan
@@ -1088,7 +1176,7 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   *L = la_layout(c.N, c.T, c.Hk, c.Hv, c.init_idx != nullptr, c.bwd, *num_sms);
   if (c.ws_bytes < L->total) return GDN_ERR_WORKSPACE;
   if (!g_la_setup.done(dev)) {
-    const int smem = sizeof(LaSmem) + 1024;
+    const int smem = sizeof(LaSmem);
     if (cudaFuncSetAttribute(la_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaFuncSetAttribute(la_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return GDN_ERR_CUDA;
@@ -1121,7 +1209,10 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   return GDN_OK;
 }
 
-// 32 rows of one head, as a warp's outputs are staged
+// 32 rows of one head, as a warp's outputs (or fp32 partial sums) are staged
+bool la_part_map(CUtensorMap* m, void* out, int T, int Hv) {
+  return make_tmap_f32_3d(m, out, kDim, Hv, T, kDim * 4, (uint64_t)Hv * kDim * 4, 32, 1, 32);
+}
 bool la_out_map(CUtensorMap* m, void* out, int T, int Hv) {
   return make_tmap_bf16_3d(m, out, kDim, Hv, T, kDim * 2, (uint64_t)Hv * kDim * 2, 64, 1, 32);
 }
@@ -1130,7 +1221,7 @@ void la_launch_chunks(LaParams& p, const LaLayout& L, bool out, int roles, int s
   p.n_roles = roles;
   const int64_t items = L.smax * p.Hv * roles;
   const dim3 grid((unsigned)(items < sms ? items : sms));
-  const size_t smem = sizeof(LaSmem) + 1024;
+  const size_t smem = sizeof(LaSmem);
   if (out)
     launch_early(la_chunk_kernel<true>, grid, LaShape<true>::kThreads, smem, s, p);
   else
@@ -1215,7 +1306,8 @@ extern "C" int gdn_la_bwd(const void* q, const void* k, const void* v, const flo
   const LaRole rdv{kMapK, kMapQ, kMapDo, 1, G, G, 1, 1, 0, scale, 1.f, dv, 0, dstart};
   const LaRole rdk{kMapV, kMapDo, kMapQ, 2, 1, 1, G, 1, 1, scale, 1.f, G > 1 ? (void*)part_k : dk, G > 1, nullptr};
   if (T > 0 && (!la_out_map(&p.map_out[1], dv, T, H_v) ||
-                (G == 1 && (!la_out_map(&p.map_out[0], dq, T, H_v) || !la_out_map(&p.map_out[2], dk, T, H_v)))))
+                (G == 1 && (!la_out_map(&p.map_out[0], dq, T, H_v) || !la_out_map(&p.map_out[2], dk, T, H_v))) ||
+                (G > 1 && (!la_part_map(&p.map_out[0], part_q, T, H_v) || !la_part_map(&p.map_out[2], part_k, T, H_v)))))
     return GDN_ERR_CUDA;
   p.end_rev = dstart;
   la_launch_starts(p, L, fwd, &rdv, sms, s);
