@@ -68,12 +68,13 @@ struct LaParams {
   LaHeader* hd;
   LaSeg* segs;
   int32_t* seg0;
+  int32_t* order;  // segments, the longest first
   int32_t* is_src;
   float *slot_f, *slot_r, *fin, *acc;
   float *end_fwd, *end_rev;  // final states, start-state gradients of the documents; null = not wanted
   const int32_t* cu;
   const int32_t* init_idx;
-  int N, T, Hv, n_init, seg_chunks, bwd;
+  int N, T, Hv, n_init, min_seg, num_sms, bwd;
 };
 
 __device__ __forceinline__ void la_status(LaHeader* hd, int code) { atomicCAS(&hd->status, 0, code); }
@@ -82,18 +83,40 @@ __device__ __forceinline__ void la_status(LaHeader* hd, int code) { atomicCAS(&h
 
 constexpr int kLaPlanThreads = 1024;
 
-// One CTA: checks cu_seqlens and init_idx and cuts the documents into segments.
+// Time of a call with documents cut to segments of L chunks (0 = uncut), in chunks of the output walk. From the
+// documents: chunks in all and in the cut ones, segments in all and in the cut ones, the longest segment.
+// Measured: an item's start (its state, the first tiles, the pipeline's fill) costs about one chunk; a chunk of
+// the states-only walk 0.6; a cut segment's slot, written, scanned in place and read, three; the two extra
+// kernels four. Items are drawn longest first, so the last ones end about half a segment apart, unless all fit
+// the SMs at once.
+__device__ __forceinline__ float la_plan_cost(const LaParams& p, int chunks, int cut_chunks, int segs, int cut_segs,
+                                              int longest) {
+  const float roles = p.bwd ? 3.f : 1.f, passes = p.bwd ? 2.f : 1.f, sms = (float)p.num_sms, Hv = (float)p.Hv;
+  auto walk = [&](float items, float work, float seg) {
+    return items <= sms ? seg : fmaxf(work / sms + 0.5f * seg, seg);
+  };
+  float t = walk(roles * Hv * segs, roles * Hv * (chunks + (float)segs), longest + 1.f);
+  if (cut_segs)
+    t += 4.f + walk(passes * Hv * cut_segs, passes * Hv * (0.6f * cut_chunks + 3.f * cut_segs), 0.6f * longest + 3.f);
+  return t;
+}
+
+// One CTA: checks cu_seqlens and init_idx, chooses the segments' length among 32 candidates (one to a warp) and
+// cuts the documents into segments.
 __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_constant__ LaParams p) {
   griddep_wait();  // the previous call on this stream may still read the workspace
   griddep_launch_dependents();
-  __shared__ int s_warp[32], s_base, s_bad, s_scan;
+  __shared__ int s_warp[32], s_base, s_bad, s_scan, s_len, s_hist[64];
+  __shared__ float s_cost[32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) {
     s_base = 0;
     s_bad = 0;
     s_scan = 0;
   }
-  for (int i = tid; i < p.N; i += kLaPlanThreads) p.is_src[i] = 0;
+  if (tid < 64) s_hist[tid] = 0;
+  if (p.init_idx)
+    for (int i = tid; i < p.N; i += kLaPlanThreads) p.is_src[i] = 0;
   __syncthreads();
   bool bad = false;
   for (int i = tid; i < p.N; i += kLaPlanThreads) {
@@ -119,7 +142,58 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
     }
     return;
   }
-  const int seg_tok = p.seg_chunks * kLaChunk;
+  if (p.min_seg) {
+    // candidates: 16 lengths spread over the logarithm, 15 from the one that gives an item to each SM, uncut
+    const float all = (float)(p.T / kLaChunk + 1);
+    int L = 0;
+    if (wid < 16)
+      L = (int)((float)p.min_seg * exp2f((float)wid / 16.f * log2f(fmaxf(1.f, all / (float)p.min_seg))));
+    else if (wid < 31)
+      L = (int)ceilf(all * (float)p.Hv * (p.bwd ? 3.f : 1.f) / (float)p.num_sms) + wid - 16;
+    if (wid < 31) L = max(L, p.min_seg);
+    int chunks = 0, cut_chunks = 0, segs = 0, cut_segs = 0, longest = 0;
+    for (int i = lane; i < p.N; i += 32) {
+      const int n = (p.cu[i + 1] - p.cu[i] + kLaChunk - 1) / kLaChunk;
+      const bool cut = L && n > L;
+      const int k = cut ? (n + L - 1) / L : 1;
+      chunks += n;
+      segs += k;
+      if (cut) {
+        cut_chunks += n;
+        cut_segs += k;
+      }
+      longest = max(longest, cut ? L : n);
+    }
+    chunks = __reduce_add_sync(0xffffffffu, chunks);
+    cut_chunks = __reduce_add_sync(0xffffffffu, cut_chunks);
+    segs = __reduce_add_sync(0xffffffffu, segs);
+    cut_segs = __reduce_add_sync(0xffffffffu, cut_segs);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      s_cost[wid] = la_plan_cost(p, chunks, cut_chunks, segs, cut_segs, longest);
+      s_warp[wid] = L;
+    }
+    __syncthreads();
+    if (wid == 0) {
+      float c = s_cost[lane];
+      int best = lane;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float c2 = __shfl_xor_sync(0xffffffffu, c, o);
+        const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+        if (c2 < c || (c2 == c && b2 > best)) {  // uncut where it is no worse
+          c = c2;
+          best = b2;
+        }
+      }
+      if (lane == 0) s_len = s_warp[best];
+    }
+    __syncthreads();
+  } else if (tid == 0) {
+    s_len = 0;
+  }
+  __syncthreads();
+  const int seg_tok = s_len * kLaChunk;
   for (int i0 = 0; i0 < p.N; i0 += kLaPlanThreads) {
     const int i = i0 + tid;
     int b = 0, len = 0, cnt = 0;
@@ -151,7 +225,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
     if (i < p.N) {
       p.seg0[i] = base;
       const int idx = p.init_idx ? p.init_idx[i] : -1;
-      const bool fork = idx >= p.n_init && idx >= 0, src = p.is_src[i] != 0;
+      const bool fork = idx >= p.n_init && idx >= 0, src = p.init_idx && p.is_src[i] != 0;
       if (cnt > 1 || fork || src) s_scan = 1;
       for (int k = 0; k < cnt; ++k) {
         LaSeg s;
@@ -165,18 +239,38 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
         // a cut document's final state, and its start's gradient where one is wanted, come from the scan
         s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0);
         p.segs[base + k] = s;
+        atomicAdd(&s_hist[63 - min(63, (s.ntok + kLaChunk - 1) / kLaChunk)], 1);
       }
     }
     __syncthreads();
     if (tid == 0) s_base += total;
     __syncthreads();
   }
+  // the order in which items are drawn: by length, the longest first (a length's order among itself is free:
+  // no result depends on it)
+  if (wid == 0) {
+    const int h0 = s_hist[2 * lane], h1 = s_hist[2 * lane + 1];
+    int x = h0 + h1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += t;
+    }
+    s_hist[2 * lane] = x - h0 - h1;
+    s_hist[2 * lane + 1] = x - h1;
+  }
+  __syncthreads();
+  const int n_segs = s_base;
+  for (int s = tid; s < n_segs; s += kLaPlanThreads)
+    p.order[atomicAdd(&s_hist[63 - min(63, (p.segs[s].ntok + kLaChunk - 1) / kLaChunk)], 1)] = s;
   if (tid == 0) {
-    p.seg0[p.N] = s_base;
+    p.seg0[p.N] = n_segs;
     p.hd->status = kOk;
-    p.hd->n_segs = s_base;
+    p.hd->n_segs = n_segs;
     p.hd->scan = s_scan;
-    p.hd->seg_chunks = p.seg_chunks;
+    p.hd->seg_chunks = s_len;
+    p.hd->ticket[0] = 0;
+    p.hd->ticket[1] = 0;
   }
 }
 
@@ -184,7 +278,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 //
 // One persistent CTA per SM walks items (segment, role, head), chunk by chunk. Warps:
 //   S (8): the state's update in registers, and its bf16 copy, the queries' operand
-//   K (8): the weighted keys into tensor memory, 32 tokens and 32 dimensions a warp at a time
+//   K (4, without outputs 8): the weighted keys into tensor memory, 32 tokens and 32 dimensions a warp at a time
 //   P/O (8): the map from Q K^T, in place in tensor memory, and the outputs
 //   then a warp for the copies and one that issues the products.
 // Per chunk the products are QK^T, Q S, P V (two terms) and K~^T V (three terms), 128^3 each: 1792
@@ -198,7 +292,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 // two terms, or two in three; the states-only walk: two accumulators, four stages in three).
 
 constexpr uint32_t kColKV = 0, kColQK = 128, kColO = 256;
-constexpr int kSWarps = 8, kKWarps = 8, kPoWarps = 8;
+constexpr int kSWarps = 8, kPoWarps = 8;
 
 // Shared memory is seven tiles of 32 KB. The role's walk keeps a ring of five (a chunk's K, Q, V in this
 // order: Q is done with first, after Q S, then K, then V), the state and the outputs on their way out;
@@ -209,12 +303,12 @@ struct LaShape {
   // the states-only walk has room for two accumulators and a stage for each quarter of a chunk's keys
   static constexpr int kKv = kOut ? 1 : 2;
   static constexpr uint32_t kColKt = kOut ? 384 : 256;
-  static constexpr int kPo0 = kSWarps + kKWarps, kTmaWarp = kPo0 + (kOut ? kPoWarps : 0), kMmaWarp = kTmaWarp + 1;
+  static constexpr int kKWarps = kOut ? 4 : 8, kPo0 = kSWarps + kKWarps, kTmaWarp = kPo0 + (kOut ? kPoWarps : 0), kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (kTmaWarp + 4);  // whole warpgroups, so that registers can move
   // registers of a thread at launch, and what the warpgroups of each role make of them
-  static constexpr int kRegs = kOut ? 72 : 96, kRegsS = kOut ? 104 : 120, kRegsK = kOut ? 56 : 88, kRegsPo = 72,
+  static constexpr int kRegs = kOut ? 80 : 96, kRegsS = kOut ? 104 : 120, kRegsK = kOut ? 72 : 88, kRegsPo = 80,
                        kRegsRest = kOut ? 40 : 64;
-  static_assert(2 * kRegsS + 2 * kRegsK + (kOut ? 2 * kRegsPo : 0) + kRegsRest == kThreads / 128 * kRegs,
+  static_assert(2 * kRegsS + kKWarps / 4 * kRegsK + (kOut ? 2 * kRegsPo : 0) + kRegsRest == kThreads / 128 * kRegs,
                 "the split is of what the block was launched with");
 };
 
@@ -224,10 +318,11 @@ struct LaSmem {
   uint4 w[2][kLaChunk / 2];  // weights of the keys, of a full chunk and of the item's last
   float col[kLaChunk];       // column factors of P''
   uint64_t full[7], free_[7], kt_ready[4], kt_free[4], kv_full[2], kv_free[2];
-  uint64_t w_sync, col_sync, drain;
+  uint64_t w_sync, col_sync, drain, item_full[2], item_free[2];
   uint64_t qk_full, p_ready[2], s_ready, qs_done, o_full, o_free;
   uint32_t tmem;
   int abort;
+  int item[2];  // what the copy warp has drawn
 };
 static_assert(sizeof(LaSmem) <= 232448, "227 KB of shared memory");
 
@@ -354,7 +449,7 @@ template <bool kOut>
 __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaItem& it) {
   it.h = i % p.Hv;
   const int r = (i / p.Hv) % roles;
-  it.sidx = i / (p.Hv * roles);
+  it.sidx = p.order[i / (p.Hv * roles)];
   it.R = &p.role[r];
   it.seg = p.segs[it.sidx];
   it.nch = (it.seg.ntok + kLaChunk - 1) / kLaChunk;
@@ -397,6 +492,11 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   }
   LaSmem& sm = *reinterpret_cast<LaSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if constexpr (!kOut) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (!p.hd->scan) return;  // no document is cut, none is forked
+  }
   if (wid == Sh::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < 7; ++i) {
@@ -405,6 +505,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.kv_full[i], 1);
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_free[i], Sh::kTmaWarp + 1);  // the other warps that work
       mbar_init(&sm.kv_free[i], kSWarps);
     }
     for (int i = 0; i < 4; ++i) {
@@ -412,7 +514,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       mbar_init(&sm.kt_ready[i], 4);
       mbar_init(&sm.kt_free[i], 1);
     }
-    mbar_init(&sm.w_sync, kKWarps);
+    mbar_init(&sm.w_sync, Sh::kKWarps);
     mbar_init(&sm.col_sync, kPoWarps);
     mbar_init(&sm.drain, 1);
     mbar_init(&sm.qk_full, 1);
@@ -427,10 +529,26 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
-  griddep_wait();
-  griddep_launch_dependents();
+  if constexpr (kOut) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   const int roles = p.n_roles;
   const int n_items = p.hd->n_segs * roles * p.Hv;
+  // The next item of a warp's walk, as the copy warp has drawn it; false at the end (or after a failed wait).
+  uint32_t items = 0;
+  auto next_item = [&](LaItem& it) {
+    for (;;) {
+      const uint32_t slot = items & 1, use = items >> 1;
+      if (!la_wait(&sm.item_full[slot], use & 1, sm)) return false;
+      const int i = *reinterpret_cast<volatile int*>(&sm.item[slot]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_free[slot]);
+      ++items;
+      if (i >= n_items) return false;
+      if (la_item<kOut>(p, roles, i, it)) return true;
+    }
+  };
   uint32_t cc = 0;  // chunks this CTA has begun, over all its items
   bool ok = true;
   LaItem it;
@@ -443,8 +561,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     const int row = 32 * quarter + lane;
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
     float S[kCols];
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      if (!la_item<kOut>(p, roles, i, it)) continue;
+    while (ok && next_item(it)) {
       const LaRole& R = *it.R;
       const float g = fmaxf(p.log_decay[it.h], -1e4f);
       const float* sp = nullptr;
@@ -541,9 +658,11 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   } else if (wid < Sh::kPo0) {
     // ------------------------------------------------------------------ keys
     set_regs<Sh::kRegsK, Sh::kRegs>();
-    const int quarter = wid & 3, ch = (wid - kSWarps) >> 2;  // dimensions 32 quarter .. +31, tokens 32 ch and 64 on
+    const int quarter = wid & 3, q0 = (wid - kSWarps) >> 2;  // dimensions 32 quarter .. +31; first quarter of the tokens
+    constexpr int kQStep = Sh::kKWarps / 4;
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
     uint32_t w_phase = 0;
+    bool was_three = false;  // terms of the chunk before
     auto sync_w = [&]() {  // these warps meet, with the limit of every other wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.w_sync);
@@ -551,8 +670,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       w_phase ^= 1;
       return met;
     };
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      if (!la_item<kOut>(p, roles, i, it)) continue;
+    while (ok && next_item(it)) {
       const LaRole& R = *it.R;
       const float g = fmaxf(p.log_decay[it.h], -1e4f);
       const float a = R.rev ? 0.f : 1.f;
@@ -572,18 +690,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         sm.w[e >> 6][t] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), w1, bf16x2_of(r));
       }
       if (!(ok = sync_w())) break;
-      // The weighted keys of chunk c (the x-th of the CTA) in two or three bf16 terms, 32 tokens and 32
-      // dimensions a warp: quarter ch + 2 half of the tokens.
-      auto convert = [&](int c, uint32_t x, int half) {
+      // The weighted keys of quarter q of chunk c (the x-th of the CTA) in two or three bf16 terms, 32 tokens
+      // and 32 dimensions a warp.
+      auto convert = [&](int c, uint32_t x, int q) {
         int n;
         la_chunk_at(it, c, n);
         const LaTile<kOut> tk(x, 0);
         const bool three = it.three(c);
-        const int q = ch + 2 * half, t0 = 32 * q;
+        const int t0 = 32 * q;
         if (!tk.wait_full(sm)) return false;
         // rows past the chunk belong to another document (or lie outside the tensor): nothing they
         // hold may reach the products
-        if (half == 0 && ch == 0 && n < kLaChunk) {
+        if (q == 0 && n < kLaChunk) {
           const LaTile<kOut> tv(x, Sh::kTileV);
           if (!tv.wait_full(sm)) return false;
           uint8_t* vt = tv.at(sm);
@@ -593,13 +711,13 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           }
           fence_proxy_async_smem();
         }
-        // The stage's last reader. Without outputs each quarter has its own stage. With them the chunk's keys
-        // follow the whole of the chunk before (two terms and three are laid out differently), and in three
-        // terms the later half takes the earlier one's place. (Each of these barriers is waited for once in
-        // every one of its phases, so that its parity cannot be mistaken.)
-        if (!kOut || half == 0) {
-          if (x > 0 && !la_wait(&sm.kt_free[kOut ? 3 : q], (x - 1) & 1, sm)) return false;
-        } else if (three && !la_wait(&sm.kt_free[ch], x & 1, sm)) {
+        // The stage's last reader: each quarter has its own, but for three terms with outputs, where the later
+        // half takes the earlier one's place. The two layouts overlap, so next to three terms a chunk follows
+        // the whole of the one before. (Every earlier phase of a barrier is over when it is waited for: this
+        // warp has waited for it, or for a later product. So its parity cannot be mistaken.)
+        if (kOut && three && q > 0) {
+          if (q >= 2 && !la_wait(&sm.kt_free[q - 2], x & 1, sm)) return false;
+        } else if (x > 0 && !la_wait(&sm.kt_free[kOut && q == 0 && (three || was_three) ? 3 : q], (x - 1) & 1, sm)) {
           return false;
         }
         tc_fence_after();
@@ -608,7 +726,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         // this lane's row of the four 8 x 8 blocks that a load takes: 8 tokens (lane bit 4), 8 dimensions (bit 3)
         const int tok = t0 + ((lane >> 4) & 1) * 8 + (lane & 7), d8 = 4 * quarter + ((lane >> 3) & 1);
         const uint32_t kr = smem_u32(tk.at(sm)) + (d8 >> 3) * (kTile / 2) + tok * 128;
-        // 16 dimensions (lanes) at a time: the loop stays rolled and the two halves share it, since the
+        // 16 dimensions (lanes) at a time: the loop stays rolled and the quarters share it, since the
         // roles' code together should stay in the instruction cache
 #pragma unroll 1
         for (int hl = 0; hl < 2; ++hl) {
@@ -664,8 +782,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       };
       for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-          if (!(ok = convert(c, cc, half))) break;
+        for (int q = q0; q < 4; q += kQStep)
+          if (!(ok = convert(c, cc, q))) break;
+        was_three = it.three(c);
       }
     }
   } else if (kOut && wid < Sh::kTmaWarp) {
@@ -682,8 +801,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       return met;
     };
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      if (!la_item<kOut>(p, roles, i, it)) continue;
+    while (ok && next_item(it)) {
       const LaRole& R = *it.R;
       const float g2 = fmaxf(p.log_decay[it.h], -1e4f) * kLaLog2e;
       const bool strong = g2 * kLaChunk < kLaCut;  // some row factor of a full chunk is below the cut
@@ -845,8 +963,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
       uint32_t loaded = 0;
-      for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-        if (!la_item<kOut>(p, roles, i, it)) continue;
+      // Items are drawn one ahead of the walk: the first by the block's number, then from a counter, so that a
+      // CTA with short ones takes more.
+      int i = blockIdx.x;
+      for (; ok; ++items) {
+        const uint32_t slot = items & 1, use = items >> 1;
+        if (use > 0 && !(ok = la_wait(&sm.item_free[slot], (use - 1) & 1, sm))) break;
+        *reinterpret_cast<volatile int*>(&sm.item[slot]) = i;
+        mbar_arrive(&sm.item_full[slot]);
+        if (i >= n_items) break;
+        const int drawn = i;
+        i = (int)gridDim.x + atomicAdd(&p.hd->ticket[kOut], 1);
+        if (!la_item<kOut>(p, roles, drawn, it)) continue;
         const LaRole& R = *it.R;
         const int hq = it.h / R.div_q, hk = it.h / R.div_k, hv = it.h / R.div_v;
         for (int c = it.first; c < it.nch; ++c, ++cc) {
@@ -878,8 +1006,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     // A chunk's order is Q K^T, Q S, the state's product, P V: the two in the middle run while the map is made.
     const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_mn = idesc_bf16(128, 128, 0, 1);
     const uint64_t ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      if (!la_item<kOut>(p, roles, i, it)) continue;
+    while (ok && next_item(it)) {
       const int first = __shfl_sync(0xffffffffu, it.first, 0), nch = __shfl_sync(0xffffffffu, it.nch, 0);
       const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
       for (int c = first; ok && c < nch; ++c, ++cc) {
@@ -919,13 +1046,13 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           if (elect_one()) {
             const uint32_t ka = tm + Sh::kColKt;
 #pragma unroll
-            for (int x = 0; x < 16; ++x)  // two terms of eight steps of 16 tokens
+            for (int x = 0; x < 16; ++x) {  // two terms of eight steps of 16 tokens
               umma_bf16_ts(tkv, ka + la_kt_col<kOut>(x >> 2, false) + 16 * ((x >> 1) & 1) + 8 * (x & 1),
                            mnmajor_step(dv, 2 * (x >> 2) + (x & 1)), id_mn, x > 0);
+              if ((x & 3) == 3) umma_commit(&sm.kt_free[x >> 2]);
+            }
             umma_commit(&sm.kv_full[kvb]);
             umma_commit(&sm.free_[tk.slot]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) umma_commit(&sm.kt_free[q]);
           }
           __syncwarp();
         } else {
@@ -1018,7 +1145,7 @@ __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ La
     const int d = rev ? p.N - 1 - i : i;
     const int s0 = p.seg0[d], cnt = p.seg0[d + 1] - s0;
     const int idx = p.init_idx ? p.init_idx[d] : -1;
-    const bool fork = idx >= 0 && idx >= p.n_init, src = p.is_src[d] != 0;
+    const bool fork = idx >= 0 && idx >= p.n_init, src = p.init_idx && p.is_src[d] != 0;
     if (cnt == 1 && !fork && !src) continue;
     const int len = p.cu[d + 1] - p.cu[d];
     const float l_last = cnt > 1 ? decay_pow(g, (float)(len - (cnt - 1) * seg_tok)) : decay_pow(g, (float)len);
@@ -1193,6 +1320,7 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   p->hd = reinterpret_cast<LaHeader*>(ws + L->header);
   p->segs = reinterpret_cast<LaSeg*>(ws + L->segs);
   p->seg0 = reinterpret_cast<int32_t*>(ws + L->seg0);
+  p->order = reinterpret_cast<int32_t*>(ws + L->order);
   p->is_src = reinterpret_cast<int32_t*>(ws + L->is_src);
   p->slot_f = reinterpret_cast<float*>(ws + L->slot_f);
   p->slot_r = reinterpret_cast<float*>(ws + L->slot_r);
@@ -1204,7 +1332,8 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   p->T = c.T;
   p->Hv = c.Hv;
   p->n_init = c.n_init;
-  p->seg_chunks = L->seg_chunks;
+  p->min_seg = L->min_seg;
+  p->num_sms = *num_sms;
   p->bwd = c.bwd;
   return GDN_OK;
 }
@@ -1232,7 +1361,7 @@ void la_launch_chunks(LaParams& p, const LaLayout& L, bool out, int roles, int s
 void la_launch_starts(const LaParams& p, const LaLayout& L, const LaRole& fwd, const LaRole* rev, int sms,
                       cudaStream_t s) {
   launch_early(la_plan_kernel, dim3(1), kLaPlanThreads, 0, s, p);
-  if (!L.seg_chunks && !p.init_idx) return;
+  if (!L.min_seg && !p.init_idx) return;
   LaParams a = p;
   a.role[0] = fwd;
   if (rev) a.role[1] = *rev;

@@ -28,32 +28,33 @@ struct LaHeader {
   int32_t n_segs;
   int32_t scan;          // some document needs the scan over its segments (or a fork)
   int32_t seg_chunks;    // longest segment (0 = documents are not cut)
-  int32_t pad[60];
+  int32_t ticket[2];     // items drawn by the states-only walk and by the output walk
+  int32_t pad[58];
 };
 static_assert(sizeof(LaHeader) == 256, "header is 256 bytes");
 
 // Workspace (byte offsets). Slots hold one state (64 KB) per segment and head: first the segment's
 // end state from zero, then, after the scan, the state the segment starts from.
 struct LaLayout {
-  size_t header, segs, seg0, is_src, slot_f, slot_r, fin, acc, dstart, part_q, part_k, total;
+  size_t header, segs, seg0, order, is_src, slot_f, slot_r, fin, acc, dstart, part_q, part_k, total;
   int64_t smax;
-  int seg_chunks;  // 0 = documents are not cut
+  int min_seg;  // shortest segment (chunks); 0 = documents are not cut
 };
 
-// Segment length (chunks): about one (segment, head) item per SM, at least kLaMinSeg chunks; 0
-// when documents and heads alone fill the SMs twice (the rule of the gated delta rule's planner).
-constexpr int kLaMinSeg = 2;
-inline int la_seg_chunks(int N, int T, int Hv, int num_sms) {
-  if ((int64_t)N * Hv >= 2LL * num_sms) return 0;
+// Shortest segment (chunks) that the planner may cut documents into: a quarter of what gives one (segment,
+// head) item to each SM, so that the slots stay a bounded part of memory; 0 where no document is long
+// enough for a cut to pay (below eight chunks the two extra kernels cost more than they save).
+inline int la_min_seg(int T, int Hv, int num_sms) {
   const int64_t chunks = (int64_t)T / kLaChunk + 1;
-  int64_t L = (chunks * Hv + num_sms - 1) / num_sms;
-  return (int)(L < kLaMinSeg ? kLaMinSeg : L);
+  if (chunks < 8) return 0;
+  const int64_t L = (chunks * Hv + 4 * num_sms - 1) / (4 * num_sms);
+  return (int)(L < 2 ? 2 : L);
 }
 
 inline LaLayout la_layout(int N, int T, int Hk, int Hv, bool has_init, bool bwd, int num_sms) {
   LaLayout L{};
-  L.seg_chunks = la_seg_chunks(N, T, Hv, num_sms);
-  L.smax = N + (L.seg_chunks ? (int64_t)T / ((int64_t)L.seg_chunks * kLaChunk) : 0);
+  L.min_seg = la_min_seg(T, Hv, num_sms);
+  L.smax = N + (L.min_seg ? (int64_t)T / ((int64_t)L.min_seg * kLaChunk) : 0);
   const size_t state = (size_t)Hv * kLaState * sizeof(float);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -64,8 +65,9 @@ inline LaLayout la_layout(int N, int T, int Hk, int Hv, bool has_init, bool bwd,
   L.header = take(sizeof(LaHeader));
   L.segs = take(sizeof(LaSeg) * L.smax);
   L.seg0 = take(sizeof(int32_t) * (N + 1));
+  L.order = take(sizeof(int32_t) * L.smax);
   L.is_src = take(sizeof(int32_t) * N);
-  const size_t slots = (L.seg_chunks || has_init) ? state * L.smax : 0;
+  const size_t slots = (L.min_seg || has_init) ? state * L.smax : 0;
   L.slot_f = take(slots);
   L.slot_r = take(bwd ? slots : 0);
   L.fin = take(has_init ? state * N : 0);               // final states of forked documents
