@@ -341,9 +341,10 @@ int gdn_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64_t 
  * gradient of y and dh that of h from elsewhere (NULL = none),
  *     dx = rs w dy - h rs^3 mean(w dy h) + dh,   dw = sum over rows of dy h rs   (rs = (mean(h^2) + eps)^{-1/2})
  * dx [T, D] of `dtype` is the gradient of x and of the residual alike, and may be dh or dy itself; dw is
- * fp32 [D], summed in a fixed order. workspace: gdn_rmsnorm_workspace_size(T, D) bytes, 256-byte aligned.
+ * fp32 [D], summed in a fixed order. workspace: gdn_rmsnorm_workspace_size(T, D, dtype) bytes, 256-byte
+ * aligned.
  */
-size_t gdn_rmsnorm_workspace_size(int64_t T, int D);
+size_t gdn_rmsnorm_workspace_size(int64_t T, int D, int dtype);
 int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D, int dtype,
                     int w_dtype, float eps, void* dx, float* dw, void* workspace, size_t ws_bytes, gdn_stream_t stream);
 

@@ -156,7 +156,7 @@ def load(path: Optional[str] = None):
         lib.gdn_la_decode_step.restype = I
         lib.gdn_rmsnorm_fwd.argtypes = [P, P, P, L, I, I, I, F, P, P, I, P, P]
         lib.gdn_rmsnorm_fwd.restype = I
-        lib.gdn_rmsnorm_workspace_size.argtypes = [L, I]
+        lib.gdn_rmsnorm_workspace_size.argtypes = [L, I, I]
         lib.gdn_rmsnorm_workspace_size.restype = Z
         lib.gdn_rmsnorm_bwd.argtypes = [P, P, P, P, L, I, I, I, F, P, P, P, Z, P]
         lib.gdn_rmsnorm_bwd.restype = I
@@ -235,22 +235,22 @@ def _torch():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    c = _torch()._C  # the current stream's handle without building a Stream object (a few microseconds)
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _check(t, name, dtype, shape=None):
-    torch = _torch()
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:  # a torch.Size is a tuple
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -460,12 +460,11 @@ def _dtype_code(t, name, allowed):
 def _rows(t, name, dtype, shape):
     """A tensor [tokens, heads, 128] whose tokens may be further apart than its heads need (a view into a
     fused projection). Returns the elements between tokens, 0 when contiguous."""
-    torch = _torch()
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.dtype != dtype:
+    if t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA {dtype} tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
@@ -660,7 +659,7 @@ def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspac
     else:
         _check(dw, "dw", torch.float32, (D,))
     if workspace is None:
-        workspace = torch.empty(int(load().gdn_rmsnorm_workspace_size(T, D)), dtype=torch.uint8, device=h.device)
+        workspace = torch.empty(int(load().gdn_rmsnorm_workspace_size(T, D, code)), dtype=torch.uint8, device=h.device)
     rc = load().gdn_rmsnorm_bwd(_ptr(h), _ptr(w), _ptr(dy), _ptr(dh), T, D, code, wcode, float(eps), _ptr(dx), _ptr(dw),
                                 _ptr(workspace), workspace.numel(), _stream_handle(stream))
     if rc != GDN_OK:

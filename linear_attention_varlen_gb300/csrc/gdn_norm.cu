@@ -7,8 +7,10 @@
 //     dx = rs w dy - h rs^3 mean(w dy h) + dh,   dw = sum over rows of dy h rs.
 //
 // Both read each input once and write each output once and do a few operations an element: they are
-// bound by HBM traffic. A thread holds 8 consecutive elements a vector in registers, in fp32; a row
-// of up to 1024 elements is one warp's, a longer one a CTA's.
+// bound by HBM traffic, as long as the arithmetic stays small beside it (pairs of elements in packed fp32,
+// no division an element) and enough bytes are in flight: by many resident rows in the forward, by bulk copies
+// into rings of row buffers in the backward, whose registers hold the weight gradient. A thread holds 8
+// consecutive elements a vector.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -18,6 +20,7 @@
 #include <type_traits>
 
 #include "../../include/gdn.h"
+#include "bw_prims.cuh"
 #include "gdn_common.cuh"
 #include "gdn_host.h"
 
@@ -27,74 +30,94 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr int kNormMaxD = 32768;
 constexpr int kRowThreads = 512;  // most threads to a row
-constexpr int kGroup = 128;  // columns to one scale
-constexpr int kWarpRows = 4;  // rows of a CTA whose warps own a row each
+constexpr int kGroup = 128;       // columns to one scale
+constexpr int kWarpRows = 8;      // rows of a CTA whose warps own a row each
+constexpr long long kNormWait = 4000000000LL;  // clock cycles (about two seconds)
 
 // ------------------------------------------------------------------------------ elements
 
+__device__ __forceinline__ float elem(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float elem(__half v) { return __half2float(v); }
+__device__ __forceinline__ float elem(float v) { return v; }
 template <typename T>
-struct Vec8;  // 8 elements as raw bits
+__device__ __forceinline__ T round_to(float v);
 template <>
-struct Vec8<__nv_bfloat16> {
-  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
-};
+__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
 template <>
-struct Vec8<__half> {
-  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
-  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
-};
+__device__ __forceinline__ __half round_to<__half>(float v) {
+  return __float2half_rn(v);
+}
 template <>
-struct Vec8<float> {
-  static __device__ __forceinline__ float get(float v) { return v; }
-  static __device__ __forceinline__ float put(float v) { return v; }
-};
+__device__ __forceinline__ float round_to<float>(float v) {
+  return v;
+}
 
-// columns c .. c + 7 of a row of D elements (zero past its end); kVec: the row is aligned and D a multiple of 8
+// 8 elements as they lie in memory
+template <typename T>
+struct alignas(16) Raw8 {
+  T t[8];
+};
+// columns c .. c + 7 of a row of D elements (zero past its end); kVec: rows are aligned and D a multiple of 8
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* row, int c, int D, float* f) {
+__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int D) {
+  Raw8<T> r;
   if constexpr (kVec) {
-    if (c < D) {
-      alignas(16) T t[8];
+    uint4* q = reinterpret_cast<uint4*>(r.t);
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(row + c)[i];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = Vec8<T>::get(t[i]);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      q[i] = c < D ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < D ? Vec8<T>::get(row[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) r.t[i] = c + i < D ? row[c + i] : round_to<T>(0.f);
   }
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 template <typename T, bool kVec>
-__device__ __forceinline__ void store8(T* row, int c, int D, const float* f) {
+__device__ __forceinline__ void store8(T* row, int c, int D, const uint64_t* f) {  // four pairs of fp32
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2 && !std::is_same_v<T, __half>) {
+      reinterpret_cast<uint32_t*>(r.t)[i] = bw::pack_bf16x2(bw::f2_lo(f[i]), bw::f2_hi(f[i]));
+    } else if constexpr (sizeof(T) == 2) {
+      reinterpret_cast<__half2*>(r.t)[i] = __floats2half2_rn(bw::f2_lo(f[i]), bw::f2_hi(f[i]));
+    } else {
+      r.t[2 * i] = bw::f2_lo(f[i]);
+      r.t[2 * i + 1] = bw::f2_hi(f[i]);
+    }
+  }
   if constexpr (kVec) {
     if (c < D) {
-      alignas(16) T t[8];
+      const uint4* q = reinterpret_cast<const uint4*>(r.t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = Vec8<T>::put(f[i]);
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        reinterpret_cast<uint4*>(row + c)[i] = reinterpret_cast<const uint4*>(t)[i];
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + c)[i] = q[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < D) row[c + i] = Vec8<T>::put(f[i]);
+      if (c + i < D) row[c + i] = r.t[i];
   }
 }
 template <bool kVec>
 __device__ __forceinline__ void load_w8(const void* w, int dtype, int c, int D, float* f) {
+  auto get = [&](auto* p) {
+    const auto r = load8<std::remove_const_t<std::remove_pointer_t<decltype(p)>>, kVec>(p, c, D);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = elem(r.t[i]);
+  };
   if (dtype == GDN_DTYPE_BF16)
-    load8<__nv_bfloat16, kVec>(static_cast<const __nv_bfloat16*>(w), c, D, f);
+    get(static_cast<const __nv_bfloat16*>(w));
   else if (dtype == GDN_DTYPE_FP16)
-    load8<__half, kVec>(static_cast<const __half*>(w), c, D, f);
+    get(static_cast<const __half*>(w));
   else
-    load8<float, kVec>(static_cast<const float*>(w), c, D, f);
+    get(static_cast<const float*>(w));
 }
 
 // maximum that keeps a NaN
@@ -103,38 +126,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 
-// Sum (or maximum) over the threads of a row: a warp, or the CTA through `s` (33 floats).
-template <bool kWarp>
-__device__ __forceinline__ float row_sum(float x, float* s) {
-  x = warp_sum(x);
+// Sums of two values (or a maximum, kMax, of one) over the threads of a row: a warp, or the CTA through the
+// 16 pairs of `s`. The caller alternates between buffers: one barrier is enough.
+template <bool kWarp, bool kMax = false>
+__device__ __forceinline__ float2 row_reduce(float2 x, float2* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float a = __shfl_xor_sync(0xffffffffu, x.x, o);
+    x.x = kMax ? max_nan(x.x, a) : x.x + a;
+    if constexpr (!kMax) x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+  }
   if constexpr (kWarp) return x;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if (lane == 0) s[wid] = x;
   __syncthreads();
-  float t = lane < nw ? s[lane] : 0.f;
-  t = warp_sum(t);
-  __syncthreads();
-  return t;
-}
-template <bool kWarp>
-__device__ __forceinline__ float row_max(float x, float* s) {
+  x = s[lane & 15];
+  if ((lane & 15) >= nw) x = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if constexpr (kWarp) return x;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  if (lane == 0) s[wid] = x;
-  __syncthreads();
-  float t = lane < nw ? s[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
-  __syncthreads();
-  return t;
+  for (int o = 8; o > 0; o >>= 1) {
+    const float a = __shfl_xor_sync(0xffffffffu, x.x, o);
+    x.x = kMax ? max_nan(x.x, a) : x.x + a;
+    if constexpr (!kMax) x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+  }
+  return x;
 }
 
 // ------------------------------------------------------------------------------ forward
@@ -149,40 +164,45 @@ struct NormFwdParams {
 };
 
 template <typename T, int kNv, bool kWarp, bool kVec>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
-  __shared__ float s_red[33];
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kNv == 1 ? 256 : kRowThreads, kNv == 1 ? 6 : kNv == 2 ? 3 : 1)
+    norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
+  __shared__ float2 s_red[2][16];
   const int tpr = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
   const int64_t row = kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= p.T) return;
-  const T* x = static_cast<const T*>(p.x) + row * p.D;
-  float v[kNv][8];
-  float ss = 0.f;
+  uint64_t v[kNv][4];  // pairs of fp32
+  uint64_t ss = 0;
+  const bool res = p.r != nullptr;
+  {
+    Raw8<T> x[kNv], r[kNv];
 #pragma unroll
-  for (int j = 0; j < kNv; ++j) load8<T, kVec>(x, (t + j * tpr) * 8, p.D, v[j]);
-  if (p.r) {
-    const T* r = static_cast<const T*>(p.r) + row * p.D;
-    T* h = static_cast<T*>(p.h) + row * p.D;
+    for (int j = 0; j < kNv; ++j) x[j] = load8<T, kVec>(static_cast<const T*>(p.x) + row * p.D, (t + j * tpr) * 8, p.D);
+    if (res) {
 #pragma unroll
-    for (int j = 0; j < kNv; ++j) {
-      float u[8];
-      load8<T, kVec>(r, (t + j * tpr) * 8, p.D, u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] += u[i];
+      for (int j = 0; j < kNv; ++j) r[j] = load8<T, kVec>(static_cast<const T*>(p.r) + row * p.D, (t + j * tpr) * 8, p.D);
     }
+#pragma unroll
+    for (int j = 0; j < kNv; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[j][i] = bw::f2_pack(elem(x[j].t[2 * i]), elem(x[j].t[2 * i + 1]));
+        if (res) v[j][i] = f2_add(v[j][i], bw::f2_pack(elem(r[j].t[2 * i]), elem(r[j].t[2 * i + 1])));
+        ss = bw::f2_fma(v[j][i], v[j][i], ss);
+      }
+  }
+  if (res) {
+    T* h = static_cast<T*>(p.h) + row * p.D;
 #pragma unroll
     for (int j = 0; j < kNv; ++j) store8<T, kVec>(h, (t + j * tpr) * 8, p.D, v[j]);
   }
-#pragma unroll
-  for (int j = 0; j < kNv; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-  const float rs = rsqrtf(row_sum<kWarp>(ss, s_red) / (float)p.D + p.eps);
+  const float rs = rsqrtf(row_reduce<kWarp>(make_float2(bw::f2_sum(ss), 0.f), s_red[0]).x / (float)p.D + p.eps);
+  const uint64_t rs2 = bw::f2_pack(rs, rs);
 #pragma unroll
   for (int j = 0; j < kNv; ++j) {
     float w[8];
     load_w8<kVec>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * rs * w[i];
+    for (int i = 0; i < 4; ++i) v[j][i] = bw::f2_mul(bw::f2_mul(v[j][i], rs2), bw::f2_pack(w[2 * i], w[2 * i + 1]));
   }
   if (p.quant == GDN_QUANT_NONE) {
     T* y = static_cast<T*>(p.y) + row * p.D;
@@ -195,13 +215,13 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) norm_fwd
   for (int j = 0; j < kNv; ++j) {
     am[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am[j] = max_nan(am[j], fabsf(v[j][i]));
+    for (int i = 0; i < 4; ++i) am[j] = max_nan(max_nan(am[j], fabsf(bw::f2_lo(v[j][i]))), fabsf(bw::f2_hi(v[j][i])));
   }
   if (p.quant == GDN_QUANT_ROW) {
     float m = am[0];
 #pragma unroll
     for (int j = 1; j < kNv; ++j) m = max_nan(m, am[j]);
-    m = row_max<kWarp>(m, s_red);
+    m = row_reduce<kWarp, true>(make_float2(m, 0.f), s_red[1]).x;
 #pragma unroll
     for (int j = 0; j < kNv; ++j) am[j] = m;
     if (t == 0) p.scales[row] = m > 0.f ? m / kE4m3Max : 1.f;
@@ -219,10 +239,16 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) norm_fwd
 #pragma unroll
   for (int j = 0; j < kNv; ++j) {
     const float sc = am[j] > 0.f ? am[j] / kE4m3Max : 1.f;
+    // one reciprocal for the thread's elements; scales so small that it would overflow are taken up by 2^100 first
+    const bool tiny = sc < 1e-30f;
+    const float inv = 1.f / (tiny ? sc * 0x1p100f : sc);
+    const uint64_t inv2 = bw::f2_pack(inv, inv), up2 = bw::f2_pack(0x1p100f, 0x1p100f);
     alignas(8) __nv_fp8x2_storage_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      b[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[j][2 * i] / sc, v[j][2 * i + 1] / sc), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t z = bw::f2_mul(tiny ? bw::f2_mul(v[j][i], up2) : v[j][i], inv2);
+      b[i] = __nv_cvt_float2_to_fp8x2(make_float2(bw::f2_lo(z), bw::f2_hi(z)), __NV_SATFINITE, __NV_E4M3);
+    }
     const int c = (t + j * tpr) * 8;
     if constexpr (kVec) {
       if (c < p.D) *reinterpret_cast<uint2*>(y + c) = *reinterpret_cast<const uint2*>(b);
@@ -245,79 +271,244 @@ struct NormBwdParams {
   float eps;
 };
 
-// Each CTA takes rows blockIdx.x, + gridDim.x, ... (a warp-row CTA kWarpRows at a time) and keeps
-// the weight gradient's part of its own columns in registers; the parts are summed in a fixed order.
-template <typename T, int kNv, bool kWarp, bool kVec>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kRowThreads) norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
-  __shared__ float s_red[33], s_red2[33];
-  const int tpr = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t first = kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t step = kWarp ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
-  float w[kNv][8], dw[kNv][8];
+// A CTA's sixteen warps are teams of kTeam; each walks rows of its own and keeps the weight gradient's part of
+// its columns in registers. Aligned rows (kRing) come through a ring of row buffers in shared memory that bulk
+// copies fill ahead of the team: the next rows are always in flight, at no cost in registers. Other rows are read
+// from memory as they come, with the same thread for the same columns, so that the results are the same bits. A
+// team reads a row twice: for the two sums, and for the outputs.
+constexpr int kBwdWarps = 16;
+constexpr uint32_t kBwdRing = 196608;  // bytes of the rings of a CTA
+
+template <typename T, int kNv, int kTeam, bool kRing>
+__global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const __grid_constant__ NormBwdParams p) {
+  constexpr int kTeams = kBwdWarps / kTeam;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t s_full[kTeams][8];
+  __shared__ float2 s_red[kTeams][2][kTeam];
+  const int team = threadIdx.x / (32 * kTeam), t = threadIdx.x % (32 * kTeam), lane = t & 31, wt = t >> 5;
+  const int tensors = p.dh ? 3 : 2;
+  const uint32_t row_bytes = (uint32_t)p.D * sizeof(T), stage_bytes = row_bytes * tensors;
+  const int stages = kRing ? min(8, (int)(kBwdRing / kTeams / stage_bytes)) : 1;
+  uint8_t* mine = ring + (size_t)team * stages * stage_bytes;
+  const T* src[3] = {static_cast<const T*>(p.h), static_cast<const T*>(p.dy), static_cast<const T*>(p.dh)};
+  const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams;
+  if (kRing && t == 0) {
+    for (int i = 0; i < stages; ++i) bw::mbar_init(&s_full[team][i], 1);
+    bw::fence_mbar_init();
+  }
+  auto team_sync = [&]() {
+    if constexpr (kTeam == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kTeam) : "memory");
+  };
+  auto fetch = [&](int64_t row, int st) {
+    bw::mbar_arrive_expect_tx(&s_full[team][st], stage_bytes);
+    for (int k = 0; k < tensors; ++k)
+      bw::bulk_load(mine + st * stage_bytes + k * row_bytes, src[k] + row * p.D, row_bytes, &s_full[team][st]);
+  };
+  if (kRing && t == 0)
+    for (int i = 0; i < stages && first + i * step < p.T; ++i) fetch(first + i * step, i);
+  float dw[kNv][8];
+  Raw8<T> w[kNv];  // the weight in the rows' type where it has it, else read from memory for each row
+  const bool same = p.w_dtype == (sizeof(T) == 4 ? GDN_DTYPE_FP32 : std::is_same_v<T, __half> ? GDN_DTYPE_FP16 : GDN_DTYPE_BF16);
 #pragma unroll
   for (int j = 0; j < kNv; ++j) {
-    load_w8<kVec>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w[j]);
+    if (same) w[j] = load8<T, kRing>(static_cast<const T*>(p.w), (t + j * 32 * kTeam) * 8, p.D);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
-  for (int64_t row = first; row < p.T; row += step) {
-    const T* h = static_cast<const T*>(p.h) + row * p.D;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.D;
-    T* dx = static_cast<T*>(p.dx) + row * p.D;
-    float hv[kNv][8], gv[kNv][8];
-    float ss = 0.f, sg = 0.f;
+  auto weight = [&](int j, float* f) {
+    if (same) {
 #pragma unroll
-    for (int j = 0; j < kNv; ++j) {
-      load8<T, kVec>(h, (t + j * tpr) * 8, p.D, hv[j]);
-      load8<T, kVec>(dy, (t + j * tpr) * 8, p.D, gv[j]);
+      for (int i = 0; i < 8; ++i) f[i] = elem(w[j].t[i]);
+    } else {
+      load_w8<kRing>(p.w, p.w_dtype, (t + j * 32 * kTeam) * 8, p.D, f);
+    }
+  };
+  team_sync();
+  int st = 0, turn = 0;
+  uint32_t phase = 0;
+  for (int64_t row = first; row < p.T; row += step, turn ^= 1) {
+    const T *h = src[0] + row * p.D, *g = src[1] + row * p.D, *e = src[2] + row * p.D;
+    if constexpr (kRing) {
+      bw::mbar_wait(&s_full[team][st], phase, kNormWait);
+      const uint8_t* b = mine + st * stage_bytes;
+      h = reinterpret_cast<const T*>(b);
+      g = reinterpret_cast<const T*>(b + row_bytes);
+      e = reinterpret_cast<const T*>(b + 2 * row_bytes);
+    }
+    float2 sum = make_float2(0.f, 0.f);
+    {
+      uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+      for (int j = 0; j < kNv; ++j) {
+        const int c = (t + j * 32 * kTeam) * 8;
+        const Raw8<T> hr = load8<T, kRing>(h, c, p.D), gr = load8<T, kRing>(g, c, p.D);
+        float wf[8];
+        weight(j, wf);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t hv = bw::f2_pack(elem(hr.t[2 * i]), elem(hr.t[2 * i + 1]));
+          s1 = bw::f2_fma(hv, hv, s1);
+          s2 = bw::f2_fma(bw::f2_mul(hv, bw::f2_pack(wf[2 * i], wf[2 * i + 1])),
+                          bw::f2_pack(elem(gr.t[2 * i]), elem(gr.t[2 * i + 1])), s2);
+        }
+      }
+      sum = make_float2(bw::f2_sum(s1), bw::f2_sum(s2));
     }
 #pragma unroll
-    for (int j = 0; j < kNv; ++j)
+    for (int o = 16; o > 0; o >>= 1) {
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+      sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+    }
+    if constexpr (kTeam > 1) {
+      if (lane == 0) s_red[team][turn][wt] = sum;
+      team_sync();
+      sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(hv[j][i], hv[j][i], ss);
-        sg = fmaf(hv[j][i] * w[j][i], gv[j][i], sg);
+      for (int k = 0; k < kTeam; ++k) {
+        const float2 x = s_red[team][turn][k];
+        sum.x += x.x;
+        sum.y += x.y;
       }
-    ss = row_sum<kWarp>(ss, s_red);
-    sg = row_sum<kWarp>(sg, s_red2);
-    const float rs = rsqrtf(ss / (float)p.D + p.eps);
-    const float c = rs * rs * rs * (sg / (float)p.D);
+    }
+    const float rs = rsqrtf(sum.x / (float)p.D + p.eps);
+    const float cc = -rs * rs * rs * (sum.y / (float)p.D);
+    const uint64_t rs2 = bw::f2_pack(rs, rs), c2 = bw::f2_pack(cc, cc);
+    T* dx = static_cast<T*>(p.dx) + row * p.D;
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
-      float o[8], e[8];
-      if (p.dh) load8<T, kVec>(static_cast<const T*>(p.dh) + row * p.D, (t + j * tpr) * 8, p.D, e);
+      const int c = (t + j * 32 * kTeam) * 8;
+      const Raw8<T> hr = load8<T, kRing>(h, c, p.D), gr = load8<T, kRing>(g, c, p.D);
+      Raw8<T> er;
+      if (p.dh) er = load8<T, kRing>(e, c, p.D);
+      float wf[8];
+      weight(j, wf);
+      uint64_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dw[j][i] = fmaf(gv[j][i] * rs, hv[j][i], dw[j][i]);
-        o[i] = fmaf(rs * w[j][i], gv[j][i], -c * hv[j][i]);
-        if (p.dh) o[i] += e[i];
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t hv = bw::f2_pack(elem(hr.t[2 * i]), elem(hr.t[2 * i + 1]));
+        const uint64_t gv = bw::f2_mul(bw::f2_pack(elem(gr.t[2 * i]), elem(gr.t[2 * i + 1])), rs2);
+        const uint64_t d = bw::f2_fma(gv, hv, bw::f2_pack(dw[j][2 * i], dw[j][2 * i + 1]));
+        dw[j][2 * i] = bw::f2_lo(d);
+        dw[j][2 * i + 1] = bw::f2_hi(d);
+        o[i] = bw::f2_fma(bw::f2_pack(wf[2 * i], wf[2 * i + 1]), gv, bw::f2_mul(c2, hv));
+        if (p.dh) o[i] = f2_add(o[i], bw::f2_pack(elem(er.t[2 * i]), elem(er.t[2 * i + 1])));
       }
-      store8<T, kVec>(dx, (t + j * tpr) * 8, p.D, o);
+      store8<T, kRing>(dx, c, p.D, o);
+    }
+    if constexpr (kRing) {
+      team_sync();  // the buffer has been read
+      if (t == 0 && row + stages * step < p.T) {
+        bw::fence_proxy_async_smem();
+        fetch(row + stages * step, st);
+      }
+      if (++st == stages) {
+        st = 0;
+        phase ^= 1;
+      }
     }
   }
-  const int64_t part = kWarp ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  // the CTA's part: its teams' in order, through the rings (every copy has landed and been read)
+  __syncthreads();
+  float* s_dw = reinterpret_cast<float*>(ring);
+  for (int k = 0; k < kTeams; ++k) {
+    if (team == k) {
+#pragma unroll
+      for (int j = 0; j < kNv; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (t + j * 32 * kTeam) * 8 + i;
+          if (c < p.D) s_dw[c] = k ? s_dw[c] + dw[j][i] : dw[j][i];
+        }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < p.D; c += 32 * kBwdWarps) p.part[(int64_t)blockIdx.x * p.D + c] = s_dw[c];
+}
+
+// Rows too long for a team's registers and ring (above 16384 elements, 8192 in fp32): one a CTA at a time, rows
+// blockIdx.x, + gridDim.x, ...
+template <typename T, int kNv>
+__global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
+  __shared__ float2 s_red[2][16];
+  const int tpr = blockDim.x, t = threadIdx.x;
+  float dw[kNv][8];
+#pragma unroll
+  for (int j = 0; j < kNv; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+    const T* h = static_cast<const T*>(p.h) + row * p.D;
+    const T* g = static_cast<const T*>(p.dy) + row * p.D;
+    const T* e = p.dh ? static_cast<const T*>(p.dh) + row * p.D : nullptr;
+    T* dx = static_cast<T*>(p.dx) + row * p.D;
+    Raw8<T> hr[kNv], gr[kNv];
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kNv; ++j) {
+      hr[j] = load8<T, false>(h, (t + j * tpr) * 8, p.D);
+      gr[j] = load8<T, false>(g, (t + j * tpr) * 8, p.D);
+    }
+#pragma unroll
+    for (int j = 0; j < kNv; ++j) {
+      float w[8];
+      load_w8<false>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float hv = elem(hr[j].t[i]);
+        sum.x = fmaf(hv, hv, sum.x);
+        sum.y = fmaf(hv * w[i], elem(gr[j].t[i]), sum.y);
+      }
+    }
+    sum = row_reduce<false>(sum, s_red[turn]);
+    const float rs = rsqrtf(sum.x / (float)p.D + p.eps);
+    const float c = rs * rs * rs * (sum.y / (float)p.D);
+#pragma unroll
+    for (int j = 0; j < kNv; ++j) {
+      float w[8], o[8];
+      load_w8<false>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w);
+      Raw8<T> er;
+      if (e) er = load8<T, false>(e, (t + j * tpr) * 8, p.D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float hv = elem(hr[j].t[i]), gv = elem(gr[j].t[i]) * rs;
+        dw[j][i] = fmaf(gv, hv, dw[j][i]);
+        o[i] = fmaf(w[i], gv, -c * hv);
+        if (e) o[i] += elem(er.t[i]);
+      }
+      uint64_t o2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o2[i] = bw::f2_pack(o[2 * i], o[2 * i + 1]);
+      store8<T, false>(dx, (t + j * tpr) * 8, p.D, o2);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < kNv; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = (t + j * tpr) * 8 + i;
-      if (c < p.D) p.part[part * p.D + c] = dw[j][i];
+      if (c < p.D) p.part[(int64_t)blockIdx.x * p.D + c] = dw[j][i];
     }
 }
 
-// dw: 32 columns to a CTA, 8 warps sum every eighth part, then the warps' sums in order
-__global__ void __launch_bounds__(256) norm_dw_kernel(const __grid_constant__ NormBwdParams p) {
-  __shared__ float s[8][32];
+// dw: 32 columns to a CTA, 32 warps sum every 32nd part, then the warps' sums in order
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ NormBwdParams p) {
+  __shared__ float s[32][33];
+  bw::griddep_wait();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
   if (c < p.D)
-    for (int i = wid; i < p.parts; i += 8) a += p.part[(size_t)i * p.D + c];
+#pragma unroll 4
+    for (int i = wid; i < p.parts; i += 32) a += p.part[(size_t)i * p.D + c];
   s[wid][lane] = a;
   __syncthreads();
   if (wid == 0 && c < p.D) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += s[i][lane];
+    for (int i = 1; i < 32; ++i) a += s[i][lane];
     p.dw[c] = a;
   }
 }
@@ -328,22 +519,28 @@ struct NormShape {
   bool warp;
   int threads, nv;  // threads to a row and vectors of 8 to a thread
 };
-// A row of up to 1024 elements is one warp's (4 vectors a thread); a longer one takes a CTA of
-// D / 16 threads (2 vectors each), from 128 up to 512, then more vectors.
+// Up to 256 elements a row is one warp's; up to 2048 a CTA's with one vector a thread; longer ones take
+// two or more vectors a thread and at most 512 threads.
 NormShape norm_shape(int D) {
   const int vecs = (D + 7) / 8;
-  if (vecs <= 128) return {true, 32, vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4};
-  int threads = 128;
-  while (threads < kRowThreads && threads * 2 < vecs) threads *= 2;
-  int nv = 2;
-  while (threads * nv < vecs) nv *= 2;
-  return {false, threads, nv};
+  if (vecs <= 32) return {true, 32, 1};
+  int nv = 1;
+  while (vecs > nv * (nv == 1 ? 256 : kRowThreads)) nv *= 2;
+  return {false, ((vecs + nv - 1) / nv + 31) / 32 * 32, nv};
 }
-int norm_parts(int64_t T, int D, int sms) {
-  const NormShape s = norm_shape(D);
-  const int64_t rows = s.warp ? (T + kWarpRows - 1) / kWarpRows : T;
-  const int64_t most = (int64_t)sms * (s.warp ? 8 : 2048 / s.threads > 4 ? 4 : 2048 / s.threads);
-  return (int)(rows < most ? (rows < 1 ? 1 : rows) : most);  // CTAs
+// The backward's teams of warps: the fewest whose vectors (at most four a thread, two in fp32) cover the row;
+// their rings then hold two rows at least. 0 where a row is too long for that.
+int norm_team(int D, size_t esize) {
+  for (int team = 1; team <= kBwdWarps; team *= 2)
+    if (team * 256 * (esize == 4 ? 2 : 4) >= D) return team;
+  return 0;
+}
+static_assert(kBwdRing / kBwdWarps >= 2 * 3 * 1024 * 2, "two rows of three tensors a warp");
+// CTAs of the backward, each with a part of the weight's gradient
+int norm_parts(int64_t T, int D, size_t esize, int sms) {
+  const int team = norm_team(D, esize), per = team ? kBwdWarps / team : 1;  // rows at a time
+  const int64_t rows = (T + per - 1) / per;
+  return (int)(rows < sms ? (rows < 1 ? 1 : rows) : sms);
 }
 
 bool al(const void* p, uintptr_t b) { return (reinterpret_cast<uintptr_t>(p) % b) == 0; }
@@ -362,41 +559,81 @@ int check_device(const void* anchor, const void* const* ptrs, int n, DeviceGuard
   return (major == 10 && minor == 3) ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
-template <typename T, bool kVec, typename F>
+// f(kNv, kWarp) as integral constants
+template <typename F>
 void by_shape(const NormShape& s, F&& f) {
-  // f(kNv, kWarp) as integral constants
   using std::integral_constant;
-  if (s.warp) {
-    if (s.nv == 1)
-      f(integral_constant<int, 1>{}, integral_constant<bool, true>{});
-    else if (s.nv == 2)
-      f(integral_constant<int, 2>{}, integral_constant<bool, true>{});
-    else
-      f(integral_constant<int, 4>{}, integral_constant<bool, true>{});
-  } else {
-    if (s.nv == 2)
-      f(integral_constant<int, 2>{}, integral_constant<bool, false>{});
-    else if (s.nv == 4)
-      f(integral_constant<int, 4>{}, integral_constant<bool, false>{});
-    else
-      f(integral_constant<int, 8>{}, integral_constant<bool, false>{});
-  }
+  if (s.warp)
+    f(integral_constant<int, 1>{}, integral_constant<bool, true>{});
+  else if (s.nv == 1)
+    f(integral_constant<int, 1>{}, integral_constant<bool, false>{});
+  else if (s.nv == 2)
+    f(integral_constant<int, 2>{}, integral_constant<bool, false>{});
+  else if (s.nv == 4)
+    f(integral_constant<int, 4>{}, integral_constant<bool, false>{});
+  else
+    f(integral_constant<int, 8>{}, integral_constant<bool, false>{});
 }
 
 template <typename T, bool kVec>
 void launch_fwd(const NormFwdParams& p, cudaStream_t st) {
   const NormShape s = norm_shape(p.D);
-  by_shape<T, kVec>(s, [&](auto nv, auto warp) {
+  by_shape(s, [&](auto nv, auto warp) {
     const unsigned grid = (unsigned)(warp ? (p.T + kWarpRows - 1) / kWarpRows : p.T);
     norm_fwd_kernel<T, nv, warp, kVec><<<grid, warp ? 32 * kWarpRows : s.threads, 0, st>>>(p);
   });
 }
-template <typename T, bool kVec>
-void launch_bwd(const NormBwdParams& p, int ctas, cudaStream_t st) {
-  const NormShape s = norm_shape(p.D);
-  by_shape<T, kVec>(s, [&](auto nv, auto warp) {
-    norm_bwd_kernel<T, nv, warp, kVec><<<ctas, warp ? 32 * kWarpRows : s.threads, 0, st>>>(p);
-  });
+template <typename T, int kNv, int kTeam>
+bool launch_team(const NormBwdParams& p, bool ring, int dev, cudaStream_t st) {
+  if (!ring) {
+    // the parts are summed in the row's bytes of shared memory
+    const size_t smem = (size_t)p.D * sizeof(float);
+    static PerDevice set;
+    if (smem > 48000 && !set.done(dev)) {
+      if (cudaFuncSetAttribute(norm_bwd_team_kernel<T, kNv, kTeam, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kNormMaxD * (int)sizeof(float)) != cudaSuccess)
+        return false;
+      set.mark(dev);
+    }
+    norm_bwd_team_kernel<T, kNv, kTeam, false><<<p.parts, 32 * kBwdWarps, smem, st>>>(p);
+    return true;
+  }
+  static PerDevice set;
+  if (!set.done(dev)) {
+    if (cudaFuncSetAttribute(norm_bwd_team_kernel<T, kNv, kTeam, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kBwdRing) != cudaSuccess)
+      return false;
+    set.mark(dev);
+  }
+  norm_bwd_team_kernel<T, kNv, kTeam, true><<<p.parts, 32 * kBwdWarps, kBwdRing, st>>>(p);
+  return true;
+}
+// vectors a thread: as the row needs in a team of one warp, the most in larger ones
+template <typename T>
+bool launch_bwd(const NormBwdParams& p, bool ring, int dev, cudaStream_t st) {
+  constexpr int kMost = sizeof(T) == 4 ? 2 : 4;
+  const int team = norm_team(p.D, sizeof(T));
+  switch (team) {
+    case 1:
+      return p.D <= 256   ? launch_team<T, 1, 1>(p, ring, dev, st)
+             : p.D <= 512 ? launch_team<T, 2, 1>(p, ring, dev, st)
+                          : launch_team<T, kMost, 1>(p, ring, dev, st);
+    case 2:
+      return launch_team<T, kMost, 2>(p, ring, dev, st);
+    case 4:
+      return launch_team<T, kMost, 4>(p, ring, dev, st);
+    case 8:
+      return launch_team<T, kMost, 8>(p, ring, dev, st);
+    case 16:
+      return launch_team<T, kMost, 16>(p, ring, dev, st);
+  }
+  // 1024 vectors at least (fp32; 2048 else): 512 threads with the fewest vectors each that cover the row
+  const int nv = (p.D + 8 * kRowThreads - 1) / (8 * kRowThreads);
+  if (nv <= 4)
+    norm_bwd_long_kernel<T, 4><<<p.parts, kRowThreads, 0, st>>>(p);
+  else
+    norm_bwd_long_kernel<T, 8><<<p.parts, kRowThreads, 0, st>>>(p);
+  return true;
 }
 
 }  // namespace
@@ -435,16 +672,15 @@ extern "C" int gdn_rmsnorm_fwd(const void* x, const void* residual, const void* 
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-extern "C" size_t gdn_rmsnorm_workspace_size(int64_t T, int D) {
-  if (T < 0 || T > (int64_t)INT32_MAX || D < 1 || D > gdn::kNormMaxD) return 0;
+extern "C" size_t gdn_rmsnorm_workspace_size(int64_t T, int D, int dtype) {
+  if (!gdn::dtype_ok(dtype) || T < 0 || T > (int64_t)INT32_MAX || D < 1 || D > gdn::kNormMaxD) return 0;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
     sms = 152;
   }
-  const size_t parts = (size_t)gdn::norm_parts(T, D, sms) * (gdn::norm_shape(D).warp ? gdn::kWarpRows : 1);
-  return parts * D * sizeof(float);
+  return (size_t)gdn::norm_parts(T, D, gdn::esize(dtype), sms) * D * sizeof(float);
 }
 
 extern "C" int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D,
@@ -463,18 +699,17 @@ extern "C" int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, con
   int sms = 0;
   const int rc = check_device(workspace, ptrs, 6, guard, &sms);
   if (rc != GDN_OK) return rc;
-  const int ctas = norm_parts(T, D, sms);
-  const int parts = ctas * (norm_shape(D).warp ? kWarpRows : 1);
+  const int parts = norm_parts(T, D, e, sms);
   if (ws_bytes < (size_t)parts * D * sizeof(float)) return GDN_ERR_WORKSPACE;
   const NormBwdParams p{h, w, dy, dh, dx, static_cast<float*>(workspace), dw, T, D, w_dtype, parts, eps};
   const bool vec = D % 8 == 0 && al(h, 16) && al(dy, 16) && al(dh, 16) && al(dx, 16) && al(w, 16);
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == GDN_DTYPE_BF16)
-    vec ? launch_bwd<__nv_bfloat16, true>(p, ctas, st) : launch_bwd<__nv_bfloat16, false>(p, ctas, st);
-  else if (dtype == GDN_DTYPE_FP16)
-    vec ? launch_bwd<__half, true>(p, ctas, st) : launch_bwd<__half, false>(p, ctas, st);
-  else
-    vec ? launch_bwd<float, true>(p, ctas, st) : launch_bwd<float, false>(p, ctas, st);
-  norm_dw_kernel<<<(D + 31) / 32, 256, 0, st>>>(p);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  const bool ok = dtype == GDN_DTYPE_BF16   ? launch_bwd<__nv_bfloat16>(p, vec, dev, st)
+                  : dtype == GDN_DTYPE_FP16 ? launch_bwd<__half>(p, vec, dev, st)
+                                            : launch_bwd<float>(p, vec, dev, st);
+  if (!ok) return GDN_ERR_CUDA;
+  launch_early(norm_dw_kernel, dim3((D + 31) / 32), 1024, 0, st, p);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
