@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
         s.src_fwd = (k > 0 || fork) ? -2 : idx;
         s.src_rev = (k < cnt - 1 || src) ? -2 : -1;
         // a cut document's final state, and its start's gradient where one is wanted, come from the scan
-        s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0);
+        s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0) | (src ? 4 : 0) |
+                 (fork ? 8 : 0);
         p.segs[base + k] = s;
         atomicAdd(&s_hist[63 - min(63, (s.ntok + kLaChunk - 1) / kLaChunk)], 1);
       }
@@ -353,9 +354,7 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, LaSmem& 
   return true;
 }
 
-__device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, LaSmem& sm) {
-  return __all_sync(0xffffffffu, la_wait(bar, parity, sm));
-}
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -431,7 +430,6 @@ struct LaTile {
   }
   __device__ __forceinline__ uint8_t* at(LaSmem& sm) const { return sm.tiles + slot * kTile; }
   __device__ __forceinline__ bool wait_full(LaSmem& sm) const { return la_wait(&sm.full[slot], use & 1, sm); }
-  __device__ __forceinline__ bool wait_full_all(LaSmem& sm) const { return la_wait_all(&sm.full[slot], use & 1, sm); }
 };
 
 struct LaItem;
@@ -464,8 +462,16 @@ __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaI
       it.exact = it.nch - (g > 0.f ? (int)fminf(ceilf(7.f / g) + 1.f, (float)it.nch) : it.nch);
   } else {
     // chunks whose part is below e^-30 of those after them leave no trace in fp32
-    it.exact = 0;
+    it.exact = it.nch;
     if (g > 0.f) it.first = it.nch - (int)fminf(ceilf(30.f / g) + 1.f, (float)it.nch);
+    // three terms where the state reaches an output of the scan (the document's last state, or its start's
+    // gradient where one is wanted, or a fork's) before it has decayed below 2^-10
+    const bool fork = (it.seg.need >> 2 >> it.R->rev) & 1;
+    if (fork || (it.R->rev ? p.end_rev : p.end_fwd) != nullptr) {
+      const int between = it.R->rev ? it.seg.k : it.seg.nseg - 1 - it.seg.k;  // whole segments, one perhaps short
+      const float away = fork ? 0.f : (float)(max(between - 1, 0) * p.hd->seg_chunks);
+      it.exact = it.nch - (g > 0.f ? (int)fminf(fmaxf(ceilf(7.f / g) + 1.f - away, 0.f), (float)it.nch) : it.nch);
+    }
   }
   return kOut || ((it.seg.need >> it.R->rev) & 1);
 }
@@ -690,20 +696,19 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         sm.w[e >> 6][t] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), w1, bf16x2_of(r));
       }
       if (!(ok = sync_w())) break;
-      // The weighted keys of quarter q of chunk c (the x-th of the CTA) in two or three bf16 terms, 32 tokens
-      // and 32 dimensions a warp.
-      auto convert = [&](int c, uint32_t x, int q) {
+      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
+        // The chunk's weighted keys, 32 tokens (a quarter) and 32 dimensions a warp at a time, in two or three
+        // bf16 terms.
         int n;
         la_chunk_at(it, c, n);
-        const LaTile<kOut> tk(x, 0);
+        const LaTile<kOut> tk(cc, 0);
         const bool three = it.three(c);
-        const int t0 = 32 * q;
-        if (!tk.wait_full(sm)) return false;
-        // rows past the chunk belong to another document (or lie outside the tensor): nothing they
-        // hold may reach the products
-        if (q == 0 && n < kLaChunk) {
-          const LaTile<kOut> tv(x, Sh::kTileV);
-          if (!tv.wait_full(sm)) return false;
+        if (!(ok = tk.wait_full(sm))) break;
+        // rows past the chunk belong to another document (or lie outside the tensor): nothing they hold may
+        // reach the products
+        if (q0 == 0 && n < kLaChunk) {
+          const LaTile<kOut> tv(cc, Sh::kTileV);
+          if (!(ok = tv.wait_full(sm))) break;
           uint8_t* vt = tv.at(sm);
           for (int e = tid - 32 * kSWarps; e < (kLaChunk - n) * 16; e += 128) {
             const int r = n + e / 16, y = e % 16;
@@ -711,80 +716,107 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           }
           fence_proxy_async_smem();
         }
+        // this lane's row of the four 8 x 8 blocks that a load takes: 8 tokens (lane bit 4), 8 dimensions (bit 3)
+        const int tok = ((lane >> 4) & 1) * 8 + (lane & 7), d8 = 4 * quarter + ((lane >> 3) & 1);
+        const uint32_t kr = smem_u32(tk.at(sm)) + (d8 >> 3) * (kTile / 2) + tok * 128;
+        const uint4* wt = &sm.w[n < kLaChunk][lane & 3];
+        auto load = [&](int q, int hl, uint32_t* k) {  // 32 tokens, 16 dimensions
+          const uint32_t ka = kr + q * 32 * 128 + ((((d8 + 2 * hl) ^ tok) & 7) << 4);
+          ldsm_x4_trans(ka, k);
+          ldsm_x4_trans(ka + 16 * 128, k + 4);
+          if (n < kLaChunk) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int t = 32 * q + 8 * y + 2 * (lane & 3);
+              const uint32_t keep = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
+              k[2 * y] &= keep;
+              k[2 * y + 1] &= keep;
+            }
+          }
+        };
         // The stage's last reader: each quarter has its own, but for three terms with outputs, where the later
         // half takes the earlier one's place. The two layouts overlap, so next to three terms a chunk follows
         // the whole of the one before. (Every earlier phase of a barrier is over when it is waited for: this
         // warp has waited for it, or for a later product. So its parity cannot be mistaken.)
-        if (kOut && three && q > 0) {
-          if (q >= 2 && !la_wait(&sm.kt_free[q - 2], x & 1, sm)) return false;
-        } else if (x > 0 && !la_wait(&sm.kt_free[kOut && q == 0 && (three || was_three) ? 3 : q], (x - 1) & 1, sm)) {
-          return false;
-        }
-        tc_fence_after();
-        const uint32_t ta = tl + Sh::kColKt + la_kt_col<kOut>(q, three);
-        const uint4* w = &sm.w[n < kLaChunk][t0 / 2 + (lane & 3)];
-        // this lane's row of the four 8 x 8 blocks that a load takes: 8 tokens (lane bit 4), 8 dimensions (bit 3)
-        const int tok = t0 + ((lane >> 4) & 1) * 8 + (lane & 7), d8 = 4 * quarter + ((lane >> 3) & 1);
-        const uint32_t kr = smem_u32(tk.at(sm)) + (d8 >> 3) * (kTile / 2) + tok * 128;
-        // 16 dimensions (lanes) at a time: the loop stays rolled and the quarters share it, since the
-        // roles' code together should stay in the instruction cache
-#pragma unroll 1
-        for (int hl = 0; hl < 2; ++hl) {
-          uint32_t k1[8], k2[8], k3[8];
-          const uint32_t ka = kr + ((((d8 + 2 * hl) ^ tok) & 7) << 4);
-          ldsm_x4_trans(ka, &k3[0]);
-          ldsm_x4_trans(ka + 16 * 128, &k3[4]);
-          if (n < kLaChunk) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int t = t0 + 8 * y + 2 * (lane & 3);
-              const uint32_t keep = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
-              k3[2 * y] &= keep;
-              k3[2 * y + 1] &= keep;
-            }
+        auto stage_free = [&](int q) {
+          bool got = true;
+          if (kOut && three && q > 0) {
+            if (q >= 2) got = la_wait(&sm.kt_free[q - 2], cc & 1, sm);
+          } else if (cc > 0) {
+            got = la_wait(&sm.kt_free[kOut && q == 0 && (three || was_three) ? 3 : q], (cc - 1) & 1, sm);
           }
-          const uint32_t tb = ta + ((uint32_t)(16 * hl) << 16);
-          if (three) {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint4 wy = w[4 * y];
-              const uint64_t f = f2_pack(__uint_as_float(wy.x), __uint_as_float(wy.y));
-#pragma unroll
-              for (int z = 2 * y; z < 2 * y + 2; ++z) {
-                const uint64_t v = f2_mul(f2_of_bf16x2(k3[z]), f);
-                k1[z] = bf16x2_of(v);
-                const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[z]));
-                k2[z] = bf16x2_of(r1);
-                k3[z] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[z])));
-              }
-            }
-            tmem_st16x128_x4(tb + 32, k3);
-          } else if (kOut) {
-            // with w = w1 + w2 in bf16: k w1 rounded, then its exact error (16 bits in all) plus k w2
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint4 wy = w[4 * y];
-#pragma unroll
-              for (int z = 2 * y; z < 2 * y + 2; ++z) {
-                k1[z] = bf2_mul(k3[z], wy.z);
-                k2[z] = bf2_fma(k3[z], wy.w, bf2_fma(k3[z], wy.z, k1[z] ^ 0x80008000u));
-              }
-            }
-          }
-          tmem_st16x128_x4(tb, k1);
-          tmem_st16x128_x4(tb + 16, k2);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.kt_ready[q]);
-        return true;
-      };
-      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
+          tc_fence_after();
+          return got;
+        };
+        auto ready = [&](int q) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.kt_ready[q]);
+        };
+        if (three) {
 #pragma unroll 1
-        for (int q = q0; q < 4; q += kQStep)
-          if (!(ok = convert(c, cc, q))) break;
-        was_three = it.three(c);
+          for (int q = q0; q < 4; q += kQStep) {
+            if (!(ok = stage_free(q))) break;
+            const uint4* w = wt + 16 * q;
+            // 16 dimensions (lanes) at a time: the loop stays rolled, since the roles' code together should
+            // stay in the instruction cache
+#pragma unroll 1
+            for (int hl = 0; hl < 2; ++hl) {
+              uint32_t k1[8], k2[8], k3[8];
+              load(q, hl, k3);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint4 wy = w[4 * y];
+                const uint64_t f = f2_pack(__uint_as_float(wy.x), __uint_as_float(wy.y));
+#pragma unroll
+                for (int z = 2 * y; z < 2 * y + 2; ++z) {
+                  const uint64_t v = f2_mul(f2_of_bf16x2(k3[z]), f);
+                  k1[z] = bf16x2_of(v);
+                  const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[z]));
+                  k2[z] = bf16x2_of(r1);
+                  k3[z] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[z])));
+                }
+              }
+              const uint32_t tb = tl + Sh::kColKt + la_kt_col<kOut>(q, true) + ((uint32_t)(16 * hl) << 16);
+              tmem_st16x128_x4(tb, k1);
+              tmem_st16x128_x4(tb + 16, k2);
+              tmem_st16x128_x4(tb + 32, k3);
+            }
+            ready(q);
+          }
+        } else {
+          // With w = w1 + w2 in bf16: k w1 rounded, then its exact error (16 bits in all) plus k w2. All of it is
+          // done before the stage is waited for: the products of the chunk before decide how soon this chunk's
+          // can follow.
+#pragma unroll 1
+          for (int q = q0; q < 4; q += kQStep) {
+            uint32_t k[2][8], k1[2][8];
+            load(q, 0, k[0]);
+            load(q, 1, k[1]);
+            const uint4* w = wt + 16 * q;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint2 wy = *reinterpret_cast<const uint2*>(&w[4 * y].z);
+#pragma unroll
+              for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                for (int z = 2 * y; z < 2 * y + 2; ++z) {
+                  k1[hl][z] = bf2_mul(k[hl][z], wy.x);
+                  k[hl][z] = bf2_fma(k[hl][z], wy.y, bf2_fma(k[hl][z], wy.x, k1[hl][z] ^ 0x80008000u));
+                }
+            }
+            if (!(ok = stage_free(q))) break;
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+              const uint32_t tb = tl + Sh::kColKt + la_kt_col<kOut>(q, false) + ((uint32_t)(16 * hl) << 16);
+              tmem_st16x128_x4(tb, k1[hl]);
+              tmem_st16x128_x4(tb + 16, k[hl]);
+            }
+            ready(q);
+          }
+        }
+        was_three = three;
       }
     }
   } else if (kOut && wid < Sh::kTmaWarp) {
@@ -1015,7 +1047,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         const uint64_t dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
         if constexpr (kOut) {
           const uint64_t dk = kmajor_desc(smem_u32(tk.at(sm)), kTile / 2, 0), dq = kmajor_desc(smem_u32(tq.at(sm)), kTile / 2, 0);
-          if (!(ok = tk.wait_full_all(sm) && tq.wait_full_all(sm))) break;
+          if (!(ok = all_ok(tk.wait_full(sm) && tq.wait_full(sm)))) break;
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -1024,7 +1056,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           }
           __syncwarp();
           // this chunk's state is in place, and the outputs of the chunk before have been read
-          if (!(ok = la_wait_all(&sm.s_ready, par, sm) && (cc == 0 || la_wait_all(&sm.o_free, (cc - 1) & 1, sm)))) break;
+          if (!(ok = all_ok(la_wait(&sm.s_ready, par, sm) && (cc == 0 || la_wait(&sm.o_free, (cc - 1) & 1, sm))))) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -1036,12 +1068,12 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           __syncwarp();
         }
         const bool three = c >= exact;
-        if (!(ok = tv.wait_full_all(sm) && (kvu == 0 || la_wait_all(&sm.kv_free[kvb], (kvu - 1) & 1, sm)))) break;
+        // (the accumulator is free: with outputs s_ready says so too)
+        if (!(ok = all_ok(tv.wait_full(sm) && (kOut || kvu == 0 || la_wait(&sm.kv_free[kvb], (kvu - 1) & 1, sm))))) break;
         // Products go out in groups as large as their operands allow: the pipe drains while this warp waits.
         if (kOut && !three) {
-          if (!(ok = la_wait_all(&sm.kt_ready[0], par, sm) && la_wait_all(&sm.kt_ready[1], par, sm) &&
-                     la_wait_all(&sm.kt_ready[2], par, sm) && la_wait_all(&sm.kt_ready[3], par, sm)))
-            break;
+          // (the last quarter's keys come after the others': one group of warps converts all four)
+          if (!(ok = all_ok(la_wait(&sm.kt_ready[3], par, sm)))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t ka = tm + Sh::kColKt;
@@ -1058,14 +1090,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         } else {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
-            if (!(ok = la_wait_all(&sm.kt_ready[q], par, sm))) break;
+            if (!(ok = all_ok(la_wait(&sm.kt_ready[q], par, sm)))) break;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t ka = tm + Sh::kColKt + la_kt_col<kOut>(q, true);
               const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
 #pragma unroll
-              for (int x = 0; x < 6; ++x)
+              for (int x = 0; x < 4; ++x)
                 umma_bf16_ts(tkv, ka + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, x & 1), id_mn, x > 0 ? 1u : (uint32_t)q);
+              if (kOut || three) {
+                umma_bf16_ts(tkv, ka + 32, mnmajor_step(dvq, 0), id_mn, 1);
+                umma_bf16_ts(tkv, ka + 40, mnmajor_step(dvq, 1), id_mn, 1);
+              }
               umma_commit(&sm.kt_free[q]);
               if (q == 3) {
                 umma_commit(&sm.kv_full[kvb]);
@@ -1080,7 +1116,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         if constexpr (kOut) {
 #pragma unroll 1
           for (int j = 0; j < 2; ++j) {  // P V for 64 key tokens
-            if (!(ok = la_wait_all(&sm.p_ready[j], par, sm))) break;
+            if (!(ok = all_ok(la_wait(&sm.p_ready[j], par, sm)))) break;
             tc_fence_after();
             if (elect_one()) {
               const uint64_t dvj = dv + (uint64_t)j * (8192u >> 4);

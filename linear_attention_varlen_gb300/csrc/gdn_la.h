@@ -20,7 +20,8 @@ struct LaSeg {
   int32_t k, nseg;       // place in the document
   int32_t src_fwd;       // state before the segment: -1 zero, >= 0 pool entry, -2 slot of this segment
   int32_t src_rev;       // state gradient after it: -1 the document's dfinal (or zero), -2 slot
-  int32_t need;          // bit 0: the end state from zero is needed (slots), bit 1: the same in reverse time
+  int32_t need;          // bit 0: the end state from zero is needed (slots), bit 1: the same in reverse time;
+                         // bit 2: documents fork from this one, bit 3: it is a fork
 };
 
 struct LaHeader {
