@@ -59,18 +59,67 @@ template <typename T>
 struct alignas(16) Raw8 {
   T t[8];
 };
-// columns c .. c + 7 of a row of D elements (zero past its end); kVec: rows are aligned and D a multiple of 8
-template <typename T, bool kVec>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int D) {
-  Raw8<T> r;
-  if constexpr (kVec) {
-    uint4* q = reinterpret_cast<uint4*>(r.t);
+// Words w[0 .. kN + 3] moved down by `bytes` (below 16, a multiple of sizeof(T), the same for the warp): the first
+// kN are valid.
+template <typename T, int kN>
+__device__ __forceinline__ void shift_words(uint32_t* w, uint32_t bytes) {
+  if (bytes & 8) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      q[i] = c < D ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kN + 2; ++i) w[i] = w[i + 2];
+  }
+  if (bytes & 4) {
+#pragma unroll
+    for (int i = 0; i < kN + 1; ++i) w[i] = w[i + 1];
+  }
+  if (sizeof(T) == 2 && (bytes & 2)) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w[i] = __byte_perm(w[i], w[i + 1], 0x5432);
+  }
+}
+
+// Columns c .. c + 7 of a row of D elements (zero past its end) of a tensor that lies in [lo, hi). kVec: rows are
+// aligned and D a multiple of 8. Other rows are read in whole 16-byte pieces too, the ones that cover the
+// columns, and moved into place: element by element a warp's lanes lie 8 elements apart, and each of the eight loads
+// touches every sector of the range (forward of 65536 x 1023: 365 us in fp32 and 265 us in bf16, now 160 us and
+// 158 us; aligned 130 us and 66 us). Only a piece that sticks out of the tensor is read by elements.
+template <typename T, bool kVec>
+__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int D, const T* lo, const T* hi) {
+  constexpr int kP = sizeof(T) / 2;  // pieces to 8 elements
+  Raw8<T> r;
+  uint4* q = reinterpret_cast<uint4*>(r.t);
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) q[i] = c < D ? reinterpret_cast<const uint4*>(row + c)[i] : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.t[i] = c + i < D ? row[c + i] : round_to<T>(0.f);
+    for (int i = 0; i < kP; ++i) q[i] = make_uint4(0, 0, 0, 0);
+    if (c >= D) return r;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + c), a0 = a & ~(uintptr_t)15;
+    const uint32_t m = (uint32_t)(a - a0);
+    if (a0 >= reinterpret_cast<uintptr_t>(lo) && a0 + 16 * (kP + (m ? 1 : 0)) <= reinterpret_cast<uintptr_t>(hi)) {
+      uint32_t w[4 * kP + 4];
+#pragma unroll
+      for (int i = 0; i < kP + 1; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (i < kP || m) x = reinterpret_cast<const uint4*>(a0)[i];
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+      shift_words<T, 4 * kP>(w, m);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) q[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      if (c + 8 > D) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i >= D) r.t[i] = round_to<T>(0.f);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < D) r.t[i] = row[c + i];
+    }
   }
   return r;
 }
@@ -79,8 +128,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// The same columns written, by whole warps whose lanes hold consecutive vectors. In rows that are not aligned a lane
+// writes the aligned pieces that begin inside its own vector, with the next lane's first elements; what no lane of
+// the warp can write whole (its first and last piece, a row's end) goes element by element.
 template <typename T, bool kVec>
 __device__ __forceinline__ void store8(T* row, int c, int D, const uint64_t* f) {  // four pairs of fp32
+  constexpr int kP = sizeof(T) / 2;
   Raw8<T> r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -93,22 +146,81 @@ __device__ __forceinline__ void store8(T* row, int c, int D, const uint64_t* f) 
       r.t[2 * i + 1] = bw::f2_hi(f[i]);
     }
   }
+  const uint4* q = reinterpret_cast<const uint4*>(r.t);
   if constexpr (kVec) {
     if (c < D) {
-      const uint4* q = reinterpret_cast<const uint4*>(r.t);
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + c)[i] = q[i];
+      for (int i = 0; i < kP; ++i) reinterpret_cast<uint4*>(row + c)[i] = q[i];
     }
   } else {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + c), a0 = a & ~(uintptr_t)15;
+    const uint32_t m = (uint32_t)(a - a0);  // the same in every lane
+    bool whole[kP + 1];                     // pieces 0 (the lane before writes it) to kP
+    const int lane = threadIdx.x & 31, head = (16 - (int)m) / (int)sizeof(T);  // elements of piece 0
+    constexpr int kE = 16 / sizeof(T);
+    whole[0] = m == 0 ? c + kE <= D : lane > 0 && c + head <= D;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < D) row[c + i] = r.t[i];
+    for (int i = 1; i <= kP; ++i) whole[i] = m == 0 ? c + kE * (i + 1) <= D : (i < kP || lane < 31) && c + head + kE * i <= D;
+    if (m == 0) {
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        if (whole[i]) reinterpret_cast<uint4*>(a0)[i] = q[i];
+    } else {
+      uint32_t w[4 * kP + 4];
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        w[4 * i] = q[i].x;
+        w[4 * i + 1] = q[i].y;
+        w[4 * i + 2] = q[i].z;
+        w[4 * i + 3] = q[i].w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[4 * kP + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+      shift_words<T, 4 * kP>(w, 16 - m);
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        if (whole[i + 1])
+          reinterpret_cast<uint4*>(a0)[i + 1] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i <= kP; ++i) all = all && (whole[i] || (m == 0 && i == kP));
+    if (!all) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t at = (m + i * (uint32_t)sizeof(T)) >> 4;
+        const bool done = at == 0 ? whole[0] : at == 1 ? whole[1] : whole[kP];
+        if (c + i < D && !done) row[c + i] = r.t[i];
+      }
+    }
+  }
+}
+// eight bytes, the same way in pieces of eight
+template <bool kVec>
+__device__ __forceinline__ void store8_bytes(uint8_t* row, int c, int D, uint64_t v) {
+  if constexpr (kVec) {
+    if (c < D) *reinterpret_cast<uint64_t*>(row + c) = v;
+  } else {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row + c), a0 = a & ~(uintptr_t)7;
+    const int m = (int)(a - a0), lane = threadIdx.x & 31, head = 8 - m;
+    const bool first = m == 0 ? c + 8 <= D : lane > 0 && c + head <= D, last = m != 0 && lane < 31 && c + head + 8 <= D;
+    if (m == 0) {
+      if (first) *reinterpret_cast<uint64_t*>(a0) = v;
+    } else {
+      const uint64_t next = __shfl_down_sync(0xffffffffu, v, 1);
+      if (last) *reinterpret_cast<uint64_t*>(a0 + 8) = v >> (8 * head) | next << (8 * m);
+    }
+    if (!first || (m != 0 && !last)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < D && !(m + i < 8 ? first : last)) row[c + i] = (uint8_t)(v >> (8 * i));
+    }
   }
 }
 template <bool kVec>
 __device__ __forceinline__ void load_w8(const void* w, int dtype, int c, int D, float* f) {
   auto get = [&](auto* p) {
-    const auto r = load8<std::remove_const_t<std::remove_pointer_t<decltype(p)>>, kVec>(p, c, D);
+    const auto r = load8<std::remove_const_t<std::remove_pointer_t<decltype(p)>>, kVec>(p, c, D, p, p + D);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = elem(r.t[i]);
   };
@@ -174,12 +286,13 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kNv == 1 ? 256 : kRow
   uint64_t ss = 0;
   const bool res = p.r != nullptr;
   {
+    const T *xs = static_cast<const T*>(p.x), *rr = static_cast<const T*>(p.r);
     Raw8<T> x[kNv], r[kNv];
 #pragma unroll
-    for (int j = 0; j < kNv; ++j) x[j] = load8<T, kVec>(static_cast<const T*>(p.x) + row * p.D, (t + j * tpr) * 8, p.D);
+    for (int j = 0; j < kNv; ++j) x[j] = load8<T, kVec>(xs + row * p.D, (t + j * tpr) * 8, p.D, xs, xs + p.T * p.D);
     if (res) {
 #pragma unroll
-      for (int j = 0; j < kNv; ++j) r[j] = load8<T, kVec>(static_cast<const T*>(p.r) + row * p.D, (t + j * tpr) * 8, p.D);
+      for (int j = 0; j < kNv; ++j) r[j] = load8<T, kVec>(rr + row * p.D, (t + j * tpr) * 8, p.D, rr, rr + p.T * p.D);
     }
 #pragma unroll
     for (int j = 0; j < kNv; ++j)
@@ -249,14 +362,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kNv == 1 ? 256 : kRow
       const uint64_t z = bw::f2_mul(tiny ? bw::f2_mul(v[j][i], up2) : v[j][i], inv2);
       b[i] = __nv_cvt_float2_to_fp8x2(make_float2(bw::f2_lo(z), bw::f2_hi(z)), __NV_SATFINITE, __NV_E4M3);
     }
-    const int c = (t + j * tpr) * 8;
-    if constexpr (kVec) {
-      if (c < p.D) *reinterpret_cast<uint2*>(y + c) = *reinterpret_cast<const uint2*>(b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < p.D) y[c + i] = reinterpret_cast<const uint8_t*>(b)[i];
-    }
+    store8_bytes<kVec>(y, (t + j * tpr) * 8, p.D, *reinterpret_cast<const uint64_t*>(b));
   }
 }
 
@@ -282,6 +388,7 @@ constexpr uint32_t kBwdRing = 196608;  // bytes of the rings of a CTA
 template <typename T, int kNv, int kTeam, bool kRing>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr int kTeams = kBwdWarps / kTeam;
+  bw::griddep_launch_dependents();  // the sum over the parts may take its place, and waits there
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t s_full[kTeams][8];
   __shared__ float2 s_red[kTeams][2][kTeam];
@@ -291,7 +398,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   const int stages = kRing ? min(8, (int)(kBwdRing / kTeams / stage_bytes)) : 1;
   uint8_t* mine = ring + (size_t)team * stages * stage_bytes;
   const T* src[3] = {static_cast<const T*>(p.h), static_cast<const T*>(p.dy), static_cast<const T*>(p.dh)};
-  const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams;
+  const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams, n = p.T * p.D;
   if (kRing && t == 0) {
     for (int i = 0; i < stages; ++i) bw::mbar_init(&s_full[team][i], 1);
     bw::fence_mbar_init();
@@ -314,7 +421,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   const bool same = p.w_dtype == (sizeof(T) == 4 ? GDN_DTYPE_FP32 : std::is_same_v<T, __half> ? GDN_DTYPE_FP16 : GDN_DTYPE_BF16);
 #pragma unroll
   for (int j = 0; j < kNv; ++j) {
-    if (same) w[j] = load8<T, kRing>(static_cast<const T*>(p.w), (t + j * 32 * kTeam) * 8, p.D);
+    const T* pw = static_cast<const T*>(p.w);
+    if (same) w[j] = load8<T, kRing>(pw, (t + j * 32 * kTeam) * 8, p.D, pw, pw + p.D);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
@@ -339,12 +447,30 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
       e = reinterpret_cast<const T*>(b + 2 * row_bytes);
     }
     float2 sum = make_float2(0.f, 0.f);
+    // Rows that had to be moved into place stay in registers where two vectors of each fit (65536 x 1023 fp32: 213 us
+    // against 259); with four, in 16 bits, that spills (288 us against 257).
+    constexpr bool kKeep = !kRing && kNv <= 2;
+    Raw8<T> hs[kKeep ? kNv : 1], gs[kKeep ? kNv : 1];
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int j = 0; j < kNv; ++j) {
+        const int c = (t + j * 32 * kTeam) * 8;
+        hs[j] = load8<T, false>(h, c, p.D, src[0], src[0] + n);
+        gs[j] = load8<T, false>(g, c, p.D, src[1], src[1] + n);
+      }
+    }
+    auto again = [&](int k, const T* from, const Raw8<T>* kept, int j, int c) {
+      if constexpr (kKeep)
+        return kept[j];
+      else
+        return load8<T, kRing>(from, c, p.D, src[k], src[k] + n);
+    };
     {
       uint64_t s1 = 0, s2 = 0;
 #pragma unroll
       for (int j = 0; j < kNv; ++j) {
         const int c = (t + j * 32 * kTeam) * 8;
-        const Raw8<T> hr = load8<T, kRing>(h, c, p.D), gr = load8<T, kRing>(g, c, p.D);
+        const Raw8<T> hr = again(0, h, hs, j, c), gr = again(1, g, gs, j, c);
         float wf[8];
         weight(j, wf);
 #pragma unroll
@@ -380,9 +506,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
       const int c = (t + j * 32 * kTeam) * 8;
-      const Raw8<T> hr = load8<T, kRing>(h, c, p.D), gr = load8<T, kRing>(g, c, p.D);
+      const Raw8<T> hr = again(0, h, hs, j, c), gr = again(1, g, gs, j, c);
       Raw8<T> er;
-      if (p.dh) er = load8<T, kRing>(e, c, p.D);
+      if (p.dh) er = load8<T, kRing>(e, c, p.D, src[2], src[2] + n);
       float wf[8];
       weight(j, wf);
       uint64_t o[4];
@@ -410,30 +536,37 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
       }
     }
   }
-  // the CTA's part: its teams' in order, through the rings (every copy has landed and been read)
+  // the CTA's part: its teams', summed in their order through the rings (every copy has landed and been read)
   __syncthreads();
   float* s_dw = reinterpret_cast<float*>(ring);
-  for (int k = 0; k < kTeams; ++k) {
-    if (team == k) {
+  const int pad = (p.D + 7) & ~7;
 #pragma unroll
-      for (int j = 0; j < kNv; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = (t + j * 32 * kTeam) * 8 + i;
-          if (c < p.D) s_dw[c] = k ? s_dw[c] + dw[j][i] : dw[j][i];
-        }
+  for (int j = 0; j < kNv; ++j) {
+    const int c = (t + j * 32 * kTeam) * 8;
+    if (c < p.D) {
+      float4* d = reinterpret_cast<float4*>(s_dw + team * pad + c);
+      d[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+      d[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
-    __syncthreads();
   }
-  for (int c = threadIdx.x; c < p.D; c += 32 * kBwdWarps) p.part[(int64_t)blockIdx.x * p.D + c] = s_dw[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.D; c += 32 * kBwdWarps) {
+    float a = s_dw[c];
+#pragma unroll
+    for (int k = 1; k < kTeams; ++k) a += s_dw[k * pad + c];
+    p.part[(int64_t)blockIdx.x * p.D + c] = a;
+  }
 }
 
 // Rows too long for a team's registers and ring (above 16384 elements, 8192 in fp32): one a CTA at a time, rows
-// blockIdx.x, + gridDim.x, ...
+// blockIdx.x, + gridDim.x, ..., read twice (with the row kept in registers 8 vectors a thread spilled).
 template <typename T, int kNv>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float2 s_red[2][16];
+  bw::griddep_launch_dependents();
   const int tpr = blockDim.x, t = threadIdx.x;
+  const T *hs = static_cast<const T*>(p.h), *gs = static_cast<const T*>(p.dy), *es = static_cast<const T*>(p.dh);
+  const int64_t n = p.T * p.D;
   float dw[kNv][8];
 #pragma unroll
   for (int j = 0; j < kNv; ++j)
@@ -441,26 +574,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __g
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-    const T* h = static_cast<const T*>(p.h) + row * p.D;
-    const T* g = static_cast<const T*>(p.dy) + row * p.D;
-    const T* e = p.dh ? static_cast<const T*>(p.dh) + row * p.D : nullptr;
+    const T *h = hs + row * p.D, *g = gs + row * p.D, *e = es ? es + row * p.D : nullptr;
     T* dx = static_cast<T*>(p.dx) + row * p.D;
-    Raw8<T> hr[kNv], gr[kNv];
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
-      hr[j] = load8<T, false>(h, (t + j * tpr) * 8, p.D);
-      gr[j] = load8<T, false>(g, (t + j * tpr) * 8, p.D);
-    }
-#pragma unroll
-    for (int j = 0; j < kNv; ++j) {
+      const int at = (t + j * tpr) * 8;
+      const Raw8<T> hr = load8<T, false>(h, at, p.D, hs, hs + n), gr = load8<T, false>(g, at, p.D, gs, gs + n);
       float w[8];
-      load_w8<false>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w);
+      load_w8<false>(p.w, p.w_dtype, at, p.D, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float hv = elem(hr[j].t[i]);
+        const float hv = elem(hr.t[i]);
         sum.x = fmaf(hv, hv, sum.x);
-        sum.y = fmaf(hv * w[i], elem(gr[j].t[i]), sum.y);
+        sum.y = fmaf(hv * w[i], elem(gr.t[i]), sum.y);
       }
     }
     sum = row_reduce<false>(sum, s_red[turn]);
@@ -468,13 +595,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __g
     const float c = rs * rs * rs * (sum.y / (float)p.D);
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
+      const int at = (t + j * tpr) * 8;
+      const Raw8<T> hr = load8<T, false>(h, at, p.D, hs, hs + n), gr = load8<T, false>(g, at, p.D, gs, gs + n);
       float w[8], o[8];
-      load_w8<false>(p.w, p.w_dtype, (t + j * tpr) * 8, p.D, w);
+      load_w8<false>(p.w, p.w_dtype, at, p.D, w);
       Raw8<T> er;
-      if (e) er = load8<T, false>(e, (t + j * tpr) * 8, p.D);
+      if (e) er = load8<T, false>(e, at, p.D, es, es + n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float hv = elem(hr[j].t[i]), gv = elem(gr[j].t[i]) * rs;
+        const float hv = elem(hr.t[i]), gv = elem(gr.t[i]) * rs;
         dw[j][i] = fmaf(gv, hv, dw[j][i]);
         o[i] = fmaf(w[i], gv, -c * hv);
         if (e) o[i] += elem(er.t[i]);
@@ -482,7 +611,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __g
       uint64_t o2[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) o2[i] = bw::f2_pack(o[2 * i], o[2 * i + 1]);
-      store8<T, false>(dx, (t + j * tpr) * 8, p.D, o2);
+      store8<T, false>(dx, at, p.D, o2);
     }
   }
 #pragma unroll
@@ -586,12 +715,12 @@ void launch_fwd(const NormFwdParams& p, cudaStream_t st) {
 template <typename T, int kNv, int kTeam>
 bool launch_team(const NormBwdParams& p, bool ring, int dev, cudaStream_t st) {
   if (!ring) {
-    // the parts are summed in the row's bytes of shared memory
-    const size_t smem = (size_t)p.D * sizeof(float);
+    // the teams' parts are summed in shared memory: 16 rows of at most 1024 floats, whatever the team
+    const size_t smem = (size_t)(kBwdWarps / kTeam) * ((p.D + 7) & ~7) * sizeof(float);
     static PerDevice set;
     if (smem > 48000 && !set.done(dev)) {
       if (cudaFuncSetAttribute(norm_bwd_team_kernel<T, kNv, kTeam, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kNormMaxD * (int)sizeof(float)) != cudaSuccess)
+                               kBwdWarps * 1024 * (int)sizeof(float)) != cudaSuccess)
         return false;
       set.mark(dev);
     }
