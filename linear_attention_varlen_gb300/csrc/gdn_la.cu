@@ -66,9 +66,8 @@ struct LaParams {
   const float* start;   // pool of start states
   const float* dfinal;  // gradient of the final states, or null
   LaHeader* hd;
-  LaSeg* segs;
-  int32_t* seg0;
-  int32_t* order;  // segments, the longest first
+  LaSeg* segs;    // the longest first
+  int32_t* seg0;  // each document's first segment, documents in order
   int32_t* is_src;
   float *slot_f, *slot_r, *fin, *acc;
   float *end_fwd, *end_rev;  // final states, start-state gradients of the documents; null = not wanted
@@ -138,6 +137,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
     if (tid == 0) {
       p.hd->status = kErrInvalid;
       p.hd->n_segs = 0;
+      p.hd->n_starts = 0;
       p.hd->scan = 0;
     }
     return;
@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
   }
   __syncthreads();
   const int seg_tok = s_len * kLaChunk;
+  auto bucket = [](int tokens) { return 63 - min(63, (tokens + kLaChunk - 1) / kLaChunk); };
   for (int i0 = 0; i0 < p.N; i0 += kLaPlanThreads) {
     const int i = i0 + tid;
     int b = 0, len = 0, cnt = 0;
@@ -225,23 +226,9 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
     if (i < p.N) {
       p.seg0[i] = base;
       const int idx = p.init_idx ? p.init_idx[i] : -1;
-      const bool fork = idx >= p.n_init && idx >= 0, src = p.init_idx && p.is_src[i] != 0;
-      if (cnt > 1 || fork || src) s_scan = 1;
-      for (int k = 0; k < cnt; ++k) {
-        LaSeg s;
-        s.doc = i;
-        s.tok0 = b + k * seg_tok;
-        s.ntok = cnt > 1 ? min(seg_tok, len - k * seg_tok) : len;
-        s.k = k;
-        s.nseg = cnt;
-        s.src_fwd = (k > 0 || fork) ? -2 : idx;
-        s.src_rev = (k < cnt - 1 || src) ? -2 : -1;
-        // a cut document's final state, and its start's gradient where one is wanted, come from the scan
-        s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0) | (src ? 4 : 0) |
-                 (fork ? 8 : 0);
-        p.segs[base + k] = s;
-        atomicAdd(&s_hist[63 - min(63, (s.ntok + kLaChunk - 1) / kLaChunk)], 1);
-      }
+      if (cnt > 1 || (idx >= 0 && idx >= p.n_init) || (p.init_idx && p.is_src[i])) s_scan = 1;
+      if (cnt > 1) atomicAdd(&s_hist[bucket(seg_tok)], cnt - 1);
+      atomicAdd(&s_hist[bucket(len - (cnt - 1) * seg_tok)], 1);
     }
     __syncthreads();
     if (tid == 0) s_base += total;
@@ -262,12 +249,34 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
   }
   __syncthreads();
   const int n_segs = s_base;
-  for (int s = tid; s < n_segs; s += kLaPlanThreads)
-    p.order[atomicAdd(&s_hist[63 - min(63, (p.segs[s].ntok + kLaChunk - 1) / kLaChunk)], 1)] = s;
+  for (int g = tid; g < n_segs; g += kLaPlanThreads) {
+    int i = 0, hi = p.N;  // the document: the last one whose first segment is not after this one
+    while (hi - i > 1) {
+      const int mid = (i + hi) >> 1;
+      (p.seg0[mid] <= g ? i : hi) = mid;
+    }
+    const int b = p.cu[i], len = p.cu[i + 1] - b;
+    const int cnt = (seg_tok && len > seg_tok) ? (len + seg_tok - 1) / seg_tok : 1, k = g - p.seg0[i];
+    const int idx = p.init_idx ? p.init_idx[i] : -1;
+    const bool fork = idx >= p.n_init && idx >= 0, src = p.init_idx && p.is_src[i] != 0;
+    LaSeg s;
+    s.doc = i;
+    s.tok0 = b + k * seg_tok;
+    s.ntok = cnt > 1 ? min(seg_tok, len - k * seg_tok) : len;
+    s.k = k;
+    s.nseg = cnt;
+    s.src_fwd = (k > 0 || fork) ? -2 : idx;
+    s.slot = g;
+    // a cut document's final state, and its start's gradient where one is wanted, come from the scan
+    s.need = ((cnt > 1 || src) ? 1 : 0) | ((k > 0 || fork || (cnt > 1 && p.end_rev)) ? 2 : 0) | (src ? 4 : 0) |
+             (fork ? 8 : 0) | ((k < cnt - 1 || src) ? 16 : 0);
+    p.segs[atomicAdd(&s_hist[bucket(s.ntok)], 1)] = s;
+  }
   if (tid == 0) {
     p.seg0[p.N] = n_segs;
     p.hd->status = kOk;
     p.hd->n_segs = n_segs;
+    p.hd->n_starts = s_scan ? n_segs : 0;
     p.hd->scan = s_scan;
     p.hd->seg_chunks = s_len;
     p.hd->ticket[0] = 0;
@@ -386,6 +395,27 @@ __device__ __forceinline__ void set_regs() {
   else if constexpr (kTo < kFrom)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTo));
 }
+// Four lanes, a row each, four columns to a quad: lane i's quad k and lane k's quad i change places. Rows then leave
+// (or come) in whole sectors, 64 bytes of a row at a time; a row to a lane, 16 bytes at a time, a state's 64 KB took
+// about 6000 cycles to write, longer than two chunks.
+__device__ __forceinline__ void swap_quads(float* x) {
+  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const float t = __shfl_xor_sync(0xffffffffu, b0 ? x[4 * k + c] : x[4 * k + 4 + c], 1);
+      x[4 * k + c] = b0 ? t : x[4 * k + c];
+      x[4 * k + 4 + c] = b0 ? x[4 * k + 4 + c] : t;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float t = __shfl_xor_sync(0xffffffffu, b1 ? x[4 * k + c] : x[4 * k + 8 + c], 2);
+      x[4 * k + c] = b1 ? t : x[4 * k + c];
+      x[4 * k + 8 + c] = b1 ? x[4 * k + 8 + c] : t;
+    }
+  }
+}
 // true in one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -423,10 +453,10 @@ __device__ __forceinline__ uint32_t la_kt_col(int q, bool three) {
 template <bool kOut>
 struct LaTile {
   uint32_t slot, use;
-  __device__ __forceinline__ LaTile(uint32_t x, uint32_t i) {
+  __device__ __forceinline__ LaTile(uint32_t slot, uint32_t use) : slot(slot), use(use) {}
+  static __device__ __forceinline__ LaTile of(uint32_t x, uint32_t i) {
     const uint32_t t = LaShape<kOut>::kPerChunk * x + i;
-    slot = t % LaShape<kOut>::kSlots;
-    use = t / LaShape<kOut>::kSlots;
+    return {t % LaShape<kOut>::kSlots, t / LaShape<kOut>::kSlots};
   }
   __device__ __forceinline__ uint8_t* at(LaSmem& sm) const { return sm.tiles + slot * kTile; }
   __device__ __forceinline__ bool wait_full(LaSmem& sm) const { return la_wait(&sm.full[slot], use & 1, sm); }
@@ -437,7 +467,7 @@ __device__ __forceinline__ bool la_writes_end(const LaParams& p, const LaItem& i
 // One item of a CTA's walk and what its roles derive from it.
 struct LaItem {
   LaSeg seg;
-  int sidx, h, nch;
+  int h, nch;
   int first;  // first chunk that the walk takes
   int exact;  // chunks from this one on update the state with three terms
   const LaRole* R;
@@ -447,9 +477,8 @@ template <bool kOut>
 __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaItem& it) {
   it.h = i % p.Hv;
   const int r = (i / p.Hv) % roles;
-  it.sidx = p.order[i / (p.Hv * roles)];
   it.R = &p.role[r];
-  it.seg = p.segs[it.sidx];
+  it.seg = p.segs[i / (p.Hv * roles)];
   it.nch = (it.seg.ntok + kLaChunk - 1) / kLaChunk;
   it.first = 0;
   const float g = -fmaxf(p.log_decay[it.h], -1e4f) * kLaChunk;  // decay of a chunk
@@ -498,11 +527,6 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   }
   LaSmem& sm = *reinterpret_cast<LaSmem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  if constexpr (!kOut) {
-    griddep_wait();
-    griddep_launch_dependents();
-    if (!p.hd->scan) return;  // no document is cut, none is forked
-  }
   if (wid == Sh::kMmaWarp) tmem_alloc(&sm.tmem, 512);
   if (tid == 0) {
     for (int i = 0; i < 7; ++i) {
@@ -535,12 +559,10 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, sm.tmem, 0);
-  if constexpr (kOut) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  griddep_wait();
+  griddep_launch_dependents();
   const int roles = p.n_roles;
-  const int n_items = p.hd->n_segs * roles * p.Hv;
+  const int n_items = (kOut ? p.hd->n_segs : p.hd->n_starts) * roles * p.Hv;
   // The next item of a warp's walk, as the copy warp has drawn it; false at the end (or after a failed wait).
   uint32_t items = 0;
   auto next_item = [&](LaItem& it) {
@@ -565,6 +587,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     const int quarter = wid & 3, ch = wid >> 2;  // tensor-memory lanes 32 quarter .. +31, columns 64 ch .. +63
     constexpr int kCols = 64;
     const int row = 32 * quarter + lane;
+    // where a lane's first four columns lie in memory once each four lanes have exchanged theirs
+    auto part = [&]() { return (row & ~3) * kDim + kCols * ch + 4 * (threadIdx.x & 3); };
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
     float S[kCols];
     while (ok && next_item(it)) {
@@ -572,9 +596,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       const float g = fmaxf(p.log_decay[it.h], -1e4f);
       const float* sp = nullptr;
       if constexpr (kOut) {
-        const int src = R.rev ? it.seg.src_rev : it.seg.src_fwd;
-        if (src == -2)
-          sp = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.sidx * p.Hv + it.h) * kLaState;
+        const int src = it.seg.src_fwd;
+        if (R.rev ? it.seg.need & 16 : src == -2)
+          sp = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.seg.slot * p.Hv + it.h) * kLaState;
         else if (R.rev)
           sp = p.dfinal ? p.dfinal + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState : nullptr;
         else if (src >= 0)
@@ -587,13 +611,18 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
 #pragma unroll
         for (int j = 0; j < kCols; ++j) S[j] = sp[(size_t)(kCols * ch + j) * kDim + row];
       } else {
+        sp += part();
 #pragma unroll
-        for (int j = 0; j < kCols; j += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + kCols * ch + j);
-          S[j] = x.x;
-          S[j + 1] = x.y;
-          S[j + 2] = x.z;
-          S[j + 3] = x.w;
+        for (int j = 0; j < kCols; j += 16) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(sp + k * kDim + j);
+            S[j + 4 * k] = x.x;
+            S[j + 4 * k + 1] = x.y;
+            S[j + 4 * k + 2] = x.z;
+            S[j + 4 * k + 3] = x.w;
+          }
+          swap_quads(S + j);
         }
       }
       float lam_hi = 1.f, lam_lo = 0.f;
@@ -651,14 +680,19 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       if (!ok) break;
       float* dst = nullptr;
       if (!kOut)
-        dst = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.sidx * p.Hv + it.h) * kLaState;
+        dst = (R.rev ? p.slot_r : p.slot_f) + ((size_t)it.seg.slot * p.Hv + it.h) * kLaState;
       else if (la_writes_end(p, it))
         dst = R.last + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState;
       if (dst) {
+        dst += part();
 #pragma unroll
-        for (int j = 0; j < kCols; j += 4)
-          *reinterpret_cast<float4*>(dst + (size_t)row * kDim + kCols * ch + j) =
-              make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < kCols; j += 16) {
+          swap_quads(S + j);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(dst + k * kDim + j) =
+                make_float4(S[j + 4 * k], S[j + 4 * k + 1], S[j + 4 * k + 2], S[j + 4 * k + 3]);
+        }
       }
     }
   } else if (wid < Sh::kPo0) {
@@ -701,13 +735,13 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         // bf16 terms.
         int n;
         la_chunk_at(it, c, n);
-        const LaTile<kOut> tk(cc, 0);
+        const LaTile<kOut> tk = LaTile<kOut>::of(cc, 0);
         const bool three = it.three(c);
         if (!(ok = tk.wait_full(sm))) break;
         // rows past the chunk belong to another document (or lie outside the tensor): nothing they hold may
         // reach the products
         if (q0 == 0 && n < kLaChunk) {
-          const LaTile<kOut> tv(cc, Sh::kTileV);
+          const LaTile<kOut> tv = LaTile<kOut>::of(cc, Sh::kTileV);
           if (!(ok = tv.wait_full(sm))) break;
           uint8_t* vt = tv.at(sm);
           for (int e = tid - 32 * kSWarps; e < (kLaChunk - n) * 16; e += 128) {
@@ -755,33 +789,48 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           if (lane == 0) mbar_arrive(&sm.kt_ready[q]);
         };
         if (three) {
+          auto split = [&](int q, int hl, uint32_t* k1, uint32_t* k2, uint32_t* k3) {
+            load(q, hl, k3);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint4 wy = wt[16 * q + 4 * y];
+              const uint64_t f = f2_pack(__uint_as_float(wy.x), __uint_as_float(wy.y));
+#pragma unroll
+              for (int z = 2 * y; z < 2 * y + 2; ++z) {
+                const uint64_t v = f2_mul(f2_of_bf16x2(k3[z]), f);
+                k1[z] = bf16x2_of(v);
+                const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[z]));
+                k2[z] = bf16x2_of(r1);
+                k3[z] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[z])));
+              }
+            }
+          };
+          auto store = [&](int q, int hl, const uint32_t* k1, const uint32_t* k2, const uint32_t* k3) {
+            const uint32_t tb = tl + Sh::kColKt + la_kt_col<kOut>(q, true) + ((uint32_t)(16 * hl) << 16);
+            tmem_st16x128_x4(tb, k1);
+            tmem_st16x128_x4(tb + 16, k2);
+            tmem_st16x128_x4(tb + 32, k3);
+          };
 #pragma unroll 1
           for (int q = q0; q < 4; q += kQStep) {
-            if (!(ok = stage_free(q))) break;
-            const uint4* w = wt + 16 * q;
-            // 16 dimensions (lanes) at a time: the loop stays rolled, since the roles' code together should
-            // stay in the instruction cache
+            if constexpr (kOut) {
+              // 16 dimensions (lanes) at a time: the loop stays rolled, since the roles' code together should
+              // stay in the instruction cache; the first half is ready before the stage is waited for
 #pragma unroll 1
-            for (int hl = 0; hl < 2; ++hl) {
-              uint32_t k1[8], k2[8], k3[8];
-              load(q, hl, k3);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint4 wy = w[4 * y];
-                const uint64_t f = f2_pack(__uint_as_float(wy.x), __uint_as_float(wy.y));
-#pragma unroll
-                for (int z = 2 * y; z < 2 * y + 2; ++z) {
-                  const uint64_t v = f2_mul(f2_of_bf16x2(k3[z]), f);
-                  k1[z] = bf16x2_of(v);
-                  const uint64_t r1 = f2_sub(v, f2_of_bf16x2(k1[z]));
-                  k2[z] = bf16x2_of(r1);
-                  k3[z] = bf16x2_of(f2_sub(r1, f2_of_bf16x2(k2[z])));
-                }
+              for (int hl = 0; hl < 2; ++hl) {
+                uint32_t k1[8], k2[8], k3[8];
+                split(q, hl, k1, k2, k3);
+                if (hl == 0 && !(ok = stage_free(q))) break;
+                store(q, hl, k1, k2, k3);
               }
-              const uint32_t tb = tl + Sh::kColKt + la_kt_col<kOut>(q, true) + ((uint32_t)(16 * hl) << 16);
-              tmem_st16x128_x4(tb, k1);
-              tmem_st16x128_x4(tb + 16, k2);
-              tmem_st16x128_x4(tb + 32, k3);
+              if (!ok) break;
+            } else {  // all of it before the stage is waited for
+              uint32_t k1[2][8], k2[2][8], k3[2][8];
+              split(q, 0, k1[0], k2[0], k3[0]);
+              split(q, 1, k1[1], k2[1], k3[1]);
+              if (!(ok = stage_free(q))) break;
+              store(q, 0, k1[0], k2[0], k3[0]);
+              store(q, 1, k1[1], k2[1], k3[1]);
             }
             ready(q);
           }
@@ -1014,7 +1063,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           const int tok = la_chunk_at(it, c, n);
 #pragma unroll
           for (uint32_t x = 0; x < Sh::kPerChunk; ++x) {
-            const LaTile<kOut> t(cc, x);
+            const LaTile<kOut> t = LaTile<kOut>::of(cc, x);
             if (t.use > 0 && !(ok = la_wait(&sm.free_[t.slot], (t.use - 1) & 1, sm))) break;
             mbar_arrive_expect_tx(&sm.full[t.slot], kTile);
             const bool key = x == 0, val = x == Sh::kTileV;
@@ -1038,15 +1087,28 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     // A chunk's order is Q K^T, Q S, the state's product, P V: the two in the middle run while the map is made.
     const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_mn = idesc_bf16(128, 128, 0, 1);
     const uint64_t ds = mnmajor_desc(smem_u32(sm.s), kTile / 2, 0);
+    // The ring's next tile and the descriptors of its first: kept as the walk goes, so that little is left to
+    // compute between a chunk's last product and the next one's first.
+    const uint64_t kmaj0 = kmajor_desc(smem_u32(sm.tiles), kTile / 2, 0), mnmaj0 = mnmajor_desc(smem_u32(sm.tiles), kTile / 2, 0);
+    uint32_t next_slot = 0, next_use = 0;
+    auto next_tile = [&]() {
+      LaTile<kOut> t(next_slot, next_use);
+      if (++next_slot == Sh::kSlots) {
+        next_slot = 0;
+        next_use ^= 1;
+      }
+      return t;
+    };
+    auto tile_at = [&](uint64_t first, const LaTile<kOut>& t) { return first + (uint64_t)(t.slot * (kTile >> 4)); };
     while (ok && next_item(it)) {
       const int first = __shfl_sync(0xffffffffu, it.first, 0), nch = __shfl_sync(0xffffffffu, it.nch, 0);
       const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
       for (int c = first; ok && c < nch; ++c, ++cc) {
         const uint32_t par = cc & 1, kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
-        const LaTile<kOut> tk(cc, 0), tq(cc, 1), tv(cc, Sh::kTileV);
-        const uint64_t dv = mnmajor_desc(smem_u32(tv.at(sm)), kTile / 2, 0);
+        const LaTile<kOut> tk = next_tile(), tq = kOut ? next_tile() : tk, tv = next_tile();
+        const uint64_t dv = tile_at(mnmaj0, tv);
         if constexpr (kOut) {
-          const uint64_t dk = kmajor_desc(smem_u32(tk.at(sm)), kTile / 2, 0), dq = kmajor_desc(smem_u32(tq.at(sm)), kTile / 2, 0);
+          const uint64_t dk = tile_at(kmaj0, tk), dq = tile_at(kmaj0, tq);
           if (!(ok = all_ok(tk.wait_full(sm) && tq.wait_full(sm)))) break;
           if (elect_one()) {
 #pragma unroll
@@ -1087,7 +1149,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
             umma_commit(&sm.free_[tk.slot]);
           }
           __syncwarp();
-        } else {
+        } else if (kOut) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
             if (!(ok = all_ok(la_wait(&sm.kt_ready[q], par, sm)))) break;
@@ -1096,17 +1158,40 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
               const uint32_t ka = tm + Sh::kColKt + la_kt_col<kOut>(q, true);
               const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
+              for (int x = 0; x < 6; ++x)
                 umma_bf16_ts(tkv, ka + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, x & 1), id_mn, x > 0 ? 1u : (uint32_t)q);
-              if (kOut || three) {
-                umma_bf16_ts(tkv, ka + 32, mnmajor_step(dvq, 0), id_mn, 1);
-                umma_bf16_ts(tkv, ka + 40, mnmajor_step(dvq, 1), id_mn, 1);
-              }
               umma_commit(&sm.kt_free[q]);
               if (q == 3) {
                 umma_commit(&sm.kv_full[kvb]);
                 umma_commit(&sm.free_[tk.slot]);
-                if (!kOut) umma_commit(&sm.free_[tv.slot]);
+              }
+            }
+            __syncwarp();
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; q += 2) {  // 64 tokens at a time, as the two groups of warps convert them
+            if (!(ok = all_ok(la_wait(&sm.kt_ready[q], par, sm) && la_wait(&sm.kt_ready[q + 1], par, sm)))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t ka = tm + Sh::kColKt + la_kt_col<kOut>(q, true);
+              const uint64_t dvq = dv + (uint64_t)q * (4096u >> 4);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  umma_bf16_ts(tkv, ka + 48 * y + 16 * (x >> 1) + 8 * (x & 1), mnmajor_step(dvq, 2 * y + (x & 1)), id_mn,
+                               x + y > 0 ? 1u : (uint32_t)q);
+                if (three) {
+                  umma_bf16_ts(tkv, ka + 48 * y + 32, mnmajor_step(dvq, 2 * y), id_mn, 1);
+                  umma_bf16_ts(tkv, ka + 48 * y + 40, mnmajor_step(dvq, 2 * y + 1), id_mn, 1);
+                }
+                umma_commit(&sm.kt_free[q + y]);
+              }
+              if (q == 2) {
+                umma_commit(&sm.kv_full[kvb]);
+                umma_commit(&sm.free_[tk.slot]);
+                umma_commit(&sm.free_[tv.slot]);
               }
             }
             __syncwarp();
@@ -1356,7 +1441,6 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   p->hd = reinterpret_cast<LaHeader*>(ws + L->header);
   p->segs = reinterpret_cast<LaSeg*>(ws + L->segs);
   p->seg0 = reinterpret_cast<int32_t*>(ws + L->seg0);
-  p->order = reinterpret_cast<int32_t*>(ws + L->order);
   p->is_src = reinterpret_cast<int32_t*>(ws + L->is_src);
   p->slot_f = reinterpret_cast<float*>(ws + L->slot_f);
   p->slot_r = reinterpret_cast<float*>(ws + L->slot_r);

@@ -19,9 +19,10 @@ struct LaSeg {
   int32_t doc, tok0, ntok;
   int32_t k, nseg;       // place in the document
   int32_t src_fwd;       // state before the segment: -1 zero, >= 0 pool entry, -2 slot of this segment
-  int32_t src_rev;       // state gradient after it: -1 the document's dfinal (or zero), -2 slot
+  int32_t slot;          // its number, documents in order
   int32_t need;          // bit 0: the end state from zero is needed (slots), bit 1: the same in reverse time;
-                         // bit 2: documents fork from this one, bit 3: it is a fork
+                         // bit 2: documents fork from this one, bit 3: it is a fork; bit 4: the state gradient
+                         // after it is its slot (else the document's dfinal, or zero)
 };
 
 struct LaHeader {
@@ -30,14 +31,15 @@ struct LaHeader {
   int32_t scan;          // some document needs the scan over its segments (or a fork)
   int32_t seg_chunks;    // longest segment (0 = documents are not cut)
   int32_t ticket[2];     // items drawn by the states-only walk and by the output walk
-  int32_t pad[58];
+  int32_t n_starts;      // segments of the states-only walk: all, or none where nothing needs the scan
+  int32_t pad[57];
 };
 static_assert(sizeof(LaHeader) == 256, "header is 256 bytes");
 
 // Workspace (byte offsets). Slots hold one state (64 KB) per segment and head: first the segment's
 // end state from zero, then, after the scan, the state the segment starts from.
 struct LaLayout {
-  size_t header, segs, seg0, order, is_src, slot_f, slot_r, fin, acc, dstart, part_q, part_k, total;
+  size_t header, segs, seg0, is_src, slot_f, slot_r, fin, acc, dstart, part_q, part_k, total;
   int64_t smax;
   int min_seg;  // shortest segment (chunks); 0 = documents are not cut
 };
@@ -66,7 +68,6 @@ inline LaLayout la_layout(int N, int T, int Hk, int Hv, bool has_init, bool bwd,
   L.header = take(sizeof(LaHeader));
   L.segs = take(sizeof(LaSeg) * L.smax);
   L.seg0 = take(sizeof(int32_t) * (N + 1));
-  L.order = take(sizeof(int32_t) * L.smax);
   L.is_src = take(sizeof(int32_t) * N);
   const size_t slots = (L.min_seg || has_init) ? state * L.smax : 0;
   L.slot_f = take(slots);
