@@ -14,17 +14,27 @@
 // the role's own time (u = t, or n-1-t reversed) and a = 1 forward, 0 reversed, every role has row
 // factors lam^{u+a} on its state term and weights lam^{n-a-u} on its key rows.
 //
-// Precision. The products' operands are bf16. The state is held in fp32 registers, and its update
-// uses the weighted keys as a sum of two bf16 terms (relative error about 2^-17 an element), because
-// the states are fp32 outputs. The map P is a sum of two bf16 terms near its diagonal (in the 32 x 32
-// blocks on it): a row may hold a single entry of weight there (the first tokens, a strong decay), and
-// its rounding would double that of the output. The rest of P, and the state that the queries read, are
-// rounded to bf16 once: an output averages many of those roundings.
+// Precision. The products' operands are bf16. The state is held in fp32 registers and its update uses the weighted
+// keys as a sum of bf16 terms: three (relative error 2.5e-8 an element) as long as the chunk's part reaches an fp32
+// state among the outputs before it has decayed below 2^-10, else two (2.5e-6: far below the rounding of the bf16
+// copy of the state that the queries read). The map P is a sum of two bf16 terms near its diagonal (in the 32 x 32
+// blocks on it): a row may hold a single entry of weight there (the first tokens, a strong decay), and its rounding
+// would double that of the output. The rest of P, and the state that the queries read, are rounded to bf16 once: an
+// output averages many of those roundings. Gradients of shared keys are summed over the heads in fp32.
 //
 // Row factors leave the products: the output is r_t (S^T q_t + sum_s P''_ts v_s) with r_t =
 // max(lam^{u+a}, 2^-86) and P'' = P / r_t, so the query enters the state product as it was loaded.
 // Below 2^-86 the state term is too large by at most that factor of the state, which is nothing
 // fp32 or the bf16 output resolves.
+//
+// A call is a planner, a walk that leaves the end state of each segment of a cut document (from zero), a scan over
+// them, the walk that forms the outputs, and in the backward the sums over shared heads. Measured on a GB300 (device
+// time of each kernel, us; 128 dimensions, 2 key heads and 8 value heads):
+//                                     planner  states  scan  outputs  sums
+//     forward, 1 x 32768 tokens             6      26     8       41     -    (HBM floor 25 for all of it)
+//     forward, 16384 tokens, 12 documents   6      19    11       39     -    (13)
+//     backward, 65536 tokens, 4 documents   6      55    14      275    87    (79)
+// The walks are bound by the chain of hand-overs between their warps, below; the sums by HBM traffic (6.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -291,14 +301,21 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 //   K (4, without outputs 8): the weighted keys into tensor memory, 32 tokens and 32 dimensions a warp at a time
 //   P/O (8): the map from Q K^T, in place in tensor memory, and the outputs
 //   then a warp for the copies and one that issues the products.
-// Per chunk the products are QK^T, Q S, P V (two terms) and K~^T V (three terms), 128^3 each: 1792
-// cycles of the tensor pipe at its nominal rate, against about 3400 cycles of HBM traffic (80 KB) at
-// four value heads to a key head. The vector work (8 K/S warps and 4 P/O warps on the SM's four
-// schedulers) is of the same order, so everything overlaps: QK of the next chunk is issued as soon as
-// this chunk's P V is, and two chunks' tiles are in flight.
+// Per chunk the products are Q K^T, Q S, K~^T V (two or three terms) and P V (two terms), each of 128^3: eight
+// instructions of 64 cycles a term, 3072 cycles (3584 with three terms), against about 2900 cycles of HBM traffic
+// (80 KB at four value heads to a key head). A chunk takes 4900 cycles in the forward and 6000 where the output is
+// fp32 partial sums: the tensor pipe is busy 56 % of the time. What it waits for is the chain through the warps: Q K^T
+// goes to P/O, whose map takes 1600 cycles, P V follows, and its result holds P/O for another 1000 (bf16) to 3000
+// (fp32) before the next map; in the meantime the state goes through S and back as an operand. With all vector work
+// taken out of it an earlier form of the backward walk still took 226 of its 313 us. Tried and slower: outputs by other warps, 16 P/O warps, two
+// issuing warps (56, 45 and 46 us against 44), partial sums stored from registers (349 us against 275), the heads of a
+// group added up in place by one CTA (341 + 36 us against 275 + 87).
 //
-// Tensor memory: Q K^T and P (in place: 16 key tokens' fp32 columns become 8 columns of the first
-// bf16 term and 8 of the second), O, K~^T V, and the weighted keys (four stages of 32 tokens in
+// The states-only walk has one product (1024 or 1536 cycles a chunk) and takes 2200: its first chunks wait for HBM
+// (every SM fills its ring at once), the later ones for the issuing warp.
+//
+// Tensor memory: K~^T V, Q K^T and P (in place: 16 key tokens' fp32 columns become 8 columns of the first
+// bf16 term and 8 of the second), O, and the weighted keys (four stages of 32 tokens in
 // two terms, or two in three; the states-only walk: two accumulators, four stages in three).
 
 constexpr uint32_t kColKV = 0, kColQK = 128, kColO = 256;
@@ -1242,7 +1259,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
 
 // Start states of the segments from their end states from zero, in place: one thread per head and
 // four elements walks the documents in order (blockIdx.y = 1: the state gradients, from the end). The
-// slots of a document do not depend on one another, so eight are read ahead of the recurrence.
+// slots of a document do not depend on one another, so eight are read ahead of the recurrence. Each slot is read and
+// written once: 19 segments of 8 heads, 20 MB through L2 in 8 us, most of it the recurrence's latency.
 __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ LaParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -1307,7 +1325,8 @@ __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ La
 
 // ---------------------------------------------------------------------------------------- sums
 
-// dq, dk of the shared key heads: the sum over each group's value heads, in their order
+// dq, dk of the shared key heads: the sum over each group's value heads, in their order. Bound by HBM traffic: four
+// partial sums in, one bf16 out, 604 MB at 65536 tokens and 8 value heads in 87 us (6.9 TB/s).
 struct LaGroupParams {
   const float *part_q, *part_k;
   __nv_bfloat16 *dq, *dk;
