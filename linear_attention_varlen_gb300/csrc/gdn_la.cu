@@ -32,7 +32,7 @@
 // time of each kernel, us; 128 dimensions, 2 key heads and 8 value heads):
 //                                     planner  states  scan  outputs  sums
 //     forward, 1 x 32768 tokens             6      26     8       41     -    (HBM floor 25 for all of it)
-//     forward, 16384 tokens, 12 documents   6      19    11       39     -    (13)
+//     forward, 16384 tokens, 12 documents   6      20     8       39     -    (13)
 //     backward, 65536 tokens, 4 documents   6      55    14      275    87    (79)
 // The walks are bound by the chain of hand-overs between their warps, below; the sums by HBM traffic (6.9 TB/s).
 #include <cuda_bf16.h>
@@ -1258,8 +1258,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
 // ---------------------------------------------------------------------------------------- scan
 
 // Start states of the segments from their end states from zero, in place: one thread per head and
-// four elements walks the documents in order (blockIdx.y = 1: the state gradients, from the end). The
-// slots of a document do not depend on one another, so eight are read ahead of the recurrence. Each slot is read and
+// four elements walks the documents in order (blockIdx.y = 1: the state gradients, from the end), every blockIdx.z-th
+// one where no document can fork from another. The slots
+// of a document do not depend on one another, so eight are read ahead of the recurrence. Each slot is read and
 // written once: 19 segments of 8 heads, 20 MB through L2 in 8 us, most of it the recurrence's latency.
 __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ LaParams p) {
   griddep_wait();
@@ -1280,7 +1281,7 @@ __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ La
   if (rev && p.init_idx)
     for (int d = 0; d < p.N; ++d)
       if (p.is_src[d]) *at(p.acc, d) = zero;
-  for (int i = 0; i < p.N; ++i) {
+  for (int i = blockIdx.z; i < p.N; i += gridDim.z) {
     const int d = rev ? p.N - 1 - i : i;
     const int s0 = p.seg0[d], cnt = p.seg0[d + 1] - s0;
     const int idx = p.init_idx ? p.init_idx[d] : -1;
@@ -1505,7 +1506,9 @@ void la_launch_starts(const LaParams& p, const LaLayout& L, const LaRole& fwd, c
   a.role[0] = fwd;
   if (rev) a.role[1] = *rev;
   la_launch_chunks(a, L, false, rev ? 2 : 1, sms, s);
-  launch_early(la_scan_kernel, dim3(16 * p.Hv, rev ? 2 : 1), 256, 0, s, a);
+  // without forks the documents do not depend on one another
+  const unsigned docs = p.init_idx ? 1 : (unsigned)(p.N < 8 ? p.N : 8);
+  launch_early(la_scan_kernel, dim3(16 * p.Hv, rev ? 2 : 1, docs), 256, 0, s, a);
 }
 
 }  // namespace
