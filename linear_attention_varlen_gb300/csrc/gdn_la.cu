@@ -33,7 +33,7 @@
 //                                     planner  states  scan  outputs  sums
 //     forward, 1 x 32768 tokens             6      26     8       41     -    (HBM floor 25 for all of it)
 //     forward, 16384 tokens, 12 documents   6      20     8       39     -    (13)
-//     backward, 65536 tokens, 4 documents   6      55    14      275    87    (79)
+//     backward, 65536 tokens, 4 documents   6      55    14      269    87    (79)
 // The walks are bound by the chain of hand-overs between their warps, below; the sums by HBM traffic (6.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -413,8 +413,9 @@ __device__ __forceinline__ void set_regs() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTo));
 }
 // Four lanes, a row each, four columns to a quad: lane i's quad k and lane k's quad i change places. Rows then leave
-// (or come) in whole sectors, 64 bytes of a row at a time; a row to a lane, 16 bytes at a time, a state's 64 KB took
-// about 6000 cycles to write, longer than two chunks.
+// in whole sectors, 64 bytes of a row at a time; a row to a lane, 16 bytes at a time, a state's 64 KB took about 6000
+// cycles to write, longer than a chunk. (Reading a state that way as well made the registers spill: 20.6 us against
+// 18.3 for 512 tokens, 277 against 269 for the backward's walk; the two halves of a sector meet in L1.)
 __device__ __forceinline__ void swap_quads(float* x) {
   const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
 #pragma unroll
@@ -604,8 +605,6 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     const int quarter = wid & 3, ch = wid >> 2;  // tensor-memory lanes 32 quarter .. +31, columns 64 ch .. +63
     constexpr int kCols = 64;
     const int row = 32 * quarter + lane;
-    // where a lane's first four columns lie in memory once each four lanes have exchanged theirs
-    auto part = [&]() { return (row & ~3) * kDim + kCols * ch + 4 * (threadIdx.x & 3); };
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
     float S[kCols];
     while (ok && next_item(it)) {
@@ -628,18 +627,13 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
 #pragma unroll
         for (int j = 0; j < kCols; ++j) S[j] = sp[(size_t)(kCols * ch + j) * kDim + row];
       } else {
-        sp += part();
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(sp + k * kDim + j);
-            S[j + 4 * k] = x.x;
-            S[j + 4 * k + 1] = x.y;
-            S[j + 4 * k + 2] = x.z;
-            S[j + 4 * k + 3] = x.w;
-          }
-          swap_quads(S + j);
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sp + (size_t)row * kDim + kCols * ch + j);
+          S[j] = x.x;
+          S[j + 1] = x.y;
+          S[j + 2] = x.z;
+          S[j + 3] = x.w;
         }
       }
       float lam_hi = 1.f, lam_lo = 0.f;
@@ -701,7 +695,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       else if (la_writes_end(p, it))
         dst = R.last + ((size_t)it.seg.doc * p.Hv + it.h) * kLaState;
       if (dst) {
-        dst += part();
+        // where a lane's first four columns lie once each four lanes have exchanged theirs
+        dst += (row & ~3) * kDim + kCols * ch + 4 * (lane & 3);
 #pragma unroll
         for (int j = 0; j < kCols; j += 16) {
           swap_quads(S + j);
