@@ -102,6 +102,8 @@ def library_path() -> str:
 def load(path: Optional[str] = None):
     """Open the compiled library (no fallback: raises if it is missing) and declare signatures."""
     global _lib
+    if _lib is not None and path is None:  # set once its signatures are declared
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -449,9 +451,14 @@ QUANT = {"none": 0, None: 0, "row": 1, "group": 2}
 NORM_GROUP = 128  # columns to one scale of quant="group"
 
 
+_codes = {}
+
+
 def _dtype_code(t, name, allowed):
-    torch = _torch()
-    code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}.get(t.dtype)
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32})
+    code = _codes.get(t.dtype)
     if code not in allowed:
         raise ValueError(f"{name}: unsupported type {t.dtype}")
     return code

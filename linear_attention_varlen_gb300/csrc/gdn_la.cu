@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 //   P/O (8): the map from Q K^T, in place in tensor memory, and the outputs
 //   then a warp for the copies and one that issues the products.
 // Per chunk the products are Q K^T, Q S, K~^T V (two or three terms) and P V (two terms), each of 128^3: eight
-// instructions of 64 cycles a term, 3072 cycles (3584 with three terms), against about 2900 cycles of HBM traffic
+// instructions of 64 cycles a term, about 3100 cycles (3600 with three terms), against about 2900 cycles of HBM traffic
 // (80 KB at four value heads to a key head). A chunk takes 4900 cycles in the forward and 6000 where the output is
 // fp32 partial sums: the tensor pipe is busy 56 % of the time. What it waits for is the chain through the warps: Q K^T
 // goes to P/O, whose map takes 1600 cycles, P V follows, and its result holds P/O for another 1000 (bf16) to 3000
