@@ -486,7 +486,6 @@ __device__ __forceinline__ bool la_writes_end(const LaParams& p, const LaItem& i
 struct LaItem {
   LaSeg seg;
   int h, nch;
-  int first;  // first chunk that the walk takes
   int exact;  // chunks from this one on update the state with three terms
   const LaRole* R;
   __device__ __forceinline__ bool three(int c) const { return c >= exact; }
@@ -498,7 +497,6 @@ __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaI
   it.R = &p.role[r];
   it.seg = p.segs[i / (p.Hv * roles)];
   it.nch = (it.seg.ntok + kLaChunk - 1) / kLaChunk;
-  it.first = 0;
   const float g = -fmaxf(p.log_decay[it.h], -1e4f) * kLaChunk;  // decay of a chunk
   if (kOut) {
     // Three terms where the state itself is an output (of an uncut document; the scan gives a cut one's)
@@ -508,9 +506,9 @@ __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaI
     if (la_writes_end(p, it))
       it.exact = it.nch - (g > 0.f ? (int)fminf(ceilf(7.f / g) + 1.f, (float)it.nch) : it.nch);
   } else {
-    // chunks whose part is below e^-30 of those after them leave no trace in fp32
+    // Every chunk is walked, however deep its decay: what the later ones hold is not known beforehand, and where it
+    // is smaller still (padding, values that fall in time), the early ones are the state.
     it.exact = it.nch;
-    if (g > 0.f) it.first = it.nch - (int)fminf(ceilf(30.f / g) + 1.f, (float)it.nch);
     // three terms where the state reaches an output of the scan (the document's last state, or its start's
     // gradient where one is wanted, or a fork's) before it has decayed below 2^-10
     const bool fork = (it.seg.need >> 2 >> it.R->rev) & 1;
@@ -653,7 +651,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         }
       };
       if (it.nch > 0) publish();
-      for (int c = it.first; c < it.nch; ++c, ++cc) {
+      for (int c = 0; c < it.nch; ++c, ++cc) {
         if (!(ok = la_wait(&sm.kv_full[cc % Sh::kKv], (cc / Sh::kKv) & 1, sm))) break;
         tc_fence_after();
         int n;
@@ -742,7 +740,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         sm.w[e >> 6][t] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), w1, bf16x2_of(r));
       }
       if (!(ok = sync_w())) break;
-      for (int c = it.first; ok && c < it.nch; ++c, ++cc) {
+      for (int c = 0; ok && c < it.nch; ++c, ++cc) {
         // The chunk's weighted keys, 32 tokens (a quarter) and 32 dimensions a warp at a time, in two or three
         // bf16 terms.
         int n;
@@ -1070,7 +1068,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         if (!la_item<kOut>(p, roles, drawn, it)) continue;
         const LaRole& R = *it.R;
         const int hq = it.h / R.div_q, hk = it.h / R.div_k, hv = it.h / R.div_v;
-        for (int c = it.first; c < it.nch; ++c, ++cc) {
+        for (int c = 0; c < it.nch; ++c, ++cc) {
           int n;
           const int tok = la_chunk_at(it, c, n);
 #pragma unroll
@@ -1113,9 +1111,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     };
     auto tile_at = [&](uint64_t first, const LaTile<kOut>& t) { return first + (uint64_t)(t.slot * (kTile >> 4)); };
     while (ok && next_item(it)) {
-      const int first = __shfl_sync(0xffffffffu, it.first, 0), nch = __shfl_sync(0xffffffffu, it.nch, 0);
+      const int nch = __shfl_sync(0xffffffffu, it.nch, 0);
       const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
-      for (int c = first; ok && c < nch; ++c, ++cc) {
+      for (int c = 0; ok && c < nch; ++c, ++cc) {
         const uint32_t par = cc & 1, kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
         const LaTile<kOut> tk = next_tile(), tq = kOut ? next_tile() : tk, tv = next_tile();
         const uint64_t dv = tile_at(mnmaj0, tv);
