@@ -285,7 +285,8 @@ int gdn_conv_bwd(const void* x, const float* w, const float* bias, const int32_t
  * with compensated products (relative error about 1e-6). gdn_la_bwd is the backward of
  * sum(dout * out) + sum(dfinal_state * final_state); dinitial_state [n_init, H_v, 128, 128] sums over
  * the documents that start from each entry, and a fork's gradient flows into the document it forked
- * from. Every sum has a fixed order (deterministic). Infinities and NaN stay in their document (and its
+ * from. Every sum has a fixed order (deterministic). Scores q.k (in the backward also dout.v), their weighted
+ * sums and S^T q stay finite up to 2^104 (2e31). Infinities and NaN stay in their document (and its
  * forks); within it they may reach any output, earlier tokens of the same 128-token chunk included.
  * workspace: gdn_la_workspace_size(...) bytes, 256-byte aligned (has_init: init_idx is given); bad
  * cu_seqlens / init_idx are reported in its status word (gdn_workspace_status). Ownership, stream

@@ -22,10 +22,14 @@
 // would double that of the output. The rest of P, and the state that the queries read, are rounded to bf16 once: an
 // output averages many of those roundings. Gradients of shared keys are summed over the heads in fp32.
 //
-// Row factors leave the products: the output is r_t (S^T q_t + sum_s P''_ts v_s) with r_t =
-// max(lam^{u+a}, 2^-86) and P'' = P / r_t, so the query enters the state product as it was loaded.
-// Below 2^-86 the state term is too large by at most that factor of the state, which is nothing
-// fp32 or the bf16 output resolves.
+// Row factors leave the products: the output is r_t (S^T q_t + sum_s P''_ts v_s) with r_t = lam^{u+a} and
+// P'' = P / r_t, so the query enters the state product as it was loaded. What is summed is then larger than the output
+// by 1 / r_t. Heads whose r_t falls below 2^-24 within a chunk (log-decay below -0.13) take another way: P as it is
+// (its weights are at most 1), and the state's term S^T q_t multiplied with its row factor in tensor memory, in fp32,
+// before P V is added. So nothing is larger than 2^24 times the product it stands for, and every row factor is
+// the decay's own down to fp32's end. (With one cut at 2^-86 for all heads, sums above 2^42 became infinite, and
+// a row whose values were all zero kept 2^-86 of a state that had decayed further. With two such heads of eight
+// the extra pass costs 3 %: 16384 tokens in 12 documents 72.5 -> 74.7 us, the backward of 65536 tokens 479 -> 492.)
 //
 // A call is a planner, a walk that leaves the end state of each segment of a cut document (from zero), a scan over
 // them, the walk that forms the outputs, and in the backward the sums over shared heads. Measured on a GB300 (device
@@ -52,7 +56,7 @@ namespace {
 using namespace bw;
 
 constexpr float kLaLog2e = 1.44269504f;
-constexpr float kLaCut = -86.f;  // log2 of the smallest row factor
+constexpr float kLaCut = -24.f;  // log2 of the smallest row factor that leaves the products
 constexpr uint32_t kTile = 32768;  // 128 x 128 bf16, two 64-column blocks
 
 enum { kMapQ = 0, kMapK = 1, kMapV = 2, kMapDo = 3 };
@@ -396,6 +400,13 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
 // 16 lanes x 16 columns: register 2i is row lane / 4, column 4i + lane % 4, register 2i + 1 row lane / 4 + 8
 __device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -487,6 +498,7 @@ struct LaItem {
   LaSeg seg;
   int h, nch;
   int exact;  // chunks from this one on update the state with three terms
+  bool strong;  // some row factor of a full chunk is below the cut
   const LaRole* R;
   __device__ __forceinline__ bool three(int c) const { return c >= exact; }
 };
@@ -502,6 +514,7 @@ __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaI
     // Three terms where the state itself is an output (of an uncut document; the scan gives a cut one's)
     // and this chunk's part of it is not below 2^-10 by then; else two, far below the rounding of the
     // state's bf16 copy that the queries read.
+    it.strong = g * kLaLog2e > -kLaCut;
     it.exact = it.nch;
     if (la_writes_end(p, it))
       it.exact = it.nch - (g > 0.f ? (int)fminf(ceilf(7.f / g) + 1.f, (float)it.nch) : it.nch);
@@ -895,10 +908,10 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     while (ok && next_item(it)) {
       const LaRole& R = *it.R;
       const float g2 = fmaxf(p.log_decay[it.h], -1e4f) * kLaLog2e;
-      const bool strong = g2 * kLaChunk < kLaCut;  // some row factor of a full chunk is below the cut
+      const bool strong = it.strong;
       const float a = R.rev ? 0.f : 1.f;
       int n_prev = -1, ut = 0;
-      float re = 0.f, of = 0.f;
+      float re = 0.f, of = 0.f, rf = 1.f;  // of the row: log2 of its factor outside the products, of its output, of S^T q
       if (!(ok = sync_col())) break;  // every warp is done with the last item's
       if (ct < kLaChunk) sm.col[ct] = R.s_in * exp2f(-g2 * ((float)(R.rev ? kLaChunk - 1 - ct : ct) + a));
       if (!(ok = sync_col())) break;
@@ -908,7 +921,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         const int tok = la_chunk_at(it, c, n);
         if (n != n_prev) {
           ut = R.rev ? n - 1 - row : row;
-          re = row < n ? fmaxf(g2 * ((float)ut + a), kLaCut) : 0.f;
+          const float e = row < n ? g2 * ((float)ut + a) : 0.f;
+          re = strong ? 0.f : e;
+          rf = strong ? exp2f(e) : 1.f;
           of = R.s_out * exp2f(re);
           n_prev = n;
         }
@@ -968,6 +983,19 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
               }
               tmem_st16(tq + 16 * k16, t);
             }
+          }
+        }
+        if (strong) {  // the state's term with its row's factor, before P V is added to it
+          if (!(ok = la_wait(&sm.qs_done, cc & 1, sm))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int jb = 0; jb < 4; ++jb) {
+            const uint32_t to = tl + kColO + 64 * half + 16 * jb;
+            uint32_t z[16];
+            tmem_ld16_wait(to, z);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] = __float_as_uint(rf * __uint_as_float(z[j]));
+            tmem_st16(to, z);
           }
         }
         tmem_st_wait();
@@ -1113,6 +1141,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     while (ok && next_item(it)) {
       const int nch = __shfl_sync(0xffffffffu, it.nch, 0);
       const int exact = __shfl_sync(0xffffffffu, it.exact, 0);
+      const bool strong = kOut && __shfl_sync(0xffffffffu, (int)it.strong, 0);
       for (int c = 0; ok && c < nch; ++c, ++cc) {
         const uint32_t par = cc & 1, kvb = cc % Sh::kKv, kvu = cc / Sh::kKv, tkv = tm + kColKV + 128 * kvb;
         const LaTile<kOut> tk = next_tile(), tq = kOut ? next_tile() : tk, tv = next_tile();
@@ -1211,7 +1240,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         if constexpr (kOut) {
 #pragma unroll 1
           for (int j = 0; j < 2; ++j) {  // P V for 64 key tokens
-            if (!(ok = all_ok(la_wait(&sm.p_ready[j], par, sm)))) break;
+            // a strong decay: both halves of O have their row factors before the first product is added to any
+            if (!(ok = all_ok(la_wait(&sm.p_ready[j], par, sm) && (!strong || la_wait(&sm.p_ready[1], par, sm))))) break;
             tc_fence_after();
             if (elect_one()) {
               const uint64_t dvj = dv + (uint64_t)j * (8192u >> 4);
