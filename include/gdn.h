@@ -273,7 +273,9 @@ int gdn_conv_bwd(const void* x, const float* w, const float* bias, const int32_t
  * packed, started and forked exactly as gdn_chunk_fwd (cu_seqlens, init_idx, initial_state; the final
  * state of an empty document is its start state). All tensor pointers are device pointers:
  *   q, k      : bf16 [T, H_k, 128];  v, out, dout : bf16 [T, H_v, 128]
- *   log_decay : fp32 [H_v], expected <= 0 (0 = plain linear attention; below -10000 reads as -10000).
+ *   log_decay : fp32 [H_v], expected <= 0 (0 = plain linear attention; below -10000 reads as -10000;
+ *               NaN makes every output of its head NaN, and of no other;
+ *               the states that an empty document hands on stay as they are).
  *               It is a constant of the model (retention- and slope-type layers do not learn it): the
  *               backward returns no gradient for it.
  *   strides   : host array or NULL. Elements from one token to the next of q, k, v (and dout in the

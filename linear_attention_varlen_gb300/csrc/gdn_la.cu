@@ -92,6 +92,13 @@ struct LaParams {
 
 __device__ __forceinline__ void la_status(LaHeader* hd, int code) { atomicCAS(&hd->status, 0, code); }
 
+// The head's log-decay, no lower than -10000 (whose exponential is zero as well). A NaN stays one, and with it every
+// output of the head: a maximum would turn it into a decay that forgets everything.
+__device__ __forceinline__ float la_decay(const LaParams& p, int h) {
+  const float g = p.log_decay[h];
+  return g < -1e4f ? -1e4f : g;
+}
+
 // ---------------------------------------------------------------------------------------- plan
 
 constexpr int kLaPlanThreads = 1024;
@@ -509,7 +516,7 @@ __device__ __forceinline__ bool la_item(const LaParams& p, int roles, int i, LaI
   it.R = &p.role[r];
   it.seg = p.segs[i / (p.Hv * roles)];
   it.nch = (it.seg.ntok + kLaChunk - 1) / kLaChunk;
-  const float g = -fmaxf(p.log_decay[it.h], -1e4f) * kLaChunk;  // decay of a chunk
+  const float g = -la_decay(p, it.h) * kLaChunk;  // decay of a chunk
   if (kOut) {
     // Three terms where the state itself is an output (of an uncut document; the scan gives a cut one's)
     // and this chunk's part of it is not below 2^-10 by then; else two, far below the rounding of the
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     float S[kCols];
     while (ok && next_item(it)) {
       const LaRole& R = *it.R;
-      const float g = fmaxf(p.log_decay[it.h], -1e4f);
+      const float g = la_decay(p, it.h);
       const float* sp = nullptr;
       if constexpr (kOut) {
         const int src = it.seg.src_fwd;
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     };
     while (ok && next_item(it)) {
       const LaRole& R = *it.R;
-      const float g = fmaxf(p.log_decay[it.h], -1e4f);
+      const float g = la_decay(p, it.h);
       const float a = R.rev ? 0.f : 1.f;
       // The weights, for full chunks and for the last one: in pairs of tokens, as fp32, and as bf16 of the
       // weight and of its rest.
@@ -907,7 +914,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
     while (ok && next_item(it)) {
       const LaRole& R = *it.R;
-      const float g2 = fmaxf(p.log_decay[it.h], -1e4f) * kLaLog2e;
+      const float g2 = la_decay(p, it.h) * kLaLog2e;
       const bool strong = it.strong;
       const float a = R.rev ? 0.f : 1.f;
       int n_prev = -1, ut = 0;
@@ -1290,7 +1297,7 @@ __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ La
   griddep_launch_dependents();
   if (!p.hd->scan) return;
   const int h = blockIdx.x / 16, e = ((blockIdx.x % 16) * 256 + threadIdx.x) * 4;
-  const float g = fmaxf(p.log_decay[h], -1e4f);
+  const float g = la_decay(p, h);
   const bool rev = blockIdx.y != 0;
   const int seg_tok = p.hd->seg_chunks * kLaChunk;
   const size_t per = (size_t)p.Hv * kLaState;
@@ -1311,7 +1318,8 @@ __global__ void __launch_bounds__(256) la_scan_kernel(const __grid_constant__ La
     const bool fork = idx >= 0 && idx >= p.n_init, src = p.init_idx && p.is_src[d] != 0;
     if (cnt == 1 && !fork && !src) continue;
     const int len = p.cu[d + 1] - p.cu[d];
-    const float l_last = cnt > 1 ? decay_pow(g, (float)(len - (cnt - 1) * seg_tok)) : decay_pow(g, (float)len);
+    // an empty document hands its start state on, whatever the decay
+    const float l_last = len > 0 ? decay_pow(g, (float)(len - (cnt - 1) * seg_tok)) : 1.f;
     float4 S;
     if (rev) {
       S = p.dfinal ? cat(p.dfinal, d) : zero;
