@@ -1394,8 +1394,9 @@ __global__ void __launch_bounds__(256) la_init_sum_kernel(const __grid_constant_
   griddep_wait();
   griddep_launch_dependents();
   if (p.hd->n_segs == 0) return;
-  const int x = blockIdx.y;
-  const size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, per = (size_t)p.Hv * kLaState;
+  // entries along the grid's x, which has room for any pool; a state is 16 blocks
+  const int x = blockIdx.x / (16 * p.Hv);
+  const size_t e = ((size_t)(blockIdx.x % (16 * p.Hv)) * 256 + threadIdx.x) * 4, per = (size_t)p.Hv * kLaState;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int d = 0; d < p.N; ++d) {
     if (p.init_idx == nullptr || p.init_idx[d] != x) continue;
@@ -1586,7 +1587,7 @@ extern "C" int gdn_la_bwd(const void* q, const void* k, const void* v, const flo
                           float* dinitial_state, void* workspace, size_t ws_bytes, gdn_stream_t stream) {
   using namespace gdn;
   if (T > 0 && (!dq || !dk || !dv)) return GDN_ERR_INVALID_ARG;
-  if (n_init > 0 && !dinitial_state) return GDN_ERR_INVALID_ARG;
+  if (n_init > 0 && (!dinitial_state || (int64_t)H_v * n_init > INT32_MAX / 16)) return GDN_ERR_INVALID_ARG;
   const LaCall c{q,       k,        v,             dout,   log_decay, cu_seqlens, N,        T,   H_k, H_v, head_dim,
                  strides, init_idx, initial_state, n_init, scale,     workspace,  ws_bytes, true};
   const void* outs[] = {dq, dk, dv, dinitial_state, dfinal_state};
@@ -1625,7 +1626,7 @@ extern "C" int gdn_la_bwd(const void* q, const void* k, const void* v, const flo
   }
   if (n_init > 0) {
     const LaInitParams ip{dstart, init_idx, p.hd, dinitial_state, N, H_v};
-    launch_early(la_init_sum_kernel, dim3(16 * H_v, n_init), 256, 0, s, ip);
+    launch_early(la_init_sum_kernel, dim3((unsigned)(16 * H_v * (int64_t)n_init)), 256, 0, s, ip);
   }
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
