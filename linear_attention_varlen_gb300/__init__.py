@@ -3,7 +3,8 @@
 A thin binding over the C ABI declared in include/gdn.h: argument marshalling
 only. Every step of the computation runs in the CUDA library
 `_build/libgdn_gb300.so`; if that library is missing, every call raises.
-PyTorch is used for device memory and streams.
+PyTorch is used for device memory and streams: a call runs on `stream` (the current one by default), and outputs and
+workspaces that are not given are allocated for it. Inputs of another stream are the caller's to order and to keep.
 
     import linear_attention_varlen_gb300 as gdn
     out, final_state = gdn.chunk_fwd(q, k, v, g, beta, cu_seqlens)
@@ -247,6 +248,22 @@ def _stream_handle(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _empty_on(stream):
+    """torch.empty for a call on `stream` beside the current one. The memory comes from that stream's share of the
+    allocator: the current stream's might still be in use by earlier work there, and a workspace, released when the
+    call returns, could be given away while the kernels are at work. Nor is it reused before the current stream, which
+    is likely to read the outputs, has gone past their release."""
+    torch = _torch()
+
+    def empty(shape, dtype, device):
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        if t.numel():
+            t.record_stream(torch.cuda.current_stream(t.device))
+        return t
+    return empty
+
+
 def _check(t, name, dtype, shape=None):
     if t is None:
         raise ValueError(f"{name} is required")
@@ -265,6 +282,7 @@ def chunk_fwd(q, k, v, g, beta, cu_seqlens, init_idx=None, initial_state=None, o
     With options.save_for_backward the workspace (allocated here when not given, of the backward's
     size) keeps the records for chunk_bwd(..., options with reuse_forward, workspace=the same)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     T, Hk, D = q.shape
     Hv = v.shape[1]
     N = cu_seqlens.shape[0] - 1
@@ -284,13 +302,13 @@ def chunk_fwd(q, k, v, g, beta, cu_seqlens, init_idx=None, initial_state=None, o
         _check(init_idx, "init_idx", torch.int32, (N,))
     dev = q.device
     if out is None:
-        out = torch.empty((T, Hv, D), dtype=torch.bfloat16, device=dev)
+        out = empty((T, Hv, D), dtype=torch.bfloat16, device=dev)
     if final_state is None:
-        final_state = torch.empty((N, Hv, D, D), dtype=torch.float32, device=dev)
+        final_state = empty((N, Hv, D, D), dtype=torch.float32, device=dev)
     o = _opts(options)
     need = int(load().gdn_fwd_workspace_size(N, T, Hk, Hv, ctypes.byref(o)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty(need, dtype=torch.uint8, device=dev)
     rc = load().gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), N, T, Hk, Hv, D,
                               _ptr(init_idx), _ptr(initial_state), n_init, _ptr(out), _ptr(final_state),
                               _ptr(workspace), workspace.numel(), ctypes.byref(o), _stream_handle(stream))
@@ -305,6 +323,7 @@ def chunk_bwd(q, k, v, g, beta, cu_seqlens, dout, dfinal_state=None, init_idx=No
     With options.reuse_forward, `workspace` must be the one a save_for_backward forward of the same
     inputs used. `grads` may hold preallocated fp32 outputs (keys dq, dk, dv, dg, dbeta, dinit)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if options is not None and options.reuse_forward and workspace is None:
         raise ValueError("reuse_forward needs the workspace of the save_for_backward forward")
     T, Hk, D = q.shape
@@ -326,7 +345,7 @@ def chunk_bwd(q, k, v, g, beta, cu_seqlens, dout, dfinal_state=None, init_idx=No
     def out_buf(key, shape):
         t = grads.get(key)
         if t is None:
-            return torch.empty(shape, dtype=f32, device=dev)
+            return empty(shape, dtype=f32, device=dev)
         return _check(t, key, f32, shape)
     dq = out_buf("dq", q.shape)
     dk = out_buf("dk", k.shape)
@@ -337,7 +356,7 @@ def chunk_bwd(q, k, v, g, beta, cu_seqlens, dout, dfinal_state=None, init_idx=No
     o = _opts(options)
     need = int(load().gdn_bwd_workspace_size(N, T, Hk, Hv, ctypes.byref(o)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty(need, dtype=torch.uint8, device=dev)
     rc = load().gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), N, T, Hk, Hv, D,
                               _ptr(init_idx), _ptr(initial_state), n_init, _ptr(dout), _ptr(dfinal_state),
                               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dinit), _ptr(workspace),
@@ -355,6 +374,7 @@ def decode_step(q, k, v, g, beta, state_pool, state_idx, options: Optional[Optio
     optional int32 device tensor of one element that receives GDN_ERR_INVALID_ARG for out-of-range
     indices (not cleared here)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     B, Hk, D = q.shape
     Hv = v.shape[1]
     half = _half_dtype(q)
@@ -371,7 +391,7 @@ def decode_step(q, k, v, g, beta, state_pool, state_idx, options: Optional[Optio
     if status is not None:
         _check(status, "status", torch.int32, (1,))
     if out is None:
-        out = torch.empty((B, Hv, D), dtype=torch.bfloat16, device=q.device)
+        out = empty((B, Hv, D), dtype=torch.bfloat16, device=q.device)
     o = _opts(options)
     rc = load().gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), B, Hk, Hv, D, _ptr(state_idx),
                                 _ptr(state_pool), state_pool.shape[0], _ptr(out), _ptr(status), ctypes.byref(o),
@@ -391,6 +411,7 @@ def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None,
     None; cu_seqlens [N+1] int32; init_idx [N] int32 or None; conv_init [n_init, 3, C] bf16 or None.
     Returns (y [T, C] bf16, final_tail [N, 3, C] bf16)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     T, C = x.shape
     N = cu_seqlens.shape[0] - 1
     _check(x, "x", torch.bfloat16, (T, C))
@@ -405,11 +426,11 @@ def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None,
         _check(conv_init, "conv_init", torch.bfloat16)
         n_init = conv_init.shape[0]
     if y is None:
-        y = torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
+        y = empty((T, C), dtype=torch.bfloat16, device=x.device)
     if final_tail is None:
-        final_tail = torch.empty((N, 3, C), dtype=torch.bfloat16, device=x.device)
+        final_tail = empty((N, 3, C), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(conv_workspace_size(N, T, C), dtype=torch.uint8, device=x.device)
+        workspace = empty(conv_workspace_size(N, T, C), dtype=torch.uint8, device=x.device)
     rc = load().gdn_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, _ptr(init_idx), _ptr(conv_init),
                              n_init, _ptr(y), _ptr(final_tail), _ptr(workspace), workspace.numel(),
                              _stream_handle(stream))
@@ -423,6 +444,7 @@ def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfi
     """Backward of conv_fwd. Returns dict dx [T, C], dw [C, 4], dbias [C] (None without bias),
     dconv_init [n_init, 3, C] (None without a pool), all fp32."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     T, C = x.shape
     N = cu_seqlens.shape[0] - 1
     _check(dy, "dy", torch.bfloat16, (T, C))
@@ -430,12 +452,12 @@ def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfi
         _check(dfinal_tail, "dfinal_tail", torch.float32, (N, 3, C))
     n_init = 0 if conv_init is None else conv_init.shape[0]
     f32 = dict(dtype=torch.float32, device=x.device)
-    dx = torch.empty((T, C), **f32)
-    dw = torch.empty((C, 4), **f32)
-    dbias = torch.empty((C,), **f32) if bias is not None else None
-    dci = torch.empty((n_init, 3, C), **f32) if n_init > 0 else None
+    dx = empty((T, C), **f32)
+    dw = empty((C, 4), **f32)
+    dbias = empty((C,), **f32) if bias is not None else None
+    dci = empty((n_init, 3, C), **f32) if n_init > 0 else None
     if workspace is None:
-        workspace = torch.empty(conv_workspace_size(N, T, C, True), dtype=torch.uint8, device=x.device)
+        workspace = empty(conv_workspace_size(N, T, C, True), dtype=torch.uint8, device=x.device)
     rc = load().gdn_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, _ptr(init_idx), _ptr(conv_init),
                              n_init, _ptr(dy), _ptr(dfinal_tail), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dci),
                              _ptr(workspace), workspace.numel(), _stream_handle(stream))
@@ -519,18 +541,19 @@ def la_chunk_fwd(q, k, v, log_decay, cu_seqlens, init_idx=None, initial_state=No
     fp32; cu_seqlens, init_idx and initial_state as in chunk_fwd. Returns (out [T, Hv, 128] bf16,
     final_state [N, Hv, 128, 128] fp32)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     T, Hk, Hv, D, N, n_init, strides = _la_inputs(q, k, v, log_decay, cu_seqlens, init_idx, initial_state)
     dev = q.device
     if out is None:
-        out = torch.empty((T, Hv, D), dtype=torch.bfloat16, device=dev)
+        out = empty((T, Hv, D), dtype=torch.bfloat16, device=dev)
     else:
         _check(out, "out", torch.bfloat16, (T, Hv, D))
     if final_state is None:
-        final_state = torch.empty((N, Hv, D, D), dtype=torch.float32, device=dev)
+        final_state = empty((N, Hv, D, D), dtype=torch.float32, device=dev)
     else:
         _check(final_state, "final_state", torch.float32, (N, Hv, D, D))
     if workspace is None:
-        workspace = torch.empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None), dtype=torch.uint8, device=dev)
+        workspace = empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None), dtype=torch.uint8, device=dev)
     rc = load().gdn_la_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), N, T, Hk, Hv, D, strides,
                            _ptr(init_idx), _ptr(initial_state), n_init, float(scale), _ptr(out), _ptr(final_state),
                            _ptr(workspace), workspace.numel(), _stream_handle(stream))
@@ -544,6 +567,7 @@ def la_chunk_bwd(q, k, v, log_decay, cu_seqlens, dout, dfinal_state=None, init_i
     """Backward of la_chunk_fwd. Returns dict of dq, dk, dv (bf16) and dinit (fp32; None without a pool).
     `grads` may hold preallocated outputs under those keys."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if dout is None:
         raise ValueError("dout is required")
     T, Hk, Hv, D, N, n_init, strides = _la_inputs(q, k, v, log_decay, cu_seqlens, init_idx, initial_state, dout)
@@ -554,14 +578,13 @@ def la_chunk_bwd(q, k, v, log_decay, cu_seqlens, dout, dfinal_state=None, init_i
 
     def out_buf(key, shape, dtype):
         t = grads.get(key)
-        return torch.empty(shape, dtype=dtype, device=dev) if t is None else _check(t, key, dtype, shape)
+        return empty(shape, dtype=dtype, device=dev) if t is None else _check(t, key, dtype, shape)
     dq = out_buf("dq", (T, Hk, D), torch.bfloat16)
     dk = out_buf("dk", (T, Hk, D), torch.bfloat16)
     dv = out_buf("dv", (T, Hv, D), torch.bfloat16)
     dinit = out_buf("dinit", (n_init, Hv, D, D), torch.float32) if n_init > 0 else None
     if workspace is None:
-        workspace = torch.empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None, True), dtype=torch.uint8,
-                                device=dev)
+        workspace = empty(la_workspace_size(N, T, Hk, Hv, init_idx is not None, True), dtype=torch.uint8, device=dev)
     rc = load().gdn_la_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), N, T, Hk, Hv, D, strides,
                            _ptr(init_idx), _ptr(initial_state), n_init, float(scale), _ptr(dout), _ptr(dfinal_state),
                            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dinit), _ptr(workspace), workspace.numel(),
@@ -576,6 +599,7 @@ def la_decode_step(q, k, v, log_decay, state_pool, state_idx, scale: float = 1.0
     v [B, Hv, 128] bf16 or fp16 (sequences may be strided); log_decay [Hv] fp32; state_pool, state_idx and
     status as in decode_step. Returns out [B, Hv, 128] of the inputs' type."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     B, Hk, D = q.shape
     Hv = v.shape[1]
     code = _dtype_code(q, "q", (DTYPE_BF16, DTYPE_FP16))
@@ -589,7 +613,7 @@ def la_decode_step(q, k, v, log_decay, state_pool, state_idx, scale: float = 1.0
     if status is not None:
         _check(status, "status", torch.int32, (1,))
     if out is None:
-        out = torch.empty((B, Hv, D), dtype=q.dtype, device=q.device)
+        out = empty((B, Hv, D), dtype=q.dtype, device=q.device)
     else:
         _check(out, "out", q.dtype, (B, Hv, D))
     rc = load().gdn_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, Hk, Hv, D, code, strides,
@@ -610,6 +634,7 @@ def rmsnorm_fwd(x, w, residual=None, eps: float = 1e-6, quant=None, y=None, resi
     [T, ceil(D / 128)]). Returns (y, h, scales); h is None without a residual, scales without quant.
     residual_out may be `residual` itself (in place)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if quant not in QUANT:
         raise ValueError('quant: expected None, "none", "row" or "group"')
     code, q = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32)), QUANT[quant]
@@ -620,20 +645,20 @@ def rmsnorm_fwd(x, w, residual=None, eps: float = 1e-6, quant=None, y=None, resi
     if residual is not None:
         _check(residual, "residual", x.dtype, (T, D))
         if residual_out is None:
-            residual_out = torch.empty_like(x)
+            residual_out = empty((T, D), dtype=x.dtype, device=x.device)
         else:
             _check(residual_out, "residual_out", x.dtype, (T, D))
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     ydt = torch.float8_e4m3fn if q else x.dtype
     if y is None:
-        y = torch.empty((T, D), dtype=ydt, device=x.device)
+        y = empty((T, D), dtype=ydt, device=x.device)
     else:
         _check(y, "y", ydt, (T, D))
     if q:
         shape = (T, 1 if q == 1 else -(-D // NORM_GROUP))
         if scales is None:
-            scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+            scales = empty(shape, dtype=torch.float32, device=x.device)
         else:
             _check(scales, "scales", torch.float32, shape)
     elif scales is not None:
@@ -649,6 +674,7 @@ def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspac
     """Backward of rmsnorm_fwd from the h it left (x without a residual), dy the gradient of y and dh that of h
     from elsewhere. Returns (dx [T, D] of h's type: the gradient of x and of the residual, dw [D] fp32)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     code = _dtype_code(h, "h", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
     T, D = h.shape
     _check(h, "h", h.dtype, (T, D))
@@ -658,15 +684,15 @@ def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspac
     if dh is not None:
         _check(dh, "dh", h.dtype, (T, D))
     if dx is None:
-        dx = torch.empty_like(h)
+        dx = empty((T, D), dtype=h.dtype, device=h.device)
     else:
         _check(dx, "dx", h.dtype, (T, D))
     if dw is None:
-        dw = torch.empty((D,), dtype=torch.float32, device=h.device)
+        dw = empty((D,), dtype=torch.float32, device=h.device)
     else:
         _check(dw, "dw", torch.float32, (D,))
     if workspace is None:
-        workspace = torch.empty(int(load().gdn_rmsnorm_workspace_size(T, D, code)), dtype=torch.uint8, device=h.device)
+        workspace = empty(int(load().gdn_rmsnorm_workspace_size(T, D, code)), dtype=torch.uint8, device=h.device)
     rc = load().gdn_rmsnorm_bwd(_ptr(h), _ptr(w), _ptr(dy), _ptr(dh), T, D, code, wcode, float(eps), _ptr(dx), _ptr(dw),
                                 _ptr(workspace), workspace.numel(), _stream_handle(stream))
     if rc != GDN_OK:
