@@ -346,11 +346,19 @@ int gdn_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64_t 
  *     dx = rs w dy - h rs^3 mean(w dy h) + dh,   dw = sum over rows of dy h rs   (rs = (mean(h^2) + eps)^{-1/2})
  * dx [T, D] of `dtype` is the gradient of x and of the residual alike, and may be dh or dy itself; dw is
  * fp32 [D], summed in a fixed order. workspace: gdn_rmsnorm_workspace_size(T, D, dtype) bytes, 256-byte
- * aligned.
+ * aligned; a bounded wait that runs out is reported in its status word (gdn_workspace_status).
  */
 size_t gdn_rmsnorm_workspace_size(int64_t T, int D, int dtype);
 int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D, int dtype,
                     int w_dtype, float eps, void* dx, float* dw, void* workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * For testing the bounded waits only: gdn_rmsnorm_bwd calls of this thread leave out one bulk copy, that of
+ * row `copy` - 1 (rows that come through bulk copies: aligned ones, up to 16384 columns, 8192 in fp32). The wait
+ * for it runs out after wait_us microseconds (0 = about 2 s) and the call reports GDN_ERR_TIMEOUT through the
+ * status word; outputs are then incomplete. copy = 0 ends it.
+ */
+int gdn_test_withhold(int copy, int wait_us);
 
 /* Copy the workspace's device status word to the host (synchronises `stream`) and return it:
  * GDN_OK or the first device-side error of the last call that used this workspace. */

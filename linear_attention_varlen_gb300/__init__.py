@@ -12,6 +12,7 @@ workspaces that are not given are allocated for it. Inputs of another stream are
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -32,7 +33,7 @@ EXPORTS = ("gdn_default_options", "gdn_fwd_workspace_size", "gdn_bwd_workspace_s
            "gdn_noalloc_scratch_bytes", "gdn_noalloc_status", "gdn_fwd_check_args", "gdn_bwd_check_args",
            "gdn_decode_step", "gdn_conv_workspace_size", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_la_workspace_size",
            "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode_step", "gdn_rmsnorm_fwd", "gdn_rmsnorm_workspace_size",
-           "gdn_rmsnorm_bwd")
+           "gdn_rmsnorm_bwd", "gdn_test_withhold")
 
 
 class GdnError(RuntimeError):
@@ -163,6 +164,8 @@ def load(path: Optional[str] = None):
         lib.gdn_rmsnorm_workspace_size.restype = Z
         lib.gdn_rmsnorm_bwd.argtypes = [P, P, P, P, L, I, I, I, F, P, P, P, Z, P]
         lib.gdn_rmsnorm_bwd.restype = I
+        lib.gdn_test_withhold.argtypes = [I, I]
+        lib.gdn_test_withhold.restype = I
         if path is None:
             _lib = lib
         return lib
@@ -698,6 +701,19 @@ def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspac
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_rmsnorm_bwd")
     return dx, dw
+
+
+@contextlib.contextmanager
+def withheld_copy(copy: int, wait_us: int = 20000):
+    """For testing the bounded waits only: the calls within (of this thread) leave out one of their bulk copies, so
+    that the wait for it runs out after wait_us and the workspace's status word says GDN_ERR_TIMEOUT."""
+    rc = load().gdn_test_withhold(copy, wait_us)
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_test_withhold")
+    try:
+        yield
+    finally:
+        load().gdn_test_withhold(0, 0)
 
 
 def workspace_status(workspace, stream=None) -> int:

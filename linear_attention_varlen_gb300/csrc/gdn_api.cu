@@ -20,6 +20,9 @@ using namespace gdn;
 
 namespace gdn {
 
+thread_local TestWithhold g_withhold{-1, kWaitBudget};
+TestWithhold test_withhold() { return g_withhold; }
+
 int device_of(const void* anchor, const void* const* ptrs, int n, int* device) {
   // 1 = device memory, 2 = managed memory, 0 = refused (host, pinned host, unregistered, error)
   auto kind = [](const void* p, int* dev) -> int {
@@ -170,6 +173,13 @@ size_t gdn_bwd_workspace_size(int N, int T, int H_k, int H_v, const gdn_options*
   o.mode = GDN_MODE_EXACT;  // the backward is always exact
   return bwd_layout(make_dims(N, T, H_k, H_v, 0, o, current_sm_count())).total +
          input_copies(T, H_k, H_v, o.flags, true).total;
+}
+
+int gdn_test_withhold(int copy, int wait_us) {
+  if (copy < 0 || wait_us < 0) return GDN_ERR_INVALID_ARG;
+  gdn::g_withhold.copy = copy - 1;
+  gdn::g_withhold.budget = wait_us > 0 ? (long long)wait_us * 2070LL : kWaitBudget;
+  return GDN_OK;
 }
 
 int gdn_workspace_status(const void* workspace, gdn_stream_t stream) {

@@ -59,6 +59,14 @@ class PerDevice {
   std::atomic<unsigned long long> mask_{0};
 };
 
+// What gdn_test_withhold asked for on this thread: the bulk copy (numbered from 0, -1 = none) that a call leaves out,
+// and the limit of a wait, in clock cycles.
+struct TestWithhold {
+  int copy;
+  long long budget;
+};
+TestWithhold test_withhold();
+
 // A launch that may start while the previous kernel of the stream finishes (programmatic stream
 // serialization): the kernel waits for it on the device (griddepcontrol.wait) before it reads or
 // writes anything that kernel touches, so only the launch and the CTAs' placement overlap its

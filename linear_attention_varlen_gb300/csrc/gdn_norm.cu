@@ -38,7 +38,6 @@ constexpr int kNormMaxD = 32768;
 constexpr int kRowThreads = 512;  // most threads to a row
 constexpr int kGroup = 128;       // columns to one scale
 constexpr int kWarpRows = 8;      // rows of a CTA whose warps own a row each
-constexpr long long kNormWait = 4000000000LL;  // clock cycles (about two seconds)
 
 // ------------------------------------------------------------------------------ elements
 
@@ -384,7 +383,9 @@ struct NormBwdParams {
   const void *h, *w, *dy, *dh;
   void* dx;
   float *part, *dw;
-  int64_t T;
+  int32_t *status, *flags;  // of the call, and of each CTA with rings (null where there are none)
+  int64_t T, withheld;      // withheld: the row that a test leaves out (-1 = none)
+  long long budget;         // limit of a wait, clock cycles
   int D, w_dtype, parts;
   float eps;
 };
@@ -393,7 +394,8 @@ struct NormBwdParams {
 // its columns in registers. Aligned rows (kRing) come through a ring of row buffers in shared memory that bulk
 // copies fill ahead of the team: the next rows are always in flight, at no cost in registers. Other rows are read
 // from memory as they come, with the same thread for the same columns, so that the results are the same bits. A
-// team reads a row twice: for the two sums, and for the outputs.
+// team reads a row twice: for the two sums, and for the outputs. The wait for a row is bounded: a team whose row does
+// not come writes nothing more, lets its copies in flight land (again bounded) and leaves; the CTA's flag tells.
 constexpr int kBwdWarps = 16;
 constexpr uint32_t kBwdRing = 196608;  // bytes of the rings of a CTA
 
@@ -404,6 +406,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t s_full[kTeams][8];
   __shared__ float2 s_red[kTeams][2][kTeam];
+  __shared__ int s_abort[kTeams];
   const int team = threadIdx.x / (32 * kTeam), t = threadIdx.x % (32 * kTeam), lane = t & 31, wt = t >> 5;
   const int tensors = p.dh ? 3 : 2;
   const uint32_t row_bytes = (uint32_t)p.D * sizeof(T), stage_bytes = row_bytes * tensors;
@@ -413,6 +416,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   const int64_t first = (int64_t)blockIdx.x * kTeams + team, step = (int64_t)gridDim.x * kTeams, n = p.T * p.D;
   if (kRing && t == 0) {
     for (int i = 0; i < stages; ++i) bw::mbar_init(&s_full[team][i], 1);
+    s_abort[team] = 0;
     bw::fence_mbar_init();
   }
   auto team_sync = [&]() {
@@ -422,6 +426,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kTeam) : "memory");
   };
   auto fetch = [&](int64_t row, int st) {
+    if (row == p.withheld) return;
     bw::mbar_arrive_expect_tx(&s_full[team][st], stage_bytes);
     for (int k = 0; k < tensors; ++k)
       bw::bulk_load(mine + st * stage_bytes + k * row_bytes, src[k] + row * p.D, row_bytes, &s_full[team][st]);
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   for (int64_t row = first; row < p.T; row += step, turn ^= 1) {
     const T *h = src[0] + row * p.D, *g = src[1] + row * p.D, *e = src[2] + row * p.D;
     if constexpr (kRing) {
-      bw::mbar_wait(&s_full[team][st], phase, kNormWait);
+      if (!bw::mbar_wait(&s_full[team][st], phase, p.budget)) *static_cast<volatile int*>(&s_abort[team]) = 1;
       const uint8_t* b = mine + st * stage_bytes;
       h = reinterpret_cast<const T*>(b);
       g = reinterpret_cast<const T*>(b + row_bytes);
@@ -510,6 +515,19 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
         sum.x += x.x;
         sum.y += x.y;
       }
+    } else if constexpr (kRing) {
+      __syncwarp();
+    }
+    // Whether some thread's wait ran out: the team has met since, and none is at the next row's before all have read it.
+    if constexpr (kRing) {
+      if (*static_cast<volatile int*>(&s_abort[team])) {
+        if (t == 0)
+          for (int i = 0; i < stages && row + i * step < p.T; ++i) {
+            const bool wrap = st + i >= stages;
+            bw::mbar_wait(&s_full[team][wrap ? st + i - stages : st + i], phase ^ (wrap ? 1 : 0), p.budget);
+          }
+        break;
+      }
     }
     const float rs = rsqrtf(sum.x / (float)p.D + p.eps);
     const float cc = -rs * rs * rs * (sum.y / (float)p.D);
@@ -550,6 +568,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
   }
   // the CTA's part: its teams', summed in their order through the rings (every copy has landed and been read)
   __syncthreads();
+  if (kRing && threadIdx.x == 0) {
+    int bad = 0;
+#pragma unroll
+    for (int k = 0; k < kTeams; ++k) bad |= s_abort[k];
+    p.flags[blockIdx.x] = bad;
+  }
   float* s_dw = reinterpret_cast<float*>(ring);
   const int pad = (p.D + 7) & ~7;
 #pragma unroll
@@ -635,7 +659,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __g
     }
 }
 
-// dw: 32 columns to a CTA, 32 warps sum every 32nd part, then the warps' sums in order
+// dw: 32 columns to a CTA, 32 warps sum every 32nd part, then the warps' sums in order. The first CTA also makes the
+// call's status of the flags.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float s[32][33];
   bw::griddep_wait();
@@ -646,7 +671,11 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const __grid_constant__ N
 #pragma unroll 4
     for (int i = wid; i < p.parts; i += 32) a += p.part[(size_t)i * p.D + c];
   s[wid][lane] = a;
-  __syncthreads();
+  int bad = 0;
+  if (blockIdx.x == 0 && p.flags)
+    for (int i = threadIdx.x; i < p.parts; i += 1024) bad |= p.flags[i];
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = bad ? kErrTimeout : kOk;
   if (wid == 0 && c < p.D) {
 #pragma unroll
     for (int i = 1; i < 32; ++i) a += s[i][lane];
@@ -683,6 +712,11 @@ int norm_parts(int64_t T, int D, size_t esize, int sms) {
   const int64_t rows = (T + per - 1) / per;
   return (int)(rows < sms ? (rows < 1 ? 1 : rows) : sms);
 }
+
+// Workspace: the status word, the CTAs' flags, their parts of the weight's gradient.
+constexpr size_t kNormHeader = 256;
+size_t norm_parts_at(int parts) { return kNormHeader + align_up(parts * sizeof(int32_t), 256); }
+size_t norm_ws_bytes(int parts, int D) { return norm_parts_at(parts) + (size_t)parts * D * sizeof(float); }
 
 bool al(const void* p, uintptr_t b) { return (reinterpret_cast<uintptr_t>(p) % b) == 0; }
 size_t esize(int dtype) { return dtype == GDN_DTYPE_FP32 ? 4 : 2; }
@@ -821,7 +855,7 @@ extern "C" size_t gdn_rmsnorm_workspace_size(int64_t T, int D, int dtype) {
     cudaGetLastError();
     sms = 152;
   }
-  return (size_t)gdn::norm_parts(T, D, gdn::esize(dtype), sms) * D * sizeof(float);
+  return gdn::norm_ws_bytes(gdn::norm_parts(T, D, gdn::esize(dtype), sms), D);
 }
 
 extern "C" int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D,
@@ -841,15 +875,33 @@ extern "C" int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, con
   const int rc = check_device(workspace, ptrs, 6, guard, &sms);
   if (rc != GDN_OK) return rc;
   const int parts = norm_parts(T, D, e, sms);
-  if (ws_bytes < (size_t)parts * D * sizeof(float)) return GDN_ERR_WORKSPACE;
-  const NormBwdParams p{h, w, dy, dh, dx, static_cast<float*>(workspace), dw, T, D, w_dtype, parts, eps};
+  if (ws_bytes < norm_ws_bytes(parts, D)) return GDN_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool vec = D % 8 == 0 && al(h, 16) && al(dy, 16) && al(dh, 16) && al(dx, 16) && al(w, 16);
+  const bool ring = vec && norm_team(D, e) != 0;
+  const TestWithhold test = test_withhold();
+  const NormBwdParams p{h,
+                        w,
+                        dy,
+                        dh,
+                        dx,
+                        reinterpret_cast<float*>(ws + norm_parts_at(parts)),
+                        dw,
+                        reinterpret_cast<int32_t*>(ws),
+                        ring ? reinterpret_cast<int32_t*>(ws + kNormHeader) : nullptr,
+                        T,
+                        test.copy,
+                        test.budget,
+                        D,
+                        w_dtype,
+                        parts,
+                        eps};
   cudaStream_t st = (cudaStream_t)stream;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
-  const bool ok = dtype == GDN_DTYPE_BF16   ? launch_bwd<__nv_bfloat16>(p, vec, dev, st)
-                  : dtype == GDN_DTYPE_FP16 ? launch_bwd<__half>(p, vec, dev, st)
-                                            : launch_bwd<float>(p, vec, dev, st);
+  const bool ok = dtype == GDN_DTYPE_BF16   ? launch_bwd<__nv_bfloat16>(p, ring, dev, st)
+                  : dtype == GDN_DTYPE_FP16 ? launch_bwd<__half>(p, ring, dev, st)
+                                            : launch_bwd<float>(p, ring, dev, st);
   if (!ok) return GDN_ERR_CUDA;
   launch_early(norm_dw_kernel, dim3((D + 31) / 32), 1024, 0, st, p);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
