@@ -353,10 +353,11 @@ int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh
                     int w_dtype, float eps, void* dx, float* dw, void* workspace, size_t ws_bytes, gdn_stream_t stream);
 
 /*
- * For testing the bounded waits only: gdn_rmsnorm_bwd calls of this thread leave out one bulk copy, that of
- * row `copy` - 1 (rows that come through bulk copies: aligned ones, up to 16384 columns, 8192 in fp32). The wait
- * for it runs out after wait_us microseconds (0 = about 2 s) and the call reports GDN_ERR_TIMEOUT through the
- * status word; outputs are then incomplete. copy = 0 ends it.
+ * For testing the bounded waits only: calls of this thread leave out one bulk copy, number `copy` (from 1). In
+ * gdn_rmsnorm_bwd that is row `copy` - 1 (rows that come through bulk copies: aligned ones, up to 16384
+ * columns, 8192 in fp32), in gdn_la_fwd and gdn_la_bwd the copy-th tile that the first CTA of each walk loads.
+ * The wait for it runs out after wait_us microseconds (0 = about 2 s) and the call reports GDN_ERR_TIMEOUT
+ * through the status word; outputs are then incomplete. copy = 0 ends it.
  */
 int gdn_test_withhold(int copy, int wait_us);
 

@@ -88,6 +88,8 @@ struct LaParams {
   const int32_t* cu;
   const int32_t* init_idx;
   int N, T, Hv, n_init, min_seg, num_sms, bwd;
+  int withheld;      // tile of each walk's first CTA that a test leaves out (-1 = none)
+  long long budget;  // limit of a wait, clock cycles
 };
 
 __device__ __forceinline__ void la_status(LaHeader* hd, int code) { atomicCAS(&hd->status, 0, code); }
@@ -360,6 +362,7 @@ struct LaSmem {
   uint64_t qk_full, p_ready[2], s_ready, qs_done, o_full, o_free;
   uint32_t tmem;
   int abort;
+  long long budget;
   int item[2];  // what the copy warp has drawn
 };
 static_assert(sizeof(LaSmem) <= 232448, "227 KB of shared memory");
@@ -377,13 +380,13 @@ __device__ __forceinline__ float decay_pow(float g, float x) {
   return isfinite(lo) ? fmaf(e, lo, e) : e;
 }
 
-// Bounded wait of one role; false once any role of the CTA has given up.
+// Bounded wait of one thread; false once any role of the CTA has given up.
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, LaSmem& sm) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-    if (clock64() - t0 > kWaitBudget) {
+    if (clock64() - t0 > sm.budget) {
       *reinterpret_cast<volatile int*>(&sm.abort) = 1;
       return false;
     }
@@ -392,6 +395,20 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, LaSmem& 
 }
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// The same of a whole warp: every lane has the same outcome, so that none leaves while others go on to an instruction
+// of the warp (ldmatrix, the tensor-memory accesses) that expects them all.
+__device__ __forceinline__ bool la_wait_warp(uint64_t* bar, uint32_t parity, LaSmem& sm) {
+  if (all_ok(mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!all_ok(mbar_try_wait(bar, parity))) {
+    if (!all_ok(!*reinterpret_cast<volatile int*>(&sm.abort) && clock64() - t0 <= sm.budget)) {
+      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+      return false;
+    }
+  }
+  return true;
+}
 
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -495,7 +512,7 @@ struct LaTile {
     return {t % LaShape<kOut>::kSlots, t / LaShape<kOut>::kSlots};
   }
   __device__ __forceinline__ uint8_t* at(LaSmem& sm) const { return sm.tiles + slot * kTile; }
-  __device__ __forceinline__ bool wait_full(LaSmem& sm) const { return la_wait(&sm.full[slot], use & 1, sm); }
+  __device__ __forceinline__ bool wait_full(LaSmem& sm) const { return la_wait_warp(&sm.full[slot], use & 1, sm); }
 };
 
 struct LaItem;
@@ -589,6 +606,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, kPoWarps);
     sm.abort = 0;
+    sm.budget = p.budget;
     fence_mbar_init();
   }
   tc_fence_before();
@@ -604,7 +622,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   auto next_item = [&](LaItem& it) {
     for (;;) {
       const uint32_t slot = items & 1, use = items >> 1;
-      if (!la_wait(&sm.item_full[slot], use & 1, sm)) return false;
+      if (!la_wait_warp(&sm.item_full[slot], use & 1, sm)) return false;
       const int i = *reinterpret_cast<volatile int*>(&sm.item[slot]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_free[slot]);
@@ -613,7 +631,8 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       if (la_item<kOut>(p, roles, i, it)) return true;
     }
   };
-  uint32_t cc = 0;  // chunks this CTA has begun, over all its items
+  uint32_t cc = 0;      // chunks this CTA has begun, over all its items
+  uint32_t loaded = 0;  // tiles that the copy warp has asked for
   bool ok = true;
   LaItem it;
 
@@ -672,7 +691,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
       };
       if (it.nch > 0) publish();
       for (int c = 0; c < it.nch; ++c, ++cc) {
-        if (!(ok = la_wait(&sm.kv_full[cc % Sh::kKv], (cc / Sh::kKv) & 1, sm))) break;
+        if (!(ok = la_wait_warp(&sm.kv_full[cc % Sh::kKv], (cc / Sh::kKv) & 1, sm))) break;
         tc_fence_after();
         int n;
         la_chunk_at(it, c, n);
@@ -703,7 +722,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         }
         // the copy of the state that the queries of this chunk read may go
         if constexpr (kOut)
-          if (!(ok = la_wait(&sm.qs_done, cc & 1, sm))) break;
+          if (!(ok = la_wait_warp(&sm.qs_done, cc & 1, sm))) break;
         if (c + 1 < it.nch) publish();
       }
       if (!ok) break;
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     auto sync_w = [&]() {  // these warps meet, with the limit of every other wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.w_sync);
-      const bool met = la_wait(&sm.w_sync, w_phase, sm);
+      const bool met = la_wait_warp(&sm.w_sync, w_phase, sm);
       w_phase ^= 1;
       return met;
     };
@@ -805,9 +824,9 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         auto stage_free = [&](int q) {
           bool got = true;
           if (kOut && three && q > 0) {
-            if (q >= 2) got = la_wait(&sm.kt_free[q - 2], cc & 1, sm);
+            if (q >= 2) got = la_wait_warp(&sm.kt_free[q - 2], cc & 1, sm);
           } else if (cc > 0) {
-            got = la_wait(&sm.kt_free[kOut && q == 0 && (three || was_three) ? 3 : q], (cc - 1) & 1, sm);
+            got = la_wait_warp(&sm.kt_free[kOut && q == 0 && (three || was_three) ? 3 : q], (cc - 1) & 1, sm);
           }
           tc_fence_after();
           return got;
@@ -907,7 +926,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
     auto sync_col = [&]() {  // the eight warps meet, with the limit of every other wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.col_sync);
-      const bool met = la_wait(&sm.col_sync, col_phase, sm);
+      const bool met = la_wait_warp(&sm.col_sync, col_phase, sm);
       col_phase ^= 1;
       return met;
     };
@@ -934,7 +953,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           of = R.s_out * exp2f(re);
           n_prev = n;
         }
-        if (!(ok = la_wait(&sm.qk_full, cc & 1, sm))) break;
+        if (!(ok = la_wait_warp(&sm.qk_full, cc & 1, sm))) break;
         tc_fence_after();
         // P'': row = query token; 16 key tokens' fp32 columns become 8 columns of each bf16 term
         float x[32];
@@ -993,7 +1012,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           }
         }
         if (strong) {  // the state's term with its row's factor, before P V is added to it
-          if (!(ok = la_wait(&sm.qs_done, cc & 1, sm))) break;
+          if (!(ok = la_wait_warp(&sm.qs_done, cc & 1, sm))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int jb = 0; jb < 4; ++jb) {
@@ -1015,7 +1034,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         uint8_t* stage = sm.o + (wid - Sh::kPo0) * (kTile / 8);
         const size_t at = ((size_t)(tok + row) * p.Hv + it.h) * kDim + 64 * half;
         if (lane == 0) bulk_wait_read_all();
-        if (!(ok = la_wait(&sm.o_full, cc & 1, sm))) break;
+        if (!(ok = la_wait_warp(&sm.o_full, cc & 1, sm))) break;
         tc_fence_after();
         __syncwarp();
         const uint64_t of2 = f2_pack(of, of);
@@ -1088,7 +1107,6 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   if (wid == Sh::kTmaWarp) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
-      uint32_t loaded = 0;
       // Items are drawn one ahead of the walk: the first by the block's number, then from a counter, so that a
       // CTA with short ones takes more.
       int i = blockIdx.x;
@@ -1110,18 +1128,16 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
           for (uint32_t x = 0; x < Sh::kPerChunk; ++x) {
             const LaTile<kOut> t = LaTile<kOut>::of(cc, x);
             if (t.use > 0 && !(ok = la_wait(&sm.free_[t.slot], (t.use - 1) & 1, sm))) break;
-            mbar_arrive_expect_tx(&sm.full[t.slot], kTile);
             const bool key = x == 0, val = x == Sh::kTileV;
-            load_tile(t.at(sm), &p.map[key ? R.mk : val ? R.mv : R.mq], key ? hk : val ? hv : hq, tok, &sm.full[t.slot]);
+            if (blockIdx.x != 0 || (int)loaded != p.withheld) {
+              mbar_arrive_expect_tx(&sm.full[t.slot], kTile);
+              load_tile(t.at(sm), &p.map[key ? R.mk : val ? R.mv : R.mq], key ? hk : val ? hv : hq, tok, &sm.full[t.slot]);
+            }
             ++loaded;
           }
           if (!ok) break;
         }
       }
-      // copies still in flight land before the shared memory goes
-      if (!ok)
-        for (uint32_t x = loaded < Sh::kSlots ? 0 : loaded - Sh::kSlots; x < loaded; ++x)
-          mbar_wait(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1, kWaitBudget);
     }
   } else if (wid == Sh::kMmaWarp) {
     // ------------------------------------------------------------------ products
@@ -1155,7 +1171,7 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
         const uint64_t dv = tile_at(mnmaj0, tv);
         if constexpr (kOut) {
           const uint64_t dk = tile_at(kmaj0, tk), dq = tile_at(kmaj0, tq);
-          if (!(ok = all_ok(tk.wait_full(sm) && tq.wait_full(sm)))) break;
+          if (!(ok = tk.wait_full(sm) && tq.wait_full(sm))) break;
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -1270,6 +1286,10 @@ __global__ void __launch_bounds__(LaShape<kOut>::kThreads, 1) la_chunk_kernel(co
   __syncthreads();
   tc_fence_after();
   if (sm.abort) {
+    // Copies still in flight land before the shared memory goes, whichever role has given up.
+    if (wid == Sh::kTmaWarp && lane == 0)
+      for (uint32_t x = loaded < Sh::kSlots ? 0 : loaded - Sh::kSlots; x < loaded; ++x)
+        mbar_wait(&sm.full[x % Sh::kSlots], (x / Sh::kSlots) & 1, sm.budget);
     // Products still in flight: everything issued reads shared memory that no copy writes any more; a last
     // commit, waited for with a limit, orders them before the tensor memory goes.
     if (wid == Sh::kMmaWarp) {
@@ -1507,6 +1527,9 @@ int la_prepare(const LaCall& c, const void* const* outs, int n_outs, LaParams* p
   p->min_seg = L->min_seg;
   p->num_sms = *num_sms;
   p->bwd = c.bwd;
+  const TestWithhold test = test_withhold();
+  p->withheld = test.copy;
+  p->budget = test.budget;
   return GDN_OK;
 }
 
