@@ -283,15 +283,19 @@ int gdn_conv_bwd(const void* x, const float* w, const float* bias, const int32_t
  *               heads * 128; the heads of a token are contiguous. out and the gradients are contiguous.
  *   initial_state : fp32 [n_init, H_v, 128, 128];  final_state, dfinal_state : fp32 [N, H_v, 128, 128]
  * out, dq, dk [T, H_k, 128] (summed over each key head's value heads) and dv are bf16: the inputs'
- * type, as a training step hands them on. The states and their gradients are fp32 and are formed
- * with compensated products (relative error about 1e-6). gdn_la_bwd is the backward of
+ * type, as a training step hands them on; the operands of their products (the state that a chunk's
+ * queries read, most of its map of scores) are rounded to bf16 too, so that they carry 1.9e-3 to 2.3e-3 of
+ * error (root mean square, relative) where one rounding of the result would be 1.7e-3. The states and their
+ * gradients are fp32 and are formed with compensated products (relative error 4e-6 at most). gdn_la_bwd is the backward of
  * sum(dout * out) + sum(dfinal_state * final_state); dinitial_state [n_init, H_v, 128, 128] sums over
  * the documents that start from each entry, and a fork's gradient flows into the document it forked
  * from. Every sum has a fixed order (deterministic). Scores q.k (in the backward also dout.v), their weighted
  * sums and S^T q stay finite up to 2^104 (2e31). Infinities and NaN stay in their document (and its
  * forks); within it they may reach any output, earlier tokens of the same 128-token chunk included.
- * workspace: gdn_la_workspace_size(...) bytes, 256-byte aligned (has_init: init_idx is given); bad
- * cu_seqlens / init_idx are reported in its status word (gdn_workspace_status). Ownership, stream
+ * workspace: gdn_la_workspace_size(...) bytes, 256-byte aligned (has_init: init_idx is given; the
+ * backward of shared key heads keeps 1 KB of partial sums for each token and value head there); bad
+ * cu_seqlens / init_idx and an expired bounded wait are reported in its status word
+ * (gdn_workspace_status). Ownership, stream
  * and device rules as for gdn_chunk_fwd; nothing is allocated.
  */
 size_t gdn_la_workspace_size(int N, int T, int H_k, int H_v, int has_init, int backward);
@@ -334,7 +338,8 @@ int gdn_la_decode_step(const void* q, const void* k, const void* v, const float*
  *   be x itself
  *   w : [D] of `w_dtype`;  y : [T, D] of `dtype`, or e4m3 bytes with `quant`
  *   scales : fp32 [T] (GDN_QUANT_ROW) or [T, ceil(D / 128)] (GDN_QUANT_GROUP), else NULL: y stands for
- *   bytes * scale, scale = amax / 448 (1 where the row or group is all zero)
+ *   bytes * scale, scale = amax / 448 (1 where the row or group is all zero); y is scaled with the reciprocal
+ *   of that, within three units of fp32, before it is rounded to e4m3
  * The sums are fp32; h is rounded once, y is formed from the unrounded sum. T = 0 is a no-op.
  */
 int gdn_rmsnorm_fwd(const void* x, const void* residual, const void* w, int64_t T, int D, int dtype, int w_dtype,

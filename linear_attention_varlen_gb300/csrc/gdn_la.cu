@@ -35,9 +35,9 @@
 // them, the walk that forms the outputs, and in the backward the sums over shared heads. Measured on a GB300 (device
 // time of each kernel, us; 128 dimensions, 2 key heads and 8 value heads):
 //                                     planner  states  scan  outputs  sums
-//     forward, 1 x 32768 tokens             6      26     8       41     -    (HBM floor 25 for all of it)
-//     forward, 16384 tokens, 12 documents   6      20     8       39     -    (13)
-//     backward, 65536 tokens, 4 documents   6      55    14      269    87    (79)
+//     forward, 1 x 32768 tokens             6      26     8       44     -    (HBM floor 25 for all of it)
+//     forward, 16384 tokens, 12 documents   6      21     8       42     -    (13)
+//     backward, 65536 tokens, 4 documents   6      74    14      296    87    (79)
 // The walks are bound by the chain of hand-overs between their warps, below; the sums by HBM traffic (6.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -316,13 +316,14 @@ __global__ void __launch_bounds__(kLaPlanThreads) la_plan_kernel(const __grid_co
 //   then a warp for the copies and one that issues the products.
 // Per chunk the products are Q K^T, Q S, K~^T V (two or three terms) and P V (two terms), each of 128^3: eight
 // instructions of 64 cycles a term, about 3100 cycles (3600 with three terms), against about 2900 cycles of HBM traffic
-// (80 KB at four value heads to a key head). A chunk takes 4900 cycles in the forward and 6000 where the output is
-// fp32 partial sums: the tensor pipe is busy 56 % of the time. What it waits for is the chain through the warps: Q K^T
+// (80 KB at four value heads to a key head). A chunk takes about 5200 cycles in the forward and 6600 where the
+// output is fp32 partial sums: the tensor pipe is busy 54 % of the time. What it waits for is the chain through the warps: Q K^T
 // goes to P/O, whose map takes 1600 cycles, P V follows, and its result holds P/O for another 1000 (bf16) to 3000
 // (fp32) before the next map; in the meantime the state goes through S and back as an operand. With all vector work
-// taken out of it an earlier form of the backward walk still took 226 of its 313 us. Tried and slower: outputs by other warps, 16 P/O warps, two
-// issuing warps (56, 45 and 46 us against 44), partial sums stored from registers (349 us against 275), the heads of a
-// group added up in place by one CTA (341 + 36 us against 275 + 87).
+// taken out of it an earlier form of the backward walk still took 226 of its 313 us. Tried on earlier forms, and slower:
+// outputs by other warps, 16 P/O warps, two issuing warps (56, 45 and 46 us against 44), partial sums stored from registers
+// (349 us against 275), the heads of a group added up in place by one CTA (341 + 36 us against 275 + 87).
+// The votes that make a wait's outcome the whole warp's cost 2 % (backward of 65536 tokens 492 -> 503 us).
 //
 // The states-only walk has one product (1024 or 1536 cycles a chunk) and takes 2200: its first chunks wait for HBM
 // (every SM fills its ring at once), the later ones for the issuing warp.
@@ -450,7 +451,7 @@ __device__ __forceinline__ void set_regs() {
 // Four lanes, a row each, four columns to a quad: lane i's quad k and lane k's quad i change places. Rows then leave
 // in whole sectors, 64 bytes of a row at a time; a row to a lane, 16 bytes at a time, a state's 64 KB took about 6000
 // cycles to write, longer than a chunk. (Reading a state that way as well made the registers spill: 20.6 us against
-// 18.3 for 512 tokens, 277 against 269 for the backward's walk; the two halves of a sector meet in L1.)
+// 18.3 for 512 tokens, 277 against 269 for the backward's walk as they then were; the two halves of a sector meet in L1.)
 __device__ __forceinline__ void swap_quads(float* x) {
   const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
 #pragma unroll

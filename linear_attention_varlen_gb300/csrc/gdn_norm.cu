@@ -13,7 +13,7 @@
 // consecutive elements a vector. Measured (device time):
 //     forward, bf16, 16384 x 8192, residual, e4m3 by groups     177 us   944 MB    5.3 TB/s
 //     forward, bf16, 65536 x 1024, residual (x itself)           66 us   403 MB    6.1 TB/s
-//     backward, bf16, 65536 x 1024, with dh                      87 us   537 MB    6.2 TB/s
+//     backward, bf16, 65536 x 1024, with dh                      88 us   537 MB    6.1 TB/s
 //     backward, fp32, 777 x 1001 (rows off alignment)            15 us, of it 4 the sum over the parts
 // The 8-bit forward issues an instruction in 56 % of the cycles and waits for its loads in most others (three CTAs of
 // 512 threads to an SM is what the registers allow); small calls are bound by their launches.
@@ -595,7 +595,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
 }
 
 // Rows too long for a team's registers and ring (above 16384 elements, 8192 in fp32): one a CTA at a time, rows
-// blockIdx.x, + gridDim.x, ..., read twice (with the row kept in registers 8 vectors a thread spilled).
+// blockIdx.x, + gridDim.x, ..., read twice (with the row kept in registers 8 vectors a thread spilled more; as it is, the
+// instances of eight vectors spill 16 bytes in 16 bits and 96 in fp32). 0.9 to 1.8 TB/s.
 template <typename T, int kNv>
 __global__ void __launch_bounds__(kRowThreads, 1) norm_bwd_long_kernel(const __grid_constant__ NormBwdParams p) {
   __shared__ float2 s_red[2][16];
