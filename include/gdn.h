@@ -357,6 +357,110 @@ size_t gdn_rmsnorm_workspace_size(int64_t T, int D, int dtype);
 int gdn_rmsnorm_bwd(const void* h, const void* w, const void* dy, const void* dh, int64_t T, int D, int dtype,
                     int w_dtype, float eps, void* dx, float* dw, void* workspace, size_t ws_bytes, gdn_stream_t stream);
 
+/* Activations of gdn_conv_act_fwd / _bwd and gdn_conv_decode_step. */
+enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* u / (1 + e^-u) */ };
+
+/*
+ * The short convolution of gdn_conv_fwd with its activation, in three types and with rows apart:
+ *     u[p] = bias[c] + sum_m w[c][m] E[p + m],  y[p] = act(u[p]),  E and final_tail as there.
+ *   x, dy, y, conv_init, final_tail : of `dtype`; C a multiple of 8, up to 2^24
+ *   x_stride, dy_stride : elements from one token to the next (0 = contiguous), rows on 16-byte boundaries;
+ *   y and dx are contiguous
+ *   w : fp32 [C, 4] on a 16-byte boundary; everything else as for gdn_conv_fwd / gdn_conv_bwd, dx in fp32
+ * u is formed in fp32, y rounded once; the backward forms u again. Sums have a fixed order. Rows of the
+ * outputs that no document holds do not exist: cu_seqlens ends at T.
+ */
+size_t gdn_conv_act_workspace_size(int N, int T, int C, int backward);
+int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w, const float* bias, const int32_t* cu_seqlens,
+                     int N, int T, int C, int dtype, int activation, const int32_t* init_idx, const void* conv_init,
+                     int n_init, void* y, void* final_tail, void* workspace, size_t ws_bytes, gdn_stream_t stream);
+int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w, const float* bias, const int32_t* cu_seqlens,
+                     int N, int T, int C, int dtype, int activation, const int32_t* init_idx, const void* conv_init,
+                     int n_init, const void* dy, int64_t dy_stride, const float* dfinal_tail, float* dx, float* dw,
+                     float* dbias, float* dconv_init, void* workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/*
+ * One token per sequence of that convolution, in place on a pool of tails: for sequence b and
+ * E = (tail_pool[i][0], tail_pool[i][1], tail_pool[i][2], x[b]), i = state_idx[b],
+ *     y[b] = act(bias + sum_m w[.][m] E[m]),  tail_pool[i] = (E[1], E[2], E[3]).
+ *   x, y : [B, C], B <= 65535;  tail_pool : [n_pool, 3, C], of `dtype`;  state_idx, status : as in
+ *   gdn_decode_step (an index out of range is skipped, its y row zero, and reported)
+ */
+int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const float* bias, int B, int C, int dtype,
+                         int activation, const int32_t* state_idx, void* tail_pool, int n_pool, void* y, int32_t* status,
+                         gdn_stream_t stream);
+
+/*
+ * Selective scan: a diagonal state-space recurrence whose step and maps depend on the token. Per channel c
+ * with states s = 0 .. S-1 and group g = c / (C / G) of the maps:
+ *     dt = softplus(dt_raw + dt_bias[c])  (or dt_raw + dt_bias[c] with dt_softplus = 0)
+ *     h[s] = exp(dt a[c][s]) h[s] + dt b[g][s] x,   y = sum_s c[g][s] h[s] + skip[c] x,   out = y silu(z)
+ * packed, started and forked as gdn_chunk_fwd (cu_seqlens, init_idx, initial_state; the final state of an
+ * empty document is its start state). All tensor pointers are device pointers:
+ *   x, dt, z, out, dout, dx, ddt, dz : [T, C] of `dtype`;  z NULL: no gate (dz is then not written)
+ *   b, c, db, dc : [T, G, S] of `dtype`;  1 <= S <= 64, C a multiple of G
+ *   a : fp32 [C, S], expected <= 0;  skip, dt_bias : fp32 [C] or NULL (zero)
+ *   strides : host array or NULL. Elements from one token to the next of x, dt, z, b, c (and dout in the
+ *   backward), for views into a projection; 0 or NULL = contiguous. Channels (and the G S entries of a map) are
+ *   contiguous within a token, as are out and the gradients throughout.
+ *   initial_state : fp32 [n_init, C, S];  final_state, dfinal_state : fp32 [N, C, S]
+ * States, steps, decays and all sums are fp32; out is rounded once. The backward is that of
+ * sum(dout out) + sum(dfinal_state final_state): dx, ddt (of dt_raw), dz, db, dc are rounded once to `dtype`;
+ * da [C, S], dskip [C], ddt_bias [C] and dinitial_state [n_init, C, S] are fp32; dskip and ddt_bias may be
+ * NULL where skip and dt_bias are. Every sum has a fixed order (deterministic). A NaN or infinity stays in its
+ * document (and its forks), within it in its channel, but for db and dc, which sum over channels, and in the
+ * backward the sums over documents.
+ * workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned; bad cu_seqlens / init_idx are reported in its
+ * status word (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd.
+ */
+size_t gdn_ssm_workspace_size(int N, int T, int C, int S, int G, int backward);
+int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
+                const float* skip, const float* dt_bias, const int32_t* cu_seqlens, int N, int T, int C, int S, int G,
+                int dtype, const int64_t* strides, int dt_softplus, const int32_t* init_idx, const float* initial_state,
+                int n_init, void* out, float* final_state, void* workspace, size_t ws_bytes, gdn_stream_t stream);
+int gdn_ssm_bwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
+                const float* skip, const float* dt_bias, const int32_t* cu_seqlens, int N, int T, int C, int S, int G,
+                int dtype, const int64_t* strides, int dt_softplus, const int32_t* init_idx, const float* initial_state,
+                int n_init, const void* dout, const float* dfinal_state, void* dx, void* ddt, void* dz, float* da, void* db,
+                void* dc, float* dskip, float* ddt_bias, float* dinitial_state, void* workspace, size_t ws_bytes,
+                gdn_stream_t stream);
+
+/*
+ * One token per sequence of the selective scan, in place on a pool of states: the scan of a one-token
+ * document that starts from state_pool[state_idx[b]] and leaves its state there.
+ *   x, dt, z, out : [B, C];  b, c : [B, G, S];  state_pool : fp32 [n_pool, C, S];  strides : of x, dt, z, b, c;
+ *   B <= 262140;  state_idx, status : as in gdn_decode_step (an index out of range is skipped, its out row
+ *   zero, and reported)
+ */
+int gdn_ssm_decode_step(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
+                        const float* skip, const float* dt_bias, int B, int C, int S, int G, int dtype,
+                        const int64_t* strides, int dt_softplus, const int32_t* state_idx, float* state_pool, int n_pool,
+                        void* out, int32_t* status, gdn_stream_t stream);
+
+/* Where the gate of the call below stands. */
+enum gdn_gate { GDN_GATE_AFTER_NORM = 0, GDN_GATE_BEFORE_NORM = 1 };
+
+/*
+ * Root-mean-square norm of each group of columns with its gate, per row of D and group of `group` consecutive
+ * columns (D a multiple of it, 1 <= group <= 16384: a head, or the whole row), gate = silu(z):
+ *     GDN_GATE_AFTER_NORM :  y = w x / sqrt(mean(x^2) + eps) gate
+ *     GDN_GATE_BEFORE_NORM : y = w u / sqrt(mean(u^2) + eps) with u = x gate
+ *   x, z, y, dy, dx, dz : [T, D] of `dtype`; the strides are the elements between rows of x, z and dy (0 =
+ *   contiguous), y, dx and dz are contiguous; y may be x or z itself, dx and dz any of x, z and dy (not the same)
+ *   w : of `w_dtype`, [group] (shared_w) or [D];  dw : fp32, as w, summed in a fixed order
+ * Sums are fp32; each output is rounded once. T = 0 is a no-op (dw is then zero). workspace:
+ * gdn_gated_rmsnorm_workspace_size(T, D, group, dtype) bytes, 256-byte aligned; its status word
+ * (gdn_workspace_status) is GDN_OK.
+ */
+int gdn_gated_rmsnorm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const void* w, int64_t T,
+                          int D, int group, int shared_w, int first, int dtype, int w_dtype, float eps, void* y,
+                          gdn_stream_t stream);
+size_t gdn_gated_rmsnorm_workspace_size(int64_t T, int D, int group, int dtype);
+int gdn_gated_rmsnorm_bwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride, const void* w,
+                          const void* dy, int64_t dy_stride, int64_t T, int D, int group, int shared_w, int first,
+                          int dtype, int w_dtype, float eps, void* dx, void* dz, float* dw, void* workspace,
+                          size_t ws_bytes, gdn_stream_t stream);
+
 /*
  * For testing the bounded waits only: calls of this thread leave out one bulk copy, number `copy` (from 1). In
  * gdn_rmsnorm_bwd that is row `copy` - 1 (rows that come through bulk copies: aligned ones, up to 16384

@@ -33,7 +33,9 @@ EXPORTS = ("gdn_default_options", "gdn_fwd_workspace_size", "gdn_bwd_workspace_s
            "gdn_noalloc_scratch_bytes", "gdn_noalloc_status", "gdn_fwd_check_args", "gdn_bwd_check_args",
            "gdn_decode_step", "gdn_conv_workspace_size", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_la_workspace_size",
            "gdn_la_fwd", "gdn_la_bwd", "gdn_la_decode_step", "gdn_rmsnorm_fwd", "gdn_rmsnorm_workspace_size",
-           "gdn_rmsnorm_bwd", "gdn_test_withhold")
+           "gdn_rmsnorm_bwd", "gdn_conv_act_workspace_size", "gdn_conv_act_fwd", "gdn_conv_act_bwd",
+           "gdn_conv_decode_step", "gdn_ssm_workspace_size", "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_decode_step",
+           "gdn_gated_rmsnorm_fwd", "gdn_gated_rmsnorm_workspace_size", "gdn_gated_rmsnorm_bwd", "gdn_test_withhold")
 
 
 class GdnError(RuntimeError):
@@ -164,6 +166,28 @@ def load(path: Optional[str] = None):
         lib.gdn_rmsnorm_workspace_size.restype = Z
         lib.gdn_rmsnorm_bwd.argtypes = [P, P, P, P, L, I, I, I, F, P, P, P, Z, P]
         lib.gdn_rmsnorm_bwd.restype = I
+        lib.gdn_conv_act_workspace_size.argtypes = [I, I, I, I]
+        lib.gdn_conv_act_workspace_size.restype = Z
+        lib.gdn_conv_act_fwd.argtypes = [P, L, P, P, P, I, I, I, I, I, P, P, I, P, P, P, Z, P]
+        lib.gdn_conv_act_fwd.restype = I
+        lib.gdn_conv_act_bwd.argtypes = [P, L, P, P, P, I, I, I, I, I, P, P, I, P, L, P, P, P, P, P, P, Z, P]
+        lib.gdn_conv_act_bwd.restype = I
+        lib.gdn_conv_decode_step.argtypes = [P, L, P, P, I, I, I, I, P, P, I, P, P, P]
+        lib.gdn_conv_decode_step.restype = I
+        lib.gdn_ssm_workspace_size.argtypes = [I, I, I, I, I, I]
+        lib.gdn_ssm_workspace_size.restype = Z
+        lib.gdn_ssm_fwd.argtypes = [P] * 9 + [I] * 6 + [P, I, P, P, I, P, P, P, Z, P]
+        lib.gdn_ssm_fwd.restype = I
+        lib.gdn_ssm_bwd.argtypes = [P] * 9 + [I] * 6 + [P, I, P, P, I] + [P] * 12 + [Z, P]
+        lib.gdn_ssm_bwd.restype = I
+        lib.gdn_ssm_decode_step.argtypes = [P] * 8 + [I] * 5 + [P, I, P, P, I, P, P, P]
+        lib.gdn_ssm_decode_step.restype = I
+        lib.gdn_gated_rmsnorm_fwd.argtypes = [P, L, P, L, P, L, I, I, I, I, I, I, F, P, P]
+        lib.gdn_gated_rmsnorm_fwd.restype = I
+        lib.gdn_gated_rmsnorm_workspace_size.argtypes = [L, I, I, I]
+        lib.gdn_gated_rmsnorm_workspace_size.restype = Z
+        lib.gdn_gated_rmsnorm_bwd.argtypes = [P, L, P, L, P, P, L, L, I, I, I, I, I, I, F, P, P, P, P, Z, P]
+        lib.gdn_gated_rmsnorm_bwd.restype = I
         lib.gdn_test_withhold.argtypes = [I, I]
         lib.gdn_test_withhold.restype = I
         if path is None:
@@ -404,17 +428,85 @@ def decode_step(q, k, v, g, beta, state_pool, state_idx, options: Optional[Optio
     return out
 
 
-def conv_workspace_size(N: int, T: int, C: int, backward: bool = False) -> int:
-    return int(load().gdn_conv_workspace_size(N, T, C, 1 if backward else 0))
+ACTIVATIONS = {"none": 0, "silu": 1}
+
+
+def conv_workspace_size(N: int, T: int, C: int, backward: bool = False, activation=None) -> int:
+    size = load().gdn_conv_workspace_size if activation is None else load().gdn_conv_act_workspace_size
+    return int(size(N, T, C, 1 if backward else 0))
+
+
+def _tokens(t, name, dtype, shape, align=1):
+    """A tensor whose tokens (the first dimension) may be further apart than they need, the rest contiguous. Returns
+    the elements between tokens, 0 when contiguous."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA {dtype} tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    need = 1
+    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and st != need:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        need *= n
+    st = t.stride(0)
+    if st < need or st % align != 0:
+        raise ValueError(f"{name}: tokens must be a multiple of {align} elements apart, at least {need}")
+    return st
+
+
+def _conv_act_inputs(x, w, cu_seqlens, bias, init_idx, conv_init, activation, step=False):
+    torch = _torch()
+    if activation not in ACTIVATIONS:
+        raise ValueError('activation: expected None, "none" or "silu"')
+    code = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
+    T, C = x.shape
+    xs = _tokens(x, "x", x.dtype, (T, C), 16 // x.element_size())
+    _check(w, "w", torch.float32, (C, 4))
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (C,))
+    if step:
+        return T, C, code, ACTIVATIONS[activation], xs
+    N = cu_seqlens.shape[0] - 1
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
+    if init_idx is not None:
+        _check(init_idx, "init_idx", torch.int32, (N,))
+    n_init = 0
+    if conv_init is not None:
+        n_init = conv_init.shape[0]
+        _check(conv_init, "conv_init", x.dtype, (n_init, 3, C))
+    return T, C, N, n_init, code, ACTIVATIONS[activation], xs
 
 
 def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None, final_tail=None, workspace=None,
-             stream=None):
+             stream=None, activation=None):
     """Width-4 causal convolution over packed documents. x [T, C] bf16; w [C, 4] fp32; bias [C] fp32 or
     None; cu_seqlens [N+1] int32; init_idx [N] int32 or None; conv_init [n_init, 3, C] bf16 or None.
-    Returns (y [T, C] bf16, final_tail [N, 3, C] bf16)."""
+    Returns (y [T, C] bf16, final_tail [N, 3, C] bf16).
+
+    With activation "silu" (or "none") x may be fp16 or fp32 too and its tokens apart (a view into a
+    projection), C is at most 2^24, and y, conv_init and final_tail are of x's type; the workspace is then
+    conv_workspace_size(..., activation=activation) bytes."""
     torch = _torch()
     empty = torch.empty if stream is None else _empty_on(stream)
+    if activation is not None:
+        T, C, N, n_init, code, act, xs = _conv_act_inputs(x, w, cu_seqlens, bias, init_idx, conv_init, activation)
+        y = empty((T, C), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (T, C))
+        if final_tail is None:
+            final_tail = empty((N, 3, C), dtype=x.dtype, device=x.device)
+        else:
+            _check(final_tail, "final_tail", x.dtype, (N, 3, C))
+        if workspace is None:
+            workspace = empty(conv_workspace_size(N, T, C, False, activation), dtype=torch.uint8, device=x.device)
+        rc = load().gdn_conv_act_fwd(_ptr(x), xs, _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, code, act,
+                                     _ptr(init_idx), _ptr(conv_init), n_init, _ptr(y), _ptr(final_tail),
+                                     _ptr(workspace), workspace.numel(), _stream_handle(stream))
+        if rc != GDN_OK:
+            raise GdnError(rc, "gdn_conv_act_fwd")
+        return y, final_tail
     T, C = x.shape
     N = cu_seqlens.shape[0] - 1
     _check(x, "x", torch.bfloat16, (T, C))
@@ -443,13 +535,32 @@ def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None,
 
 
 def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfinal_tail=None, workspace=None,
-             stream=None):
+             stream=None, activation=None):
     """Backward of conv_fwd. Returns dict dx [T, C], dw [C, 4], dbias [C] (None without bias),
-    dconv_init [n_init, 3, C] (None without a pool), all fp32."""
+    dconv_init [n_init, 3, C] (None without a pool), all fp32. `activation` as given to conv_fwd; with it dy may be
+    strided as x."""
     torch = _torch()
     empty = torch.empty if stream is None else _empty_on(stream)
     T, C = x.shape
     N = cu_seqlens.shape[0] - 1
+    if activation is not None:
+        T, C, N, n_init, code, act, xs = _conv_act_inputs(x, w, cu_seqlens, bias, init_idx, conv_init, activation)
+        gs = _tokens(dy, "dy", x.dtype, (T, C), 16 // x.element_size())
+        if dfinal_tail is not None:
+            _check(dfinal_tail, "dfinal_tail", torch.float32, (N, 3, C))
+        f32 = dict(dtype=torch.float32, device=x.device)
+        dx, dw = empty((T, C), **f32), empty((C, 4), **f32)
+        dbias = empty((C,), **f32) if bias is not None else None
+        dci = empty((n_init, 3, C), **f32) if n_init > 0 else None
+        if workspace is None:
+            workspace = empty(conv_workspace_size(N, T, C, True, activation), dtype=torch.uint8, device=x.device)
+        rc = load().gdn_conv_act_bwd(_ptr(x), xs, _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, code, act,
+                                     _ptr(init_idx), _ptr(conv_init), n_init, _ptr(dy), gs, _ptr(dfinal_tail), _ptr(dx),
+                                     _ptr(dw), _ptr(dbias), _ptr(dci), _ptr(workspace), workspace.numel(),
+                                     _stream_handle(stream))
+        if rc != GDN_OK:
+            raise GdnError(rc, "gdn_conv_act_bwd")
+        return dict(dx=dx, dw=dw, dbias=dbias, dconv_init=dci)
     _check(dy, "dy", torch.bfloat16, (T, C))
     if dfinal_tail is not None:
         _check(dfinal_tail, "dfinal_tail", torch.float32, (N, 3, C))
@@ -467,6 +578,27 @@ def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfi
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_conv_bwd")
     return dict(dx=dx, dw=dw, dbias=dbias, dconv_init=dci)
+
+
+def conv_decode_step(x, w, tail_pool, state_idx, bias=None, activation="none", y=None, status=None, stream=None):
+    """One token per sequence of the convolution with its activation ("none" or "silu"), in place on a pool of tails.
+    x [B, C] (bf16, fp16 or fp32; sequences may be strided); w [C, 4], bias [C] fp32; tail_pool [n_pool, 3, C] of x's
+    type (updated); state_idx [B] int32 (distinct entries); status as in decode_step. Returns y [B, C]."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    B, C, code, act, xs = _conv_act_inputs(x, w, None, bias, None, None, activation, step=True)
+    _check(state_idx, "state_idx", torch.int32, (B,))
+    if tail_pool is None:
+        raise ValueError("tail_pool is required")
+    _check(tail_pool, "tail_pool", x.dtype, (tail_pool.shape[0], 3, C))
+    if status is not None:
+        _check(status, "status", torch.int32, (1,))
+    y = empty((B, C), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (B, C))
+    rc = load().gdn_conv_decode_step(_ptr(x), xs, _ptr(w), _ptr(bias), B, C, code, act, _ptr(state_idx),
+                                     _ptr(tail_pool), tail_pool.shape[0], _ptr(y), _ptr(status), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_conv_decode_step")
+    return y
 
 
 # ----------------------------------------------------------------------------- decayed linear attention
@@ -701,6 +833,200 @@ def rmsnorm_bwd(h, w, dy, dh=None, eps: float = 1e-6, dx=None, dw=None, workspac
     if rc != GDN_OK:
         raise GdnError(rc, "gdn_rmsnorm_bwd")
     return dx, dw
+
+
+# ----------------------------------------------------------------------------- selective scan
+
+
+def ssm_workspace_size(N: int, T: int, C: int, S: int, G: int = 1, backward: bool = False) -> int:
+    return int(load().gdn_ssm_workspace_size(N, T, C, S, G, 1 if backward else 0))
+
+
+def _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias, dout=None):
+    torch = _torch()
+    code = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
+    T, C = x.shape
+    _, G, S = b.shape
+    h = x.dtype
+    strides = [_tokens(x, "x", h, (T, C)), _tokens(dt, "dt", h, (T, C)),
+               0 if z is None else _tokens(z, "z", h, (T, C)),
+               _tokens(b, "b", h, (T, G, S)), _tokens(c, "c", h, (T, G, S))]
+    if dout is not None:
+        strides.append(_tokens(dout, "dout", h, (T, C)))
+    _check(a, "a", torch.float32, (C, S))
+    if skip is not None:
+        _check(skip, "skip", torch.float32, (C,))
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", torch.float32, (C,))
+    return code, T, C, S, G, _strides(strides)
+
+
+def _ssm_packed(cu_seqlens, init_idx, initial_state, C, S):
+    torch = _torch()
+    N = cu_seqlens.shape[0] - 1
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
+    n_init = 0
+    if initial_state is not None:
+        n_init = initial_state.shape[0]
+        _check(initial_state, "initial_state", torch.float32, (n_init, C, S))
+    if init_idx is not None:
+        _check(init_idx, "init_idx", torch.int32, (N,))
+    return N, n_init
+
+
+def ssm_scan_fwd(x, dt, a, b, c, cu_seqlens, skip=None, z=None, dt_bias=None, init_idx=None, initial_state=None,
+                 dt_softplus: bool = True, out=None, final_state=None, workspace=None, stream=None):
+    """Selective scan over a packed batch: with step = softplus(dt + dt_bias), h = exp(step a) h + step b x,
+    out = (c . h + skip x) silu(z), per channel. Shapes: x, dt, z [T, C], b, c [T, G, S] (bf16, fp16 or fp32, all the
+    same; tokens may be strided; S <= 64, channel c uses maps c // (C / G)); a [C, S], skip, dt_bias [C] fp32;
+    initial_state [n_init, C, S] fp32; cu_seqlens and init_idx as in chunk_fwd. Returns (out [T, C], final_state
+    [N, C, S] fp32)."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    code, T, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias)
+    N, n_init = _ssm_packed(cu_seqlens, init_idx, initial_state, C, S)
+    dev = x.device
+    out = empty((T, C), dtype=x.dtype, device=dev) if out is None else _check(out, "out", x.dtype, (T, C))
+    if final_state is None:
+        final_state = empty((N, C, S), dtype=torch.float32, device=dev)
+    else:
+        _check(final_state, "final_state", torch.float32, (N, C, S))
+    if workspace is None:
+        workspace = empty(ssm_workspace_size(N, T, C, S, G), dtype=torch.uint8, device=dev)
+    rc = load().gdn_ssm_fwd(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias),
+                            _ptr(cu_seqlens), N, T, C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(init_idx),
+                            _ptr(initial_state), n_init, _ptr(out), _ptr(final_state), _ptr(workspace),
+                            workspace.numel(), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_ssm_fwd")
+    return out, final_state
+
+
+def ssm_scan_bwd(x, dt, a, b, c, cu_seqlens, dout, dfinal_state=None, skip=None, z=None, dt_bias=None, init_idx=None,
+                 initial_state=None, dt_softplus: bool = True, workspace=None, stream=None, grads=None):
+    """Backward of ssm_scan_fwd. Returns dict of dx, ddt, dz (None without z), db, dc of x's type and da, dskip,
+    ddt_bias and dinit in fp32 (None without skip, dt_bias or a pool). `grads` may hold preallocated outputs under
+    those keys."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if dout is None:
+        raise ValueError("dout is required")
+    code, T, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias, dout)
+    N, n_init = _ssm_packed(cu_seqlens, init_idx, initial_state, C, S)
+    if dfinal_state is not None:
+        _check(dfinal_state, "dfinal_state", torch.float32, (N, C, S))
+    dev, h, f32 = x.device, x.dtype, torch.float32
+    grads = grads or {}
+
+    def out_buf(key, shape, dtype, wanted=True):
+        if not wanted:
+            return None
+        t = grads.get(key)
+        return empty(shape, dtype=dtype, device=dev) if t is None else _check(t, key, dtype, shape)
+    g = dict(dx=out_buf("dx", (T, C), h), ddt=out_buf("ddt", (T, C), h), dz=out_buf("dz", (T, C), h, z is not None),
+             da=out_buf("da", (C, S), f32), db=out_buf("db", (T, G, S), h), dc=out_buf("dc", (T, G, S), h),
+             dskip=out_buf("dskip", (C,), f32, skip is not None),
+             ddt_bias=out_buf("ddt_bias", (C,), f32, dt_bias is not None),
+             dinit=out_buf("dinit", (n_init, C, S), f32, n_init > 0))
+    if workspace is None:
+        workspace = empty(ssm_workspace_size(N, T, C, S, G, True), dtype=torch.uint8, device=dev)
+    rc = load().gdn_ssm_bwd(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias),
+                            _ptr(cu_seqlens), N, T, C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(init_idx),
+                            _ptr(initial_state), n_init, _ptr(dout), _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["ddt"]),
+                            _ptr(g["dz"]), _ptr(g["da"]), _ptr(g["db"]), _ptr(g["dc"]), _ptr(g["dskip"]),
+                            _ptr(g["ddt_bias"]), _ptr(g["dinit"]), _ptr(workspace), workspace.numel(),
+                            _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_ssm_bwd")
+    return g
+
+
+def ssm_decode_step(x, dt, a, b, c, state_pool, state_idx, skip=None, z=None, dt_bias=None, dt_softplus: bool = True,
+                    out=None, status=None, stream=None):
+    """One token per sequence of the selective scan, in place on a pool of states. x, dt, z [B, C], b, c [B, G, S]
+    (sequences may be strided); state_pool [n_pool, C, S] fp32 (updated); state_idx [B] int32 (distinct entries);
+    status as in decode_step. Returns out [B, C] of x's type."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    code, B, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias)
+    _check(state_idx, "state_idx", torch.int32, (B,))
+    if state_pool is None:
+        raise ValueError("state_pool is required")
+    _check(state_pool, "state_pool", torch.float32, (state_pool.shape[0], C, S))
+    if status is not None:
+        _check(status, "status", torch.int32, (1,))
+    out = empty((B, C), dtype=x.dtype, device=x.device) if out is None else _check(out, "out", x.dtype, (B, C))
+    rc = load().gdn_ssm_decode_step(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias), B,
+                                    C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(state_idx), _ptr(state_pool),
+                                    state_pool.shape[0], _ptr(out), _ptr(status), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_ssm_decode_step")
+    return out
+
+
+# ----------------------------------------------------------------------------- norm with its gate
+
+GATE_ORDER = {"norm": 0, "gate": 1}  # what comes first
+
+
+def _gnorm_inputs(x, z, w, group, first, dy=None):
+    if first not in GATE_ORDER:
+        raise ValueError('first: expected "norm" or "gate"')
+    allowed = (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32)
+    code = _dtype_code(x, "x", allowed)
+    T, D = x.shape
+    group = D if group is None else int(group)
+    if group < 1 or D % group:
+        raise ValueError(f"group: {D} columns are no multiple of {group}")
+    strides = [_tokens(x, "x", x.dtype, (T, D)), _tokens(z, "z", x.dtype, (T, D))]
+    if dy is not None:
+        strides.append(_tokens(dy, "dy", x.dtype, (T, D)))
+    wcode = _dtype_code(w, "w", allowed)
+    if tuple(w.shape) not in ((group,), (D,)):
+        raise ValueError(f"w: expected {group} or {D} weights, got {tuple(w.shape)}")
+    _check(w, "w", w.dtype)
+    return T, D, group, 1 if w.shape[0] == group else 0, GATE_ORDER[first], code, wcode, strides
+
+
+def gated_rmsnorm_fwd(x, z, w, group=None, eps: float = 1e-6, first: str = "norm", y=None, stream=None):
+    """The norm of each `group` consecutive columns (a head; None = the whole row) with its gate: first="norm" gives
+    y = w norm(x) silu(z), first="gate" y = w norm(x silu(z)), norm(u) = u / sqrt(mean(u^2) + eps). x, z [T, D] (bf16,
+    fp16 or fp32; rows may be strided); w [group] (the same for every group) or [D], of any of the types; group <=
+    16384. Returns y [T, D] of x's type; it may be x or z itself, when contiguous."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    T, D, group, shared, order, code, wcode, (xs, zs) = _gnorm_inputs(x, z, w, group, first)
+    y = empty((T, D), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (T, D))
+    rc = load().gdn_gated_rmsnorm_fwd(_ptr(x), xs, _ptr(z), zs, _ptr(w), T, D, group, shared, order, code, wcode,
+                                      float(eps), _ptr(y), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_gated_rmsnorm_fwd")
+    return y
+
+
+def gated_rmsnorm_bwd(x, z, w, dy, group=None, eps: float = 1e-6, first: str = "norm", dx=None, dz=None, dw=None,
+                      workspace=None, stream=None):
+    """Backward of gated_rmsnorm_fwd. Returns (dx, dz [T, D] of x's type, dw fp32 of w's shape)."""
+    torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
+    if dy is None:
+        raise ValueError("dy is required")
+    T, D, group, shared, order, code, wcode, (xs, zs, gs) = _gnorm_inputs(x, z, w, group, first, dy)
+    dx = empty((T, D), dtype=x.dtype, device=x.device) if dx is None else _check(dx, "dx", x.dtype, (T, D))
+    dz = empty((T, D), dtype=x.dtype, device=x.device) if dz is None else _check(dz, "dz", x.dtype, (T, D))
+    if dw is None:
+        dw = empty(tuple(w.shape), dtype=torch.float32, device=x.device)
+    else:
+        _check(dw, "dw", torch.float32, tuple(w.shape))
+    if workspace is None:
+        workspace = empty(int(load().gdn_gated_rmsnorm_workspace_size(T, D, group, code)), dtype=torch.uint8,
+                          device=x.device)
+    rc = load().gdn_gated_rmsnorm_bwd(_ptr(x), xs, _ptr(z), zs, _ptr(w), _ptr(dy), gs, T, D, group, shared, order, code,
+                                      wcode, float(eps), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(workspace),
+                                      workspace.numel(), _stream_handle(stream))
+    if rc != GDN_OK:
+        raise GdnError(rc, "gdn_gated_rmsnorm_bwd")
+    return dx, dz, dw
 
 
 @contextlib.contextmanager

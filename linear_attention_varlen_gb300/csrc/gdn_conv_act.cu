@@ -1,0 +1,607 @@
+// Width-4 causal depthwise convolution with its activation over packed documents, forward and backward, and its step
+// for single tokens (sm_103a). Per channel c and document with inputs x[0 .. n-1], as in the convolution without one:
+//     E = (start[0], start[1], start[2], x[0], ..., x[n-1]),  u[p] = bias[c] + sum_m w[c][m] E[p + m],
+//     y[p] = silu(u[p]),  tail = (E[n], E[n+1], E[n+2]);
+// backward du = dy silu'(u), dE[e] = sum_m w[c][m] du[e - m] (+ dtail), dw[c][m] = sum_p du[p] E[p + m],
+// dbias = sum_p du[p]. u is formed again from x: nothing but the inputs is kept between the two directions.
+//
+// All of it is bound by memory traffic: each input is read once, each output written once, but for the three rows
+// before a block of tokens (and the three behind it in the backward). A thread takes 16 bytes of channels down the
+// tokens of a block, the window of three inputs in registers.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gdn.h"
+#include "bw_prims.cuh"
+#include "elem.cuh"
+#include "gdn_common.cuh"
+#include "gdn_host.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kActThreads = 128;
+constexpr int kFwdTokens = 32, kBwdTokens = 64;  // tokens to a block
+constexpr int kAhead = 4;                        // rows in flight
+
+struct ActHeader {
+  int32_t status, forks;
+  int32_t pad[62];
+};
+
+struct ActParams {
+  const void *x, *dy;
+  int64_t sx, sdy;  // elements between tokens
+  const float *w, *bias;
+  const int32_t *cu, *init_idx;
+  const void* conv_init;
+  int N, T, C, n_init, silu, n_tb;
+  void *y, *tail;
+  const float* dtail;  // given gradient of the tails
+  float *dx, *dw, *dbias, *dinit;
+  ActHeader* hd;
+  float *dstart, *dend, *part;
+};
+
+struct ActLayout {
+  size_t header, dstart, dend, part, total;
+  int n_tb;
+};
+inline ActLayout act_layout(int N, int T, int C, bool bwd) {
+  ActLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o = align_up(o + b, 256);
+    return at;
+  };
+  const int per = bwd ? kBwdTokens : kFwdTokens;
+  L.n_tb = (T + per - 1) / per;
+  L.header = take(sizeof(ActHeader));
+  if (bwd) {
+    L.dstart = take((size_t)N * 3 * C * 4);     // gradient at each document's start
+    L.dend = take((size_t)N * 3 * C * 4);       // gradient at its tail from forks
+    L.part = take((size_t)L.n_tb * C * 5 * 4);  // dw, dbias of each block of tokens: [block][5][C]
+  }
+  L.total = o;
+  return L;
+}
+
+template <typename T>
+constexpr int kVecOf = 16 / (int)sizeof(T);
+
+// Row e (of three) in front of document d, and row k of its tail: an input, an entry of the pool, or null for zero.
+// A fork's start is the tail of an earlier document, so the walk ends.
+template <typename T>
+__device__ __forceinline__ const T* start_row(const ActParams& p, int d, int e) {
+  for (;;) {
+    const int s = p.init_idx ? p.init_idx[d] : -1;
+    if (s < 0) return nullptr;
+    if (s < p.n_init) return static_cast<const T*>(p.conv_init) + ((int64_t)s * 3 + e) * p.C;
+    d = s - p.n_init;
+    e += p.cu[d + 1] - p.cu[d];
+    if (e >= 3) return static_cast<const T*>(p.x) + ((int64_t)p.cu[d] + e - 3) * p.sx;
+  }
+}
+
+__device__ __forceinline__ int doc_at(const int32_t* cu, int N, int t) {  // the document that holds token t
+  int lo = 0, hi = N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T, int K>
+__device__ __forceinline__ void unpack(const Pack<T, K>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < K; ++i) f[i] = to_float(r.t[i]);
+}
+template <typename T, int K>
+__device__ __forceinline__ void row_or_zero(const T* row, int c, float* f) {
+  Pack<T, K> r{};
+  if (row) r = *reinterpret_cast<const Pack<T, K>*>(row + c);
+  unpack(r, f);
+}
+
+__global__ void __launch_bounds__(256) act_check_kernel(const __grid_constant__ ActParams p) {
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  __shared__ int s_bad, s_forks;
+  if (threadIdx.x == 0) s_bad = s_forks = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.N; i += 256) {
+    const int b = p.cu[i], e = p.cu[i + 1];
+    bool bad = b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T);
+    if (p.init_idx) {
+      const int s = p.init_idx[i];
+      if (s < -1 || (s >= p.n_init && s - p.n_init >= i))
+        bad = true;
+      else if (s >= p.n_init)
+        s_forks = 1;
+    }
+    if (bad) s_bad = 1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.hd->forks = s_forks;
+    p.hd->status = s_bad ? kErrInvalid : 0;
+  }
+}
+
+// Blocks of kFwdTokens tokens, then one block for each document's tail.
+template <typename T>
+__global__ void __launch_bounds__(kActThreads) act_fwd_kernel(const __grid_constant__ ActParams p) {
+  constexpr int K = kVecOf<T>;
+  using P = Pack<T, K>;
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int c = (blockIdx.y * kActThreads + threadIdx.x) * K;
+  if (c >= p.C) return;
+  if ((int)blockIdx.x >= p.n_tb) {
+    const int d = blockIdx.x - p.n_tb, n = p.cu[d + 1] - p.cu[d];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const T* row = n + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)p.cu[d] + n + k - 3) * p.sx : start_row<T>(p, d, n + k);
+      P r{};
+      if (row) r = *reinterpret_cast<const P*>(row + c);
+      *reinterpret_cast<P*>(static_cast<T*>(p.tail) + ((int64_t)d * 3 + k) * p.C + c) = r;
+    }
+    return;
+  }
+  const int t0 = blockIdx.x * kFwdTokens, t1 = min(t0 + kFwdTokens, p.T);
+  const T* x = static_cast<const T*>(p.x) + c;
+  float w[4][K], bias[K], win[3][K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
+    w[0][i] = wv.x, w[1][i] = wv.y, w[2][i] = wv.z, w[3][i] = wv.w;
+    bias[i] = p.bias ? p.bias[c + i] : 0.f;
+  }
+  int d = doc_at(p.cu, p.N, t0), end = p.cu[d + 1];
+  auto window = [&](int t) {  // the three inputs before token t of document d
+    const int at = t - p.cu[d];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      row_or_zero<T, K>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c,
+                        win[k]);
+  };
+  window(t0);
+  for (int ta = t0; ta < t1; ta += kAhead) {
+    P r[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (ta + k < t1) r[k] = *reinterpret_cast<const P*>(x + (int64_t)(ta + k) * p.sx);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = ta + k;
+      if (t >= t1) break;
+      if (t >= end) {
+        while (p.cu[d + 1] <= t) ++d;
+        end = p.cu[d + 1];
+        window(t);
+      }
+      float cur[K];
+      unpack(r[k], cur);
+      P o;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        float u = fmaf(w[0][i], win[0][i], bias[i]);
+        u = fmaf(w[1][i], win[1][i], u);
+        u = fmaf(w[2][i], win[2][i], u);
+        u = fmaf(w[3][i], cur[i], u);
+        if (p.silu) u = silu_of(u, sigmoid(u));
+        o.t[i] = from_float<T>(u);
+        win[0][i] = win[1][i];
+        win[1][i] = win[2][i];
+        win[2][i] = cur[i];
+      }
+      *reinterpret_cast<P*>(static_cast<T*>(p.y) + (int64_t)t * p.C + c) = o;
+    }
+  }
+}
+
+// Blocks of kBwdTokens tokens. du runs up the tokens once; the gradient of an input is complete three tokens later.
+template <typename T>
+__global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_constant__ ActParams p) {
+  constexpr int K = kVecOf<T>;
+  using P = Pack<T, K>;
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int c = (blockIdx.y * kActThreads + threadIdx.x) * K;
+  if (c >= p.C) return;
+  const int t0 = blockIdx.x * kBwdTokens, t1 = min(t0 + kBwdTokens, p.T);
+  const T *x = static_cast<const T*>(p.x) + c, *dy = static_cast<const T*>(p.dy) + c;
+  float w[4][K], bias[K], win[3][K], pend[3][K], dw[5][K];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
+    w[0][i] = wv.x, w[1][i] = wv.y, w[2][i] = wv.z, w[3][i] = wv.w;
+    bias[i] = p.bias ? p.bias[c + i] : 0.f;
+#pragma unroll
+    for (int m = 0; m < 5; ++m) dw[m][i] = 0.f;
+#pragma unroll
+    for (int m = 0; m < 3; ++m) pend[m][i] = 0.f;
+  }
+  int d = doc_at(p.cu, p.N, t0), begin = p.cu[d], end = p.cu[d + 1];
+  auto window = [&](int t) {
+    const int at = t - begin;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      row_or_zero<T, K>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c,
+                        win[k]);
+  };
+  // the gradient of E[e] of document d, complete: an input of this block, or a row of the document's start
+  auto emit = [&](int e, const float* g) {
+    float* to = nullptr;
+    if (e < 3) {
+      if (begin >= t0) to = p.dstart + ((int64_t)d * 3 + e) * p.C + c;
+    } else if (begin + e - 3 >= t0 && begin + e - 3 < t1) {
+      to = p.dx + ((int64_t)begin + e - 3) * p.C + c;
+    }
+    if (to) {
+#pragma unroll
+      for (int i = 0; i < K; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+    }
+  };
+  window(t0);
+  const int stop = min(p.T, t1 + 3);
+  int t = t0;
+  for (int ta = t0; ta < stop; ta += kAhead) {
+    P xr[kAhead], gr[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (ta + k < stop) {
+        xr[k] = *reinterpret_cast<const P*>(x + (int64_t)(ta + k) * p.sx);
+        gr[k] = *reinterpret_cast<const P*>(dy + (int64_t)(ta + k) * p.sdy);
+      }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      t = ta + k;
+      if (t >= stop) break;
+      if (t >= end) {
+        if (t >= t1) break;  // behind the block only the rest of its last document counts
+#pragma unroll
+        for (int m = 0; m < 3; ++m) emit(end - begin + m, pend[m]);
+        while (p.cu[d + 1] <= t) ++d;
+        begin = p.cu[d];
+        end = p.cu[d + 1];
+        window(t);
+#pragma unroll
+        for (int i = 0; i < K; ++i) pend[0][i] = pend[1][i] = pend[2][i] = 0.f;
+      }
+      float cur[K], du[K], done[K];
+      unpack(xr[k], cur);
+      unpack(gr[k], du);
+      const bool mine = t < t1;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        float u = fmaf(w[0][i], win[0][i], bias[i]);
+        u = fmaf(w[1][i], win[1][i], u);
+        u = fmaf(w[2][i], win[2][i], u);
+        u = fmaf(w[3][i], cur[i], u);
+        if (p.silu) du[i] *= silu_slope(u, sigmoid(u));
+        if (mine) {
+          dw[0][i] = fmaf(du[i], win[0][i], dw[0][i]);
+          dw[1][i] = fmaf(du[i], win[1][i], dw[1][i]);
+          dw[2][i] = fmaf(du[i], win[2][i], dw[2][i]);
+          dw[3][i] = fmaf(du[i], cur[i], dw[3][i]);
+          dw[4][i] += du[i];
+        }
+        done[i] = fmaf(w[0][i], du[i], pend[0][i]);
+        pend[0][i] = fmaf(w[1][i], du[i], pend[1][i]);
+        pend[1][i] = fmaf(w[2][i], du[i], pend[2][i]);
+        pend[2][i] = w[3][i] * du[i];
+        win[0][i] = win[1][i];
+        win[1][i] = win[2][i];
+        win[2][i] = cur[i];
+      }
+      emit(t - begin, done);
+    }
+  }
+  if (end <= stop) {  // the document ended within reach: its last inputs are complete
+#pragma unroll
+    for (int m = 0; m < 3; ++m) emit(end - begin + m, pend[m]);
+  }
+#pragma unroll
+  for (int m = 0; m < 5; ++m)
+#pragma unroll
+    for (int i = 0; i < K; i += 4)
+      *reinterpret_cast<float4*>(p.part + ((int64_t)blockIdx.x * 5 + m) * p.C + c + i) =
+          make_float4(dw[m][i], dw[m][i + 1], dw[m][i + 2], dw[m][i + 3]);
+}
+
+// dw and dbias over the blocks of tokens, in their order: 32 channels a CTA, each summed by eight threads.
+__global__ void __launch_bounds__(256) act_sum_kernel(const __grid_constant__ ActParams p) {
+  __shared__ float s[8][5][32];
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float v[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < p.C)
+    for (int b = r; b < p.n_tb; b += 8)
+#pragma unroll
+      for (int m = 0; m < 5; ++m) v[m] += p.part[((int64_t)b * 5 + m) * p.C + c];
+#pragma unroll
+  for (int m = 0; m < 5; ++m) s[r][m][lane] = v[m];
+  __syncthreads();
+  if (r < 5 && c < p.C) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += s[k][r][lane];
+    if (r < 4)
+      p.dw[(int64_t)c * 4 + r] = sum;
+    else if (p.dbias)
+      p.dbias[c] = sum;
+  }
+}
+
+// The tails' gradients, given ones and those of forks, into the inputs they copy or on into the document's start;
+// each document's start gradient where it belongs. One thread to a channel; all documents from the last on where some
+// fork, else those of blockIdx.y.
+__global__ void __launch_bounds__(256) act_ends_kernel(const __grid_constant__ ActParams p) {
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  const bool forks = p.hd->forks != 0;
+  if (c >= p.C || (forks && blockIdx.y > 0)) return;
+  const int step = forks ? 1 : gridDim.y, d0 = forks ? 0 : blockIdx.y;
+  if (forks)
+    for (int64_t i = 0; i < 3 * (int64_t)p.N; ++i) p.dend[i * p.C + c] = 0.f;
+  for (int d = d0 + (p.N - 1 - d0) / step * step; d >= 0; d -= step) {
+    const int t0 = p.cu[d], n = p.cu[d + 1] - t0;
+    float* start = p.dstart + (int64_t)d * 3 * p.C + c;
+    float g[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) g[e] = n > 0 ? start[(int64_t)e * p.C] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      float v = p.dtail ? p.dtail[((int64_t)d * 3 + k) * p.C + c] : 0.f;
+      if (forks) v += p.dend[((int64_t)d * 3 + k) * p.C + c];
+      if (n + k >= 3) {
+        if (p.dtail || forks) p.dx[((int64_t)t0 + n + k - 3) * p.C + c] += v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e == n + k) g[e] += v;
+      }
+    }
+    const int s = p.init_idx ? p.init_idx[d] : -1;
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      start[(int64_t)e * p.C] = g[e];
+      if (s >= p.n_init && p.init_idx) p.dend[((int64_t)(s - p.n_init) * 3 + e) * p.C + c] += g[e];
+    }
+  }
+}
+
+// The pool entries' gradients: the start gradients of their documents, in order.
+__global__ void __launch_bounds__(256) act_pool_kernel(const __grid_constant__ ActParams p) {
+  bw::griddep_wait();
+  if (p.hd->status != 0) return;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = 3 * (int64_t)p.C;
+  if (i >= p.n_init * row) return;
+  const int e = (int)(i / row);
+  float v = 0.f;
+  if (p.init_idx)
+    for (int d = 0; d < p.N; ++d)
+      if (p.init_idx[d] == e) v += p.dstart[d * row + i % row];
+  p.dinit[i] = v;
+}
+
+struct StepParams {
+  const void* x;
+  int64_t sx;
+  const float *w, *bias;
+  const int32_t* idx;
+  void *pool, *y;
+  int32_t* status;
+  int B, C, n_pool, silu;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kActThreads) act_step_kernel(const __grid_constant__ StepParams p) {
+  constexpr int K = kVecOf<T>;
+  using P = Pack<T, K>;
+  const int64_t b = blockIdx.y;
+  const int c = (blockIdx.x * kActThreads + threadIdx.x) * K, e = p.idx[b];
+  if (c >= p.C) return;
+  P* out = reinterpret_cast<P*>(static_cast<T*>(p.y) + b * p.C + c);
+  if (e < 0 || e >= p.n_pool) {  // skipped, reported
+    P o;
+#pragma unroll
+    for (int i = 0; i < K; ++i) o.t[i] = from_float<T>(0.f);
+    *out = o;
+    if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
+    return;
+  }
+  T* tail = static_cast<T*>(p.pool) + (int64_t)e * 3 * p.C + c;
+  P r[4];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) r[k] = *reinterpret_cast<const P*>(tail + (int64_t)k * p.C);
+  r[3] = *reinterpret_cast<const P*>(static_cast<const T*>(p.x) + b * p.sx + c);
+  P o;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
+    float u = fmaf(wv.x, to_float(r[0].t[i]), p.bias ? p.bias[c + i] : 0.f);
+    u = fmaf(wv.y, to_float(r[1].t[i]), u);
+    u = fmaf(wv.z, to_float(r[2].t[i]), u);
+    u = fmaf(wv.w, to_float(r[3].t[i]), u);
+    if (p.silu) u = silu_of(u, sigmoid(u));
+    o.t[i] = from_float<T>(u);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *reinterpret_cast<P*>(tail + (int64_t)k * p.C) = r[k + 1];
+  *out = o;
+}
+
+// ------------------------------------------------------------------------------ host
+
+bool al(const void* p, uintptr_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; }
+int elem_size(int dtype) { return dtype == GDN_DTYPE_FP32 ? 4 : 2; }
+
+int check_device(const void* anchor, const void* const* ptrs, int n, DeviceGuard& guard) {
+  int dev = 0;
+  if (device_of(anchor, ptrs, n, &dev) != kOk) return GDN_ERR_INVALID_ARG;
+  if (!guard.set(dev)) return GDN_ERR_CUDA;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  return major == 10 && minor == 3 ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+int check_kind(int dtype, int activation) {
+  if (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_FP16 && dtype != GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED;
+  return activation == GDN_ACT_NONE || activation == GDN_ACT_SILU ? GDN_OK : GDN_ERR_UNSUPPORTED;
+}
+
+// Block counts and the token loops' bounds stay within 31 bits.
+bool sizes_ok(int N, int T, int C) {
+  return N >= 1 && N <= (1 << 30) && T >= 0 && T <= INT32_MAX - 4096 && C >= 8 && C <= (1 << 24) && C % 8 == 0 &&
+         (int64_t)T * C <= ((int64_t)1 << 40);
+}
+
+// The elements between two tokens: 0 = contiguous; rows start on 16 bytes.
+bool stride_ok(int64_t* s, int C, int dtype) {
+  if (*s == 0) *s = C;
+  return *s >= C && *s <= ((int64_t)1 << 40) && *s * elem_size(dtype) % 16 == 0;
+}
+
+int check_packed(ActParams* p, int dtype, const void* workspace) {
+  if (!sizes_ok(p->N, p->T, p->C) || p->n_init < 0) return GDN_ERR_INVALID_ARG;
+  if (!p->cu || !p->w || !workspace || (p->T > 0 && !p->x) || (p->n_init > 0 && !p->conv_init)) return GDN_ERR_INVALID_ARG;
+  if (!stride_ok(&p->sx, p->C, dtype) || !stride_ok(&p->sdy, p->C, dtype)) return GDN_ERR_INVALID_ARG;
+  if (!al(p->x, 16) || !al(p->dy, 16) || !al(p->w, 16) || !al(p->conv_init, 16) || !al(workspace, 256) || !al(p->bias, 4) ||
+      !al(p->cu, 4) || !al(p->init_idx, 4))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+template <typename F>
+void by_type(int dtype, F f) {
+  if (dtype == GDN_DTYPE_BF16)
+    f(__nv_bfloat16{});
+  else if (dtype == GDN_DTYPE_FP16)
+    f(__half{});
+  else
+    f(float{});
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" size_t gdn_conv_act_workspace_size(int N, int T, int C, int backward) {
+  if (!gdn::sizes_ok(N, T, C)) return 0;
+  return gdn::act_layout(N, T, C, backward != 0).total;
+}
+
+extern "C" int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w, const float* bias,
+                                const int32_t* cu_seqlens, int N, int T, int C, int dtype, int activation,
+                                const int32_t* init_idx, const void* conv_init, int n_init, void* y, void* final_tail,
+                                void* workspace, size_t ws_bytes, gdn_stream_t stream) {
+  using namespace gdn;
+  int rc = check_kind(dtype, activation);
+  if (rc != GDN_OK) return rc;
+  ActParams p{};
+  p.x = x, p.sx = x_stride, p.w = w, p.bias = bias, p.cu = cu_seqlens, p.init_idx = init_idx, p.conv_init = conv_init;
+  p.N = N, p.T = T, p.C = C, p.n_init = n_init, p.silu = activation == GDN_ACT_SILU, p.y = y, p.tail = final_tail;
+  if ((rc = check_packed(&p, dtype, workspace)) != GDN_OK) return rc;
+  if (!final_tail || (T > 0 && !y) || !al(y, 16) || !al(final_tail, 16)) return GDN_ERR_INVALID_ARG;
+  const ActLayout L = act_layout(N, T, C, false);
+  if (ws_bytes < L.total) return GDN_ERR_WORKSPACE;
+  const void* ptrs[] = {x, w, bias, cu_seqlens, init_idx, conv_init, y, final_tail};
+  DeviceGuard guard;
+  if ((rc = check_device(workspace, ptrs, (int)(sizeof(ptrs) / sizeof(ptrs[0])), guard)) != GDN_OK) return rc;
+  p.hd = static_cast<ActHeader*>(workspace);
+  p.n_tb = L.n_tb;
+  cudaStream_t s = (cudaStream_t)stream;
+  launch_early(act_check_kernel, dim3(1), 256, 0, s, p);
+  by_type(dtype, [&](auto t) {
+    using T_ = decltype(t);
+    const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+    launch_early(act_fwd_kernel<T_>, dim3((unsigned)(L.n_tb + N), cb), kActThreads, 0, s, p);
+  });
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w, const float* bias,
+                                const int32_t* cu_seqlens, int N, int T, int C, int dtype, int activation,
+                                const int32_t* init_idx, const void* conv_init, int n_init, const void* dy,
+                                int64_t dy_stride, const float* dfinal_tail, float* dx, float* dw, float* dbias,
+                                float* dconv_init, void* workspace, size_t ws_bytes, gdn_stream_t stream) {
+  using namespace gdn;
+  int rc = check_kind(dtype, activation);
+  if (rc != GDN_OK) return rc;
+  ActParams p{};
+  p.x = x, p.sx = x_stride, p.w = w, p.bias = bias, p.cu = cu_seqlens, p.init_idx = init_idx, p.conv_init = conv_init;
+  p.N = N, p.T = T, p.C = C, p.n_init = n_init, p.silu = activation == GDN_ACT_SILU, p.dy = dy, p.sdy = dy_stride;
+  p.dtail = dfinal_tail, p.dx = dx, p.dw = dw, p.dbias = dbias, p.dinit = dconv_init;
+  if ((rc = check_packed(&p, dtype, workspace)) != GDN_OK) return rc;
+  if (!dw || (T > 0 && (!dy || !dx)) || (n_init > 0 && !dconv_init)) return GDN_ERR_INVALID_ARG;
+  if (!al(dx, 16) || !al(dw, 4) || !al(dbias, 4) || !al(dfinal_tail, 4) || !al(dconv_init, 4)) return GDN_ERR_INVALID_ARG;
+  const ActLayout L = act_layout(N, T, C, true);
+  if (ws_bytes < L.total) return GDN_ERR_WORKSPACE;
+  const void* ptrs[] = {x, w, bias, cu_seqlens, init_idx, conv_init, dy, dfinal_tail, dx, dw, dbias, dconv_init};
+  DeviceGuard guard;
+  if ((rc = check_device(workspace, ptrs, (int)(sizeof(ptrs) / sizeof(ptrs[0])), guard)) != GDN_OK) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.hd = reinterpret_cast<ActHeader*>(ws + L.header);
+  p.dstart = reinterpret_cast<float*>(ws + L.dstart);
+  p.dend = reinterpret_cast<float*>(ws + L.dend);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.n_tb = L.n_tb;
+  cudaStream_t s = (cudaStream_t)stream;
+  launch_early(act_check_kernel, dim3(1), 256, 0, s, p);
+  if (T > 0)
+    by_type(dtype, [&](auto t) {
+      using T_ = decltype(t);
+      const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+      launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kActThreads, 0, s, p);
+    });
+  launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32)), 256, 0, s, p);
+  if (dfinal_tail || init_idx)
+    launch_early(act_ends_kernel, dim3((unsigned)((C + 255) / 256), (unsigned)(N < 64 ? N : 64)), 256, 0, s, p);
+  if (n_init > 0) {
+    const int64_t n = (int64_t)n_init * 3 * C;
+    if (n > (int64_t)256 * INT32_MAX) return GDN_ERR_INVALID_ARG;
+    launch_early(act_pool_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, s, p);
+  }
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const float* bias, int B, int C,
+                                    int dtype, int activation, const int32_t* state_idx, void* tail_pool, int n_pool,
+                                    void* y, int32_t* status, gdn_stream_t stream) {
+  using namespace gdn;
+  int rc = check_kind(dtype, activation);
+  if (rc != GDN_OK) return rc;
+  if (B < 0 || B > 65535 || C < 8 || C > (1 << 24) || C % 8 != 0 || n_pool < 0) return GDN_ERR_INVALID_ARG;
+  if (!stride_ok(&x_stride, C, dtype)) return GDN_ERR_INVALID_ARG;
+  if (B == 0) return GDN_OK;
+  if (!x || !w || !state_idx || !tail_pool || !y || n_pool == 0) return GDN_ERR_INVALID_ARG;
+  if (!al(x, 16) || !al(w, 16) || !al(tail_pool, 16) || !al(y, 16) || !al(bias, 4) || !al(state_idx, 4) || !al(status, 4))
+    return GDN_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, w, bias, state_idx, y, status};
+  DeviceGuard guard;
+  if ((rc = check_device(tail_pool, ptrs, (int)(sizeof(ptrs) / sizeof(ptrs[0])), guard)) != GDN_OK) return rc;
+  const StepParams p{x, x_stride, w, bias, state_idx, tail_pool, y, status, B, C, n_pool, activation == GDN_ACT_SILU};
+  by_type(dtype, [&](auto t) {
+    using T_ = decltype(t);
+    const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+    act_step_kernel<T_><<<dim3(cb, (unsigned)B), kActThreads, 0, (cudaStream_t)stream>>>(p);
+  });
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}

@@ -1,0 +1,1082 @@
+// Selective scan over packed documents, forward and backward (sm_103a). Per channel c with states s (group g of the
+// maps b, c: channel / (channels / groups)):
+//     dt = softplus(raw + dt_bias),  h_t = exp(dt_t a) h_{t-1} + dt_t x_t b_t,  y_t = sum_s c_t h_t + skip x_t,
+//     out = y silu(z)
+// with a decay for each channel and state and a step for each token and channel, so that a token's map has no
+// low-rank form to put on the tensor cores: the walk is fp32 arithmetic, an exponential, two products and two
+// multiply-adds for each token, channel and state.
+//
+// Documents are cut into segments so that a long one fills the GPU. The first walk leaves each segment's end state
+// from zero and its summed time; the scan kernel makes start states of them (exp(a sum dt) carries a state across a
+// segment); the second walk starts from those. A document of one segment is walked once. Backward, with k_t the
+// gradient of h_t:
+//     k_t = c_t dy_t + exp(dt_{t+1} a) k_{t+1},  dc = dy h,  db = dt x k,  du = sum_s k b  (u = dt x),
+//     d dt = x du + sum_s a k exp(dt a) h_{t-1},  da = sum_t dt k exp(dt a) h_{t-1}
+// the first walk also leaves the gradient of each segment's start state for a zero gradient behind it
+// (sum_t exp(a (dt_1 + .. + dt_t)) c_t dy_t, formed forward in time) and the state at every 16th token, so that the
+// walk in reverse needs no state but a tile's.
+//
+// Every sum has a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gdn.h"
+#include "bw_prims.cuh"
+#include "elem.cuh"
+#include "gdn_common.cuh"
+#include "gdn_host.h"
+#include "gdn_ssm.h"
+
+namespace gdn {
+namespace {
+
+using bw::f2_fma;
+using bw::f2_hi;
+using bw::f2_lo;
+using bw::f2_mul;
+using bw::f2_pack;
+using bw::f2_sum;
+
+constexpr int kPlanThreads = 1024;
+
+struct SsmParams {
+  const void *x, *dt, *z, *b, *c, *dout;
+  int64_t sx, sdt, sz, sb, sc, sdo;  // elements between tokens
+  const float *a, *skip, *dt_bias, *init;
+  const int32_t *cu, *init_idx;
+  int N, T, C, S, G, n_init, softplus, dtype;
+  void* out;
+  float* final_state;
+  // backward
+  const float* dfinal;
+  void *dx, *ddt, *dz, *db, *dc;
+  float *da, *dskip, *dbias, *dinit;
+  // workspace
+  SsmHeader* hd;
+  SsmSeg* segs;
+  int32_t *seg0, *is_src;
+  float *maps, *slot, *sums, *slot_r, *ckpt, *csum, *dstart, *facc, *part_a, *part_c, *part_m;
+  int64_t smax;
+  int parts, seg_tokens, bwd;
+};
+
+// ------------------------------------------------------------------------------ planner, maps in fp32
+
+template <typename T>
+__device__ void maps_to_float(const SsmParams& p, int block, int blocks) {
+  const int Sp = ssm_padded(p.S), row = p.G * 2 * Sp;
+  const int64_t n = (int64_t)p.T * row;
+  for (int64_t i = (int64_t)block * blockDim.x + threadIdx.x; i < n; i += (int64_t)blocks * blockDim.x) {
+    const int64_t t = i / row;
+    const int r = (int)(i - t * row), g = r / (2 * Sp), m = r % (2 * Sp) / Sp, s = r % Sp;
+    float v = 0.f;
+    if (s < p.S)
+      v = m == 0 ? to_float(static_cast<const T*>(p.b)[t * p.sb + g * p.S + s])
+                 : to_float(static_cast<const T*>(p.c)[t * p.sc + g * p.S + s]);
+    p.maps[i] = v;
+  }
+}
+
+// Block 0: checks cu_seqlens and init_idx and cuts the documents into segments of at most seg_tokens. The others:
+// the maps b and c in fp32, [T][G][2][Sp], zero behind the last state.
+__global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_constant__ SsmParams p) {
+  bw::griddep_wait();  // the call before on this stream may still read the workspace
+  bw::griddep_launch_dependents();
+  if (blockIdx.x > 0) {
+    if (p.dtype == GDN_DTYPE_BF16)
+      maps_to_float<__nv_bfloat16>(p, blockIdx.x - 1, gridDim.x - 1);
+    else if (p.dtype == GDN_DTYPE_FP16)
+      maps_to_float<__half>(p, blockIdx.x - 1, gridDim.x - 1);
+    else
+      maps_to_float<float>(p, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  __shared__ int s_warp[32], s_base, s_bad, s_forks;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (tid == 0) s_base = s_bad = s_forks = 0;
+  for (int i = tid; i < p.N; i += kPlanThreads) p.is_src[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < p.N; i += kPlanThreads) {
+    const int b = p.cu[i], e = p.cu[i + 1];
+    bool bad = b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T);
+    if (p.init_idx) {
+      const int x = p.init_idx[i];
+      if (x < -1 || (x >= p.n_init && x - p.n_init >= i)) {
+        bad = true;
+      } else if (x >= p.n_init) {
+        p.is_src[x - p.n_init] = 1;
+        s_forks = 1;
+      }
+    }
+    if (bad) s_bad = 1;
+  }
+  __syncthreads();
+  if (s_bad) {
+    if (tid == 0) {
+      p.hd->status = kErrInvalid;
+      p.hd->n_segs = 0;
+    }
+    return;
+  }
+  const int L = p.seg_tokens;
+  for (int i0 = 0; i0 < p.N; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int n = 0, k = 0, t0 = 0;
+    if (i < p.N) {
+      t0 = p.cu[i];
+      n = p.cu[i + 1] - t0;
+      k = (n + L - 1) / L;
+    }
+    int upto = k;  // inclusive sum over the warp, then over the block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) s_warp[wid] = upto;
+    __syncthreads();
+    if (wid == 0) {
+      int v = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+      }
+      s_warp[lane] = v;
+    }
+    __syncthreads();
+    const int at = s_base + upto - k + (wid ? s_warp[wid - 1] : 0);
+    if (i < p.N) {
+      p.seg0[i] = at;
+      const int src = p.init_idx ? p.init_idx[i] : -1;
+      // equal segments, in whole tiles
+      const int len = k ? ((n + k - 1) / k + kSsmTile - 1) / kSsmTile * kSsmTile : 0;
+      for (int j = 0; j < k; ++j) {
+        SsmSeg s;
+        s.doc = i;
+        s.tok0 = t0 + min(n, j * len);
+        s.ntok = min(n, (j + 1) * len) - min(n, j * len);
+        s.first = j == 0;
+        s.last = j == k - 1;
+        s.src = j > 0 || src >= p.n_init ? -2 : src;
+        s.need = p.bwd || j < k - 1 || p.is_src[i];
+        s.pad = 0;
+        p.segs[at + j] = s;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) s_base += s_warp[31];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.seg0[p.N] = s_base;
+    p.hd->n_segs = s_base;
+    p.hd->forks = s_forks;
+    p.hd->status = 0;
+  }
+}
+
+// ------------------------------------------------------------------------------ walks forward in time
+
+enum { kWalkState = 0, kWalkOut = 1, kWalkGrad = 2 };
+
+__device__ __forceinline__ void cp_async16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(bw::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+// The state that document `src` (encoded as init_idx's pool entries) starts from, for four states of a channel.
+__device__ __forceinline__ float4 pool_quad(const float* pool, int64_t entry, int C, int S, int c, int q) {
+  const float* h = pool + (entry * C + c) * S + 4 * q;
+  float4 v;
+  v.x = 4 * q < S ? h[0] : 0.f;
+  v.y = 4 * q + 1 < S ? h[1] : 0.f;
+  v.z = 4 * q + 2 < S ? h[2] : 0.f;
+  v.w = 4 * q + 3 < S ? h[3] : 0.f;
+  return v;
+}
+__device__ __forceinline__ void store_quad(float* pool, int64_t entry, int C, int S, int c, int q, float4 v) {
+  float* h = pool + (entry * C + c) * S + 4 * q;
+  if (4 * q < S) h[0] = v.x;
+  if (4 * q + 1 < S) h[1] = v.y;
+  if (4 * q + 2 < S) h[2] = v.z;
+  if (4 * q + 3 < S) h[3] = v.w;
+}
+
+// A warp walks one segment for 32 kDt / kNl channels: kNl lanes share a channel, each lane holds kNt states of kDt
+// channels in registers, pairs of states in packed fp32. kWalkState leaves the end state from zero and the summed
+// time; kWalkGrad also the states at each tile and the start state's gradient; kWalkOut the outputs.
+template <typename T, int kSp, int kMode, bool kVec>
+__global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_constant__ SsmParams p) {
+  constexpr int kNl = kSp == 64 ? 2 : 1, kNt = kSp / kNl, kDt = kSp <= 16 ? 2 : 1, kCh = 32 / kNl * kDt;
+  constexpr int kTb = kMode == kWalkGrad ? 4 : 8;  // tokens in flight while the ones before are worked on
+  constexpr int kQt = kNt / 4, kQ = kSp / 4;
+  constexpr bool kGate = kMode != kWalkState;  // z is read
+  static_assert(kCh == 64 || kCh == 32 || kCh == 16);
+  __shared__ __align__(16) float s_maps[kSsmWarps][2][kTb][2 * kSp];
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, nl = lane % kNl, dl = lane / kNl;
+  const int Cg = p.C / p.G, nb = (Cg + kCh - 1) / kCh, blocks = nb * p.G;
+  const int64_t items = (int64_t)p.hd->n_segs * blocks;
+  const bool has_z = kGate && p.z != nullptr;
+  for (int64_t item = (int64_t)blockIdx.x * kSsmWarps + wid; item < items; item += (int64_t)gridDim.x * kSsmWarps) {
+    const int seg = (int)(item / blocks), blk = (int)(item % blocks), g = blk / nb;
+    const SsmSeg sg = p.segs[seg];
+    if (kMode == kWalkState && !sg.need) continue;
+    const int cg = (blk % nb) * kCh + dl * kDt;  // channel in its group
+    const int nch = max(0, min(kDt, Cg - cg));
+    const int c0 = g * Cg + min(cg, Cg - 1);     // a channel that exists
+    uint64_t A[kDt][kNt / 2], h[kDt][kNt / 2], ga[kMode == kWalkGrad ? kDt : 1][kNt / 2], pr[kMode == kWalkGrad ? kDt : 1][kNt / 2];
+    float bias[kDt], skip[kDt], total[kDt];
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+      const int c = min(c0 + d, g * Cg + Cg - 1);
+      bias[d] = p.dt_bias ? p.dt_bias[c] : 0.f;
+      skip[d] = kMode == kWalkOut && p.skip ? p.skip[c] : 0.f;
+      total[d] = 0.f;
+#pragma unroll
+      for (int q = 0; q < kQt; ++q) {
+        const int qq = nl * kQt + q;
+        const float4 av = pool_quad(p.a, 0, p.C, p.S, c, qq);
+        A[d][2 * q] = f2_pack(av.x * kLog2e, av.y * kLog2e);
+        A[d][2 * q + 1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
+        float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kMode == kWalkOut) {
+          if (sg.src >= 0)
+            hv = pool_quad(p.init, sg.src, p.C, p.S, c, qq);
+          else if (sg.src == -2)
+            hv = *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + qq) * p.C + c) * 4);
+        }
+        h[d][2 * q] = f2_pack(hv.x, hv.y);
+        h[d][2 * q + 1] = f2_pack(hv.z, hv.w);
+        if constexpr (kMode == kWalkGrad) {
+          ga[d][2 * q] = ga[d][2 * q + 1] = 0;
+          pr[d][2 * q] = pr[d][2 * q + 1] = f2_pack(1.f, 1.f);
+        }
+      }
+    }
+    const T* xs = static_cast<const T*>(p.x) + c0;
+    const T* ds = static_cast<const T*>(p.dt) + c0;
+    const T* zs = static_cast<const T*>(p.z) + c0;
+    const T* os = static_cast<const T*>(p.dout) + c0;
+    using P = Pack<T, kDt>;
+    P xr[kTb], dr[kTb], zr[kGate ? kTb : 1], gr[kMode == kWalkGrad ? kTb : 1];
+    auto fetch = [&](int i0) {  // the inputs of tokens i0 .. i0 + kTb - 1 of the segment
+#pragma unroll
+      for (int k = 0; k < kTb; ++k) {
+        const int64_t t = sg.tok0 + i0 + k;
+        const int n = i0 + k < sg.ntok ? nch : 0;
+        xr[k] = load_pack<T, kDt, kVec>(xs + t * p.sx, n);
+        dr[k] = load_pack<T, kDt, kVec>(ds + t * p.sdt, n);
+        if constexpr (kGate) {
+          if (has_z) zr[k] = load_pack<T, kDt, kVec>(zs + t * p.sz, n);
+        }
+        if constexpr (kMode == kWalkGrad) gr[k] = load_pack<T, kDt, kVec>(os + t * p.sdo, n);
+      }
+    };
+    auto fetch_maps = [&](int i0, int buf) {
+      const int n = min(kTb, sg.ntok - i0) * (2 * kSp / 4);
+      for (int i = lane; i < n; i += 32) {
+        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
+        cp_async16(&s_maps[wid][buf][k][4 * r], p.maps + (((int64_t)sg.tok0 + i0 + k) * p.G + g) * 2 * kSp + 4 * r);
+      }
+      cp_async_commit();
+    };
+    fetch(0);
+    fetch_maps(0, 0);
+    for (int i0 = 0, it = 0; i0 < sg.ntok; i0 += kTb, ++it) {
+      if constexpr (kMode == kWalkGrad) {
+        if (i0 % kSsmTile == 0 && nch > 0) {
+          const int64_t tile = sg.tok0 / kSsmTile + seg + i0 / kSsmTile;
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) {
+            if (d >= nch) break;
+#pragma unroll
+            for (int q = 0; q < kQt; ++q)
+              *reinterpret_cast<float4*>(p.ckpt + ((tile * kQ + nl * kQt + q) * p.C + c0 + d) * 4) =
+                  make_float4(f2_lo(h[d][2 * q]), f2_hi(h[d][2 * q]), f2_lo(h[d][2 * q + 1]), f2_hi(h[d][2 * q + 1]));
+            if (nl == 0) p.csum[tile * p.C + c0 + d] = total[d];
+          }
+        }
+      }
+      P xc[kTb], dc[kTb], zc[kGate ? kTb : 1], gc[kMode == kWalkGrad ? kTb : 1];
+#pragma unroll
+      for (int k = 0; k < kTb; ++k) {
+        xc[k] = xr[k];
+        dc[k] = dr[k];
+        if constexpr (kGate) zc[k] = zr[k];
+        if constexpr (kMode == kWalkGrad) gc[k] = gr[k];
+      }
+      if (i0 + kTb < sg.ntok) {
+        fetch(i0 + kTb);
+        fetch_maps(i0 + kTb, (it + 1) & 1);
+        cp_async_wait<1>();
+      } else {
+        cp_async_wait<0>();
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kTb; ++k) {
+        if (i0 + k >= sg.ntok) break;
+        const float* mp = s_maps[wid][it & 1][k];
+        float delta[kDt], u[kDt], y[kDt], dy[kDt];
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) {
+          const float raw = to_float(dc[k].t[d]) + bias[d];
+          delta[d] = p.softplus ? softplus(raw) : raw;
+          u[d] = delta[d] * to_float(xc[k].t[d]);
+          total[d] += delta[d];
+          if constexpr (kMode == kWalkGrad) {
+            dy[d] = to_float(gc[k].t[d]);
+            if (has_z) {
+              const float zv = to_float(zc[k].t[d]);
+              dy[d] *= silu_of(zv, sigmoid(zv));
+            }
+          }
+        }
+        uint64_t y2[kDt];
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) y2[d] = 0;
+#pragma unroll
+        for (int q = 0; q < kQt; ++q) {
+          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(mp + nl * kNt + 4 * q);
+          ulonglong2 cv;
+          if (kMode != kWalkState) cv = *reinterpret_cast<const ulonglong2*>(mp + kSp + nl * kNt + 4 * q);
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) {
+            const uint64_t dd = f2_pack(delta[d], delta[d]), uu = f2_pack(u[d], u[d]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint64_t arg = f2_mul(dd, A[d][2 * q + j]);
+              const uint64_t e = f2_pack(exp2_approx(f2_lo(arg)), exp2_approx(f2_hi(arg)));
+              h[d][2 * q + j] = f2_fma(e, h[d][2 * q + j], f2_mul(uu, j ? bv.y : bv.x));
+              if constexpr (kMode == kWalkOut) y2[d] = f2_fma(h[d][2 * q + j], j ? cv.y : cv.x, y2[d]);
+              if constexpr (kMode == kWalkGrad) {
+                pr[d][2 * q + j] = f2_mul(pr[d][2 * q + j], e);
+                ga[d][2 * q + j] = f2_fma(pr[d][2 * q + j], f2_mul(f2_pack(dy[d], dy[d]), j ? cv.y : cv.x), ga[d][2 * q + j]);
+              }
+            }
+          }
+        }
+        if constexpr (kMode == kWalkOut) {
+          P r;
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) {
+            y[d] = f2_sum(y2[d]);
+            if constexpr (kNl == 2) y[d] += __shfl_xor_sync(0xffffffffu, y[d], 1);
+            y[d] = fmaf(skip[d], to_float(xc[k].t[d]), y[d]);
+            if (has_z) {
+              const float zv = to_float(zc[k].t[d]);
+              y[d] *= silu_of(zv, sigmoid(zv));
+            }
+            r.t[d] = from_float<T>(y[d]);
+          }
+          if (nl == 0 && nch > 0)
+            store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + ((int64_t)sg.tok0 + i0 + k) * p.C + c0, r, nch);
+        }
+      }
+      __syncwarp();  // the buffer is free
+    }
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+      if (d >= nch) break;
+      if (kMode != kWalkOut && nl == 0) p.sums[(int64_t)seg * p.C + c0 + d] = total[d];
+#pragma unroll
+      for (int q = 0; q < kQt; ++q) {
+        const int qq = nl * kQt + q;
+        const float4 hv = make_float4(f2_lo(h[d][2 * q]), f2_hi(h[d][2 * q]), f2_lo(h[d][2 * q + 1]), f2_hi(h[d][2 * q + 1]));
+        if constexpr (kMode == kWalkOut) {
+          if (sg.last) store_quad(p.final_state, sg.doc, p.C, p.S, c0 + d, qq, hv);
+        } else {
+          *reinterpret_cast<float4*>(p.slot + (((int64_t)seg * kQ + qq) * p.C + c0 + d) * 4) = hv;
+        }
+        if constexpr (kMode == kWalkGrad)
+          *reinterpret_cast<float4*>(p.slot_r + (((int64_t)seg * kQ + qq) * p.C + c0 + d) * 4) = make_float4(
+              f2_lo(ga[d][2 * q]), f2_hi(ga[d][2 * q]), f2_lo(ga[d][2 * q + 1]), f2_hi(ga[d][2 * q + 1]));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ scan over segments
+
+__device__ __forceinline__ float4 carry(float4 a, float time, float4 h, float4 add) {
+  return make_float4(fmaf(exp2_approx(a.x * time), h.x, add.x), fmaf(exp2_approx(a.y * time), h.y, add.y),
+                     fmaf(exp2_approx(a.z * time), h.z, add.z), fmaf(exp2_approx(a.w * time), h.w, add.w));
+}
+
+// Start states of the segments from their end states, in place; final states of empty documents and of those that
+// others fork from; in the backward the gradients behind the segments from those before them, and each document's
+// start-state gradient. A thread takes four states of a channel through the documents: all of them in order where
+// some fork, else the ones of blockIdx.y.
+__global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int Sp = ssm_padded(p.S), Q = Sp / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)Q * p.C) return;
+  const int q = (int)(i / p.C), c = (int)(i % p.C);
+  const bool forks = p.hd->forks != 0;
+  if (forks && blockIdx.y > 0) return;
+  const int step = forks ? 1 : gridDim.y, d0 = forks ? 0 : blockIdx.y;
+  const int64_t state = (int64_t)Q * p.C * 4;
+  float4 a = pool_quad(p.a, 0, p.C, p.S, c, q);
+  a = make_float4(a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e);
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  // final states of documents that others fork from: the output in the forward, the workspace in the backward
+  auto fin = [&](int d) { return reinterpret_cast<float4*>(p.dstart + d * state + i * 4); };
+  for (int d = d0; d < p.N; d += step) {
+    const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
+    const int src = p.init_idx ? p.init_idx[d] : -1;
+    const bool fork = src >= p.n_init && p.init_idx;
+    if (!p.bwd && s1 - s0 == 1 && !fork && !p.is_src[d]) continue;
+    float4 h = zero;
+    if (fork)
+      h = p.bwd ? *fin(src - p.n_init) : pool_quad(p.final_state, src - p.n_init, p.C, p.S, c, q);
+    else if (src >= 0)
+      h = pool_quad(p.init, src, p.C, p.S, c, q);
+    const int se = p.is_src[d] ? s1 : s1 - 1;  // the last segment's end state is wanted for forks only
+    for (int s = s0; s < s1; ++s) {
+      float4* at = reinterpret_cast<float4*>(p.slot + s * state + i * 4);
+      float4 e = zero;
+      float time = 0.f;
+      if (s < se) {
+        e = *at;
+        time = p.sums[(int64_t)s * p.C + c];
+      }
+      *at = h;
+      if (s < se) h = carry(a, time, h, e);
+    }
+    if (p.bwd) {
+      if (p.is_src[d]) *fin(d) = h;
+    } else if (s1 == s0 || p.is_src[d]) {
+      store_quad(p.final_state, d, p.C, p.S, c, q, h);
+    }
+  }
+  if (!p.bwd) return;
+  auto facc = [&](int d) { return reinterpret_cast<float4*>(p.facc + d * state + i * 4); };
+  if (forks)
+    for (int d = 0; d < p.N; ++d) *facc(d) = zero;
+  const int dn = forks ? p.N - 1 : d0 + (p.N - 1 - d0) / step * step;
+  for (int d = dn; d >= 0; d -= step) {
+    const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
+    const int src = p.init_idx ? p.init_idx[d] : -1;
+    float4 k = p.dfinal ? pool_quad(p.dfinal, d, p.C, p.S, c, q) : zero;
+    if (forks) {
+      const float4 f = *facc(d);
+      k = make_float4(k.x + f.x, k.y + f.y, k.z + f.z, k.w + f.w);
+    }
+    for (int s = s1 - 1; s >= s0; --s) {
+      float4* at = reinterpret_cast<float4*>(p.slot_r + s * state + i * 4);
+      const float4 e = *at;
+      const float time = p.sums[(int64_t)s * p.C + c];
+      *at = k;
+      k = carry(a, time, k, e);
+    }
+    *fin(d) = k;  // its final state has been read by every fork
+    if (src >= p.n_init && p.init_idx) {
+      float4* f = facc(src - p.n_init);
+      *f = make_float4(f->x + k.x, f->y + k.y, f->z + k.z, f->w + k.w);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ walk of the backward
+
+// A CTA of four warps walks a segment in reverse, tile by tile, each warp for 4 * 32 / kNl channels: a lane holds four
+// states of four channels, kNl = kSp / 4 lanes share a channel. Within a tile the states go forward again from the
+// kept one, every fourth of them through shared memory; four tokens at a time come back in reverse.
+template <int kSp>
+struct GradSmem {
+  static constexpr int kNl = kSp / 4, kDl = 32 / kNl, kCh = 4 * kDl;
+  float maps[kSsmTile][2 * kSp];
+  float part[kSsmWarps][kSsmTile][2 * kSp];  // db and dc of each warp's channels
+  float delta[kSsmWarps][kSsmTile][kCh];
+  float u[kSsmWarps][kSsmTile][kCh];         // then du
+  float dy[kSsmWarps][kSsmTile][kCh];        // then sum_s a k exp(dt a) h_{t-1}
+  float y[kSsmWarps][kSsmTile][kCh];
+  float4 keep[kSsmWarps][kSsmTile / 4][4][32];
+};
+
+template <typename T, int kSp, bool kVec>
+__global__ void __launch_bounds__(32 * kSsmWarps) ssm_grad_kernel(const __grid_constant__ SsmParams p) {
+  using Smem = GradSmem<kSp>;
+  constexpr int kNl = Smem::kNl, kCh = Smem::kCh, kQ = kSp / 4, kTb = kSsmTile;
+  extern __shared__ __align__(16) uint8_t raw_smem[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
+  bw::griddep_wait();
+  bw::griddep_launch_dependents();
+  if (p.hd->status != 0) return;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, nl = lane % kNl, dl = lane / kNl;
+  const int Cg = p.C / p.G, blocks = p.parts * p.G;
+  const int64_t items = (int64_t)p.hd->n_segs * blocks;
+  const bool has_z = p.z != nullptr;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int seg = (int)(item / blocks), blk = (int)(item % blocks), g = blk / p.parts, part = blk % p.parts;
+    const SsmSeg sg = p.segs[seg];
+    const int cb = (part * kSsmWarps + wid) * kCh;  // this warp's first channel in the group
+    const int cg = cb + 4 * dl;                     // this lane's
+    const int nch = max(0, min(4, Cg - cg));
+    const int c0 = g * Cg + min(cg, Cg - 1);
+    float A[4][4], K[4][4], dA[4][4], h0[4][4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int c = min(c0 + d, g * Cg + Cg - 1);
+      const float4 av = pool_quad(p.a, 0, p.C, p.S, c, nl);
+      const int64_t at = (((int64_t)seg * kQ + nl) * p.C + c) * 4;
+      const float4 kv = *reinterpret_cast<const float4*>(p.slot_r + at);
+      float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (sg.src >= 0)
+        hv = pool_quad(p.init, sg.src, p.C, p.S, c, nl);
+      else if (sg.src == -2)
+        hv = *reinterpret_cast<const float4*>(p.slot + at);
+      A[d][0] = av.x, A[d][1] = av.y, A[d][2] = av.z, A[d][3] = av.w;
+      K[d][0] = kv.x, K[d][1] = kv.y, K[d][2] = kv.z, K[d][3] = kv.w;
+      h0[d][0] = hv.x, h0[d][1] = hv.y, h0[d][2] = hv.z, h0[d][3] = hv.w;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) dA[d][n] = 0.f;
+    }
+    // for loads and stores a lane takes four channels of every (32 / (kCh / 4))th token
+    constexpr int kLq = kCh / 4, kLt = 32 / kLq;
+    const int lq = lane % kLq, lt = lane / kLq;
+    const int lcg = cb + 4 * lq, ln = max(0, min(4, Cg - lcg)), lc0 = g * Cg + min(lcg, Cg - 1);
+    float bias[4], skip[4], dskip[4] = {0.f, 0.f, 0.f, 0.f}, dbias[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = min(lc0 + j, g * Cg + Cg - 1);
+      bias[j] = p.dt_bias ? p.dt_bias[c] : 0.f;
+      skip[j] = p.skip ? p.skip[c] : 0.f;
+    }
+    const int tiles = (sg.ntok + kTb - 1) / kTb;
+    for (int tile = tiles - 1; tile >= 0; --tile) {
+      const int64_t t0 = sg.tok0 + tile * kTb;
+      const int nt = min(kTb, sg.ntok - tile * kTb);
+      for (int i = threadIdx.x; i < kTb * 2 * kSp / 4; i += 32 * kSsmWarps) {
+        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < nt) v = *reinterpret_cast<const float4*>(p.maps + ((t0 + k) * p.G + g) * 2 * kSp + 4 * r);
+        reinterpret_cast<float4*>(sm.maps[k])[r] = v;
+      }
+      for (int k = lt; k < kTb; k += kLt) {
+        float dv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f}, gv[4] = {0.f, 0.f, 0.f, 0.f};
+        if (k < nt) {
+          const int64_t t = t0 + k;
+          const auto xr = load_pack<T, 4, kVec>(static_cast<const T*>(p.x) + t * p.sx + lc0, ln);
+          const auto dr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dt) + t * p.sdt + lc0, ln);
+          const auto gr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dout) + t * p.sdo + lc0, ln);
+          Pack<T, 4> zr{};
+          if (has_z) zr = load_pack<T, 4, kVec>(static_cast<const T*>(p.z) + t * p.sz + lc0, ln);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float raw = to_float(dr.t[j]) + bias[j];
+            dv[j] = p.softplus ? softplus(raw) : raw;
+            uv[j] = dv[j] * to_float(xr.t[j]);
+            gv[j] = to_float(gr.t[j]);
+            if (has_z) {
+              const float zv = to_float(zr.t[j]);
+              gv[j] *= silu_of(zv, sigmoid(zv));
+            }
+          }
+        }
+        *reinterpret_cast<float4*>(&sm.delta[wid][k][4 * lq]) = make_float4(dv[0], dv[1], dv[2], dv[3]);
+        *reinterpret_cast<float4*>(&sm.u[wid][k][4 * lq]) = make_float4(uv[0], uv[1], uv[2], uv[3]);
+        *reinterpret_cast<float4*>(&sm.dy[wid][k][4 * lq]) = make_float4(gv[0], gv[1], gv[2], gv[3]);
+      }
+      __syncthreads();
+      auto row4 = [&](const float* r, float* v) {
+        const float4 f = *reinterpret_cast<const float4*>(r);
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      };
+      float h[4][4];
+      {
+        const int64_t tl = sg.tok0 / kSsmTile + seg + tile;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int c = min(c0 + d, g * Cg + Cg - 1);
+          const float time = p.csum[tl * p.C + c] * kLog2e;
+          const float4 f = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
+          h[d][0] = fmaf(exp2_approx(A[d][0] * time), h0[d][0], f.x);
+          h[d][1] = fmaf(exp2_approx(A[d][1] * time), h0[d][1], f.y);
+          h[d][2] = fmaf(exp2_approx(A[d][2] * time), h0[d][2], f.z);
+          h[d][3] = fmaf(exp2_approx(A[d][3] * time), h0[d][3], f.w);
+        }
+      }
+      // one token forward: h = e h + u b
+      auto forward = [&](int k) {
+        float dv[4], uv[4], bv[4];
+        row4(&sm.delta[wid][k][4 * dl], dv);
+        row4(&sm.u[wid][k][4 * dl], uv);
+        row4(&sm.maps[k][4 * nl], bv);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            h[d][n] = fmaf(exp2_approx(dv[d] * kLog2e * A[d][n]), h[d][n], uv[d] * bv[n]);
+      };
+      const int subs = (nt + 3) / 4;
+      for (int s = 0; s < subs; ++s) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) sm.keep[wid][s][d][lane] = make_float4(h[d][0], h[d][1], h[d][2], h[d][3]);
+        if (s + 1 < subs) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) forward(4 * s + k);
+        }
+      }
+      for (int s = subs - 1; s >= 0; --s) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float4 f = sm.keep[wid][s][d][lane];
+          h[d][0] = f.x, h[d][1] = f.y, h[d][2] = f.z, h[d][3] = f.w;
+        }
+        float hb[4][4][4];  // states before each of the four tokens
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) hb[k][d][n] = h[d][n];
+          forward(4 * s + k);  // behind the last token dt, u, b and c are 0: the state stays
+        }
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const int t = 4 * s + k;
+          float dv[4], uv[4], gv[4], bv[4], cv[4], du[4], va[4], yv[4], db[4], dc[4];
+          row4(&sm.delta[wid][t][4 * dl], dv);
+          row4(&sm.u[wid][t][4 * dl], uv);
+          row4(&sm.dy[wid][t][4 * dl], gv);
+          row4(&sm.maps[t][4 * nl], bv);
+          row4(&sm.maps[t][kSp + 4 * nl], cv);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) db[n] = dc[n] = 0.f;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            du[d] = va[d] = yv[d] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float hn = k == 3 ? h[d][n] : hb[k == 3 ? 3 : k + 1][d][n];
+              K[d][n] = fmaf(gv[d], cv[n], K[d][n]);
+              yv[d] = fmaf(cv[n], hn, yv[d]);
+              dc[n] = fmaf(gv[d], hn, dc[n]);
+              db[n] = fmaf(uv[d], K[d][n], db[n]);
+              du[d] = fmaf(bv[n], K[d][n], du[d]);
+              const float w = K[d][n] * exp2_approx(dv[d] * kLog2e * A[d][n]);
+              const float v = w * hb[k][d][n];
+              va[d] = fmaf(A[d][n], v, va[d]);
+              dA[d][n] = fmaf(dv[d], v, dA[d][n]);
+              K[d][n] = w;
+            }
+          }
+          // sums over the states (lanes of one channel) and over this warp's channels
+#pragma unroll
+          for (int o = 1; o < kNl; o <<= 1)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              du[d] += __shfl_xor_sync(0xffffffffu, du[d], o);
+              va[d] += __shfl_xor_sync(0xffffffffu, va[d], o);
+              yv[d] += __shfl_xor_sync(0xffffffffu, yv[d], o);
+            }
+#pragma unroll
+          for (int o = kNl; o < 32; o <<= 1)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              db[n] += __shfl_xor_sync(0xffffffffu, db[n], o);
+              dc[n] += __shfl_xor_sync(0xffffffffu, dc[n], o);
+            }
+          __syncwarp();
+          if (nl == 0) {
+            *reinterpret_cast<float4*>(&sm.u[wid][t][4 * dl]) = make_float4(du[0], du[1], du[2], du[3]);
+            *reinterpret_cast<float4*>(&sm.dy[wid][t][4 * dl]) = make_float4(va[0], va[1], va[2], va[3]);
+            *reinterpret_cast<float4*>(&sm.y[wid][t][4 * dl]) = make_float4(yv[0], yv[1], yv[2], yv[3]);
+          }
+          if (dl == 0) {
+            *reinterpret_cast<float4*>(&sm.part[wid][t][4 * nl]) = make_float4(db[0], db[1], db[2], db[3]);
+            *reinterpret_cast<float4*>(&sm.part[wid][t][kSp + 4 * nl]) = make_float4(dc[0], dc[1], dc[2], dc[3]);
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < nt * 2 * kSp; i += 32 * kSsmWarps) {
+        const int k = i / (2 * kSp), r = i % (2 * kSp);
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSsmWarps; ++w) v += sm.part[w][k][r];
+        p.part_m[(((int64_t)part * p.T + t0 + k) * p.G + g) * 2 * kSp + r] = v;
+      }
+      for (int k = lt; k < nt; k += kLt) {
+        const int64_t t = t0 + k;
+        const auto xr = load_pack<T, 4, kVec>(static_cast<const T*>(p.x) + t * p.sx + lc0, ln);
+        const auto dr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dt) + t * p.sdt + lc0, ln);
+        const auto gr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dout) + t * p.sdo + lc0, ln);
+        Pack<T, 4> zr{}, dxr, ddr, dzr;
+        if (has_z) zr = load_pack<T, 4, kVec>(static_cast<const T*>(p.z) + t * p.sz + lc0, ln);
+        float du[4], va[4], yv[4], dv[4];
+        row4(&sm.u[wid][k][4 * lq], du);
+        row4(&sm.dy[wid][k][4 * lq], va);
+        row4(&sm.y[wid][k][4 * lq], yv);
+        row4(&sm.delta[wid][k][4 * lq], dv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float xv = to_float(xr.t[j]);
+          float dyv = to_float(gr.t[j]);
+          if (has_z) {
+            const float zv = to_float(zr.t[j]), sig = sigmoid(zv);
+            dzr.t[j] = from_float<T>(dyv * fmaf(skip[j], xv, yv[j]) * silu_slope(zv, sig));
+            dyv *= silu_of(zv, sig);
+          }
+          dxr.t[j] = from_float<T>(fmaf(dv[j], du[j], skip[j] * dyv));
+          float dd = fmaf(xv, du[j], va[j]);
+          if (p.softplus) dd *= sigmoid(to_float(dr.t[j]) + bias[j]);
+          ddr.t[j] = from_float<T>(dd);
+          dbias[j] += dd;
+          dskip[j] = fmaf(dyv, xv, dskip[j]);
+        }
+        if (ln > 0) {
+          store_pack<T, 4, kVec>(static_cast<T*>(p.dx) + t * p.C + lc0, dxr, ln);
+          store_pack<T, 4, kVec>(static_cast<T*>(p.ddt) + t * p.C + lc0, ddr, ln);
+          if (has_z) store_pack<T, 4, kVec>(static_cast<T*>(p.dz) + t * p.C + lc0, dzr, ln);
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (d < nch)
+        *reinterpret_cast<float4*>(p.part_a + (((int64_t)seg * kQ + nl) * p.C + c0 + d) * 4) =
+            make_float4(dA[d][0], dA[d][1], dA[d][2], dA[d][3]);
+#pragma unroll
+    for (int o = kLq; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dskip[j] += __shfl_xor_sync(0xffffffffu, dskip[j], o);
+        dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], o);
+      }
+    if (lt == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < ln) {
+          p.part_c[((int64_t)seg * 2) * p.C + lc0 + j] = dskip[j];
+          p.part_c[((int64_t)seg * 2 + 1) * p.C + lc0 + j] = dbias[j];
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ sums of the backward
+
+template <typename T>
+__device__ void maps_grad(const SsmParams& p, int64_t i) {  // i over [T][G][2][S]
+  const int Sp = ssm_padded(p.S);
+  const int s = (int)(i % p.S), m = (int)(i / p.S % 2);
+  const int64_t tg = i / (2 * p.S);
+  float v = 0.f;
+  for (int k = 0; k < p.parts; ++k) v += p.part_m[((int64_t)k * p.T * p.G + tg) * 2 * Sp + m * Sp + s];
+  static_cast<T*>(m ? p.dc : p.db)[tg * p.S + s] = from_float<T>(v);
+}
+
+// blockIdx.y 0: db and dc over the CTAs of the channels; 1: da over the segments; 2: dskip and ddt_bias; 3: the start
+// states' gradients over the documents of each pool entry.
+__global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ SsmParams p) {
+  bw::griddep_wait();
+  if (p.hd->status != 0) return;
+  const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  const int Sp = ssm_padded(p.S), Q = Sp / 4, segs = p.hd->n_segs;
+  const int64_t state = (int64_t)Q * p.C * 4;
+  if (blockIdx.y == 0) {
+    const int64_t n = (int64_t)p.T * p.G * 2 * p.S;
+    for (int64_t i = i0; i < n; i += step) {
+      if (p.dtype == GDN_DTYPE_BF16)
+        maps_grad<__nv_bfloat16>(p, i);
+      else if (p.dtype == GDN_DTYPE_FP16)
+        maps_grad<__half>(p, i);
+      else
+        maps_grad<float>(p, i);
+    }
+  } else if (blockIdx.y == 1) {
+    for (int64_t i = i0; i < (int64_t)Q * p.C; i += step) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < segs; ++s) {
+        const float4 f = *reinterpret_cast<const float4*>(p.part_a + s * state + i * 4);
+        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+      }
+      store_quad(p.da, 0, p.C, p.S, (int)(i % p.C), (int)(i / p.C), v);
+    }
+  } else if (blockIdx.y == 2) {
+    for (int64_t i = i0; i < 2 * p.C; i += step) {
+      float v = 0.f;
+      for (int s = 0; s < segs; ++s) v += p.part_c[(int64_t)s * 2 * p.C + i];
+      float* out = i < p.C ? p.dskip : p.dbias;
+      if (out) out[i % p.C] = v;
+    }
+  } else {
+    for (int64_t i = i0; i < (int64_t)p.n_init * Q * p.C; i += step) {
+      const int e = (int)(i / ((int64_t)Q * p.C));
+      const int64_t r = i % ((int64_t)Q * p.C);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.init_idx)
+        for (int d = 0; d < p.N; ++d)
+          if (p.init_idx[d] == e) {
+            const float4 f = *reinterpret_cast<const float4*>(p.dstart + d * state + r * 4);
+            v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+          }
+      store_quad(p.dinit, e, p.C, p.S, (int)(r % p.C), (int)(r / p.C), v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ host
+
+bool sizes_ok(int N, int T, int C, int S, int G) {
+  return N >= 1 && T >= 0 && C >= 1 && S >= 1 && S <= kSsmMaxState && G >= 1 && C % G == 0 &&
+         (int64_t)T * C <= ((int64_t)1 << 40) && (int64_t)C * S <= ((int64_t)1 << 28) &&
+         (int64_t)N * C <= ((int64_t)1 << 36);
+}
+
+struct SsmCall {
+  const void *x, *dt, *z;
+  const float* a;
+  const void *b, *c;
+  const float *skip, *dt_bias;
+  const int32_t* cu;
+  int N, T, C, S, G, dtype;
+  const int64_t* strides;
+  int softplus;
+  const int32_t* init_idx;
+  const float* init;
+  int n_init;
+  const void* dout;
+  void* ws;
+  size_t ws_bytes;
+  bool bwd;
+};
+
+int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p, SsmLayout* L, DeviceGuard& guard, int* sms) {
+  if (c.dtype != GDN_DTYPE_BF16 && c.dtype != GDN_DTYPE_FP16 && c.dtype != GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED;
+  if (!sizes_ok(c.N, c.T, c.C, c.S, c.G) || c.n_init < 0) return GDN_ERR_INVALID_ARG;
+  if (!c.a || !c.cu || !c.ws || (c.n_init > 0 && !c.init)) return GDN_ERR_INVALID_ARG;
+  if (c.T > 0 && (!c.x || !c.dt || !c.b || !c.c || (c.bwd && !c.dout))) return GDN_ERR_INVALID_ARG;
+  const int64_t rows[6] = {c.C, c.C, c.C, (int64_t)c.G * c.S, (int64_t)c.G * c.S, c.C};
+  int64_t st[6];
+  for (int i = 0; i < 6; ++i) {
+    st[i] = c.strides && (i < 5 || c.bwd) && c.strides[i] ? c.strides[i] : rows[i];
+    if (st[i] < rows[i] || st[i] > ((int64_t)1 << 40)) return GDN_ERR_INVALID_ARG;
+  }
+  const int es = c.dtype == GDN_DTYPE_FP32 ? 4 : 2;
+  auto al = [](const void* q, uintptr_t n) { return reinterpret_cast<uintptr_t>(q) % n == 0; };
+  for (const void* q : {c.x, c.dt, c.z, c.b, c.c, c.dout})
+    if (!al(q, es)) return GDN_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)c.a, (const void*)c.skip, (const void*)c.dt_bias, (const void*)c.init, (const void*)c.cu,
+                        (const void*)c.init_idx})
+    if (!al(q, 4)) return GDN_ERR_INVALID_ARG;
+  if (!al(c.ws, 256)) return GDN_ERR_INVALID_ARG;
+  *L = ssm_layout(c.N, c.T, c.C, c.S, c.G, c.bwd);
+  if (c.ws_bytes < L->total) return GDN_ERR_WORKSPACE;
+  const void* ptrs[24] = {c.x, c.dt, c.z, c.a, c.b, c.c, c.skip, c.dt_bias, c.cu, c.init_idx, c.init, c.dout};
+  int n = 12;
+  for (int i = 0; i < n_outs; ++i) {
+    if (!al(outs[i], 4) && !al(outs[i], es)) return GDN_ERR_INVALID_ARG;
+    ptrs[n++] = outs[i];
+  }
+  int dev = 0;
+  if (device_of(c.ws, ptrs, n, &dev) != kOk) return GDN_ERR_INVALID_ARG;
+  if (!guard.set(dev)) return GDN_ERR_CUDA;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GDN_ERR_CUDA;
+  if (major != 10 || minor != 3) return GDN_ERR_UNSUPPORTED;
+  *p = SsmParams{};
+  p->x = c.x, p->dt = c.dt, p->z = c.z, p->b = c.b, p->c = c.c, p->dout = c.dout;
+  p->sx = st[0], p->sdt = st[1], p->sz = st[2], p->sb = st[3], p->sc = st[4], p->sdo = st[5];
+  p->a = c.a, p->skip = c.skip, p->dt_bias = c.dt_bias, p->init = c.init, p->cu = c.cu, p->init_idx = c.init_idx;
+  p->N = c.N, p->T = c.T, p->C = c.C, p->S = c.S, p->G = c.G, p->n_init = c.n_init, p->softplus = c.softplus != 0;
+  p->dtype = c.dtype;
+  uint8_t* ws = static_cast<uint8_t*>(c.ws);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  p->hd = reinterpret_cast<SsmHeader*>(ws + L->header);
+  p->segs = reinterpret_cast<SsmSeg*>(ws + L->segs);
+  p->seg0 = reinterpret_cast<int32_t*>(ws + L->seg0);
+  p->is_src = reinterpret_cast<int32_t*>(ws + L->is_src);
+  p->maps = f(L->maps), p->slot = f(L->slot), p->sums = f(L->sums);
+  if (c.bwd) {
+    p->slot_r = f(L->slot_r), p->ckpt = f(L->ckpt), p->csum = f(L->csum), p->dstart = f(L->dstart);
+    p->facc = f(L->facc), p->part_a = f(L->part_a), p->part_c = f(L->part_c), p->part_m = f(L->part_m);
+  }
+  p->smax = L->smax;
+  p->parts = L->parts;
+  p->bwd = c.bwd;
+  // one segment for each of eight warps on an SM
+  const int blocks = c.G * ((c.C / c.G + ssm_walk_channels(ssm_padded(c.S)) - 1) / ssm_walk_channels(ssm_padded(c.S)));
+  const int64_t per = ((int64_t)c.T * blocks + 8 * *sms - 1) / (8 * *sms);
+  const int64_t len = (per + kSsmTile - 1) / kSsmTile * kSsmTile;
+  p->seg_tokens = (int)(len < kSsmMinSeg ? kSsmMinSeg : len);
+  return GDN_OK;
+}
+
+// Whether a lane's channels can be read as one piece everywhere: k elements to a piece.
+bool vectors_ok(const SsmParams& p, int k) {
+  const int es = p.dtype == GDN_DTYPE_FP32 ? 4 : 2;
+  if (p.C / p.G % k) return false;
+  for (int64_t s : {p.sx, p.sdt, p.z ? p.sz : 0, p.dout ? p.sdo : 0})
+    if (s % k) return false;
+  for (const void* q : {p.x, p.dt, p.z, p.dout, (const void*)p.out, (const void*)p.dx, (const void*)p.ddt, (const void*)p.dz})
+    if (reinterpret_cast<uintptr_t>(q) % (uintptr_t)(k * es)) return false;
+  return true;
+}
+
+template <typename F>
+void by_type(int dtype, F f) {
+  if (dtype == GDN_DTYPE_BF16)
+    f(__nv_bfloat16{});
+  else if (dtype == GDN_DTYPE_FP16)
+    f(__half{});
+  else
+    f(float{});
+}
+template <int kN>
+struct Int {
+  static constexpr int value = kN;
+};
+template <typename F>
+void by_state(int Sp, F f) {
+  if (Sp == 8)
+    f(Int<8>{});
+  else if (Sp == 16)
+    f(Int<16>{});
+  else if (Sp == 32)
+    f(Int<32>{});
+  else
+    f(Int<64>{});
+}
+
+template <int kMode>
+void launch_walk(const SsmParams& p, int sms, cudaStream_t s) {
+  const int Sp = ssm_padded(p.S), ch = ssm_walk_channels(Sp);
+  const int64_t items = p.smax * p.G * ((p.C / p.G + ch - 1) / ch), ctas = (items + kSsmWarps - 1) / kSsmWarps;
+  const unsigned grid = (unsigned)(ctas < 8 * sms ? ctas : 8 * sms);
+  const bool vec = vectors_ok(p, Sp <= 16 ? 2 : 1);
+  by_type(p.dtype, [&](auto t) {
+    using T = decltype(t);
+    by_state(Sp, [&](auto n) {
+      constexpr int kSp = decltype(n)::value;
+      launch_early(vec ? ssm_walk_kernel<T, kSp, kMode, true> : ssm_walk_kernel<T, kSp, kMode, false>, dim3(grid),
+                   32 * kSsmWarps, 0, s, p);
+    });
+  });
+}
+
+void launch_plan(const SsmParams& p, int sms, cudaStream_t s) {
+  const int64_t n = (int64_t)p.T * p.G * 2 * ssm_padded(p.S), blocks = (n + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  launch_early(ssm_plan_kernel, dim3((unsigned)(1 + (blocks < 2 * sms ? blocks : 2 * sms))), kPlanThreads, 0, s, p);
+}
+
+void launch_scan(const SsmParams& p, cudaStream_t s) {
+  const int64_t n = (int64_t)ssm_padded(p.S) / 4 * p.C;
+  launch_early(ssm_scan_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)(p.N < 16 ? p.N : 16)), 256, 0, s, p);
+}
+
+template <typename T, int kSp, bool kVec>
+bool launch_grad_of(const SsmParams& p, unsigned grid, int dev, cudaStream_t s) {
+  static PerDevice ready;
+  constexpr size_t bytes = sizeof(GradSmem<kSp>);
+  if (!ready.done(dev)) {
+    if (cudaFuncSetAttribute(ssm_grad_kernel<T, kSp, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+        cudaSuccess)
+      return false;
+    ready.mark(dev);
+  }
+  launch_early(ssm_grad_kernel<T, kSp, kVec>, dim3(grid), 32 * kSsmWarps, bytes, s, p);
+  return true;
+}
+
+bool launch_grad(const SsmParams& p, int sms, cudaStream_t s) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const int64_t items = p.smax * p.G * p.parts;
+  const unsigned grid = (unsigned)(items < 4 * sms ? items : 4 * sms);
+  const bool vec = vectors_ok(p, 4);
+  bool ok = false;
+  by_type(p.dtype, [&](auto t) {
+    using T = decltype(t);
+    by_state(ssm_padded(p.S), [&](auto n) {
+      constexpr int kSp = decltype(n)::value;
+      ok = vec ? launch_grad_of<T, kSp, true>(p, grid, dev, s) : launch_grad_of<T, kSp, false>(p, grid, dev, s);
+    });
+  });
+  return ok;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" size_t gdn_ssm_workspace_size(int N, int T, int C, int S, int G, int backward) {
+  if (!gdn::sizes_ok(N, T, C, S, G)) return 0;
+  return gdn::ssm_layout(N, T, C, S, G, backward != 0).total;
+}
+
+extern "C" int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
+                           const float* skip, const float* dt_bias, const int32_t* cu_seqlens, int N, int T, int C, int S,
+                           int G, int dtype, const int64_t* strides, int dt_softplus, const int32_t* init_idx,
+                           const float* initial_state, int n_init, void* out, float* final_state, void* workspace,
+                           size_t ws_bytes, gdn_stream_t stream) {
+  using namespace gdn;
+  if (!final_state || (T > 0 && !out)) return GDN_ERR_INVALID_ARG;
+  const SsmCall call{x,       dt,          z,        a,             b,      c,       skip,      dt_bias,  cu_seqlens, N, T, C, S, G, dtype,
+                     strides, dt_softplus, init_idx, initial_state, n_init, nullptr, workspace, ws_bytes, false};
+  const void* outs[] = {out, final_state};
+  SsmParams p;
+  SsmLayout L;
+  DeviceGuard guard;
+  int sms = 0;
+  const int rc = prepare(call, outs, 2, &p, &L, guard, &sms);
+  if (rc != GDN_OK) return rc;
+  p.out = out;
+  p.final_state = final_state;
+  cudaStream_t s = (cudaStream_t)stream;
+  launch_plan(p, sms, s);
+  launch_walk<kWalkState>(p, sms, s);
+  launch_scan(p, s);
+  if (T > 0) launch_walk<kWalkOut>(p, sms, s);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
+                           const float* skip, const float* dt_bias, const int32_t* cu_seqlens, int N, int T, int C, int S,
+                           int G, int dtype, const int64_t* strides, int dt_softplus, const int32_t* init_idx,
+                           const float* initial_state, int n_init, const void* dout, const float* dfinal_state, void* dx,
+                           void* ddt, void* dz, float* da, void* db, void* dc, float* dskip, float* ddt_bias,
+                           float* dinitial_state, void* workspace, size_t ws_bytes, gdn_stream_t stream) {
+  using namespace gdn;
+  if (!da || (T > 0 && (!dx || !ddt || !db || !dc)) || (n_init > 0 && !dinitial_state)) return GDN_ERR_INVALID_ARG;
+  if ((z != nullptr && T > 0 && !dz) || (skip != nullptr && !dskip) || (dt_bias != nullptr && !ddt_bias))
+    return GDN_ERR_INVALID_ARG;
+  const SsmCall call{x,       dt,          z,        a,             b,      c,    skip,      dt_bias,  cu_seqlens, N, T, C, S, G, dtype,
+                     strides, dt_softplus, init_idx, initial_state, n_init, dout, workspace, ws_bytes, true};
+  const void* outs[] = {dx, ddt, dz, da, db, dc, dskip, ddt_bias, dinitial_state, dfinal_state};
+  SsmParams p;
+  SsmLayout L;
+  DeviceGuard guard;
+  int sms = 0;
+  const int rc = prepare(call, outs, 10, &p, &L, guard, &sms);
+  if (rc != GDN_OK) return rc;
+  p.dfinal = dfinal_state;
+  p.dx = dx, p.ddt = ddt, p.dz = dz, p.db = db, p.dc = dc;
+  p.da = da, p.dskip = dskip, p.dbias = ddt_bias, p.dinit = dinitial_state;
+  cudaStream_t s = (cudaStream_t)stream;
+  launch_plan(p, sms, s);
+  if (T > 0) launch_walk<kWalkGrad>(p, sms, s);
+  launch_scan(p, s);
+  if (T > 0 && !launch_grad(p, sms, s)) return GDN_ERR_CUDA;
+  launch_early(ssm_sum_kernel, dim3((unsigned)(4 * sms), n_init > 0 ? 4u : 3u), 256, 0, s, p);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}

@@ -1,0 +1,83 @@
+// Selective scan over packed documents: parameters shared by the host entry points and the kernels
+// (csrc/gdn_ssm.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+constexpr int kSsmTile = 16;     // tokens between two states that the backward keeps
+constexpr int kSsmMinSeg = 64;   // shortest segment, a multiple of the tile
+constexpr int kSsmMaxState = 64;
+
+// A segment: consecutive tokens of one document that one warp walks for its channels.
+struct SsmSeg {
+  int32_t doc, tok0, ntok;
+  int32_t first, last;  // of its document
+  int32_t src;          // state before it: -1 zero, >= 0 pool entry, -2 its slot
+  int32_t need;         // the end state from zero is needed
+  int32_t pad;
+};
+
+struct SsmHeader {
+  int32_t status;
+  int32_t n_segs;
+  int32_t forks;     // some document starts from another one
+  int32_t pad[61];
+};
+static_assert(sizeof(SsmHeader) == 256, "header is 256 bytes");
+
+__host__ __device__ constexpr int ssm_padded(int S) { return S <= 8 ? 8 : S <= 16 ? 16 : S <= 32 ? 32 : 64; }
+// channels to a warp of the walks forward in time, and of the backward's walk
+inline int ssm_walk_channels(int Sp) { return Sp <= 16 ? 64 : Sp == 32 ? 32 : 16; }
+inline int ssm_grad_channels(int Sp) { return 4 * 32 / (Sp / 4); }
+constexpr int kSsmWarps = 4;  // warps to a CTA
+
+// Workspace (byte offsets). State-sized arrays hold [Sp / 4][C][4] floats: four states of one channel together,
+// channels beside one another.
+struct SsmLayout {
+  size_t header, segs, seg0, is_src, maps, slot, sums, slot_r, ckpt, csum, dstart, facc, part_a, part_c, part_m, total;
+  int64_t smax, tiles;
+  int parts;  // CTAs of the backward's walk to a group of channels
+};
+
+inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
+  SsmLayout L{};
+  const int Sp = ssm_padded(S);
+  L.smax = N + (int64_t)T / kSsmMinSeg;
+  L.tiles = L.smax + T / kSsmTile + 1;
+  const int per = kSsmWarps * ssm_grad_channels(Sp);
+  L.parts = (C / G + per - 1) / per;
+  const size_t state = (size_t)C * Sp * sizeof(float);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  L.header = take(sizeof(SsmHeader));
+  L.segs = take(sizeof(SsmSeg) * L.smax);
+  L.seg0 = take(sizeof(int32_t) * (N + 1));
+  L.is_src = take(sizeof(int32_t) * N);
+  L.maps = take((size_t)T * G * 2 * Sp * sizeof(float));  // b and c in fp32, token by token
+  L.slot = take(state * L.smax);                          // end states from zero, then start states
+  L.sums = take(sizeof(float) * C * L.smax);              // time of each segment
+  if (bwd) {
+    L.slot_r = take(state * L.smax);                      // the same for the state's gradient, in reverse
+    L.ckpt = take(state * L.tiles);                       // states from zero at each tile of a segment
+    L.csum = take(sizeof(float) * C * L.tiles);           // time from the segment's start to each tile
+    L.dstart = take(state * N);
+    L.facc = take(state * N);                             // gradients that forks send back
+    L.part_a = take(state * L.smax);                      // sums of each segment: da,
+    L.part_c = take(sizeof(float) * 2 * C * L.smax);      //   dskip and ddt_bias
+    L.part_m = take((size_t)L.parts * T * G * 2 * Sp * sizeof(float));  // db and dc of each CTA's channels
+  }
+  L.total = o;
+  return L;
+}
+
+}  // namespace gdn
