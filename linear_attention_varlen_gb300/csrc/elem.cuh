@@ -77,6 +77,19 @@ __device__ __forceinline__ float silu_slope(float x, float sig) {
   return sig == 0.f || sig == 1.f ? sig : sig * fmaf(x, 1.f - sig, 1.f);
 }
 
-__device__ __forceinline__ float softplus(float r) { return r > 20.f ? r : log1pf(expf(r)); }
+// log(1 + e^r) = max(r, 0) + log1p(e^-|r|), with log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its series
+// 2 s (1 + s^2 / 3 + s^4 / 5 + ...), cut where the next term is below 2^-25 of the sum. Relative error about 2^-21 (the
+// exponential's, and its argument's rounding); NaN stays NaN.
+__device__ __forceinline__ float softplus(float r) {
+  const float e = exp2_approx(-kLog2e * fabsf(r));
+  const float s = e * rcp_approx(2.f + e), q = s * s;
+  float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  const float t = s + s;
+  return fmaxf(r, 0.f) + fmaf(t * q, p, t);
+}
 
 }  // namespace gdn

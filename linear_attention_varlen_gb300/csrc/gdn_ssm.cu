@@ -65,19 +65,22 @@ struct SsmParams {
 
 // ------------------------------------------------------------------------------ planner, maps in fp32
 
+// A warp takes whole tokens, its lanes four states of a map each.
 template <typename T>
 __device__ void maps_to_float(const SsmParams& p, int block, int blocks) {
-  const int Sp = ssm_padded(p.S), row = p.G * 2 * Sp;
-  const int64_t n = (int64_t)p.T * row;
-  for (int64_t i = (int64_t)block * blockDim.x + threadIdx.x; i < n; i += (int64_t)blocks * blockDim.x) {
-    const int64_t t = i / row;
-    const int r = (int)(i - t * row), g = r / (2 * Sp), m = r % (2 * Sp) / Sp, s = r % Sp;
-    float v = 0.f;
-    if (s < p.S)
-      v = m == 0 ? to_float(static_cast<const T*>(p.b)[t * p.sb + g * p.S + s])
-                 : to_float(static_cast<const T*>(p.c)[t * p.sc + g * p.S + s]);
-    p.maps[i] = v;
-  }
+  const int Q = ssm_padded(p.S) / 4, row = p.G * 2 * Q;  // quads to a token
+  const int lane = threadIdx.x & 31, per = row < 32 ? 32 / row : 1, sub = row < 32 ? lane / row : 0;
+  const int64_t step = (int64_t)blocks * (blockDim.x / 32) * per;
+  if (sub >= per) return;
+  for (int64_t t = ((int64_t)block * (blockDim.x / 32) + (threadIdx.x >> 5)) * per + sub; t < p.T; t += step)
+    for (int i = row < 32 ? lane - sub * row : lane; i < row; i += 32) {
+      const int g = i / (2 * Q), r = i - g * 2 * Q, q = r < Q ? r : r - Q;
+      const T* from = r < Q ? static_cast<const T*>(p.b) + t * p.sb : static_cast<const T*>(p.c) + t * p.sc;
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = 4 * q + k < p.S ? to_float(from[g * p.S + 4 * q + k]) : 0.f;
+      *reinterpret_cast<float4*>(p.maps + (t * row + i) * 4) = make_float4(v[0], v[1], v[2], v[3]);
+    }
 }
 
 // Block 0: checks cu_seqlens and init_idx and cuts the documents into segments of at most seg_tokens. The others:
@@ -183,14 +186,74 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
 
 enum { kWalkState = 0, kWalkOut = 1, kWalkGrad = 2 };
 
-__device__ __forceinline__ void cp_async16(float* dst, const float* src) {
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(bw::smem_u32(dst)), "l"(src) : "memory");
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_if(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(bw::smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kN>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
+
+// Rows of a [T, C] tensor on their way into shared memory: the kN channels from `first` on, of tokens one after the
+// other, by asynchronous copies of 16 bytes. kVec: everything is aligned to them. Other rows bring the pieces that
+// cover the channels, and each row's place within its first piece is found again from its address; a piece that
+// sticks out of the tensor is copied by elements.
+template <typename T, int kN, bool kVec>
+struct Rows {
+  static constexpr int K = 16 / (int)sizeof(T);
+  static constexpr int kBytes = (kN * (int)sizeof(T) + 15) / 16 * 16 + (kVec ? 0 : 16);  // of a row in shared memory
+  static constexpr int kPieces = kBytes / 16;
+  const T* src;  // channel `first` of token 0
+  int64_t stride;
+  const T *lo, *hi;
+  int n;  // channels that exist
+  __device__ __forceinline__ Rows(const void* base, int64_t stride_, int64_t first, int n_, int T_, int C) : stride(stride_), n(n_) {
+    lo = static_cast<const T*>(base);
+    src = lo + first;
+    hi = kVec ? nullptr : lo + (T_ - 1) * stride_ + C;
+  }
+  // tokens t .. t + rows - 1 (at most kRows), by thread `tid` of `threads`
+  template <int kRows>
+  __device__ __forceinline__ void fetch(uint8_t* dst, int64_t t, int rows, int tid, int threads) const {
+    for (int i = tid; i < kRows * kPieces; i += threads) {
+      const int r = i / kPieces, q = i - r * kPieces;
+      if (r >= rows) break;
+      const T* p = src + (t + r) * stride;
+      uint8_t* to = dst + r * kBytes + q * 16;
+      if constexpr (kVec) {
+        if (q * K < n) cp_async16(to, p + q * K);
+      } else {
+        const T* piece = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15) + q * K;
+        if (piece >= p + n) continue;
+        if (piece >= lo && piece + K <= hi) {
+          cp_async16(to, piece);
+        } else {
+          for (int e = 0; e < K; ++e)
+            if (piece + e >= p && piece + e < p + n) reinterpret_cast<T*>(to)[e] = piece[e];
+        }
+      }
+    }
+  }
+  // channels c .. c + kK - 1 of row r, token t
+  template <int kK>
+  __device__ __forceinline__ Pack<T, kK> get(const uint8_t* from, int r, int64_t t, int c) const {
+    const uint8_t* row = from + r * kBytes;
+    Pack<T, kK> v;
+    if constexpr (kVec) {
+      v = *reinterpret_cast<const Pack<T, kK>*>(row + c * sizeof(T));
+    } else {
+      const uint32_t at = ((uint32_t)reinterpret_cast<uintptr_t>(src) + (uint32_t)(t * stride) * (uint32_t)sizeof(T)) & 15u;
+#pragma unroll
+      for (int i = 0; i < kK; ++i) v.t[i] = *reinterpret_cast<const T*>(row + at + (c + i) * sizeof(T));
+    }
+    return v;
+  }
+};
 
 // The state that document `src` (encoded as init_idx's pool entries) starts from, for four states of a channel.
 __device__ __forceinline__ float4 pool_quad(const float* pool, int64_t entry, int C, int S, int c, int q) {
@@ -212,19 +275,34 @@ __device__ __forceinline__ void store_quad(float* pool, int64_t entry, int C, in
 
 // A warp walks one segment for 32 kDt / kNl channels: kNl lanes share a channel, each lane holds kNt states of kDt
 // channels in registers, pairs of states in packed fp32. kWalkState leaves the end state from zero and the summed
-// time; kWalkGrad also the states at each tile and the start state's gradient; kWalkOut the outputs.
+// time; kWalkGrad also the states at each tile and the start state's gradient; kWalkOut the outputs. The inputs of kTb
+// tokens are on their way into the warp's part of shared memory while the ones before are worked on.
 template <typename T, int kSp, int kMode, bool kVec>
-__global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_constant__ SsmParams p) {
-  constexpr int kNl = kSp == 64 ? 2 : 1, kNt = kSp / kNl, kDt = kSp <= 16 ? 2 : 1, kCh = 32 / kNl * kDt;
-  constexpr int kTb = kMode == kWalkGrad ? 4 : 8;  // tokens in flight while the ones before are worked on
-  constexpr int kQt = kNt / 4, kQ = kSp / 4;
+struct WalkShape {
+  static constexpr int kNl = kSp == 64 ? 2 : 1, kNt = kSp / kNl, kDt = kSp <= 16 ? 2 : 1, kCh = 32 / kNl * kDt;
+  static constexpr int kTb = 8;
+  using R = Rows<T, kCh, kVec>;
+  static constexpr int kTensors = kMode == kWalkState ? 2 : kMode == kWalkOut ? 3 : 4;
+  static constexpr int kRowsBytes = kTb * R::kBytes, kMapBytes = kTb * 2 * kSp * 4;
+  static constexpr int kStage = kTensors * kRowsBytes + kMapBytes;
+  static constexpr int kSmem = kSsmWarps * 2 * kStage;
+};
+
+template <typename T, int kSp, int kMode, bool kVec>
+__global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : kMode == kWalkOut || kSp == 32 ? 3 : 4)
+    ssm_walk_kernel(const __grid_constant__ SsmParams p) {
+  using W = WalkShape<T, kSp, kMode, kVec>;
+  using R = typename W::R;
+  constexpr int kNl = W::kNl, kNt = W::kNt, kDt = W::kDt, kCh = W::kCh, kTb = W::kTb;
+  constexpr int kQt = kNt / 4, kQ = kSp / 4, kP = kNt / 2;
   constexpr bool kGate = kMode != kWalkState;  // z is read
-  static_assert(kCh == 64 || kCh == 32 || kCh == 16);
-  __shared__ __align__(16) float s_maps[kSsmWarps][2][kTb][2 * kSp];
+  static_assert(kCh == ssm_walk_channels(kSp));
+  extern __shared__ __align__(16) uint8_t raw_smem[];
   bw::griddep_wait();
   bw::griddep_launch_dependents();
   if (p.hd->status != 0) return;
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, nl = lane % kNl, dl = lane / kNl;
+  uint8_t* ring = raw_smem + wid * 2 * W::kStage;
   const int Cg = p.C / p.G, nb = (Cg + kCh - 1) / kCh, blocks = nb * p.G;
   const int64_t items = (int64_t)p.hd->n_segs * blocks;
   const bool has_z = kGate && p.z != nullptr;
@@ -232,10 +310,31 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_c
     const int seg = (int)(item / blocks), blk = (int)(item % blocks), g = blk / nb;
     const SsmSeg sg = p.segs[seg];
     if (kMode == kWalkState && !sg.need) continue;
-    const int cg = (blk % nb) * kCh + dl * kDt;  // channel in its group
+    const int cb = (blk % nb) * kCh, cg = cb + dl * kDt;  // the warp's first channel in its group, the lane's
     const int nch = max(0, min(kDt, Cg - cg));
-    const int c0 = g * Cg + min(cg, Cg - 1);     // a channel that exists
-    uint64_t A[kDt][kNt / 2], h[kDt][kNt / 2], ga[kMode == kWalkGrad ? kDt : 1][kNt / 2], pr[kMode == kWalkGrad ? kDt : 1][kNt / 2];
+    const int c0 = g * Cg + min(cg, Cg - 1);              // a channel that exists
+    const int64_t first = (int64_t)g * Cg + cb;
+    const int have = min(kCh, Cg - cb);
+    const R rx(p.x, p.sx, first, have, p.T, p.C), rd(p.dt, p.sdt, first, have, p.T, p.C);
+    const R rz(p.z, p.sz, first, have, p.T, p.C), ro(p.dout, p.sdo, first, have, p.T, p.C);
+    auto fetch = [&](int i0, uint8_t* st) {  // the inputs of tokens i0 .. i0 + kTb - 1 of the segment
+      const int64_t t = sg.tok0 + i0;
+      const int rows = min(kTb, sg.ntok - i0);
+      rx.template fetch<kTb>(st, t, rows, lane, 32);
+      rd.template fetch<kTb>(st + W::kRowsBytes, t, rows, lane, 32);
+      if constexpr (kGate) {
+        if (has_z) rz.template fetch<kTb>(st + 2 * W::kRowsBytes, t, rows, lane, 32);
+      }
+      if constexpr (kMode == kWalkGrad) ro.template fetch<kTb>(st + 3 * W::kRowsBytes, t, rows, lane, 32);
+      uint8_t* mp = st + W::kTensors * W::kRowsBytes;
+      for (int i = lane; i < rows * (2 * kSp / 4); i += 32) {
+        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
+        cp_async16(mp + i * 16, p.maps + ((t + k) * p.G + g) * 2 * kSp + 4 * r);
+      }
+      cp_async_commit();
+    };
+    fetch(0, ring);
+    uint64_t A[kDt][kP], h[kDt][kP], ga[kMode == kWalkGrad ? kDt : 1][kP], pr[kMode == kWalkGrad ? kDt : 1][kP];
     float bias[kDt], skip[kDt], total[kDt];
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
@@ -264,35 +363,6 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_c
         }
       }
     }
-    const T* xs = static_cast<const T*>(p.x) + c0;
-    const T* ds = static_cast<const T*>(p.dt) + c0;
-    const T* zs = static_cast<const T*>(p.z) + c0;
-    const T* os = static_cast<const T*>(p.dout) + c0;
-    using P = Pack<T, kDt>;
-    P xr[kTb], dr[kTb], zr[kGate ? kTb : 1], gr[kMode == kWalkGrad ? kTb : 1];
-    auto fetch = [&](int i0) {  // the inputs of tokens i0 .. i0 + kTb - 1 of the segment
-#pragma unroll
-      for (int k = 0; k < kTb; ++k) {
-        const int64_t t = sg.tok0 + i0 + k;
-        const int n = i0 + k < sg.ntok ? nch : 0;
-        xr[k] = load_pack<T, kDt, kVec>(xs + t * p.sx, n);
-        dr[k] = load_pack<T, kDt, kVec>(ds + t * p.sdt, n);
-        if constexpr (kGate) {
-          if (has_z) zr[k] = load_pack<T, kDt, kVec>(zs + t * p.sz, n);
-        }
-        if constexpr (kMode == kWalkGrad) gr[k] = load_pack<T, kDt, kVec>(os + t * p.sdo, n);
-      }
-    };
-    auto fetch_maps = [&](int i0, int buf) {
-      const int n = min(kTb, sg.ntok - i0) * (2 * kSp / 4);
-      for (int i = lane; i < n; i += 32) {
-        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
-        cp_async16(&s_maps[wid][buf][k][4 * r], p.maps + (((int64_t)sg.tok0 + i0 + k) * p.G + g) * 2 * kSp + 4 * r);
-      }
-      cp_async_commit();
-    };
-    fetch(0);
-    fetch_maps(0, 0);
     for (int i0 = 0, it = 0; i0 < sg.ntok; i0 += kTb, ++it) {
       if constexpr (kMode == kWalkGrad) {
         if (i0 % kSsmTile == 0 && nch > 0) {
@@ -308,57 +378,62 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_c
           }
         }
       }
-      P xc[kTb], dc[kTb], zc[kGate ? kTb : 1], gc[kMode == kWalkGrad ? kTb : 1];
-#pragma unroll
-      for (int k = 0; k < kTb; ++k) {
-        xc[k] = xr[k];
-        dc[k] = dr[k];
-        if constexpr (kGate) zc[k] = zr[k];
-        if constexpr (kMode == kWalkGrad) gc[k] = gr[k];
-      }
+      uint8_t* st = ring + (it & 1) * W::kStage;
       if (i0 + kTb < sg.ntok) {
-        fetch(i0 + kTb);
-        fetch_maps(i0 + kTb, (it + 1) & 1);
+        fetch(i0 + kTb, ring + (~it & 1) * W::kStage);
         cp_async_wait<1>();
       } else {
         cp_async_wait<0>();
       }
       __syncwarp();
-#pragma unroll
-      for (int k = 0; k < kTb; ++k) {
-        if (i0 + k >= sg.ntok) break;
-        const float* mp = s_maps[wid][it & 1][k];
-        float delta[kDt], u[kDt], y[kDt], dy[kDt];
+      const int rows = min(kTb, sg.ntok - i0);
+      const float* maps = reinterpret_cast<const float*>(st + W::kTensors * W::kRowsBytes) + nl * kNt;
+#pragma unroll 2
+      for (int k = 0; k < rows; ++k) {
+        const int64_t t = sg.tok0 + i0 + k;
+        const float* mp = maps + k * 2 * kSp;
+        const auto xv = rx.template get<kDt>(st, k, t, dl * kDt);
+        const auto dv = rd.template get<kDt>(st + W::kRowsBytes, k, t, dl * kDt);
+        float x[kDt], gate[kDt], dy[kDt];
+        uint64_t dd[kDt], uu[kDt], y2[kDt];
 #pragma unroll
         for (int d = 0; d < kDt; ++d) {
-          const float raw = to_float(dc[k].t[d]) + bias[d];
-          delta[d] = p.softplus ? softplus(raw) : raw;
-          u[d] = delta[d] * to_float(xc[k].t[d]);
-          total[d] += delta[d];
-          if constexpr (kMode == kWalkGrad) {
-            dy[d] = to_float(gc[k].t[d]);
-            if (has_z) {
-              const float zv = to_float(zc[k].t[d]);
-              dy[d] *= silu_of(zv, sigmoid(zv));
+          x[d] = to_float(xv.t[d]);
+          const float raw = to_float(dv.t[d]) + bias[d];
+          const float delta = p.softplus ? softplus(raw) : raw, u = delta * x[d];
+          total[d] += delta;
+          dd[d] = f2_pack(delta, delta);
+          uu[d] = f2_pack(u, u);
+          y2[d] = 0;
+          gate[d] = 1.f;
+        }
+        if constexpr (kGate) {
+          if (has_z) {
+            const auto zv = rz.template get<kDt>(st + 2 * W::kRowsBytes, k, t, dl * kDt);
+#pragma unroll
+            for (int d = 0; d < kDt; ++d) {
+              const float z = to_float(zv.t[d]);
+              gate[d] = silu_of(z, sigmoid(z));
             }
           }
         }
-        uint64_t y2[kDt];
+        if constexpr (kMode == kWalkGrad) {
+          const auto ov = ro.template get<kDt>(st + 3 * W::kRowsBytes, k, t, dl * kDt);
 #pragma unroll
-        for (int d = 0; d < kDt; ++d) y2[d] = 0;
+          for (int d = 0; d < kDt; ++d) dy[d] = to_float(ov.t[d]) * gate[d];
+        }
 #pragma unroll
         for (int q = 0; q < kQt; ++q) {
-          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(mp + nl * kNt + 4 * q);
+          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(mp + 4 * q);
           ulonglong2 cv;
-          if (kMode != kWalkState) cv = *reinterpret_cast<const ulonglong2*>(mp + kSp + nl * kNt + 4 * q);
+          if (kMode != kWalkState) cv = *reinterpret_cast<const ulonglong2*>(mp + kSp + 4 * q);
 #pragma unroll
           for (int d = 0; d < kDt; ++d) {
-            const uint64_t dd = f2_pack(delta[d], delta[d]), uu = f2_pack(u[d], u[d]);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint64_t arg = f2_mul(dd, A[d][2 * q + j]);
+              const uint64_t arg = f2_mul(dd[d], A[d][2 * q + j]);
               const uint64_t e = f2_pack(exp2_approx(f2_lo(arg)), exp2_approx(f2_hi(arg)));
-              h[d][2 * q + j] = f2_fma(e, h[d][2 * q + j], f2_mul(uu, j ? bv.y : bv.x));
+              h[d][2 * q + j] = f2_fma(e, h[d][2 * q + j], f2_mul(uu[d], j ? bv.y : bv.x));
               if constexpr (kMode == kWalkOut) y2[d] = f2_fma(h[d][2 * q + j], j ? cv.y : cv.x, y2[d]);
               if constexpr (kMode == kWalkGrad) {
                 pr[d][2 * q + j] = f2_mul(pr[d][2 * q + j], e);
@@ -368,24 +443,20 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_c
           }
         }
         if constexpr (kMode == kWalkOut) {
-          P r;
+          Pack<T, kDt> r;
 #pragma unroll
           for (int d = 0; d < kDt; ++d) {
-            y[d] = f2_sum(y2[d]);
-            if constexpr (kNl == 2) y[d] += __shfl_xor_sync(0xffffffffu, y[d], 1);
-            y[d] = fmaf(skip[d], to_float(xc[k].t[d]), y[d]);
-            if (has_z) {
-              const float zv = to_float(zc[k].t[d]);
-              y[d] *= silu_of(zv, sigmoid(zv));
-            }
-            r.t[d] = from_float<T>(y[d]);
+            float y = f2_sum(y2[d]);
+            if constexpr (kNl == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
+            r.t[d] = from_float<T>(fmaf(skip[d], x[d], y) * gate[d]);
           }
-          if (nl == 0 && nch > 0)
-            store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + ((int64_t)sg.tok0 + i0 + k) * p.C + c0, r, nch);
+          if (nl == 0 && nch > 0) store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + t * p.C + c0, r, nch);
         }
       }
-      __syncwarp();  // the buffer is free
+      __syncwarp();  // the stage is free
     }
+    cp_async_wait<0>();
+    __syncwarp();
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
       if (d >= nch) break;
@@ -408,6 +479,8 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_walk_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------------------ scan over segments
+
+constexpr int kScanAhead = 8;  // segments whose loads are in flight
 
 __device__ __forceinline__ float4 carry(float4 a, float time, float4 h, float4 add) {
   return make_float4(fmaf(exp2_approx(a.x * time), h.x, add.x), fmaf(exp2_approx(a.y * time), h.y, add.y),
@@ -446,16 +519,20 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
     else if (src >= 0)
       h = pool_quad(p.init, src, p.C, p.S, c, q);
     const int se = p.is_src[d] ? s1 : s1 - 1;  // the last segment's end state is wanted for forks only
-    for (int s = s0; s < s1; ++s) {
-      float4* at = reinterpret_cast<float4*>(p.slot + s * state + i * 4);
-      float4 e = zero;
-      float time = 0.f;
-      if (s < se) {
-        e = *at;
-        time = p.sums[(int64_t)s * p.C + c];
+    for (int sb = s0; sb < s1; sb += kScanAhead) {
+      float4 e[kScanAhead];
+      float time[kScanAhead];
+#pragma unroll
+      for (int k = 0; k < kScanAhead; ++k)
+        if (sb + k < se) {
+          e[k] = *reinterpret_cast<const float4*>(p.slot + (sb + k) * state + i * 4);
+          time[k] = p.sums[(int64_t)(sb + k) * p.C + c];
+        }
+#pragma unroll
+      for (int k = 0; k < kScanAhead; ++k) {
+        if (sb + k < s1) *reinterpret_cast<float4*>(p.slot + (sb + k) * state + i * 4) = h;
+        if (sb + k < se) h = carry(a, time[k], h, e[k]);
       }
-      *at = h;
-      if (s < se) h = carry(a, time, h, e);
     }
     if (p.bwd) {
       if (p.is_src[d]) *fin(d) = h;
@@ -476,12 +553,21 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
       const float4 f = *facc(d);
       k = make_float4(k.x + f.x, k.y + f.y, k.z + f.z, k.w + f.w);
     }
-    for (int s = s1 - 1; s >= s0; --s) {
-      float4* at = reinterpret_cast<float4*>(p.slot_r + s * state + i * 4);
-      const float4 e = *at;
-      const float time = p.sums[(int64_t)s * p.C + c];
-      *at = k;
-      k = carry(a, time, k, e);
+    for (int sb = s1 - 1; sb >= s0; sb -= kScanAhead) {
+      float4 e[kScanAhead];
+      float time[kScanAhead];
+#pragma unroll
+      for (int j = 0; j < kScanAhead; ++j)
+        if (sb - j >= s0) {
+          e[j] = *reinterpret_cast<const float4*>(p.slot_r + (sb - j) * state + i * 4);
+          time[j] = p.sums[(int64_t)(sb - j) * p.C + c];
+        }
+#pragma unroll
+      for (int j = 0; j < kScanAhead; ++j)
+        if (sb - j >= s0) {
+          *reinterpret_cast<float4*>(p.slot_r + (sb - j) * state + i * 4) = k;
+          k = carry(a, time[j], k, e[j]);
+        }
     }
     *fin(d) = k;  // its final state has been read by every fork
     if (src >= p.n_init && p.init_idx) {
@@ -836,7 +922,7 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
 // ------------------------------------------------------------------------------ host
 
 bool sizes_ok(int N, int T, int C, int S, int G) {
-  return N >= 1 && T >= 0 && C >= 1 && S >= 1 && S <= kSsmMaxState && G >= 1 && C % G == 0 &&
+  return N >= 1 && T >= 0 && T <= INT32_MAX - 4096 && C >= 1 && S >= 1 && S <= kSsmMaxState && G >= 1 && C % G == 0 &&
          (int64_t)T * C <= ((int64_t)1 << 40) && (int64_t)C * S <= ((int64_t)1 << 28) &&
          (int64_t)N * C <= ((int64_t)1 << 36);
 }
@@ -915,22 +1001,27 @@ int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p,
   p->smax = L->smax;
   p->parts = L->parts;
   p->bwd = c.bwd;
-  // one segment for each of eight warps on an SM
-  const int blocks = c.G * ((c.C / c.G + ssm_walk_channels(ssm_padded(c.S)) - 1) / ssm_walk_channels(ssm_padded(c.S)));
-  const int64_t per = ((int64_t)c.T * blocks + 8 * *sms - 1) / (8 * *sms);
-  const int64_t len = (per + kSsmTile - 1) / kSsmTile * kSsmTile;
-  p->seg_tokens = (int)(len < kSsmMinSeg ? kSsmMinSeg : len);
+  p->seg_tokens = L->seg_tokens;
   return GDN_OK;
 }
 
-// Whether a lane's channels can be read as one piece everywhere: k elements to a piece.
-bool vectors_ok(const SsmParams& p, int k) {
-  const int es = p.dtype == GDN_DTYPE_FP32 ? 4 : 2;
+// Whether every row of every block of channels begins on 16 bytes.
+bool vectors_ok(const SsmParams& p) {
+  const int k = p.dtype == GDN_DTYPE_FP32 ? 4 : 8;
   if (p.C / p.G % k) return false;
   for (int64_t s : {p.sx, p.sdt, p.z ? p.sz : 0, p.dout ? p.sdo : 0})
     if (s % k) return false;
   for (const void* q : {p.x, p.dt, p.z, p.dout, (const void*)p.out, (const void*)p.dx, (const void*)p.ddt, (const void*)p.dz})
-    if (reinterpret_cast<uintptr_t>(q) % (uintptr_t)(k * es)) return false;
+    if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+  return true;
+}
+
+// One attribute a kernel and device: shared memory beyond the default limit.
+template <typename K>
+bool allow_smem(K kernel, PerDevice& ready, int dev, size_t bytes) {
+  if (bytes <= 48 * 1024 || ready.done(dev)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  ready.mark(dev);
   return true;
 }
 
@@ -959,20 +1050,32 @@ void by_state(int Sp, F f) {
     f(Int<64>{});
 }
 
+template <typename T, int kSp, int kMode, bool kVec>
+bool launch_walk_of(const SsmParams& p, unsigned grid, int dev, cudaStream_t s) {
+  static PerDevice ready;
+  constexpr size_t bytes = WalkShape<T, kSp, kMode, kVec>::kSmem;
+  if (!allow_smem(ssm_walk_kernel<T, kSp, kMode, kVec>, ready, dev, bytes)) return false;
+  launch_early(ssm_walk_kernel<T, kSp, kMode, kVec>, dim3(grid), 32 * kSsmWarps, bytes, s, p);
+  return true;
+}
+
 template <int kMode>
-void launch_walk(const SsmParams& p, int sms, cudaStream_t s) {
+bool launch_walk(const SsmParams& p, int sms, cudaStream_t s) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const int Sp = ssm_padded(p.S), ch = ssm_walk_channels(Sp);
   const int64_t items = p.smax * p.G * ((p.C / p.G + ch - 1) / ch), ctas = (items + kSsmWarps - 1) / kSsmWarps;
   const unsigned grid = (unsigned)(ctas < 8 * sms ? ctas : 8 * sms);
-  const bool vec = vectors_ok(p, Sp <= 16 ? 2 : 1);
+  const bool vec = vectors_ok(p);
+  bool ok = false;
   by_type(p.dtype, [&](auto t) {
     using T = decltype(t);
     by_state(Sp, [&](auto n) {
       constexpr int kSp = decltype(n)::value;
-      launch_early(vec ? ssm_walk_kernel<T, kSp, kMode, true> : ssm_walk_kernel<T, kSp, kMode, false>, dim3(grid),
-                   32 * kSsmWarps, 0, s, p);
+      ok = vec ? launch_walk_of<T, kSp, kMode, true>(p, grid, dev, s) : launch_walk_of<T, kSp, kMode, false>(p, grid, dev, s);
     });
   });
+  return ok;
 }
 
 void launch_plan(const SsmParams& p, int sms, cudaStream_t s) {
@@ -989,12 +1092,7 @@ template <typename T, int kSp, bool kVec>
 bool launch_grad_of(const SsmParams& p, unsigned grid, int dev, cudaStream_t s) {
   static PerDevice ready;
   constexpr size_t bytes = sizeof(GradSmem<kSp>);
-  if (!ready.done(dev)) {
-    if (cudaFuncSetAttribute(ssm_grad_kernel<T, kSp, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-      return false;
-    ready.mark(dev);
-  }
+  if (!allow_smem(ssm_grad_kernel<T, kSp, kVec>, ready, dev, bytes)) return false;
   launch_early(ssm_grad_kernel<T, kSp, kVec>, dim3(grid), 32 * kSsmWarps, bytes, s, p);
   return true;
 }
@@ -1004,7 +1102,7 @@ bool launch_grad(const SsmParams& p, int sms, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const int64_t items = p.smax * p.G * p.parts;
   const unsigned grid = (unsigned)(items < 4 * sms ? items : 4 * sms);
-  const bool vec = vectors_ok(p, 4);
+  const bool vec = vectors_ok(p);
   bool ok = false;
   by_type(p.dtype, [&](auto t) {
     using T = decltype(t);
@@ -1044,9 +1142,9 @@ extern "C" int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const f
   p.final_state = final_state;
   cudaStream_t s = (cudaStream_t)stream;
   launch_plan(p, sms, s);
-  launch_walk<kWalkState>(p, sms, s);
+  if (T > 0 && !launch_walk<kWalkState>(p, sms, s)) return GDN_ERR_CUDA;
   launch_scan(p, s);
-  if (T > 0) launch_walk<kWalkOut>(p, sms, s);
+  if (T > 0 && !launch_walk<kWalkOut>(p, sms, s)) return GDN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -1074,7 +1172,7 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* z, const f
   p.da = da, p.dskip = dskip, p.dbias = ddt_bias, p.dinit = dinitial_state;
   cudaStream_t s = (cudaStream_t)stream;
   launch_plan(p, sms, s);
-  if (T > 0) launch_walk<kWalkGrad>(p, sms, s);
+  if (T > 0 && !launch_walk<kWalkGrad>(p, sms, s)) return GDN_ERR_CUDA;
   launch_scan(p, s);
   if (T > 0 && !launch_grad(p, sms, s)) return GDN_ERR_CUDA;
   launch_early(ssm_sum_kernel, dim3((unsigned)(4 * sms), n_init > 0 ? 4u : 3u), 256, 0, s, p);

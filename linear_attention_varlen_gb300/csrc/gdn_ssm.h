@@ -11,7 +11,8 @@
 namespace gdn {
 
 constexpr int kSsmTile = 16;     // tokens between two states that the backward keeps
-constexpr int kSsmMinSeg = 64;   // shortest segment, a multiple of the tile
+constexpr int kSsmMinSeg = 16;   // shortest segment, a multiple of the tile
+constexpr int kSsmFill = 8 * 152;  // warps of a walk that segments are cut for: eight to each of the GPU's SMs
 constexpr int kSsmMaxState = 64;
 
 // A segment: consecutive tokens of one document that one warp walks for its channels.
@@ -33,8 +34,8 @@ static_assert(sizeof(SsmHeader) == 256, "header is 256 bytes");
 
 __host__ __device__ constexpr int ssm_padded(int S) { return S <= 8 ? 8 : S <= 16 ? 16 : S <= 32 ? 32 : 64; }
 // channels to a warp of the walks forward in time, and of the backward's walk
-inline int ssm_walk_channels(int Sp) { return Sp <= 16 ? 64 : Sp == 32 ? 32 : 16; }
-inline int ssm_grad_channels(int Sp) { return 4 * 32 / (Sp / 4); }
+__host__ __device__ constexpr int ssm_walk_channels(int Sp) { return Sp <= 16 ? 64 : Sp == 32 ? 32 : 16; }
+__host__ __device__ constexpr int ssm_grad_channels(int Sp) { return 4 * 32 / (Sp / 4); }
 constexpr int kSsmWarps = 4;  // warps to a CTA
 
 // Workspace (byte offsets). State-sized arrays hold [Sp / 4][C][4] floats: four states of one channel together,
@@ -42,13 +43,19 @@ constexpr int kSsmWarps = 4;  // warps to a CTA
 struct SsmLayout {
   size_t header, segs, seg0, is_src, maps, slot, sums, slot_r, ckpt, csum, dstart, facc, part_a, part_c, part_m, total;
   int64_t smax, tiles;
+  int seg_tokens;  // most tokens to a segment
   int parts;  // CTAs of the backward's walk to a group of channels
 };
 
 inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   SsmLayout L{};
   const int Sp = ssm_padded(S);
-  L.smax = N + (int64_t)T / kSsmMinSeg;
+  const int ch = ssm_walk_channels(Sp);
+  const int64_t blocks = (int64_t)G * ((C / G + ch - 1) / ch), each = ((int64_t)T * blocks + kSsmFill - 1) / kSsmFill;
+  const int64_t len = (each + kSsmTile - 1) / kSsmTile * kSsmTile;
+  const int64_t all = ((int64_t)T + kSsmTile - 1) / kSsmTile * kSsmTile, most = len < all ? len : all;
+  L.seg_tokens = (int)(most < kSsmMinSeg ? kSsmMinSeg : most);
+  L.smax = N + (int64_t)T / L.seg_tokens;
   L.tiles = L.smax + T / kSsmTile + 1;
   const int per = kSsmWarps * ssm_grad_channels(Sp);
   L.parts = (C / G + per - 1) / per;
