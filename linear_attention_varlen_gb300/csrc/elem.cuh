@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "bw_prims.cuh"
+
 namespace gdn {
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -77,19 +79,35 @@ __device__ __forceinline__ float silu_slope(float x, float sig) {
   return sig == 0.f || sig == 1.f ? sig : sig * fmaf(x, 1.f - sig, 1.f);
 }
 
-// log(1 + e^r) = max(r, 0) + log1p(e^-|r|), with log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its series
-// 2 s (1 + s^2 / 3 + s^4 / 5 + ...), cut where the next term is below 2^-25 of the sum. Relative error about 2^-21 (the
-// exponential's, and its argument's rounding); NaN stays NaN.
-__device__ __forceinline__ float softplus(float r) {
-  const float e = exp2_approx(-kLog2e * fabsf(r));
-  const float s = e * rcp_approx(2.f + e), q = s * s;
-  float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  const float t = s + s;
-  return fmaxf(r, 0.f) + fmaf(t * q, p, t);
+// Pairs of the same in packed arithmetic.
+__device__ __forceinline__ uint64_t f2_dup(float v) { return bw::f2_pack(v, v); }
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) { return bw::f2_pack(exp2_approx(bw::f2_lo(x)), exp2_approx(bw::f2_hi(x))); }
+__device__ __forceinline__ uint64_t rcp_pair(uint64_t x) { return bw::f2_pack(rcp_approx(bw::f2_lo(x)), rcp_approx(bw::f2_hi(x))); }
+__device__ __forceinline__ uint64_t sigmoid_pair(uint64_t x) {
+  return rcp_pair(bw::f2_add(exp2_pair(bw::f2_mul(x, f2_dup(-kLog2e))), f2_dup(1.f)));
 }
+__device__ __forceinline__ float at_least(float x, float lo) {  // NaN stays NaN
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(lo));
+  return y;
+}
+// x sigmoid(x); from -128 down that is 0, and x is held there so that -inf gives 0 too
+__device__ __forceinline__ uint64_t silu_pair(uint64_t x) {
+  x = bw::f2_pack(at_least(bw::f2_lo(x), -128.f), at_least(bw::f2_hi(x), -128.f));
+  return bw::f2_mul(x, sigmoid_pair(x));
+}
+// log(1 + e^r) = max(r, 0) + log1p(e^-|r|), with log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, and the rest of
+// artanh(s) / s = 1 + s^2 p(s^2) by the cubic p nearest to 1/3 + q / 5 + q^2 / 7 + ... on [0, 1/9] (relative error of the
+// sum 6e-9). About 2^-21 in all (the exponential's error, and its argument's rounding); NaN stays NaN.
+__device__ __forceinline__ uint64_t softplus_pair(uint64_t r) {
+  const float lo = bw::f2_lo(r), hi = bw::f2_hi(r);
+  const uint64_t e = bw::f2_pack(exp2_approx(-kLog2e * fabsf(lo)), exp2_approx(-kLog2e * fabsf(hi)));
+  const uint64_t s = bw::f2_mul(e, rcp_pair(bw::f2_add(e, f2_dup(2.f)))), q = bw::f2_mul(s, s), t = bw::f2_add(s, s);
+  uint64_t p = bw::f2_fma(q, f2_dup(0.139937878f), f2_dup(0.140037894f));
+  p = bw::f2_fma(p, q, f2_dup(0.200105488f));
+  p = bw::f2_fma(p, q, f2_dup(0.333332121f));
+  return bw::f2_add(bw::f2_pack(fmaxf(lo, 0.f), fmaxf(hi, 0.f)), bw::f2_fma(bw::f2_mul(t, q), p, t));
+}
+__device__ __forceinline__ float softplus(float r) { return bw::f2_lo(softplus_pair(bw::f2_pack(r, 0.f))); }
 
 }  // namespace gdn

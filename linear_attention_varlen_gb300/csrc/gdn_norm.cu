@@ -128,11 +128,6 @@ __device__ __forceinline__ Raw8<T> load8(const T* row, int c, int D, const T* lo
   }
   return r;
 }
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // The same columns written, by whole warps whose lanes hold consecutive vectors. In rows that are not aligned a lane
 // writes the aligned pieces that begin inside its own vector, with the next lane's first elements; what no lane of
 // the warp can write whole (its first and last piece, a row's end) goes element by element.
@@ -304,7 +299,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kNv == 1 ? 256 : kRow
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[j][i] = bw::f2_pack(elem(x[j].t[2 * i]), elem(x[j].t[2 * i + 1]));
-        if (res) v[j][i] = f2_add(v[j][i], bw::f2_pack(elem(r[j].t[2 * i]), elem(r[j].t[2 * i + 1])));
+        if (res) v[j][i] = bw::f2_add(v[j][i], bw::f2_pack(elem(r[j].t[2 * i]), elem(r[j].t[2 * i + 1])));
         ss = bw::f2_fma(v[j][i], v[j][i], ss);
       }
   }
@@ -550,7 +545,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_team_kernel(const 
         dw[j][2 * i] = bw::f2_lo(d);
         dw[j][2 * i + 1] = bw::f2_hi(d);
         o[i] = bw::f2_fma(bw::f2_pack(wf[2 * i], wf[2 * i + 1]), gv, bw::f2_mul(c2, hv));
-        if (p.dh) o[i] = f2_add(o[i], bw::f2_pack(elem(er.t[2 * i]), elem(er.t[2 * i + 1])));
+        if (p.dh) o[i] = bw::f2_add(o[i], bw::f2_pack(elem(er.t[2 * i]), elem(er.t[2 * i + 1])));
       }
       store8<T, kRing>(dx, c, p.D, o);
     }

@@ -40,6 +40,12 @@ using bw::f2_mul;
 using bw::f2_pack;
 using bw::f2_sum;
 
+#ifndef SSM_BATCH
+#define SSM_BATCH 4
+#endif
+#ifndef SSM_OCC
+#define SSM_OCC 3
+#endif
 constexpr int kPlanThreads = 1024;
 
 struct SsmParams {
@@ -289,12 +295,12 @@ struct WalkShape {
 };
 
 template <typename T, int kSp, int kMode, bool kVec>
-__global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : kMode == kWalkOut || kSp == 32 ? 3 : 4)
+__global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : SSM_OCC)
     ssm_walk_kernel(const __grid_constant__ SsmParams p) {
   using W = WalkShape<T, kSp, kMode, kVec>;
   using R = typename W::R;
   constexpr int kNl = W::kNl, kNt = W::kNt, kDt = W::kDt, kCh = W::kCh, kTb = W::kTb;
-  constexpr int kQt = kNt / 4, kQ = kSp / 4, kP = kNt / 2;
+  constexpr int kQt = kNt / 4, kQ = kSp / 4, kP = kNt / 2, kBatch = SSM_BATCH;
   constexpr bool kGate = kMode != kWalkState;  // z is read
   static_assert(kCh == ssm_walk_channels(kSp));
   extern __shared__ __align__(16) uint8_t raw_smem[];
@@ -388,69 +394,93 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : kMode
       __syncwarp();
       const int rows = min(kTb, sg.ntok - i0);
       const float* maps = reinterpret_cast<const float*>(st + W::kTensors * W::kRowsBytes) + nl * kNt;
-#pragma unroll 2
-      for (int k = 0; k < rows; ++k) {
-        const int64_t t = sg.tok0 + i0 + k;
-        const float* mp = maps + k * 2 * kSp;
-        const auto xv = rx.template get<kDt>(st, k, t, dl * kDt);
-        const auto dv = rd.template get<kDt>(st + W::kRowsBytes, k, t, dl * kDt);
-        float x[kDt], gate[kDt], dy[kDt];
-        uint64_t dd[kDt], uu[kDt], y2[kDt];
+      for (int kb = 0; kb < rows; kb += kBatch) {
+        // steps and gates of kBatch tokens side by side (behind the last one of whatever lies there: not used)
+        constexpr int kN = kBatch * kDt;
+        float x[kN], delta[kN], gate[kN];
 #pragma unroll
-        for (int d = 0; d < kDt; ++d) {
-          x[d] = to_float(xv.t[d]);
-          const float raw = to_float(dv.t[d]) + bias[d];
-          const float delta = p.softplus ? softplus(raw) : raw, u = delta * x[d];
-          total[d] += delta;
-          dd[d] = f2_pack(delta, delta);
-          uu[d] = f2_pack(u, u);
-          y2[d] = 0;
-          gate[d] = 1.f;
-        }
-        if constexpr (kGate) {
-          if (has_z) {
-            const auto zv = rz.template get<kDt>(st + 2 * W::kRowsBytes, k, t, dl * kDt);
+        for (int k = 0; k < kBatch; ++k) {
+          const int64_t t = sg.tok0 + i0 + kb + k;
+          const auto xv = rx.template get<kDt>(st, kb + k, t, dl * kDt);
+          const auto dv = rd.template get<kDt>(st + W::kRowsBytes, kb + k, t, dl * kDt);
 #pragma unroll
-            for (int d = 0; d < kDt; ++d) {
-              const float z = to_float(zv.t[d]);
-              gate[d] = silu_of(z, sigmoid(z));
+          for (int d = 0; d < kDt; ++d) {
+            x[k * kDt + d] = to_float(xv.t[d]);
+            delta[k * kDt + d] = to_float(dv.t[d]) + bias[d];
+            gate[k * kDt + d] = 1.f;
+          }
+          if constexpr (kGate) {
+            if (has_z) {
+              const auto zv = rz.template get<kDt>(st + 2 * W::kRowsBytes, kb + k, t, dl * kDt);
+#pragma unroll
+              for (int d = 0; d < kDt; ++d) gate[k * kDt + d] = to_float(zv.t[d]);
             }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) {
+          if (p.softplus) {
+            const uint64_t v = softplus_pair(f2_pack(delta[i], delta[i + 1]));
+            delta[i] = f2_lo(v), delta[i + 1] = f2_hi(v);
+          }
+          if (has_z) {
+            const uint64_t v = silu_pair(f2_pack(gate[i], gate[i + 1]));
+            gate[i] = f2_lo(v), gate[i + 1] = f2_hi(v);
           }
         }
         if constexpr (kMode == kWalkGrad) {
-          const auto ov = ro.template get<kDt>(st + 3 * W::kRowsBytes, k, t, dl * kDt);
 #pragma unroll
-          for (int d = 0; d < kDt; ++d) dy[d] = to_float(ov.t[d]) * gate[d];
+          for (int k = 0; k < kBatch; ++k) {
+            const auto ov = ro.template get<kDt>(st + 3 * W::kRowsBytes, kb + k, sg.tok0 + i0 + kb + k, dl * kDt);
+#pragma unroll
+            for (int d = 0; d < kDt; ++d) gate[k * kDt + d] *= to_float(ov.t[d]);  // the gradient of y
+          }
         }
 #pragma unroll
-        for (int q = 0; q < kQt; ++q) {
-          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(mp + 4 * q);
-          ulonglong2 cv;
-          if (kMode != kWalkState) cv = *reinterpret_cast<const ulonglong2*>(mp + kSp + 4 * q);
+        for (int k = 0; k < kBatch; ++k) {
+          if (kb + k >= rows) break;
+          const float* mp = maps + (kb + k) * 2 * kSp;
+          uint64_t dd[kDt], uu[kDt], gg[kDt], y2[kDt];
 #pragma unroll
           for (int d = 0; d < kDt; ++d) {
+            const int i = k * kDt + d;
+            total[d] += delta[i];
+            dd[d] = f2_dup(delta[i]);
+            uu[d] = f2_dup(delta[i] * x[i]);
+            gg[d] = f2_dup(gate[i]);
+            y2[d] = 0;
+          }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint64_t arg = f2_mul(dd[d], A[d][2 * q + j]);
-              const uint64_t e = f2_pack(exp2_approx(f2_lo(arg)), exp2_approx(f2_hi(arg)));
-              h[d][2 * q + j] = f2_fma(e, h[d][2 * q + j], f2_mul(uu[d], j ? bv.y : bv.x));
-              if constexpr (kMode == kWalkOut) y2[d] = f2_fma(h[d][2 * q + j], j ? cv.y : cv.x, y2[d]);
-              if constexpr (kMode == kWalkGrad) {
-                pr[d][2 * q + j] = f2_mul(pr[d][2 * q + j], e);
-                ga[d][2 * q + j] = f2_fma(pr[d][2 * q + j], f2_mul(f2_pack(dy[d], dy[d]), j ? cv.y : cv.x), ga[d][2 * q + j]);
+          for (int q = 0; q < kQt; ++q) {
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(mp + 4 * q);
+            ulonglong2 cv;
+            if (kMode != kWalkState) cv = *reinterpret_cast<const ulonglong2*>(mp + kSp + 4 * q);
+#pragma unroll
+            for (int d = 0; d < kDt; ++d) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint64_t arg = f2_mul(dd[d], A[d][2 * q + j]);
+                const uint64_t e = exp2_pair(arg);
+                h[d][2 * q + j] = f2_fma(e, h[d][2 * q + j], f2_mul(uu[d], j ? bv.y : bv.x));
+                if constexpr (kMode == kWalkOut) y2[d] = f2_fma(h[d][2 * q + j], j ? cv.y : cv.x, y2[d]);
+                if constexpr (kMode == kWalkGrad) {
+                  pr[d][2 * q + j] = f2_mul(pr[d][2 * q + j], e);
+                  ga[d][2 * q + j] = f2_fma(pr[d][2 * q + j], f2_mul(gg[d], j ? cv.y : cv.x), ga[d][2 * q + j]);
+                }
               }
             }
           }
-        }
-        if constexpr (kMode == kWalkOut) {
-          Pack<T, kDt> r;
+          if constexpr (kMode == kWalkOut) {
+            Pack<T, kDt> r;
 #pragma unroll
-          for (int d = 0; d < kDt; ++d) {
-            float y = f2_sum(y2[d]);
-            if constexpr (kNl == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
-            r.t[d] = from_float<T>(fmaf(skip[d], x[d], y) * gate[d]);
+            for (int d = 0; d < kDt; ++d) {
+              float y = f2_sum(y2[d]);
+              if constexpr (kNl == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
+              r.t[d] = from_float<T>(fmaf(skip[d], x[k * kDt + d], y) * gate[k * kDt + d]);
+            }
+            if (nl == 0 && nch > 0)
+              store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + ((int64_t)sg.tok0 + i0 + kb + k) * p.C + c0, r, nch);
           }
-          if (nl == 0 && nch > 0) store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + t * p.C + c0, r, nch);
         }
       }
       __syncwarp();  // the stage is free
@@ -580,24 +610,40 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
 // ------------------------------------------------------------------------------ walk of the backward
 
 // A CTA of four warps walks a segment in reverse, tile by tile, each warp for 4 * 32 / kNl channels: a lane holds four
-// states of four channels, kNl = kSp / 4 lanes share a channel. Within a tile the states go forward again from the
-// kept one, every fourth of them through shared memory; four tokens at a time come back in reverse.
-template <int kSp>
+// states of four channels, pairs of states in packed fp32, kNl = kSp / 4 lanes share a channel. Within a tile the states
+// go forward again from the kept one, every fourth of them through shared memory; four tokens at a time come back in
+// reverse. The sums over the states of a channel and over the warp's channels are made by halving: at each exchange
+// between two lanes each keeps half of the values, so that a lane ends up with one channel's sums, and writes that
+// channel's gradients of the token.
+template <typename T, int kSp, bool kVec>
 struct GradSmem {
-  static constexpr int kNl = kSp / 4, kDl = 32 / kNl, kCh = 4 * kDl;
-  float maps[kSsmTile][2 * kSp];
-  float part[kSsmWarps][kSsmTile][2 * kSp];  // db and dc of each warp's channels
-  float delta[kSsmWarps][kSsmTile][kCh];
-  float u[kSsmWarps][kSsmTile][kCh];         // then du
-  float dy[kSsmWarps][kSsmTile][kCh];        // then sum_s a k exp(dt a) h_{t-1}
-  float y[kSsmWarps][kSsmTile][kCh];
+  static constexpr int kNl = kSp / 4, kDl = 32 / kNl, kCh = 4 * kDl, kCtaCh = kSsmWarps * kCh;
+  static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;  // two CTAs to an SM either way
+  using R = Rows<T, kCtaCh, kVec>;
+  uint8_t raw[kStages][4][kSsmTile * R::kBytes];  // x, dt, z, dout
+  float maps[kStages][kSsmTile][2 * kSp];
+  float part[kSsmWarps][kSsmTile][2 * kSp];       // db and dc of each warp's channels
+  float delta[kSsmWarps][kSsmTile][kCh], u[kSsmWarps][kSsmTile][kCh], dy[kSsmWarps][kSsmTile][kCh];
   float4 keep[kSsmWarps][kSsmTile / 4][4][32];
 };
 
+// v[0 .. kN - 1] of two lanes that differ in `mask` become the sums of the first half in the one without the bit, of
+// the second half in the other.
+template <int kN>
+__device__ __forceinline__ void halve(float* v, int mask, bool up) {
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) {
+    const float send = up ? v[i] : v[i + kN / 2], keep = up ? v[i + kN / 2] : v[i];
+    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, mask);
+  }
+}
+
 template <typename T, int kSp, bool kVec>
-__global__ void __launch_bounds__(32 * kSsmWarps) ssm_grad_kernel(const __grid_constant__ SsmParams p) {
-  using Smem = GradSmem<kSp>;
-  constexpr int kNl = Smem::kNl, kCh = Smem::kCh, kQ = kSp / 4, kTb = kSsmTile;
+__global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __grid_constant__ SsmParams p) {
+  using Smem = GradSmem<T, kSp, kVec>;
+  using R = typename Smem::R;
+  constexpr int kNl = Smem::kNl, kDl = Smem::kDl, kCh = Smem::kCh, kQ = kSp / 4, kTb = kSsmTile, kStages = Smem::kStages;
+  constexpr int kCl = kNl >= 4 ? 1 : 2;  // channels whose sums a lane ends up with
   extern __shared__ __align__(16) uint8_t raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
   bw::griddep_wait();
@@ -610,109 +656,135 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_grad_kernel(const __grid_c
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int seg = (int)(item / blocks), blk = (int)(item % blocks), g = blk / p.parts, part = blk % p.parts;
     const SsmSeg sg = p.segs[seg];
-    const int cb = (part * kSsmWarps + wid) * kCh;  // this warp's first channel in the group
-    const int cg = cb + 4 * dl;                     // this lane's
-    const int nch = max(0, min(4, Cg - cg));
-    const int c0 = g * Cg + min(cg, Cg - 1);
-    float A[4][4], K[4][4], dA[4][4], h0[4][4];
+    const int ctab = part * Smem::kCtaCh, cb = ctab + wid * kCh;  // first channel in the group: the CTA's, the warp's
+    const int nch = max(0, min(4, Cg - cb - 4 * dl));
+    const int c0 = g * Cg + min(cb + 4 * dl, Cg - 1), cmax = g * Cg + Cg - 1;
+    const int64_t first = (int64_t)g * Cg + ctab;
+    const int have = min(Smem::kCtaCh, Cg - ctab);
+    const R rx(p.x, p.sx, first, have, p.T, p.C), rd(p.dt, p.sdt, first, have, p.T, p.C);
+    const R rz(p.z, p.sz, first, have, p.T, p.C), ro(p.dout, p.sdo, first, have, p.T, p.C);
+    auto fetch = [&](int tile) {
+      const int st = tile % kStages, rows = min(kTb, sg.ntok - tile * kTb);
+      const int64_t t = sg.tok0 + tile * kTb;
+      rx.template fetch<kTb>(sm.raw[st][0], t, rows, threadIdx.x, 32 * kSsmWarps);
+      rd.template fetch<kTb>(sm.raw[st][1], t, rows, threadIdx.x, 32 * kSsmWarps);
+      if (has_z) rz.template fetch<kTb>(sm.raw[st][2], t, rows, threadIdx.x, 32 * kSsmWarps);
+      ro.template fetch<kTb>(sm.raw[st][3], t, rows, threadIdx.x, 32 * kSsmWarps);
+      for (int i = threadIdx.x; i < kTb * (kSp / 2); i += 32 * kSsmWarps) {  // zeros behind the last token
+        const int k = i / (kSp / 2), r = i % (kSp / 2);
+        cp_async16_if(&sm.maps[st][k][4 * r], p.maps + ((t + min(k, rows - 1)) * p.G + g) * 2 * kSp + 4 * r, k < rows);
+      }
+      cp_async_commit();
+    };
+    const int tiles = (sg.ntok + kTb - 1) / kTb;
+    if (tiles > 0) fetch(tiles - 1);
+    uint64_t A[4][2], K[4][2], dA[4][2];  // A in units of log2 e
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const int c = min(c0 + d, g * Cg + Cg - 1);
+      const int c = min(c0 + d, cmax);
       const float4 av = pool_quad(p.a, 0, p.C, p.S, c, nl);
-      const int64_t at = (((int64_t)seg * kQ + nl) * p.C + c) * 4;
-      const float4 kv = *reinterpret_cast<const float4*>(p.slot_r + at);
-      float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (sg.src >= 0)
-        hv = pool_quad(p.init, sg.src, p.C, p.S, c, nl);
-      else if (sg.src == -2)
-        hv = *reinterpret_cast<const float4*>(p.slot + at);
-      A[d][0] = av.x, A[d][1] = av.y, A[d][2] = av.z, A[d][3] = av.w;
-      K[d][0] = kv.x, K[d][1] = kv.y, K[d][2] = kv.z, K[d][3] = kv.w;
-      h0[d][0] = hv.x, h0[d][1] = hv.y, h0[d][2] = hv.z, h0[d][3] = hv.w;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) dA[d][n] = 0.f;
+      const float4 kv = *reinterpret_cast<const float4*>(p.slot_r + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
+      A[d][0] = f2_pack(av.x * kLog2e, av.y * kLog2e), A[d][1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
+      K[d][0] = f2_pack(kv.x, kv.y), K[d][1] = f2_pack(kv.z, kv.w);
+      dA[d][0] = dA[d][1] = 0;
     }
-    // for loads and stores a lane takes four channels of every (32 / (kCh / 4))th token
-    constexpr int kLq = kCh / 4, kLt = 32 / kLq;
-    const int lq = lane % kLq, lt = lane / kLq;
-    const int lcg = cb + 4 * lq, ln = max(0, min(4, Cg - lcg)), lc0 = g * Cg + min(lcg, Cg - 1);
-    float bias[4], skip[4], dskip[4] = {0.f, 0.f, 0.f, 0.f}, dbias[4] = {0.f, 0.f, 0.f, 0.f};
+    // for the steps a lane takes four channels of every kNl-th token
+    const int lq = lane % kDl, lt = lane / kDl, lcg = cb + 4 * lq, ln = max(0, min(4, Cg - lcg));
+    // and the gradients of channel ec[j], where it exists
+    int ec[kCl];
+    bool ev[kCl];
+    float bias[kCl], skip[kCl], dskip[kCl], dbias[kCl];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = min(lc0 + j, g * Cg + Cg - 1);
-      bias[j] = p.dt_bias ? p.dt_bias[c] : 0.f;
-      skip[j] = p.skip ? p.skip[c] : 0.f;
+    for (int j = 0; j < kCl; ++j) {
+      const int at = 4 * dl + (kCl == 1 ? (nl & 3) : 2 * nl + j);  // in the warp
+      ev[j] = nl < 4 && cb + at < Cg;
+      ec[j] = g * Cg + min(cb + at, Cg - 1);
+      bias[j] = p.dt_bias ? p.dt_bias[ec[j]] : 0.f;
+      skip[j] = p.skip ? p.skip[ec[j]] : 0.f;
+      dskip[j] = dbias[j] = 0.f;
     }
-    const int tiles = (sg.ntok + kTb - 1) / kTb;
     for (int tile = tiles - 1; tile >= 0; --tile) {
+      const int st = tile % kStages;
       const int64_t t0 = sg.tok0 + tile * kTb;
       const int nt = min(kTb, sg.ntok - tile * kTb);
-      for (int i = threadIdx.x; i < kTb * 2 * kSp / 4; i += 32 * kSsmWarps) {
-        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < nt) v = *reinterpret_cast<const float4*>(p.maps + ((t0 + k) * p.G + g) * 2 * kSp + 4 * r);
-        reinterpret_cast<float4*>(sm.maps[k])[r] = v;
+      // the state before the tile: kept from zero, and what is left of the segment's start state
+      uint64_t h[4][2];
+      {
+        const int64_t tl = sg.tok0 / kSsmTile + seg + tile;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int c = min(c0 + d, cmax);
+          float4 f = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
+          if (sg.src != -1) {
+            const float4 s = sg.src >= 0 ? pool_quad(p.init, sg.src, p.C, p.S, c, nl)
+                                         : *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
+            const float time = p.csum[tl * p.C + c];
+            const float4 a = make_float4(f2_lo(A[d][0]), f2_hi(A[d][0]), f2_lo(A[d][1]), f2_hi(A[d][1]));
+            f = make_float4(fmaf(exp2_approx(a.x * time), s.x, f.x), fmaf(exp2_approx(a.y * time), s.y, f.y),
+                            fmaf(exp2_approx(a.z * time), s.z, f.z), fmaf(exp2_approx(a.w * time), s.w, f.w));
+          }
+          h[d][0] = f2_pack(f.x, f.y), h[d][1] = f2_pack(f.z, f.w);
+        }
       }
-      for (int k = lt; k < kTb; k += kLt) {
+      cp_async_wait<0>();
+      __syncthreads();  // this tile has landed, and every warp is done with the one before
+      if (kStages == 2 && tile > 0) fetch(tile - 1);
+      for (int k = lt; k < kTb; k += kNl) {
         float dv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f}, gv[4] = {0.f, 0.f, 0.f, 0.f};
         if (k < nt) {
           const int64_t t = t0 + k;
-          const auto xr = load_pack<T, 4, kVec>(static_cast<const T*>(p.x) + t * p.sx + lc0, ln);
-          const auto dr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dt) + t * p.sdt + lc0, ln);
-          const auto gr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dout) + t * p.sdo + lc0, ln);
+          const int at = wid * kCh + 4 * lq;
+          const auto xr = rx.template get<4>(sm.raw[st][0], k, t, at);
+          const auto dr = rd.template get<4>(sm.raw[st][1], k, t, at);
+          const auto gr = ro.template get<4>(sm.raw[st][3], k, t, at);
           Pack<T, 4> zr{};
-          if (has_z) zr = load_pack<T, 4, kVec>(static_cast<const T*>(p.z) + t * p.sz + lc0, ln);
+          if (has_z) zr = rz.template get<4>(sm.raw[st][2], k, t, at);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < ln) dv[j] = to_float(dr.t[j]) + (p.dt_bias ? p.dt_bias[g * Cg + lcg + j] : 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            if (p.softplus) {
+              const uint64_t v = softplus_pair(f2_pack(dv[j], dv[j + 1]));
+              dv[j] = f2_lo(v), dv[j + 1] = f2_hi(v);
+            }
+            uint64_t gate = f2_dup(1.f);
+            if (has_z) gate = silu_pair(f2_pack(to_float(zr.t[j]), to_float(zr.t[j + 1])));
+            gv[j] = to_float(gr.t[j]) * f2_lo(gate), gv[j + 1] = to_float(gr.t[j + 1]) * f2_hi(gate);
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float raw = to_float(dr.t[j]) + bias[j];
-            dv[j] = p.softplus ? softplus(raw) : raw;
             uv[j] = dv[j] * to_float(xr.t[j]);
-            gv[j] = to_float(gr.t[j]);
-            if (has_z) {
-              const float zv = to_float(zr.t[j]);
-              gv[j] *= silu_of(zv, sigmoid(zv));
-            }
+            if (j >= ln) dv[j] = uv[j] = gv[j] = 0.f;
           }
         }
         *reinterpret_cast<float4*>(&sm.delta[wid][k][4 * lq]) = make_float4(dv[0], dv[1], dv[2], dv[3]);
         *reinterpret_cast<float4*>(&sm.u[wid][k][4 * lq]) = make_float4(uv[0], uv[1], uv[2], uv[3]);
         *reinterpret_cast<float4*>(&sm.dy[wid][k][4 * lq]) = make_float4(gv[0], gv[1], gv[2], gv[3]);
       }
-      __syncthreads();
+      __syncwarp();
       auto row4 = [&](const float* r, float* v) {
         const float4 f = *reinterpret_cast<const float4*>(r);
         v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
       };
-      float h[4][4];
-      {
-        const int64_t tl = sg.tok0 / kSsmTile + seg + tile;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int c = min(c0 + d, g * Cg + Cg - 1);
-          const float time = p.csum[tl * p.C + c] * kLog2e;
-          const float4 f = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
-          h[d][0] = fmaf(exp2_approx(A[d][0] * time), h0[d][0], f.x);
-          h[d][1] = fmaf(exp2_approx(A[d][1] * time), h0[d][1], f.y);
-          h[d][2] = fmaf(exp2_approx(A[d][2] * time), h0[d][2], f.z);
-          h[d][3] = fmaf(exp2_approx(A[d][3] * time), h0[d][3], f.w);
-        }
-      }
       // one token forward: h = e h + u b
       auto forward = [&](int k) {
-        float dv[4], uv[4], bv[4];
+        float dv[4], uv[4];
         row4(&sm.delta[wid][k][4 * dl], dv);
         row4(&sm.u[wid][k][4 * dl], uv);
-        row4(&sm.maps[k][4 * nl], bv);
+        const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sm.maps[st][k][4 * nl]);
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            h[d][n] = fmaf(exp2_approx(dv[d] * kLog2e * A[d][n]), h[d][n], uv[d] * bv[n]);
+        for (int d = 0; d < 4; ++d) {
+          const uint64_t dd = f2_dup(dv[d]), uu = f2_dup(uv[d]);
+          h[d][0] = f2_fma(exp2_pair(f2_mul(dd, A[d][0])), h[d][0], f2_mul(uu, bv.x));
+          h[d][1] = f2_fma(exp2_pair(f2_mul(dd, A[d][1])), h[d][1], f2_mul(uu, bv.y));
+        }
       };
       const int subs = (nt + 3) / 4;
       for (int s = 0; s < subs; ++s) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d) sm.keep[wid][s][d][lane] = make_float4(h[d][0], h[d][1], h[d][2], h[d][3]);
+        for (int d = 0; d < 4; ++d)
+          *reinterpret_cast<ulonglong2*>(&sm.keep[wid][s][d][lane]) = make_ulonglong2(h[d][0], h[d][1]);
         if (s + 1 < subs) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) forward(4 * s + k);
@@ -721,139 +793,131 @@ __global__ void __launch_bounds__(32 * kSsmWarps) ssm_grad_kernel(const __grid_c
       for (int s = subs - 1; s >= 0; --s) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const float4 f = sm.keep[wid][s][d][lane];
-          h[d][0] = f.x, h[d][1] = f.y, h[d][2] = f.z, h[d][3] = f.w;
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sm.keep[wid][s][d][lane]);
+          h[d][0] = f.x, h[d][1] = f.y;
         }
-        float hb[4][4][4];  // states before each of the four tokens
+        uint64_t hb[4][4][2];  // states before each of the four tokens
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) hb[k][d][n] = h[d][n];
+          for (int d = 0; d < 4; ++d) hb[k][d][0] = h[d][0], hb[k][d][1] = h[d][1];
           forward(4 * s + k);  // behind the last token dt, u, b and c are 0: the state stays
         }
 #pragma unroll
         for (int k = 3; k >= 0; --k) {
-          const int t = 4 * s + k;
-          float dv[4], uv[4], gv[4], bv[4], cv[4], du[4], va[4], yv[4], db[4], dc[4];
-          row4(&sm.delta[wid][t][4 * dl], dv);
-          row4(&sm.u[wid][t][4 * dl], uv);
-          row4(&sm.dy[wid][t][4 * dl], gv);
-          row4(&sm.maps[t][4 * nl], bv);
-          row4(&sm.maps[t][kSp + 4 * nl], cv);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) db[n] = dc[n] = 0.f;
+          const int tk = 4 * s + k;
+          float dv[4], uv[4], gv[4];
+          row4(&sm.delta[wid][tk][4 * dl], dv);
+          row4(&sm.u[wid][tk][4 * dl], uv);
+          row4(&sm.dy[wid][tk][4 * dl], gv);
+          const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sm.maps[st][tk][4 * nl]);
+          const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sm.maps[st][tk][kSp + 4 * nl]);
+          uint64_t db[2] = {0, 0}, dc[2] = {0, 0};
+          float v[12], w[8];  // of each channel the sums of K b, A (K e) h and c h; of each state those of u K and dy h
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            du[d] = va[d] = yv[d] = 0.f;
+            const uint64_t dd = f2_dup(dv[d]), uu = f2_dup(uv[d]), gg = f2_dup(gv[d]);
+            uint64_t du = 0, va = 0, yv = 0;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const float hn = k == 3 ? h[d][n] : hb[k == 3 ? 3 : k + 1][d][n];
-              K[d][n] = fmaf(gv[d], cv[n], K[d][n]);
-              yv[d] = fmaf(cv[n], hn, yv[d]);
-              dc[n] = fmaf(gv[d], hn, dc[n]);
-              db[n] = fmaf(uv[d], K[d][n], db[n]);
-              du[d] = fmaf(bv[n], K[d][n], du[d]);
-              const float w = K[d][n] * exp2_approx(dv[d] * kLog2e * A[d][n]);
-              const float v = w * hb[k][d][n];
-              va[d] = fmaf(A[d][n], v, va[d]);
-              dA[d][n] = fmaf(dv[d], v, dA[d][n]);
-              K[d][n] = w;
+            for (int n = 0; n < 2; ++n) {
+              const uint64_t hn = k == 3 ? h[d][n] : hb[k == 3 ? 3 : k + 1][d][n], b = n ? bv.y : bv.x, c = n ? cv.y : cv.x;
+              K[d][n] = f2_fma(gg, c, K[d][n]);
+              yv = f2_fma(c, hn, yv);
+              dc[n] = f2_fma(gg, hn, dc[n]);
+              db[n] = f2_fma(uu, K[d][n], db[n]);
+              du = f2_fma(b, K[d][n], du);
+              K[d][n] = f2_mul(K[d][n], exp2_pair(f2_mul(dd, A[d][n])));
+              const uint64_t kh = f2_mul(K[d][n], hb[k][d][n]);
+              va = f2_fma(A[d][n], kh, va);
+              dA[d][n] = f2_fma(dd, kh, dA[d][n]);
             }
+            v[3 * d] = f2_sum(du), v[3 * d + 1] = f2_sum(va), v[3 * d + 2] = f2_sum(yv);
           }
-          // sums over the states (lanes of one channel) and over this warp's channels
+          // over the states: the lane's channels at the end are those of ec
+          if constexpr (kNl >= 4) {
+            halve<12>(v, 2, nl & 2);
+            halve<6>(v, 1, nl & 1);
 #pragma unroll
-          for (int o = 1; o < kNl; o <<= 1)
+            for (int o = 4; o < kNl; o <<= 1)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              du[d] += __shfl_xor_sync(0xffffffffu, du[d], o);
-              va[d] += __shfl_xor_sync(0xffffffffu, va[d], o);
-              yv[d] += __shfl_xor_sync(0xffffffffu, yv[d], o);
-            }
-#pragma unroll
-          for (int o = kNl; o < 32; o <<= 1)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              db[n] += __shfl_xor_sync(0xffffffffu, db[n], o);
-              dc[n] += __shfl_xor_sync(0xffffffffu, dc[n], o);
-            }
-          __syncwarp();
-          if (nl == 0) {
-            *reinterpret_cast<float4*>(&sm.u[wid][t][4 * dl]) = make_float4(du[0], du[1], du[2], du[3]);
-            *reinterpret_cast<float4*>(&sm.dy[wid][t][4 * dl]) = make_float4(va[0], va[1], va[2], va[3]);
-            *reinterpret_cast<float4*>(&sm.y[wid][t][4 * dl]) = make_float4(yv[0], yv[1], yv[2], yv[3]);
+              for (int i = 0; i < 3; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+          } else {
+            halve<12>(v, 1, nl & 1);
           }
-          if (dl == 0) {
-            *reinterpret_cast<float4*>(&sm.part[wid][t][4 * nl]) = make_float4(db[0], db[1], db[2], db[3]);
-            *reinterpret_cast<float4*>(&sm.part[wid][t][kSp + 4 * nl]) = make_float4(dc[0], dc[1], dc[2], dc[3]);
+          // over the channels: a lane keeps kW of the eight sums
+          constexpr int kW = kDl >= 8 ? 1 : kDl == 4 ? 2 : 4;
+          w[0] = f2_lo(db[0]), w[1] = f2_hi(db[0]), w[2] = f2_lo(db[1]), w[3] = f2_hi(db[1]);
+          w[4] = f2_lo(dc[0]), w[5] = f2_hi(dc[0]), w[6] = f2_lo(dc[1]), w[7] = f2_hi(dc[1]);
+          int at = 0;  // the first of them
+          if constexpr (kDl >= 8) {
+            halve<8>(w, 4 * kNl, dl & 4);
+            halve<4>(w, 2 * kNl, dl & 2);
+            halve<2>(w, kNl, dl & 1);
+            if constexpr (kDl == 16) w[0] += __shfl_xor_sync(0xffffffffu, w[0], 8 * kNl);
+            at = dl & 7;
+          } else if constexpr (kDl == 4) {
+            halve<8>(w, 2 * kNl, dl & 2);
+            halve<4>(w, kNl, dl & 1);
+            at = 2 * dl;
+          } else {
+            halve<8>(w, kNl, dl & 1);
+            at = 4 * dl;
+          }
+          if (dl < 8) {
+#pragma unroll
+            for (int i = 0; i < kW; ++i) sm.part[wid][tk][(at + i) / 4 * kSp + 4 * nl + (at + i) % 4] = w[i];
+          }
+          if (tk < nt) {
+            const int64_t t = t0 + tk;
+#pragma unroll
+            for (int j = 0; j < kCl; ++j) {
+              if (!ev[j]) continue;
+              const int rc = ec[j] - (int)first, wc = rc - wid * kCh;  // in the CTA's rows, in the warp's
+              const float x = to_float(rx.template get<1>(sm.raw[st][0], tk, t, rc).t[0]);
+              const float raw = to_float(rd.template get<1>(sm.raw[st][1], tk, t, rc).t[0]) + bias[j];
+              float dyv = to_float(ro.template get<1>(sm.raw[st][3], tk, t, rc).t[0]);
+              const float du = v[3 * j], va = v[3 * j + 1] * (1.f / kLog2e), yv = v[3 * j + 2];
+              const int64_t o = t * p.C + ec[j];
+              if (has_z) {
+                const float zv = to_float(rz.template get<1>(sm.raw[st][2], tk, t, rc).t[0]), sig = sigmoid(zv);
+                static_cast<T*>(p.dz)[o] = from_float<T>(dyv * fmaf(skip[j], x, yv) * silu_slope(zv, sig));
+                dyv = sm.dy[wid][tk][wc];
+              }
+              static_cast<T*>(p.dx)[o] = from_float<T>(fmaf(sm.delta[wid][tk][wc], du, skip[j] * dyv));
+              float dd = fmaf(x, du, va);
+              if (p.softplus) dd *= sigmoid(raw);
+              static_cast<T*>(p.ddt)[o] = from_float<T>(dd);
+              dbias[j] += dd;
+              dskip[j] = fmaf(dyv, x, dskip[j]);
+            }
           }
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < nt * 2 * kSp; i += 32 * kSsmWarps) {
-        const int k = i / (2 * kSp), r = i % (2 * kSp);
-        float v = 0.f;
+      if (kStages == 1 && tile > 0) fetch(tile - 1);
+      for (int i = threadIdx.x; i < nt * (kSp / 2); i += 32 * kSsmWarps) {
+        const int k = i / (kSp / 2), r = i % (kSp / 2);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kSsmWarps; ++w) v += sm.part[w][k][r];
-        p.part_m[(((int64_t)part * p.T + t0 + k) * p.G + g) * 2 * kSp + r] = v;
-      }
-      for (int k = lt; k < nt; k += kLt) {
-        const int64_t t = t0 + k;
-        const auto xr = load_pack<T, 4, kVec>(static_cast<const T*>(p.x) + t * p.sx + lc0, ln);
-        const auto dr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dt) + t * p.sdt + lc0, ln);
-        const auto gr = load_pack<T, 4, kVec>(static_cast<const T*>(p.dout) + t * p.sdo + lc0, ln);
-        Pack<T, 4> zr{}, dxr, ddr, dzr;
-        if (has_z) zr = load_pack<T, 4, kVec>(static_cast<const T*>(p.z) + t * p.sz + lc0, ln);
-        float du[4], va[4], yv[4], dv[4];
-        row4(&sm.u[wid][k][4 * lq], du);
-        row4(&sm.dy[wid][k][4 * lq], va);
-        row4(&sm.y[wid][k][4 * lq], yv);
-        row4(&sm.delta[wid][k][4 * lq], dv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float xv = to_float(xr.t[j]);
-          float dyv = to_float(gr.t[j]);
-          if (has_z) {
-            const float zv = to_float(zr.t[j]), sig = sigmoid(zv);
-            dzr.t[j] = from_float<T>(dyv * fmaf(skip[j], xv, yv[j]) * silu_slope(zv, sig));
-            dyv *= silu_of(zv, sig);
-          }
-          dxr.t[j] = from_float<T>(fmaf(dv[j], du[j], skip[j] * dyv));
-          float dd = fmaf(xv, du[j], va[j]);
-          if (p.softplus) dd *= sigmoid(to_float(dr.t[j]) + bias[j]);
-          ddr.t[j] = from_float<T>(dd);
-          dbias[j] += dd;
-          dskip[j] = fmaf(dyv, xv, dskip[j]);
+        for (int w = 0; w < kSsmWarps; ++w) {
+          const float4 e = *reinterpret_cast<const float4*>(&sm.part[w][k][4 * r]);
+          f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
         }
-        if (ln > 0) {
-          store_pack<T, 4, kVec>(static_cast<T*>(p.dx) + t * p.C + lc0, dxr, ln);
-          store_pack<T, 4, kVec>(static_cast<T*>(p.ddt) + t * p.C + lc0, ddr, ln);
-          if (has_z) store_pack<T, 4, kVec>(static_cast<T*>(p.dz) + t * p.C + lc0, dzr, ln);
-        }
+        *reinterpret_cast<float4*>(p.part_m + (((int64_t)part * p.T + t0 + k) * p.G + g) * 2 * kSp + 4 * r) = f;
       }
-      __syncthreads();
     }
+    __syncthreads();  // the next item's copies go where this one's tiles were
 #pragma unroll
     for (int d = 0; d < 4; ++d)
       if (d < nch)
         *reinterpret_cast<float4*>(p.part_a + (((int64_t)seg * kQ + nl) * p.C + c0 + d) * 4) =
-            make_float4(dA[d][0], dA[d][1], dA[d][2], dA[d][3]);
+            make_float4(f2_lo(dA[d][0]), f2_hi(dA[d][0]), f2_lo(dA[d][1]), f2_hi(dA[d][1]));
 #pragma unroll
-    for (int o = kLq; o < 32; o <<= 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        dskip[j] += __shfl_xor_sync(0xffffffffu, dskip[j], o);
-        dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], o);
+    for (int j = 0; j < kCl; ++j)
+      if (ev[j]) {
+        p.part_c[((int64_t)seg * 2) * p.C + ec[j]] = dskip[j];
+        p.part_c[((int64_t)seg * 2 + 1) * p.C + ec[j]] = dbias[j];
       }
-    if (lt == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < ln) {
-          p.part_c[((int64_t)seg * 2) * p.C + lc0 + j] = dskip[j];
-          p.part_c[((int64_t)seg * 2 + 1) * p.C + lc0 + j] = dbias[j];
-        }
-    }
   }
 }
 
@@ -1091,7 +1155,7 @@ void launch_scan(const SsmParams& p, cudaStream_t s) {
 template <typename T, int kSp, bool kVec>
 bool launch_grad_of(const SsmParams& p, unsigned grid, int dev, cudaStream_t s) {
   static PerDevice ready;
-  constexpr size_t bytes = sizeof(GradSmem<kSp>);
+  constexpr size_t bytes = sizeof(GradSmem<T, kSp, kVec>);
   if (!allow_smem(ssm_grad_kernel<T, kSp, kVec>, ready, dev, bytes)) return false;
   launch_early(ssm_grad_kernel<T, kSp, kVec>, dim3(grid), 32 * kSsmWarps, bytes, s, p);
   return true;
