@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bw_prims.cuh"
 
@@ -56,6 +57,20 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, K>& r, int n) {
   }
 }
 
+// Asynchronous copies of 16 bytes into shared memory.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(bw::smem_u32(dst)), "l"(src) : "memory");
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_if(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(bw::smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
 // 2^x, relative error about 2^-22
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -79,6 +94,60 @@ __device__ __forceinline__ float silu_slope(float x, float sig) {
   return sig == 0.f || sig == 1.f ? sig : sig * fmaf(x, 1.f - sig, 1.f);
 }
 
+// 16 bytes of elements, kept as words until they are used: pair i of them, and its place taken by two values rounded.
+struct alignas(16) Words {
+  uint32_t w[4];
+};
+template <typename T>
+constexpr int kPairs = 8 / (int)sizeof(T);
+template <typename T>
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* w, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return bw::f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    return bw::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+    return bw::f2_pack(f.x, f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint64_t pair_of(const Words& r, int i) {
+  return pair_of<T>(r.w, i);
+}
+template <typename T>
+__device__ __forceinline__ void set_pair(uint32_t* w, int i, uint64_t v) {
+  if constexpr (sizeof(T) == 4) {
+    w[2 * i] = __float_as_uint(bw::f2_lo(v));
+    w[2 * i + 1] = __float_as_uint(bw::f2_hi(v));
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    w[i] = bw::pack_bf16x2(bw::f2_lo(v), bw::f2_hi(v));
+  } else {
+    const __half2 h = __floats2half2_rn(bw::f2_lo(v), bw::f2_hi(v));
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void set_pair(Words& r, int i, uint64_t v) {
+  set_pair<T>(r.w, i, v);
+}
+template <typename T>
+__device__ __forceinline__ T element_of(const Words& r, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(r.w[i]);
+  } else {
+    const uint16_t h = (uint16_t)(r.w[i / 2] >> (i % 2 * 16));
+    return *reinterpret_cast<const T*>(&h);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void set_element(Words& r, int i, T v) {  // into zeros
+  if constexpr (sizeof(T) == 4)
+    r.w[i] = __float_as_uint(v);
+  else
+    r.w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(&v) << (i % 2 * 16);
+}
+
 // Pairs of the same in packed arithmetic.
 __device__ __forceinline__ uint64_t f2_dup(float v) { return bw::f2_pack(v, v); }
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) { return bw::f2_pack(exp2_approx(bw::f2_lo(x)), exp2_approx(bw::f2_hi(x))); }
@@ -95,6 +164,14 @@ __device__ __forceinline__ float at_least(float x, float lo) {  // NaN stays NaN
 __device__ __forceinline__ uint64_t silu_pair(uint64_t x) {
   x = bw::f2_pack(at_least(bw::f2_lo(x), -128.f), at_least(bw::f2_hi(x), -128.f));
   return bw::f2_mul(x, sigmoid_pair(x));
+}
+// d silu / dx = sig (1 + x (1 - sig)), x held within its limits' reach
+__device__ __forceinline__ uint64_t silu_slope_pair(uint64_t x, uint64_t sig) {
+  float lo, hi;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(at_least(bw::f2_lo(x), -128.f)), "f"(128.f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(at_least(bw::f2_hi(x), -128.f)), "f"(128.f));
+  const uint64_t rest = bw::f2_fma(sig, f2_dup(-1.f), f2_dup(1.f));
+  return bw::f2_mul(sig, bw::f2_fma(bw::f2_pack(lo, hi), rest, f2_dup(1.f)));
 }
 // log(1 + e^r) = max(r, 0) + log1p(e^-|r|), with log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, and the rest of
 // artanh(s) / s = 1 + s^2 p(s^2) by the cubic p nearest to 1/3 + q / 5 + q^2 / 7 + ... on [0, 1/9] (relative error of the

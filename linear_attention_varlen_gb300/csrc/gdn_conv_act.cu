@@ -6,8 +6,9 @@
 // dbias = sum_p du[p]. u is formed again from x: nothing but the inputs is kept between the two directions.
 //
 // All of it is bound by memory traffic: each input is read once, each output written once, but for the three rows
-// before a block of tokens (and the three behind it in the backward). A thread takes 16 bytes of channels down the
-// tokens of a block, the window of three inputs in registers.
+// before a block of tokens (and the three behind it in the backward). A thread takes four channels, in packed pairs, down
+// the tokens of a block, the window of three inputs in registers; four rows at a time are worked on while the next four
+// are on their way. Four rows of one document go without a look at its bounds.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,7 +26,15 @@ namespace {
 
 constexpr int kActThreads = 128;
 constexpr int kFwdTokens = 32, kBwdTokens = 64;  // tokens to a block
-constexpr int kAhead = 4;                        // rows in flight
+constexpr int kRows = 4;                         // rows at a time
+constexpr int kCh = 4, kPr = kCh / 2;             // channels of a thread, and their pairs
+
+using bw::f2_add;
+using bw::f2_fma;
+using bw::f2_hi;
+using bw::f2_lo;
+using bw::f2_mul;
+using bw::f2_pack;
 
 struct ActHeader {
   int32_t status, forks;
@@ -70,9 +79,6 @@ inline ActLayout act_layout(int N, int T, int C, bool bwd) {
   return L;
 }
 
-template <typename T>
-constexpr int kVecOf = 16 / (int)sizeof(T);
-
 // Row e (of three) in front of document d, and row k of its tail: an input, an entry of the pool, or null for zero.
 // A fork's start is the tail of an earlier document, so the walk ends.
 template <typename T>
@@ -99,16 +105,21 @@ __device__ __forceinline__ int doc_at(const int32_t* cu, int N, int t) {  // the
   return lo;
 }
 
-template <typename T, int K>
-__device__ __forceinline__ void unpack(const Pack<T, K>& r, float* f) {
-#pragma unroll
-  for (int i = 0; i < K; ++i) f[i] = to_float(r.t[i]);
+// Four channels as they lie in memory.
+template <typename T>
+struct alignas(sizeof(T) * kCh) Raw4 {
+  uint32_t w[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw4<T> row_or_zero(const T* row, int c) {
+  Raw4<T> r{};
+  if (row) r = *reinterpret_cast<const Raw4<T>*>(row + c);
+  return r;
 }
-template <typename T, int K>
-__device__ __forceinline__ void row_or_zero(const T* row, int c, float* f) {
-  Pack<T, K> r{};
-  if (row) r = *reinterpret_cast<const Pack<T, K>*>(row + c);
-  unpack(r, f);
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw4<T>& r, uint64_t* f) {
+#pragma unroll
+  for (int i = 0; i < kPr; ++i) f[i] = pair_of<T>(r.w, i);
 }
 
 __global__ void __launch_bounds__(256) act_check_kernel(const __grid_constant__ ActParams p) {
@@ -136,52 +147,98 @@ __global__ void __launch_bounds__(256) act_check_kernel(const __grid_constant__ 
   }
 }
 
+struct Taps {
+  uint64_t w[4][kPr], bias[kPr];
+  __device__ __forceinline__ Taps(const float* wp, const float* bp, int c) {
+    float4 v[kCh];
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) v[i] = *reinterpret_cast<const float4*>(wp + (int64_t)(c + i) * 4);
+#pragma unroll
+    for (int i = 0; i < kPr; ++i) {
+      w[0][i] = f2_pack(v[2 * i].x, v[2 * i + 1].x), w[1][i] = f2_pack(v[2 * i].y, v[2 * i + 1].y);
+      w[2][i] = f2_pack(v[2 * i].z, v[2 * i + 1].z), w[3][i] = f2_pack(v[2 * i].w, v[2 * i + 1].w);
+      bias[i] = bp ? f2_pack(bp[c + 2 * i], bp[c + 2 * i + 1]) : 0;
+    }
+  }
+  // u of the fourth of four consecutive inputs
+  __device__ __forceinline__ uint64_t dot(int i, uint64_t a, uint64_t b, uint64_t c, uint64_t d) const {
+    return f2_fma(w[3][i], d, f2_fma(w[2][i], c, f2_fma(w[1][i], b, f2_fma(w[0][i], a, bias[i]))));
+  }
+};
+
 // Blocks of kFwdTokens tokens, then one block for each document's tail.
 template <typename T>
 __global__ void __launch_bounds__(kActThreads) act_fwd_kernel(const __grid_constant__ ActParams p) {
-  constexpr int K = kVecOf<T>;
-  using P = Pack<T, K>;
+  using P = Raw4<T>;
   bw::griddep_wait();
   bw::griddep_launch_dependents();
   if (p.hd->status != 0) return;
-  const int c = (blockIdx.y * kActThreads + threadIdx.x) * K;
+  const int c = (blockIdx.y * kActThreads + threadIdx.x) * kCh;
   if (c >= p.C) return;
   if ((int)blockIdx.x >= p.n_tb) {
     const int d = blockIdx.x - p.n_tb, n = p.cu[d + 1] - p.cu[d];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const T* row = n + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)p.cu[d] + n + k - 3) * p.sx : start_row<T>(p, d, n + k);
-      P r{};
-      if (row) r = *reinterpret_cast<const P*>(row + c);
-      *reinterpret_cast<P*>(static_cast<T*>(p.tail) + ((int64_t)d * 3 + k) * p.C + c) = r;
+      *reinterpret_cast<P*>(static_cast<T*>(p.tail) + ((int64_t)d * 3 + k) * p.C + c) = row_or_zero<T>(row, c);
     }
     return;
   }
   const int t0 = blockIdx.x * kFwdTokens, t1 = min(t0 + kFwdTokens, p.T);
   const T* x = static_cast<const T*>(p.x) + c;
-  float w[4][K], bias[K], win[3][K];
+  T* y = static_cast<T*>(p.y) + c;
+  P next[kRows];
+  auto fetch = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
-    w[0][i] = wv.x, w[1][i] = wv.y, w[2][i] = wv.z, w[3][i] = wv.w;
-    bias[i] = p.bias ? p.bias[c + i] : 0.f;
-  }
+    for (int k = 0; k < kRows; ++k)
+      if (t + k < t1) next[k] = *reinterpret_cast<const P*>(x + (int64_t)(t + k) * p.sx);
+  };
+  fetch(t0);
+  const Taps taps(p.w, p.bias, c);
   int d = doc_at(p.cu, p.N, t0), end = p.cu[d + 1];
-  auto window = [&](int t) {  // the three inputs before token t of document d
+  uint64_t win[3][kPr];  // the three inputs before the token
+  auto window = [&](int t) {
     const int at = t - p.cu[d];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      row_or_zero<T, K>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c,
-                        win[k]);
+      unpack(row_or_zero<T>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c),
+             win[k]);
+  };
+  auto put = [&](int t, const uint64_t* u) {
+    P o;
+#pragma unroll
+    for (int i = 0; i < kPr; ++i) set_pair<T>(o.w, i, p.silu ? silu_pair(u[i]) : u[i]);
+    *reinterpret_cast<P*>(y + (int64_t)t * p.C) = o;
   };
   window(t0);
-  for (int ta = t0; ta < t1; ta += kAhead) {
-    P r[kAhead];
+  for (int ta = t0; ta < t1; ta += kRows) {
+    P r[kRows];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (ta + k < t1) r[k] = *reinterpret_cast<const P*>(x + (int64_t)(ta + k) * p.sx);
+    for (int k = 0; k < kRows; ++k) r[k] = next[k];
+    fetch(ta + kRows);
+    if (ta + kRows <= t1 && ta + kRows <= end) {
+      uint64_t e[kRows + 3][kPr];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < kPr; ++i) e[k][i] = win[k][i];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) unpack(r[k], e[k + 3]);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        uint64_t u[kPr];
+#pragma unroll
+        for (int i = 0; i < kPr; ++i) u[i] = taps.dot(i, e[k][i], e[k + 1][i], e[k + 2][i], e[k + 3][i]);
+        put(ta + k, u);
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < kPr; ++i) win[k][i] = e[kRows + k][i];
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
       const int t = ta + k;
       if (t >= t1) break;
       if (t >= end) {
@@ -189,84 +246,110 @@ __global__ void __launch_bounds__(kActThreads) act_fwd_kernel(const __grid_const
         end = p.cu[d + 1];
         window(t);
       }
-      float cur[K];
+      uint64_t cur[kPr], u[kPr];
       unpack(r[k], cur);
-      P o;
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        float u = fmaf(w[0][i], win[0][i], bias[i]);
-        u = fmaf(w[1][i], win[1][i], u);
-        u = fmaf(w[2][i], win[2][i], u);
-        u = fmaf(w[3][i], cur[i], u);
-        if (p.silu) u = silu_of(u, sigmoid(u));
-        o.t[i] = from_float<T>(u);
+      for (int i = 0; i < kPr; ++i) {
+        u[i] = taps.dot(i, win[0][i], win[1][i], win[2][i], cur[i]);
         win[0][i] = win[1][i];
         win[1][i] = win[2][i];
         win[2][i] = cur[i];
       }
-      *reinterpret_cast<P*>(static_cast<T*>(p.y) + (int64_t)t * p.C + c) = o;
+      put(t, u);
     }
   }
 }
 
-// Blocks of kBwdTokens tokens. du runs up the tokens once; the gradient of an input is complete three tokens later.
+// Blocks of kBwdTokens tokens. du runs up the tokens once; the gradient of an input is complete three tokens later, so a
+// block goes three tokens beyond its own (as far as its last document) and leaves dw and dbias of those to the next.
 template <typename T>
 __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_constant__ ActParams p) {
-  constexpr int K = kVecOf<T>;
-  using P = Pack<T, K>;
+  using P = Raw4<T>;
   bw::griddep_wait();
   bw::griddep_launch_dependents();
   if (p.hd->status != 0) return;
-  const int c = (blockIdx.y * kActThreads + threadIdx.x) * K;
+  const int c = (blockIdx.y * kActThreads + threadIdx.x) * kCh;
   if (c >= p.C) return;
-  const int t0 = blockIdx.x * kBwdTokens, t1 = min(t0 + kBwdTokens, p.T);
+  const int t0 = blockIdx.x * kBwdTokens, t1 = min(t0 + kBwdTokens, p.T), stop = min(p.T, t1 + 3);
   const T *x = static_cast<const T*>(p.x) + c, *dy = static_cast<const T*>(p.dy) + c;
-  float w[4][K], bias[K], win[3][K], pend[3][K], dw[5][K];
+  P xn[kRows], gn[kRows];
+  auto fetch = [&](int t) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
-    w[0][i] = wv.x, w[1][i] = wv.y, w[2][i] = wv.z, w[3][i] = wv.w;
-    bias[i] = p.bias ? p.bias[c + i] : 0.f;
+    for (int k = 0; k < kRows; ++k)
+      if (t + k < stop) {
+        xn[k] = *reinterpret_cast<const P*>(x + (int64_t)(t + k) * p.sx);
+        gn[k] = *reinterpret_cast<const P*>(dy + (int64_t)(t + k) * p.sdy);
+      }
+  };
+  fetch(t0);
+  const Taps taps(p.w, p.bias, c);
+  uint64_t win[3][kPr], pend[3][kPr], dw[5][kPr];
 #pragma unroll
-    for (int m = 0; m < 5; ++m) dw[m][i] = 0.f;
+  for (int i = 0; i < kPr; ++i) {
 #pragma unroll
-    for (int m = 0; m < 3; ++m) pend[m][i] = 0.f;
+    for (int m = 0; m < 5; ++m) dw[m][i] = 0;
+    pend[0][i] = pend[1][i] = pend[2][i] = 0;
   }
   int d = doc_at(p.cu, p.N, t0), begin = p.cu[d], end = p.cu[d + 1];
   auto window = [&](int t) {
     const int at = t - begin;
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      row_or_zero<T, K>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c,
-                        win[k]);
+      unpack(row_or_zero<T>(at + k >= 3 ? static_cast<const T*>(p.x) + ((int64_t)t + k - 3) * p.sx : start_row<T>(p, d, at + k), c),
+             win[k]);
+  };
+  auto slope = [&](uint64_t u) { return silu_slope_pair(u, sigmoid_pair(u)); };
+  auto write = [&](float* to, const uint64_t* g) {
+    *reinterpret_cast<float4*>(to + c) = make_float4(f2_lo(g[0]), f2_hi(g[0]), f2_lo(g[1]), f2_hi(g[1]));
   };
   // the gradient of E[e] of document d, complete: an input of this block, or a row of the document's start
-  auto emit = [&](int e, const float* g) {
-    float* to = nullptr;
+  auto emit = [&](int e, const uint64_t* g) {
     if (e < 3) {
-      if (begin >= t0) to = p.dstart + ((int64_t)d * 3 + e) * p.C + c;
+      if (begin >= t0) write(p.dstart + ((int64_t)d * 3 + e) * p.C, g);
     } else if (begin + e - 3 >= t0 && begin + e - 3 < t1) {
-      to = p.dx + ((int64_t)begin + e - 3) * p.C + c;
-    }
-    if (to) {
-#pragma unroll
-      for (int i = 0; i < K; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+      write(p.dx + ((int64_t)begin + e - 3) * p.C, g);
     }
   };
   window(t0);
-  const int stop = min(p.T, t1 + 3);
-  int t = t0;
-  for (int ta = t0; ta < stop; ta += kAhead) {
-    P xr[kAhead], gr[kAhead];
+  for (int ta = t0; ta < stop; ta += kRows) {
+    P xr[kRows], gr[kRows];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (ta + k < stop) {
-        xr[k] = *reinterpret_cast<const P*>(x + (int64_t)(ta + k) * p.sx);
-        gr[k] = *reinterpret_cast<const P*>(dy + (int64_t)(ta + k) * p.sdy);
+    for (int k = 0; k < kRows; ++k) xr[k] = xn[k], gr[k] = gn[k];
+    fetch(ta + kRows);
+    if (ta + kRows <= t1 && ta + kRows <= end && ta - 3 >= t0 && ta - 3 >= begin) {
+      uint64_t e[kRows + 3][kPr], g[kRows + 3][kPr];
+#pragma unroll
+      for (int i = 0; i < kPr; ++i) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) e[k][i] = win[k][i], g[k][i] = pend[k][i];
       }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      t = ta + k;
+      for (int k = 0; k < kRows; ++k) {
+        unpack(xr[k], e[k + 3]);
+        uint64_t du[kPr];
+        unpack(gr[k], du);
+#pragma unroll
+        for (int i = 0; i < kPr; ++i) {
+          if (p.silu) du[i] = f2_mul(du[i], slope(taps.dot(i, e[k][i], e[k + 1][i], e[k + 2][i], e[k + 3][i])));
+#pragma unroll
+          for (int m = 0; m < 4; ++m) dw[m][i] = f2_fma(du[i], e[k + m][i], dw[m][i]);
+          dw[4][i] = f2_add(dw[4][i], du[i]);
+#pragma unroll
+          for (int m = 0; m < 3; ++m) g[k + m][i] = f2_fma(taps.w[m][i], du[i], g[k + m][i]);
+          g[k + 3][i] = f2_mul(taps.w[3][i], du[i]);
+        }
+        write(p.dx + (int64_t)(ta + k - 3) * p.C, g[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < kPr; ++i) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) win[k][i] = e[kRows + k][i], pend[k][i] = g[kRows + k][i];
+      }
+      continue;
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int t = ta + k;
       if (t >= stop) break;
       if (t >= end) {
         if (t >= t1) break;  // behind the block only the rest of its last document counts
@@ -277,30 +360,25 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_const
         end = p.cu[d + 1];
         window(t);
 #pragma unroll
-        for (int i = 0; i < K; ++i) pend[0][i] = pend[1][i] = pend[2][i] = 0.f;
+        for (int i = 0; i < kPr; ++i) pend[0][i] = pend[1][i] = pend[2][i] = 0;
       }
-      float cur[K], du[K], done[K];
+      uint64_t cur[kPr], du[kPr], done[kPr];
       unpack(xr[k], cur);
       unpack(gr[k], du);
-      const bool mine = t < t1;
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        float u = fmaf(w[0][i], win[0][i], bias[i]);
-        u = fmaf(w[1][i], win[1][i], u);
-        u = fmaf(w[2][i], win[2][i], u);
-        u = fmaf(w[3][i], cur[i], u);
-        if (p.silu) du[i] *= silu_slope(u, sigmoid(u));
-        if (mine) {
-          dw[0][i] = fmaf(du[i], win[0][i], dw[0][i]);
-          dw[1][i] = fmaf(du[i], win[1][i], dw[1][i]);
-          dw[2][i] = fmaf(du[i], win[2][i], dw[2][i]);
-          dw[3][i] = fmaf(du[i], cur[i], dw[3][i]);
-          dw[4][i] += du[i];
+      for (int i = 0; i < kPr; ++i) {
+        if (p.silu) du[i] = f2_mul(du[i], slope(taps.dot(i, win[0][i], win[1][i], win[2][i], cur[i])));
+        if (t < t1) {
+          dw[0][i] = f2_fma(du[i], win[0][i], dw[0][i]);
+          dw[1][i] = f2_fma(du[i], win[1][i], dw[1][i]);
+          dw[2][i] = f2_fma(du[i], win[2][i], dw[2][i]);
+          dw[3][i] = f2_fma(du[i], cur[i], dw[3][i]);
+          dw[4][i] = f2_add(dw[4][i], du[i]);
         }
-        done[i] = fmaf(w[0][i], du[i], pend[0][i]);
-        pend[0][i] = fmaf(w[1][i], du[i], pend[1][i]);
-        pend[1][i] = fmaf(w[2][i], du[i], pend[2][i]);
-        pend[2][i] = w[3][i] * du[i];
+        done[i] = f2_fma(taps.w[0][i], du[i], pend[0][i]);
+        pend[0][i] = f2_fma(taps.w[1][i], du[i], pend[1][i]);
+        pend[1][i] = f2_fma(taps.w[2][i], du[i], pend[2][i]);
+        pend[2][i] = f2_mul(taps.w[3][i], du[i]);
         win[0][i] = win[1][i];
         win[1][i] = win[2][i];
         win[2][i] = cur[i];
@@ -313,11 +391,7 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_const
     for (int m = 0; m < 3; ++m) emit(end - begin + m, pend[m]);
   }
 #pragma unroll
-  for (int m = 0; m < 5; ++m)
-#pragma unroll
-    for (int i = 0; i < K; i += 4)
-      *reinterpret_cast<float4*>(p.part + ((int64_t)blockIdx.x * 5 + m) * p.C + c + i) =
-          make_float4(dw[m][i], dw[m][i + 1], dw[m][i + 2], dw[m][i + 3]);
+  for (int m = 0; m < 5; ++m) write(p.part + ((int64_t)blockIdx.x * 5 + m) * p.C, dw[m]);
 }
 
 // dw and dbias over the blocks of tokens, in their order: 32 channels a CTA, each summed by eight threads.
@@ -329,6 +403,7 @@ __global__ void __launch_bounds__(256) act_sum_kernel(const __grid_constant__ Ac
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float v[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < p.C)
+#pragma unroll 4
     for (int b = r; b < p.n_tb; b += 8)
 #pragma unroll
       for (int m = 0; m < 5; ++m) v[m] += p.part[((int64_t)b * 5 + m) * p.C + c];
@@ -412,17 +487,13 @@ struct StepParams {
 
 template <typename T>
 __global__ void __launch_bounds__(kActThreads) act_step_kernel(const __grid_constant__ StepParams p) {
-  constexpr int K = kVecOf<T>;
-  using P = Pack<T, K>;
+  using P = Raw4<T>;
   const int64_t b = blockIdx.y;
-  const int c = (blockIdx.x * kActThreads + threadIdx.x) * K, e = p.idx[b];
+  const int c = (blockIdx.x * kActThreads + threadIdx.x) * kCh, e = p.idx[b];
   if (c >= p.C) return;
   P* out = reinterpret_cast<P*>(static_cast<T*>(p.y) + b * p.C + c);
   if (e < 0 || e >= p.n_pool) {  // skipped, reported
-    P o;
-#pragma unroll
-    for (int i = 0; i < K; ++i) o.t[i] = from_float<T>(0.f);
-    *out = o;
+    *out = P{};
     if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
     return;
   }
@@ -431,16 +502,12 @@ __global__ void __launch_bounds__(kActThreads) act_step_kernel(const __grid_cons
 #pragma unroll
   for (int k = 0; k < 3; ++k) r[k] = *reinterpret_cast<const P*>(tail + (int64_t)k * p.C);
   r[3] = *reinterpret_cast<const P*>(static_cast<const T*>(p.x) + b * p.sx + c);
+  const Taps taps(p.w, p.bias, c);
   P o;
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const float4 wv = *reinterpret_cast<const float4*>(p.w + (int64_t)(c + i) * 4);
-    float u = fmaf(wv.x, to_float(r[0].t[i]), p.bias ? p.bias[c + i] : 0.f);
-    u = fmaf(wv.y, to_float(r[1].t[i]), u);
-    u = fmaf(wv.z, to_float(r[2].t[i]), u);
-    u = fmaf(wv.w, to_float(r[3].t[i]), u);
-    if (p.silu) u = silu_of(u, sigmoid(u));
-    o.t[i] = from_float<T>(u);
+  for (int i = 0; i < kPr; ++i) {
+    const uint64_t u = taps.dot(i, pair_of<T>(r[0].w, i), pair_of<T>(r[1].w, i), pair_of<T>(r[2].w, i), pair_of<T>(r[3].w, i));
+    set_pair<T>(o.w, i, p.silu ? silu_pair(u) : u);
   }
 #pragma unroll
   for (int k = 0; k < 3; ++k) *reinterpret_cast<P*>(tail + (int64_t)k * p.C) = r[k + 1];
@@ -531,7 +598,7 @@ extern "C" int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w,
   launch_early(act_check_kernel, dim3(1), 256, 0, s, p);
   by_type(dtype, [&](auto t) {
     using T_ = decltype(t);
-    const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+    const unsigned cb = (unsigned)((C / kCh + kActThreads - 1) / kActThreads);
     launch_early(act_fwd_kernel<T_>, dim3((unsigned)(L.n_tb + N), cb), kActThreads, 0, s, p);
   });
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -568,7 +635,7 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   if (T > 0)
     by_type(dtype, [&](auto t) {
       using T_ = decltype(t);
-      const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+      const unsigned cb = (unsigned)((C / kCh + kActThreads - 1) / kActThreads);
       launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kActThreads, 0, s, p);
     });
   launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32)), 256, 0, s, p);
@@ -600,7 +667,7 @@ extern "C" int gdn_conv_decode_step(const void* x, int64_t x_stride, const float
   const StepParams p{x, x_stride, w, bias, state_idx, tail_pool, y, status, B, C, n_pool, activation == GDN_ACT_SILU};
   by_type(dtype, [&](auto t) {
     using T_ = decltype(t);
-    const unsigned cb = (unsigned)((C / kVecOf<T_> + kActThreads - 1) / kActThreads);
+    const unsigned cb = (unsigned)((C / kCh + kActThreads - 1) / kActThreads);
     act_step_kernel<T_><<<dim3(cb, (unsigned)B), kActThreads, 0, (cudaStream_t)stream>>>(p);
   });
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

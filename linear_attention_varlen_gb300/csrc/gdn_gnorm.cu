@@ -24,6 +24,13 @@
 namespace gdn {
 namespace {
 
+using bw::f2_fma;
+using bw::f2_hi;
+using bw::f2_lo;
+using bw::f2_mul;
+using bw::f2_pack;
+using bw::f2_sum;
+
 constexpr int kMaxGroup = 16384;
 constexpr int kWarpTeamThreads = 256;  // threads of a CTA whose teams lie within a warp
 constexpr int kMaxTeam = 512;
@@ -60,25 +67,35 @@ struct Share {
   static constexpr int K = kElems<T>;
   int lane, L, n;
   __device__ __forceinline__ int col(int v, int i) const { return kVec ? (v * L + lane) * K + i : (v * K + i) * L + lane; }
-  __device__ __forceinline__ Pack<T, K> load(const T* p, int v, bool live) const {
-    Pack<T, K> r{};
+  __device__ __forceinline__ Words load(const T* p, int v, bool live) const {
+    Words r{};
     if constexpr (kVec) {
-      if (live && col(v, 0) < n) r = *reinterpret_cast<const Pack<T, K>*>(p + col(v, 0));
+      if (live && col(v, 0) < n) r = *reinterpret_cast<const Words*>(p + col(v, 0));
     } else {
 #pragma unroll
       for (int i = 0; i < K; ++i)
-        if (live && col(v, i) < n) r.t[i] = p[col(v, i)];
+        if (live && col(v, i) < n) set_element<T>(r, i, p[col(v, i)]);
     }
     return r;
   }
-  __device__ __forceinline__ void store(T* p, int v, const Pack<T, K>& r) const {
+  __device__ __forceinline__ void store(T* p, int v, const Words& r) const {
     if constexpr (kVec) {
-      if (col(v, 0) < n) *reinterpret_cast<Pack<T, K>*>(p + col(v, 0)) = r;
+      if (col(v, 0) < n) *reinterpret_cast<Words*>(p + col(v, 0)) = r;
     } else {
 #pragma unroll
       for (int i = 0; i < K; ++i)
-        if (col(v, i) < n) p[col(v, i)] = r.t[i];
+        if (col(v, i) < n) p[col(v, i)] = element_of<T>(r, i);
     }
+  }
+};
+
+// The next rows' vectors of a thread's share on their way into its own places in shared memory: kN tensors, kStages rows.
+template <int kN, int kNv, int kStages>
+struct Ring {
+  static constexpr int kBytes = kN * kNv * kStages * 16;  // a thread
+  static __device__ __forceinline__ Words* at(int k, int tensor, int v) {
+    extern __shared__ Words ring[];
+    return ring + (((k % (kStages > 0 ? kStages : 1)) * kN + tensor) * kNv + v) * (int)blockDim.x + threadIdx.x;
   }
 };
 
@@ -109,145 +126,228 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], int L, float (*buf)[kN]
   turn ^= 1;
 }
 
-// L threads to a team; a CTA of blockDim.x / L teams (one, where a team is more than a warp).
+// Rows in flight for a thread, this one's included (0: read when they are needed).
 template <typename T, int kNv, bool kVec>
+__host__ __device__ constexpr int fwd_stages() {
+  return !kVec ? 0 : kNv == 1 ? 4 : kNv == 2 ? 2 : 0;
+}
+template <typename T, int kNv, bool kVec>
+__host__ __device__ constexpr int bwd_stages() {
+  return !kVec ? 0 : kNv == 1 ? 3 : kNv == 2 ? 2 : 0;
+}
+
+// L threads to a team; a CTA of blockDim.x / L teams (one, where a team is more than a warp). Either order's output is
+// x gate rs w; they differ in whose squares rs has. Rows ahead are on their way into
+// shared memory.
+template <typename T, int kNv, bool kVec, bool kGateFirst>
 __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_constant__ GnormParams p, int L) {
-  constexpr int K = kElems<T>;
+  constexpr int P = kPairs<T>, kStages = fwd_stages<T, kNv, kVec>();
+  using R = Ring<2, kNv, kStages>;
   __shared__ float buf[2][1][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
-  const int grp = (int)(team % p.ng);
-  const int64_t row0 = team / p.ng;
+  const int64_t row0 = team / p.ng, at = (team - row0 * p.ng) * p.group;
   const Share<T, kNv, kVec> sh{(int)(threadIdx.x % L), L, p.group};
-  float w[kNv][K];
+  uint64_t w[kNv][P];
 #pragma unroll
   for (int v = 0; v < kNv; ++v)
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const int c = sh.col(v, i);
-      w[v][i] = c < p.group ? load_w(p.w, p.w_dtype, p.shared ? c : (int64_t)grp * p.group + c) : 0.f;
+    for (int i = 0; i < P; ++i) {
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = sh.col(v, 2 * i + j);
+        f[j] = c < p.group ? load_w(p.w, p.w_dtype, p.shared ? c : at + c) : 0.f;
+      }
+      w[v][i] = f2_pack(f[0], f[1]);
     }
-  const int64_t trips = (p.T + p.rows - 1) / p.rows;  // the same for every team: the sums take whole warps
+  const int trips = (int)((p.T + p.rows - 1) / p.rows);  // the same for every team: the sums take whole warps
   const float inv = 1.f / (float)p.group;
-  for (int64_t k = 0; k < trips; ++k) {
-    const int64_t row = row0 + k * p.rows;
-    const bool live = row0 < p.rows && row < p.T;
-    const int64_t at = (int64_t)grp * p.group;
-    Pack<T, K> xr[kNv], zr[kNv];
+  const T *x = static_cast<const T*>(p.x) + row0 * p.sx + at, *z = static_cast<const T*>(p.z) + row0 * p.sz + at;
+  T* y = static_cast<T*>(p.y) + row0 * p.D + at;
+  // rows behind the last one (and those of threads behind the last team) are left out
+  const int64_t mine = row0 < p.rows && row0 < p.T ? (p.T - row0 + p.rows - 1) / p.rows : 0;
+  auto issue = [&](int k) {
+    if (k < mine) {
 #pragma unroll
-    for (int v = 0; v < kNv; ++v) {
-      xr[v] = sh.load(static_cast<const T*>(p.x) + row * p.sx + at, v, live);
-      zr[v] = sh.load(static_cast<const T*>(p.z) + row * p.sz + at, v, live);
-    }
-    float sum[1] = {0.f};
-#pragma unroll
-    for (int v = 0; v < kNv; ++v)
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        float u = to_float(xr[v].t[i]);
-        if (p.gate_first) {
-          const float z = to_float(zr[v].t[i]);
-          u *= silu_of(z, sigmoid(z));
+      for (int v = 0; v < kNv; ++v)
+        if (sh.col(v, 0) < p.group) {
+          cp_async16(R::at(k, 0, v), x + k * p.rows * p.sx + sh.col(v, 0));
+          cp_async16(R::at(k, 1, v), z + k * p.rows * p.sz + sh.col(v, 0));
         }
-        sum[0] = fmaf(u, u, sum[0]);
-      }
-    team_sum(sum, L, buf, turn);
-    const float rs = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
-    if (!live) continue;
+    }
+    cp_async_commit();
+  };
+  if constexpr (kStages > 0) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k);
+  }
+  for (int k = 0; k < trips; ++k) {
+    if constexpr (kStages > 0) {
+      issue(k + kStages - 1);
+      cp_async_wait<(kStages > 0 ? kStages - 1 : 0)>();
+    }
+    uint64_t xg[kNv][P], sum2 = 0;
 #pragma unroll
     for (int v = 0; v < kNv; ++v) {
-      Pack<T, K> o;
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const float z = to_float(zr[v].t[i]);
-        o.t[i] = from_float<T>(to_float(xr[v].t[i]) * silu_of(z, sigmoid(z)) * (rs * w[v][i]));
+      Words xr{}, zr{};
+      if constexpr (kStages > 0) {
+        if (k < mine && sh.col(v, 0) < p.group) xr = *R::at(k, 0, v), zr = *R::at(k, 1, v);
+      } else {
+        xr = sh.load(x + k * p.rows * p.sx, v, k < mine);
+        zr = sh.load(z + k * p.rows * p.sz, v, k < mine);
       }
-      sh.store(static_cast<T*>(p.y) + row * p.D + at, v, o);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint64_t u = pair_of<T>(xr, i);
+        xg[v][i] = f2_mul(u, silu_pair(pair_of<T>(zr, i)));
+        sum2 = kGateFirst ? f2_fma(xg[v][i], xg[v][i], sum2) : f2_fma(u, u, sum2);
+      }
     }
+    float sum[1] = {f2_sum(sum2)};
+    team_sum(sum, L, buf, turn);
+    const uint64_t rs = f2_dup(1.f / sqrtf(fmaf(sum[0], inv, p.eps)));
+    if (k < mine) {
+#pragma unroll
+      for (int v = 0; v < kNv; ++v) {
+        Words o;
+#pragma unroll
+        for (int i = 0; i < P; ++i) set_pair<T>(o, i, f2_mul(xg[v][i], f2_mul(rs, w[v][i])));
+        sh.store(y, v, o);
+      }
+    }
+    y += p.rows * p.D;
   }
 }
 
-// Up to 16 elements a thread, the row stays in registers between the sums and the gradients, and the weights for all
-// rows; longer shares are read again (from L2).
-template <typename T, int kNv, bool kVec>
-__global__ void __launch_bounds__(kMaxTeam) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
-  constexpr int K = kElems<T>;
-  constexpr bool kKeep = kNv * K <= 16;
+// Either order: the sum of u w dn and dw are those of x gate w dy and x gate dy rs. Up to eight elements a thread, the
+// weights and the row stay in registers; longer shares take both again. Rows ahead are on their way into shared memory
+// where that holds enough of them, else a row's second reading comes from L2.
+template <typename T, int kNv, bool kVec, bool kGateFirst>
+__global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
+  constexpr int K = kElems<T>, P = kPairs<T>;
+  constexpr bool kKeep = kNv * K <= 8;
+  constexpr int kStages = bwd_stages<T, kNv, kVec>();
+  using R = Ring<3, kNv, kStages>;
   __shared__ float buf[2][2][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
-  const int grp = (int)(team % p.ng);
-  const int64_t row0 = team / p.ng;
+  const int64_t row0 = team / p.ng, at = (team - row0 * p.ng) * p.group;
   const Share<T, kNv, kVec> sh{(int)(threadIdx.x % L), L, p.group};
-  const int64_t wat = p.shared ? 0 : (int64_t)grp * p.group;
-  float wk[kKeep ? kNv : 1][K], dw[kNv][K];
+  uint64_t wk[kKeep ? kNv : 1][P] = {}, dw[kNv][P];
   auto weight = [&](int v, int i) {
-    const int c = sh.col(v, i);
-    return c < p.group ? load_w(p.w, p.w_dtype, wat + c) : 0.f;
-  };
+    float f[2];
 #pragma unroll
-  for (int v = 0; v < kNv; ++v)
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      if constexpr (kKeep) wk[v][i] = weight(v, i);
-      dw[v][i] = 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const int c = sh.col(v, 2 * i + j);
+      f[j] = c < p.group ? load_w(p.w, p.w_dtype, p.shared ? c : at + c) : 0.f;
     }
+    return f2_pack(f[0], f[1]);
+  };
   auto wt = [&](int v, int i) {
     if constexpr (kKeep)
       return wk[v][i];
     else
       return weight(v, i);
   };
-  const int64_t trips = (p.T + p.rows - 1) / p.rows;
+#pragma unroll
+  for (int v = 0; v < kNv; ++v)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if constexpr (kKeep) wk[v][i] = weight(v, i);
+      dw[v][i] = 0;
+    }
+  const int trips = (int)((p.T + p.rows - 1) / p.rows);
   const float inv = 1.f / (float)p.group;
-  const int64_t at = (int64_t)grp * p.group;
-  for (int64_t k = 0; k < trips; ++k) {
-    const int64_t row = row0 + k * p.rows;
-    const bool live = row0 < p.rows && row < p.T;
-    const T *xp = static_cast<const T*>(p.x) + row * p.sx + at, *zp = static_cast<const T*>(p.z) + row * p.sz + at,
-            *gp = static_cast<const T*>(p.dy) + row * p.sdy + at;
-    Pack<T, K> xr[kNv], zr[kNv], gr[kNv];
-    auto fetch = [&](int v, bool l) {
-      xr[v] = sh.load(xp, v, l);
-      zr[v] = sh.load(zp, v, l);
-      gr[v] = sh.load(gp, v, l);
+  const T *x = static_cast<const T*>(p.x) + row0 * p.sx + at, *z = static_cast<const T*>(p.z) + row0 * p.sz + at,
+          *g = static_cast<const T*>(p.dy) + row0 * p.sdy + at;
+  int64_t out = row0 * p.D + at;
+  const int64_t mine = row0 < p.rows && row0 < p.T ? (p.T - row0 + p.rows - 1) / p.rows : 0;
+  constexpr int kHold = kKeep ? kNv : 1;
+  auto issue = [&](int k) {
+    if (k < mine) {
+#pragma unroll
+      for (int v = 0; v < kNv; ++v)
+        if (sh.col(v, 0) < p.group) {
+          cp_async16(R::at(k, 0, v), x + k * p.rows * p.sx + sh.col(v, 0));
+          cp_async16(R::at(k, 1, v), z + k * p.rows * p.sz + sh.col(v, 0));
+          cp_async16(R::at(k, 2, v), g + k * p.rows * p.sdy + sh.col(v, 0));
+        }
+    }
+    cp_async_commit();
+  };
+  if constexpr (kStages > 0) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k);
+  }
+  for (int k = 0; k < trips; ++k) {
+    Words xr[kHold], zr[kHold], gr[kHold];
+    uint64_t sig[kHold][P], sq = 0, dot = 0;
+    auto sums = [&](int v, int hold) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint64_t u = pair_of<T>(xr[hold], i), zz = pair_of<T>(zr[hold], i);
+        sig[hold][i] = sigmoid_pair(zz);
+        const uint64_t zc = f2_pack(at_least(f2_lo(zz), -128.f), at_least(f2_hi(zz), -128.f));
+        const uint64_t xg = f2_mul(u, f2_mul(zc, sig[hold][i]));
+        sq = kGateFirst ? f2_fma(xg, xg, sq) : f2_fma(u, u, sq);
+        dot = f2_fma(f2_mul(xg, wt(v, i)), pair_of<T>(gr[hold], i), dot);
+      }
     };
-    if constexpr (kKeep) {
-#pragma unroll
-      for (int v = 0; v < kNv; ++v) fetch(v, live);
+    const T *xk = x + k * p.rows * p.sx, *zk = z + k * p.rows * p.sz, *gk = g + k * p.rows * p.sdy;
+    if constexpr (kStages > 0) {
+      issue(k + kStages - 1);
+      cp_async_wait<(kStages > 0 ? kStages - 1 : 0)>();
     }
-    float sum[2] = {0.f, 0.f};  // of u^2 and of u w dn
+    auto fetch = [&](int v, int hold, bool live) {
+      if constexpr (kStages > 0) {
+        xr[hold] = zr[hold] = gr[hold] = Words{};
+        if (live && sh.col(v, 0) < p.group) xr[hold] = *R::at(k, 0, v), zr[hold] = *R::at(k, 1, v), gr[hold] = *R::at(k, 2, v);
+      } else {
+        xr[hold] = sh.load(xk, v, live);
+        zr[hold] = sh.load(zk, v, live);
+        gr[hold] = sh.load(gk, v, live);
+      }
+    };
 #pragma unroll
     for (int v = 0; v < kNv; ++v) {
-      if constexpr (!kKeep) fetch(v, live);
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const float x = to_float(xr[v].t[i]), z = to_float(zr[v].t[i]), gate = silu_of(z, sigmoid(z));
-        const float xg = x * gate, u = p.gate_first ? xg : x;
-        sum[0] = fmaf(u, u, sum[0]);
-        sum[1] = fmaf(xg * wt(v, i), to_float(gr[v].t[i]), sum[1]);  // u dn is x gate dy either way
-      }
+      fetch(v, kKeep ? v : 0, k < mine);
+      sums(v, kKeep ? v : 0);
     }
+    float sum[2] = {f2_sum(sq), f2_sum(dot)};
     team_sum(sum, L, buf, turn);
-    const float rs = 1.f / sqrtf(fmaf(sum[0], inv, p.eps)), mean = sum[1] * inv * rs;  // of g hat
-    if (!live) continue;
+    const float r = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
+    const uint64_t rs = f2_dup(r), mean = f2_dup(-sum[1] * inv * r * r);  // - rs mean(g hat)
+    if (k < mine) {
 #pragma unroll
-    for (int v = 0; v < kNv; ++v) {
-      if constexpr (!kKeep) fetch(v, true);
-      Pack<T, K> dx, dz;
+      for (int v = 0; v < kNv; ++v) {
+        const int hold = kKeep ? v : 0;
+        if constexpr (!kKeep) fetch(v, 0, true);
+        Words dx, dz;
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const float x = to_float(xr[v].t[i]), z = to_float(zr[v].t[i]), dy = to_float(gr[v].t[i]);
-        const float sig = sigmoid(z), gate = silu_of(z, sig), slope = silu_slope(z, sig);
-        const float hat = (p.gate_first ? x * gate : x) * rs, dn = p.gate_first ? dy : dy * gate;
-        const float w = wt(v, i), du = rs * fmaf(w, dn, -hat * mean);
-        dw[v][i] = fmaf(dn, hat, dw[v][i]);
-        dx.t[i] = from_float<T>(p.gate_first ? du * gate : du);
-        dz.t[i] = from_float<T>((p.gate_first ? du * x : dy * hat * w) * slope);
+        for (int i = 0; i < P; ++i) {
+          const uint64_t xx = pair_of<T>(xr[hold], i), zz = pair_of<T>(zr[hold], i), dy = pair_of<T>(gr[hold], i);
+          const uint64_t sg = kKeep ? sig[hold][i] : sigmoid_pair(zz);
+          const uint64_t zc = f2_pack(at_least(f2_lo(zz), -128.f), at_least(f2_hi(zz), -128.f));
+          const uint64_t gate = f2_mul(zc, sg), slope = silu_slope_pair(zz, sg), xg = f2_mul(xx, gate);
+          const uint64_t ry = f2_mul(rs, dy), wv = wt(v, i);
+          dw[v][i] = f2_fma(ry, xg, dw[v][i]);
+          const uint64_t wr = f2_mul(ry, wv);  // rs w dy
+          if constexpr (kGateFirst) {
+            const uint64_t du = f2_fma(f2_mul(xg, rs), mean, wr);
+            set_pair<T>(dx, i, f2_mul(du, gate));
+            set_pair<T>(dz, i, f2_mul(f2_mul(du, xx), slope));
+          } else {
+            const uint64_t hat = f2_mul(xx, rs);
+            set_pair<T>(dx, i, f2_fma(hat, mean, f2_mul(wr, gate)));
+            set_pair<T>(dz, i, f2_mul(f2_mul(wr, xx), slope));
+          }
+        }
+        sh.store(static_cast<T*>(p.dx) + out, v, dx);
+        sh.store(static_cast<T*>(p.dz) + out, v, dz);
       }
-      sh.store(static_cast<T*>(p.dx) + row * p.D + at, v, dx);
-      sh.store(static_cast<T*>(p.dz) + row * p.D + at, v, dz);
     }
+    out += p.rows * p.D;
   }
   if (row0 < p.rows) {
 #pragma unroll
@@ -255,7 +355,7 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_bwd_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         const int c = sh.col(v, i);
-        if (c < p.group) p.part[row0 * p.D + at + c] = dw[v][i];
+        if (c < p.group) p.part[row0 * p.D + at + c] = i % 2 ? f2_hi(dw[v][i / 2]) : f2_lo(dw[v][i / 2]);
       }
   }
 }
@@ -269,6 +369,7 @@ __global__ void __launch_bounds__(256) gnorm_sum_kernel(const __grid_constant__ 
   const int64_t parts = p.shared ? p.rows * p.ng : p.rows;  // a shared weight's parts lie `group` apart
   float v = 0.f;
   if (c < n)
+#pragma unroll 8
     for (int64_t k = r; k < parts; k += 8) v += p.part[k * n + c];
   s[r][lane] = v;
   __syncthreads();
@@ -293,14 +394,12 @@ int next_pow2(int n) {
   return p;
 }
 
-// The team for a group of `n` elements: one vector a thread while a warp holds the group, then two while a CTA does.
-// Rows off alignment keep to one, which leaves registers for their addresses.
+// The team for a group of `n` elements: one vector a thread as long as a CTA holds the group.
 Shape shape_of(int n, int64_t T, int ng, int es, bool vec, int sms, int threads_per_sm) {
   Shape s{};
   const int K = 16 / es, nvec = (n + K - 1) / K;
   s.vec = vec;
   int L = next_pow2(nvec);
-  if (L > 32 && vec) L /= 2;
   if (L > kMaxTeam) L = kMaxTeam;
   s.L = L;
   s.nv = next_pow2((nvec + L - 1) / L);
@@ -371,7 +470,14 @@ void by_share(int nv, F f) {
   if constexpr (sizeof(T) == 4) f(Int<8>{});  // kMaxGroup / kElems / kMaxTeam vectors at most
 }
 
-constexpr int kFwdThreads = 1536, kBwdThreads = 640;  // resident threads to an SM that the grids are made for
+// Shared memory beyond the default limit.
+template <typename K>
+bool allow_smem(K kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+constexpr int kFwdThreads = 1024, kBwdThreads = 768;  // resident threads to an SM that the grids are made for
 
 // The most rows of parts that any shape of the backward writes: what a team of the smallest size would.
 size_t part_bytes(int64_t T, int D, int group, int es, int sms) {
@@ -398,17 +504,19 @@ extern "C" int gdn_gated_rmsnorm_fwd(const void* x, int64_t x_stride, const void
   if ((rc = check_device(y, ptrs, 3, guard, &sms)) != GDN_OK) return rc;
   const Shape s = shape_of(group, T, p.ng, dtype == GDN_DTYPE_FP32 ? 4 : 2, vec, sms, kFwdThreads);
   p.rows = s.rows;
+  bool ok = true;
   by_type(dtype, [&](auto t) {
     using T_ = decltype(t);
     by_share<T_>(s.nv, [&](auto n) {
       constexpr int kNv = decltype(n)::value;
-      if (vec)
-        gnorm_fwd_kernel<T_, kNv, true><<<(unsigned)s.ctas, s.threads, 0, (cudaStream_t)stream>>>(p, s.L);
-      else
-        gnorm_fwd_kernel<T_, kNv, false><<<(unsigned)s.ctas, s.threads, 0, (cudaStream_t)stream>>>(p, s.L);
+      auto* kernel = p.gate_first ? (vec ? gnorm_fwd_kernel<T_, kNv, true, true> : gnorm_fwd_kernel<T_, kNv, false, true>)
+                                  : (vec ? gnorm_fwd_kernel<T_, kNv, true, false> : gnorm_fwd_kernel<T_, kNv, false, false>);
+      const size_t ring = vec ? (size_t)s.threads * Ring<2, kNv, fwd_stages<T_, kNv, true>()>::kBytes : 0;
+      ok = allow_smem(kernel, ring);
+      if (ok) kernel<<<(unsigned)s.ctas, s.threads, ring, (cudaStream_t)stream>>>(p, s.L);
     });
   });
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 extern "C" size_t gdn_gated_rmsnorm_workspace_size(int64_t T, int D, int group, int dtype) {
@@ -439,17 +547,19 @@ extern "C" int gdn_gated_rmsnorm_bwd(const void* x, int64_t x_stride, const void
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(GnormHeader));
   const Shape s = shape_of(group, T, p.ng, dtype == GDN_DTYPE_FP32 ? 4 : 2, vec, kSms, kBwdThreads);
   p.rows = s.rows;
+  bool ok = true;
   if (T > 0)
     by_type(dtype, [&](auto t) {
       using T_ = decltype(t);
       by_share<T_>(s.nv, [&](auto n) {
         constexpr int kNv = decltype(n)::value;
-        if (vec)
-          gnorm_bwd_kernel<T_, kNv, true><<<(unsigned)s.ctas, s.threads, 0, (cudaStream_t)stream>>>(p, s.L);
-        else
-          gnorm_bwd_kernel<T_, kNv, false><<<(unsigned)s.ctas, s.threads, 0, (cudaStream_t)stream>>>(p, s.L);
+        auto* kernel = p.gate_first ? (vec ? gnorm_bwd_kernel<T_, kNv, true, true> : gnorm_bwd_kernel<T_, kNv, false, true>)
+                                    : (vec ? gnorm_bwd_kernel<T_, kNv, true, false> : gnorm_bwd_kernel<T_, kNv, false, false>);
+        const size_t ring = vec ? (size_t)s.threads * Ring<3, kNv, bwd_stages<T_, kNv, true>()>::kBytes : 0;
+        ok = allow_smem(kernel, ring);
+        if (ok) kernel<<<(unsigned)s.ctas, s.threads, ring, (cudaStream_t)stream>>>(p, s.L);
       });
     });
   launch_early(gnorm_sum_kernel, dim3((unsigned)(((p.shared ? group : D) + 31) / 32)), 256, 0, (cudaStream_t)stream, p);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

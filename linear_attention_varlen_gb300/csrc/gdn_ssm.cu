@@ -40,12 +40,6 @@ using bw::f2_mul;
 using bw::f2_pack;
 using bw::f2_sum;
 
-#ifndef SSM_BATCH
-#define SSM_BATCH 4
-#endif
-#ifndef SSM_OCC
-#define SSM_OCC 3
-#endif
 constexpr int kPlanThreads = 1024;
 
 struct SsmParams {
@@ -192,19 +186,6 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
 
 enum { kWalkState = 0, kWalkOut = 1, kWalkGrad = 2 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(bw::smem_u32(dst)), "l"(src) : "memory");
-}
-// 16 bytes, or zeros
-__device__ __forceinline__ void cp_async16_if(void* dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(bw::smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
-
 // Rows of a [T, C] tensor on their way into shared memory: the kN channels from `first` on, of tokens one after the
 // other, by asynchronous copies of 16 bytes. kVec: everything is aligned to them. Other rows bring the pieces that
 // cover the channels, and each row's place within its first piece is found again from its address; a piece that
@@ -295,12 +276,12 @@ struct WalkShape {
 };
 
 template <typename T, int kSp, int kMode, bool kVec>
-__global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : SSM_OCC)
+__global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
     ssm_walk_kernel(const __grid_constant__ SsmParams p) {
   using W = WalkShape<T, kSp, kMode, kVec>;
   using R = typename W::R;
   constexpr int kNl = W::kNl, kNt = W::kNt, kDt = W::kDt, kCh = W::kCh, kTb = W::kTb;
-  constexpr int kQt = kNt / 4, kQ = kSp / 4, kP = kNt / 2, kBatch = SSM_BATCH;
+  constexpr int kQt = kNt / 4, kQ = kSp / 4, kP = kNt / 2, kBatch = 2;
   constexpr bool kGate = kMode != kWalkState;  // z is read
   static_assert(kCh == ssm_walk_channels(kSp));
   extern __shared__ __align__(16) uint8_t raw_smem[];

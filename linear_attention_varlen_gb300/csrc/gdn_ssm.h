@@ -12,10 +12,7 @@ namespace gdn {
 
 constexpr int kSsmTile = 16;     // tokens between two states that the backward keeps
 constexpr int kSsmMinSeg = 16;   // shortest segment, a multiple of the tile
-#ifndef SSM_FILL
-#define SSM_FILL 12
-#endif
-constexpr int kSsmFill = SSM_FILL * 152;  // warps of a walk that segments are cut for: eight to each of the GPU's SMs
+constexpr int kSsmFill = 16 * 152;  // warps of a walk that segments are cut for: sixteen to each of the GPU's SMs
 constexpr int kSsmMaxState = 64;
 
 // A segment: consecutive tokens of one document that one warp walks for its channels.

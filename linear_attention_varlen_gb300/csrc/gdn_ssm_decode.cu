@@ -50,9 +50,23 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
     entry[r] = b0 + r < p.B ? p.state_idx[b0 + r] : -1;
     if (entry[r] >= p.n_pool) entry[r] = -1;
   }
+  // every load first
+  Pack<T, 4> bm[kRows], cm[kRows];
+  T x[kRows], dt[kRows], z[kRows];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
-    h[r] = load_pack<float, 4, kVec>(p.pool + ((int64_t)max(entry[r], 0) * p.C + c) * p.S + 4 * q, entry[r] < 0 ? 0 : n);
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t b = b0 + r;
+    const bool live = entry[r] >= 0;
+    h[r] = load_pack<float, 4, kVec>(p.pool + ((int64_t)max(entry[r], 0) * p.C + c) * p.S + 4 * q, live ? n : 0);
+    x[r] = dt[r] = z[r] = from_float<T>(0.f);
+    if (live) {
+      x[r] = static_cast<const T*>(p.x)[b * p.sx + c];
+      dt[r] = static_cast<const T*>(p.dt)[b * p.sdt + c];
+      if (p.z) z[r] = static_cast<const T*>(p.z)[b * p.sz + c];
+    }
+    bm[r] = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + b * p.sb + g * p.S + 4 * q, live ? n : 0);
+    cm[r] = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + b * p.sc + g * p.S + 4 * q, live ? n : 0);
+  }
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     const int64_t b = b0 + r;
@@ -63,25 +77,22 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
       if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
       continue;
     }
-    const float raw = to_float(static_cast<const T*>(p.dt)[b * p.sdt + c]) + bias;
-    const float delta = p.softplus ? softplus(raw) : raw, x = to_float(static_cast<const T*>(p.x)[b * p.sx + c]);
-    const T* bp = static_cast<const T*>(p.b) + b * p.sb + g * p.S + 4 * q;
-    const T* cp = static_cast<const T*>(p.c) + b * p.sc + g * p.S + 4 * q;
+    const float raw = to_float(dt[r]) + bias, delta = p.softplus ? softplus(raw) : raw, u = delta * to_float(x[r]);
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i < n) {
-        h[r].t[i] = fmaf(exp2_approx(delta * (kLog2e * A.t[i])), h[r].t[i], delta * x * to_float(bp[i]));
-        y = fmaf(to_float(cp[i]), h[r].t[i], y);
+        h[r].t[i] = fmaf(exp2_approx(delta * (kLog2e * A.t[i])), h[r].t[i], u * to_float(bm[r].t[i]));
+        y = fmaf(to_float(cm[r].t[i]), h[r].t[i], y);
       }
     }
     store_pack<float, 4, kVec>(p.pool + ((int64_t)entry[r] * p.C + c) * p.S + 4 * q, h[r], n);
 #pragma unroll
     for (int o = 1; o < kQ; o <<= 1) y += __shfl_xor_sync(team, y, o);
     if (q == 0) {
-      y = fmaf(skip, x, y);
+      y = fmaf(skip, to_float(x[r]), y);
       if (p.z) {
-        const float zv = to_float(static_cast<const T*>(p.z)[b * p.sz + c]);
+        const float zv = to_float(z[r]);
         y *= silu_of(zv, sigmoid(zv));
       }
       *out = from_float<T>(y);
@@ -155,7 +166,7 @@ extern "C" int gdn_ssm_decode_step(const void* x, const void* dt, const void* z,
   if (major != 10 || minor != 3) return GDN_ERR_UNSUPPORTED;
   const SsmStepParams p{x, dt, z, b, c, st[0], st[1], st[2], st[3], st[4], a, skip, dt_bias, state_idx, state_pool, out, status,
                         B, C, S, G, n_pool, dt_softplus != 0};
-  const bool vec = S % 4 == 0 && al(a, 16) && al(state_pool, 16);
+  const bool vec = S % 4 == 0 && al(a, 16) && al(state_pool, 16) && al(b, 4 * es) && al(c, 4 * es) && st[3] % 4 == 0 && st[4] % 4 == 0;
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == GDN_DTYPE_BF16)
     launch_step_of<__nv_bfloat16>(p, vec, s);
