@@ -92,17 +92,22 @@ struct Share {
 // The next rows' vectors of a thread's share on their way into its own places in shared memory: kN tensors, kStages rows.
 template <int kN, int kNv, int kStages>
 struct Ring {
-  static constexpr int kBytes = kN * kNv * kStages * 16;  // a thread
-  static __device__ __forceinline__ Words* at(int k, int tensor, int v) {
+  static constexpr int bytes(int threads) { return kN * kNv * kStages * 16 * threads; }
+  static __device__ __forceinline__ Words* at(int slot, int tensor, int v) {
     extern __shared__ Words ring[];
-    return ring + (((k % (kStages > 0 ? kStages : 1)) * kN + tensor) * kNv + v) * (int)blockDim.x + threadIdx.x;
+    return ring + ((slot * kN + tensor) * kNv + v) * (int)blockDim.x + threadIdx.x;
   }
+  static __device__ __forceinline__ void step(int& slot) { slot = slot + 1 == kStages ? 0 : slot + 1; }
 };
 
-// Sums over the team; every thread of it gets them. `buf` has room for two rows of a CTA's warps, used in turn, so that
-// one barrier a row is enough.
+// Sums over the team; every thread of it gets them, added up in the same order. `buf` has room for two rows of a CTA's
+// warps, used in turn, so that one barrier a row is enough.
 template <int kN>
-__device__ __forceinline__ void team_sum(float (&v)[kN], int L, float (*buf)[kN][kMaxTeam / 32], int& turn) {
+struct alignas(4 * kN) Sums {
+  float v[kN];
+};
+template <int kN>
+__device__ __forceinline__ void team_sum(float (&v)[kN], int L, Sums<kN> (*buf)[kMaxTeam / 32], int& turn) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     if (o >= L) break;
@@ -110,18 +115,21 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], int L, float (*buf)[kN]
     for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   }
   if (L <= 32) return;
-  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, W = L >> 5;
-  if (lane == 0) {
+  const int W = L >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    Sums<kN> s;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) buf[turn][i][wid] = v[i];
+    for (int i = 0; i < kN; ++i) s.v[i] = v[i];
+    buf[turn][threadIdx.x >> 5] = s;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float s = lane < W ? buf[turn][i][lane] : 0.f;
+  for (int i = 0; i < kN; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int w = 0; w < W; ++w) {
+    const Sums<kN> s = buf[turn][w];
 #pragma unroll
-    for (int o = 1; o < kMaxTeam / 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    v[i] = __shfl_sync(0xffffffffu, s, 0);
+    for (int i = 0; i < kN; ++i) v[i] += s.v[i];
   }
   turn ^= 1;
 }
@@ -143,7 +151,7 @@ template <typename T, int kNv, bool kVec, bool kGateFirst>
 __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_constant__ GnormParams p, int L) {
   constexpr int P = kPairs<T>, kStages = fwd_stages<T, kNv, kVec>();
   using R = Ring<2, kNv, kStages>;
-  __shared__ float buf[2][1][kMaxTeam / 32];
+  __shared__ Sums<1> buf[2][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
   const int64_t row0 = team / p.ng, at = (team - row0 * p.ng) * p.group;
@@ -165,18 +173,22 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
   const float inv = 1.f / (float)p.group;
   const T *x = static_cast<const T*>(p.x) + row0 * p.sx + at, *z = static_cast<const T*>(p.z) + row0 * p.sz + at;
   T* y = static_cast<T*>(p.y) + row0 * p.D + at;
+  const int64_t dx = p.rows * p.sx, dz = p.rows * p.sz, dy = p.rows * p.D;
   // rows behind the last one (and those of threads behind the last team) are left out
-  const int64_t mine = row0 < p.rows && row0 < p.T ? (p.T - row0 + p.rows - 1) / p.rows : 0;
+  const int mine = row0 < p.rows && row0 < p.T ? (int)((p.T - row0 + p.rows - 1) / p.rows) : 0;
+  int put = 0, take = 0;  // places in the ring; x and z: the row that comes next
   auto issue = [&](int k) {
     if (k < mine) {
 #pragma unroll
       for (int v = 0; v < kNv; ++v)
         if (sh.col(v, 0) < p.group) {
-          cp_async16(R::at(k, 0, v), x + k * p.rows * p.sx + sh.col(v, 0));
-          cp_async16(R::at(k, 1, v), z + k * p.rows * p.sz + sh.col(v, 0));
+          cp_async16(R::at(put, 0, v), x + sh.col(v, 0));
+          cp_async16(R::at(put, 1, v), z + sh.col(v, 0));
         }
     }
     cp_async_commit();
+    x += dx, z += dz;
+    R::step(put);
   };
   if constexpr (kStages > 0) {
 #pragma unroll
@@ -192,10 +204,10 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
     for (int v = 0; v < kNv; ++v) {
       Words xr{}, zr{};
       if constexpr (kStages > 0) {
-        if (k < mine && sh.col(v, 0) < p.group) xr = *R::at(k, 0, v), zr = *R::at(k, 1, v);
+        if (k < mine && sh.col(v, 0) < p.group) xr = *R::at(take, 0, v), zr = *R::at(take, 1, v);
       } else {
-        xr = sh.load(x + k * p.rows * p.sx, v, k < mine);
-        zr = sh.load(z + k * p.rows * p.sz, v, k < mine);
+        xr = sh.load(x, v, k < mine);
+        zr = sh.load(z, v, k < mine);
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -204,9 +216,13 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
         sum2 = kGateFirst ? f2_fma(xg[v][i], xg[v][i], sum2) : f2_fma(u, u, sum2);
       }
     }
+    if constexpr (kStages > 0)
+      R::step(take);
+    else
+      x += dx, z += dz;
     float sum[1] = {f2_sum(sum2)};
     team_sum(sum, L, buf, turn);
-    const uint64_t rs = f2_dup(1.f / sqrtf(fmaf(sum[0], inv, p.eps)));
+    const uint64_t rs = f2_dup(rsqrtf(fmaf(sum[0], inv, p.eps)));
     if (k < mine) {
 #pragma unroll
       for (int v = 0; v < kNv; ++v) {
@@ -216,7 +232,7 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
         sh.store(y, v, o);
       }
     }
-    y += p.rows * p.D;
+    y += dy;
   }
 }
 
@@ -224,12 +240,12 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
 // weights and the row stay in registers; longer shares take both again. Rows ahead are on their way into shared memory
 // where that holds enough of them, else a row's second reading comes from L2.
 template <typename T, int kNv, bool kVec, bool kGateFirst>
-__global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
+__global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
   constexpr int K = kElems<T>, P = kPairs<T>;
   constexpr bool kKeep = kNv * K <= 8;
   constexpr int kStages = bwd_stages<T, kNv, kVec>();
   using R = Ring<3, kNv, kStages>;
-  __shared__ float buf[2][2][kMaxTeam / 32];
+  __shared__ Sums<2> buf[2][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
   const int64_t row0 = team / p.ng, at = (team - row0 * p.ng) * p.group;
@@ -261,20 +277,24 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(con
   const float inv = 1.f / (float)p.group;
   const T *x = static_cast<const T*>(p.x) + row0 * p.sx + at, *z = static_cast<const T*>(p.z) + row0 * p.sz + at,
           *g = static_cast<const T*>(p.dy) + row0 * p.sdy + at;
-  int64_t out = row0 * p.D + at;
-  const int64_t mine = row0 < p.rows && row0 < p.T ? (p.T - row0 + p.rows - 1) / p.rows : 0;
+  const int64_t ex = p.rows * p.sx, ez = p.rows * p.sz, eg = p.rows * p.sdy, eo = p.rows * p.D;
+  T *dxp = static_cast<T*>(p.dx) + row0 * p.D + at, *dzp = static_cast<T*>(p.dz) + row0 * p.D + at;
+  const int mine = row0 < p.rows && row0 < p.T ? (int)((p.T - row0 + p.rows - 1) / p.rows) : 0;
+  int put = 0, take = 0;  // places in the ring; x, z and g: the row that comes next
   constexpr int kHold = kKeep ? kNv : 1;
   auto issue = [&](int k) {
     if (k < mine) {
 #pragma unroll
       for (int v = 0; v < kNv; ++v)
         if (sh.col(v, 0) < p.group) {
-          cp_async16(R::at(k, 0, v), x + k * p.rows * p.sx + sh.col(v, 0));
-          cp_async16(R::at(k, 1, v), z + k * p.rows * p.sz + sh.col(v, 0));
-          cp_async16(R::at(k, 2, v), g + k * p.rows * p.sdy + sh.col(v, 0));
+          cp_async16(R::at(put, 0, v), x + sh.col(v, 0));
+          cp_async16(R::at(put, 1, v), z + sh.col(v, 0));
+          cp_async16(R::at(put, 2, v), g + sh.col(v, 0));
         }
     }
     cp_async_commit();
+    x += ex, z += ez, g += eg;
+    R::step(put);
   };
   if constexpr (kStages > 0) {
 #pragma unroll
@@ -294,7 +314,6 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(con
         dot = f2_fma(f2_mul(xg, wt(v, i)), pair_of<T>(gr[hold], i), dot);
       }
     };
-    const T *xk = x + k * p.rows * p.sx, *zk = z + k * p.rows * p.sz, *gk = g + k * p.rows * p.sdy;
     if constexpr (kStages > 0) {
       issue(k + kStages - 1);
       cp_async_wait<(kStages > 0 ? kStages - 1 : 0)>();
@@ -302,11 +321,11 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(con
     auto fetch = [&](int v, int hold, bool live) {
       if constexpr (kStages > 0) {
         xr[hold] = zr[hold] = gr[hold] = Words{};
-        if (live && sh.col(v, 0) < p.group) xr[hold] = *R::at(k, 0, v), zr[hold] = *R::at(k, 1, v), gr[hold] = *R::at(k, 2, v);
+        if (live && sh.col(v, 0) < p.group) xr[hold] = *R::at(take, 0, v), zr[hold] = *R::at(take, 1, v), gr[hold] = *R::at(take, 2, v);
       } else {
-        xr[hold] = sh.load(xk, v, live);
-        zr[hold] = sh.load(zk, v, live);
-        gr[hold] = sh.load(gk, v, live);
+        xr[hold] = sh.load(x, v, live);
+        zr[hold] = sh.load(z, v, live);
+        gr[hold] = sh.load(g, v, live);
       }
     };
 #pragma unroll
@@ -316,7 +335,7 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(con
     }
     float sum[2] = {f2_sum(sq), f2_sum(dot)};
     team_sum(sum, L, buf, turn);
-    const float r = 1.f / sqrtf(fmaf(sum[0], inv, p.eps));
+    const float r = rsqrtf(fmaf(sum[0], inv, p.eps));
     const uint64_t rs = f2_dup(r), mean = f2_dup(-sum[1] * inv * r * r);  // - rs mean(g hat)
     if (k < mine) {
 #pragma unroll
@@ -343,11 +362,15 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 84 : 128) gnorm_bwd_kernel(con
             set_pair<T>(dz, i, f2_mul(f2_mul(wr, xx), slope));
           }
         }
-        sh.store(static_cast<T*>(p.dx) + out, v, dx);
-        sh.store(static_cast<T*>(p.dz) + out, v, dz);
+        sh.store(dxp, v, dx);
+        sh.store(dzp, v, dz);
       }
     }
-    out += p.rows * p.D;
+    dxp += eo, dzp += eo;
+    if constexpr (kStages > 0)
+      R::step(take);
+    else
+      x += ex, z += ez, g += eg;
   }
   if (row0 < p.rows) {
 #pragma unroll
@@ -477,7 +500,7 @@ bool allow_smem(K kernel, size_t bytes) {
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-constexpr int kFwdThreads = 1024, kBwdThreads = 768;  // resident threads to an SM that the grids are made for
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // resident threads to an SM that the grids are made for
 
 // The most rows of parts that any shape of the backward writes: what a team of the smallest size would.
 size_t part_bytes(int64_t T, int D, int group, int es, int sms) {
@@ -511,7 +534,7 @@ extern "C" int gdn_gated_rmsnorm_fwd(const void* x, int64_t x_stride, const void
       constexpr int kNv = decltype(n)::value;
       auto* kernel = p.gate_first ? (vec ? gnorm_fwd_kernel<T_, kNv, true, true> : gnorm_fwd_kernel<T_, kNv, false, true>)
                                   : (vec ? gnorm_fwd_kernel<T_, kNv, true, false> : gnorm_fwd_kernel<T_, kNv, false, false>);
-      const size_t ring = vec ? (size_t)s.threads * Ring<2, kNv, fwd_stages<T_, kNv, true>()>::kBytes : 0;
+      const size_t ring = vec ? Ring<2, kNv, fwd_stages<T_, kNv, true>()>::bytes(s.threads) : 0;
       ok = allow_smem(kernel, ring);
       if (ok) kernel<<<(unsigned)s.ctas, s.threads, ring, (cudaStream_t)stream>>>(p, s.L);
     });
@@ -555,7 +578,7 @@ extern "C" int gdn_gated_rmsnorm_bwd(const void* x, int64_t x_stride, const void
         constexpr int kNv = decltype(n)::value;
         auto* kernel = p.gate_first ? (vec ? gnorm_bwd_kernel<T_, kNv, true, true> : gnorm_bwd_kernel<T_, kNv, false, true>)
                                     : (vec ? gnorm_bwd_kernel<T_, kNv, true, false> : gnorm_bwd_kernel<T_, kNv, false, false>);
-        const size_t ring = vec ? (size_t)s.threads * Ring<3, kNv, bwd_stages<T_, kNv, true>()>::kBytes : 0;
+        const size_t ring = vec ? Ring<3, kNv, bwd_stages<T_, kNv, true>()>::bytes(s.threads) : 0;
         ok = allow_smem(kernel, ring);
         if (ok) kernel<<<(unsigned)s.ctas, s.threads, ring, (cudaStream_t)stream>>>(p, s.L);
       });

@@ -186,35 +186,43 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
 
 enum { kWalkState = 0, kWalkOut = 1, kWalkGrad = 2 };
 
-// Rows of a [T, C] tensor on their way into shared memory: the kN channels from `first` on, of tokens one after the
-// other, by asynchronous copies of 16 bytes. kVec: everything is aligned to them. Other rows bring the pieces that
-// cover the channels, and each row's place within its first piece is found again from its address; a piece that
-// sticks out of the tensor is copied by elements.
-template <typename T, int kN, bool kVec>
+// Rows of a [T, C] tensor on their way into shared memory: the kN channels from `first` on, of up to kRows tokens one
+// after the other, by asynchronous copies of 16 bytes from kThreads threads. kVec: everything is aligned to them, and a
+// thread keeps its place. Other rows bring the pieces that cover the channels, and each row's place within its first
+// piece is found again from its address; a piece that sticks out of the tensor is copied by elements.
+template <typename T, int kN, int kRows, int kThreads, bool kVec>
 struct Rows {
   static constexpr int K = 16 / (int)sizeof(T);
   static constexpr int kBytes = (kN * (int)sizeof(T) + 15) / 16 * 16 + (kVec ? 0 : 16);  // of a row in shared memory
   static constexpr int kPieces = kBytes / 16;
+  static_assert(!kVec || kThreads % kPieces == 0);
   const T* src;  // channel `first` of token 0
   int64_t stride;
   const T *lo, *hi;
-  int n;  // channels that exist
-  __device__ __forceinline__ Rows(const void* base, int64_t stride_, int64_t first, int n_, int T_, int C) : stride(stride_), n(n_) {
+  int n, tid;  // channels that exist
+  __device__ __forceinline__ Rows(const void* base, int64_t stride_, int64_t first, int n_, int T_, int C, int tid_)
+      : stride(stride_), n(n_), tid(tid_) {
     lo = static_cast<const T*>(base);
     src = lo + first;
     hi = kVec ? nullptr : lo + (T_ - 1) * stride_ + C;
   }
-  // tokens t .. t + rows - 1 (at most kRows), by thread `tid` of `threads`
-  template <int kRows>
-  __device__ __forceinline__ void fetch(uint8_t* dst, int64_t t, int rows, int tid, int threads) const {
-    for (int i = tid; i < kRows * kPieces; i += threads) {
-      const int r = i / kPieces, q = i - r * kPieces;
-      if (r >= rows) break;
-      const T* p = src + (t + r) * stride;
-      uint8_t* to = dst + r * kBytes + q * 16;
-      if constexpr (kVec) {
-        if (q * K < n) cp_async16(to, p + q * K);
-      } else {
+  // tokens t .. t + rows - 1
+  __device__ __forceinline__ void fetch(uint8_t* dst, int64_t t, int rows) const {
+    if constexpr (kVec) {
+      constexpr int kAbreast = kThreads / kPieces;  // rows that the threads take at once
+      const int r0 = tid / kPieces, q = tid % kPieces;
+      if (q * K >= n) return;
+      const T* p = src + (t + r0) * stride + q * K;
+#pragma unroll
+      for (int i = 0; i < (kRows + kAbreast - 1) / kAbreast; ++i) {
+        if (r0 + i * kAbreast < rows) cp_async16(dst + tid * 16 + i * kThreads * 16, p);
+        p += kAbreast * stride;
+      }
+    } else {
+      for (int i = tid; i < rows * kPieces; i += kThreads) {
+        const int r = i / kPieces, q = i - r * kPieces;
+        const T* p = src + (t + r) * stride;
+        uint8_t* to = dst + r * kBytes + q * 16;
         const T* piece = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15) + q * K;
         if (piece >= p + n) continue;
         if (piece >= lo && piece + K <= hi) {
@@ -268,7 +276,7 @@ template <typename T, int kSp, int kMode, bool kVec>
 struct WalkShape {
   static constexpr int kNl = kSp == 64 ? 2 : 1, kNt = kSp / kNl, kDt = kSp <= 16 ? 2 : 1, kCh = 32 / kNl * kDt;
   static constexpr int kTb = 8;
-  using R = Rows<T, kCh, kVec>;
+  using R = Rows<T, kCh, kTb, 32, kVec>;
   static constexpr int kTensors = kMode == kWalkState ? 2 : kMode == kWalkOut ? 3 : 4;
   static constexpr int kRowsBytes = kTb * R::kBytes, kMapBytes = kTb * 2 * kSp * 4;
   static constexpr int kStage = kTensors * kRowsBytes + kMapBytes;
@@ -302,21 +310,24 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
     const int c0 = g * Cg + min(cg, Cg - 1);              // a channel that exists
     const int64_t first = (int64_t)g * Cg + cb;
     const int have = min(kCh, Cg - cb);
-    const R rx(p.x, p.sx, first, have, p.T, p.C), rd(p.dt, p.sdt, first, have, p.T, p.C);
-    const R rz(p.z, p.sz, first, have, p.T, p.C), ro(p.dout, p.sdo, first, have, p.T, p.C);
+    const R rx(p.x, p.sx, first, have, p.T, p.C, lane), rd(p.dt, p.sdt, first, have, p.T, p.C, lane);
+    const R rz(p.z, p.sz, first, have, p.T, p.C, lane), ro(p.dout, p.sdo, first, have, p.T, p.C, lane);
     auto fetch = [&](int i0, uint8_t* st) {  // the inputs of tokens i0 .. i0 + kTb - 1 of the segment
       const int64_t t = sg.tok0 + i0;
       const int rows = min(kTb, sg.ntok - i0);
-      rx.template fetch<kTb>(st, t, rows, lane, 32);
-      rd.template fetch<kTb>(st + W::kRowsBytes, t, rows, lane, 32);
+      rx.fetch(st, t, rows);
+      rd.fetch(st + W::kRowsBytes, t, rows);
       if constexpr (kGate) {
-        if (has_z) rz.template fetch<kTb>(st + 2 * W::kRowsBytes, t, rows, lane, 32);
+        if (has_z) rz.fetch(st + 2 * W::kRowsBytes, t, rows);
       }
-      if constexpr (kMode == kWalkGrad) ro.template fetch<kTb>(st + 3 * W::kRowsBytes, t, rows, lane, 32);
+      if constexpr (kMode == kWalkGrad) ro.fetch(st + 3 * W::kRowsBytes, t, rows);
       uint8_t* mp = st + W::kTensors * W::kRowsBytes;
-      for (int i = lane; i < rows * (2 * kSp / 4); i += 32) {
-        const int k = i / (2 * kSp / 4), r = i % (2 * kSp / 4);
-        cp_async16(mp + i * 16, p.maps + ((t + k) * p.G + g) * 2 * kSp + 4 * r);
+      constexpr int kM = kSp / 2;  // pieces of a token's maps
+      const float* from = p.maps + ((t + lane / kM) * p.G + g) * 2 * kSp + lane % kM * 4;
+#pragma unroll
+      for (int i = 0; i < kTb * kM / 32; ++i) {
+        if (i * 32 + lane < rows * kM) cp_async16(mp + (i * 32 + lane) * 16, from);
+        from += (int64_t)(32 / kM) * p.G * 2 * kSp;
       }
       cp_async_commit();
     };
@@ -600,7 +611,7 @@ template <typename T, int kSp, bool kVec>
 struct GradSmem {
   static constexpr int kNl = kSp / 4, kDl = 32 / kNl, kCh = 4 * kDl, kCtaCh = kSsmWarps * kCh;
   static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;  // two CTAs to an SM either way
-  using R = Rows<T, kCtaCh, kVec>;
+  using R = Rows<T, kCtaCh, kSsmTile, 32 * kSsmWarps, kVec>;
   uint8_t raw[kStages][4][kSsmTile * R::kBytes];  // x, dt, z, dout
   float maps[kStages][kSsmTile][2 * kSp];
   float part[kSsmWarps][kSsmTile][2 * kSp];       // db and dc of each warp's channels
@@ -642,15 +653,16 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
     const int c0 = g * Cg + min(cb + 4 * dl, Cg - 1), cmax = g * Cg + Cg - 1;
     const int64_t first = (int64_t)g * Cg + ctab;
     const int have = min(Smem::kCtaCh, Cg - ctab);
-    const R rx(p.x, p.sx, first, have, p.T, p.C), rd(p.dt, p.sdt, first, have, p.T, p.C);
-    const R rz(p.z, p.sz, first, have, p.T, p.C), ro(p.dout, p.sdo, first, have, p.T, p.C);
+    const int tid = threadIdx.x;
+    const R rx(p.x, p.sx, first, have, p.T, p.C, tid), rd(p.dt, p.sdt, first, have, p.T, p.C, tid);
+    const R rz(p.z, p.sz, first, have, p.T, p.C, tid), ro(p.dout, p.sdo, first, have, p.T, p.C, tid);
     auto fetch = [&](int tile) {
       const int st = tile % kStages, rows = min(kTb, sg.ntok - tile * kTb);
       const int64_t t = sg.tok0 + tile * kTb;
-      rx.template fetch<kTb>(sm.raw[st][0], t, rows, threadIdx.x, 32 * kSsmWarps);
-      rd.template fetch<kTb>(sm.raw[st][1], t, rows, threadIdx.x, 32 * kSsmWarps);
-      if (has_z) rz.template fetch<kTb>(sm.raw[st][2], t, rows, threadIdx.x, 32 * kSsmWarps);
-      ro.template fetch<kTb>(sm.raw[st][3], t, rows, threadIdx.x, 32 * kSsmWarps);
+      rx.fetch(sm.raw[st][0], t, rows);
+      rd.fetch(sm.raw[st][1], t, rows);
+      if (has_z) rz.fetch(sm.raw[st][2], t, rows);
+      ro.fetch(sm.raw[st][3], t, rows);
       for (int i = threadIdx.x; i < kTb * (kSp / 2); i += 32 * kSsmWarps) {  // zeros behind the last token
         const int k = i / (kSp / 2), r = i % (kSp / 2);
         cp_async16_if(&sm.maps[st][k][4 * r], p.maps + ((t + min(k, rows - 1)) * p.G + g) * 2 * kSp + 4 * r, k < rows);

@@ -3,8 +3,9 @@
 //     dt = softplus(raw + dt_bias),  h = exp(dt a) h + dt x b (stored back),  y = sum_s c h + skip x,  out = y silu(z).
 // It is the scan on a document of one token that starts from the pool entry.
 //
-// The step reads and writes each state once and does seven operations an element: it is bound by HBM traffic. Four
-// states of a channel to a thread; kRows sequences at once, so that a thread's decays are read once for them.
+// The step reads and writes each state once and does seven operations an element: it is bound by HBM traffic as long as
+// what is done for each channel stays small beside it. A thread takes four states of two channels of one sequence, in
+// packed pairs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,89 +34,92 @@ struct SsmStepParams {
   int B, C, S, G, n_pool, softplus;
 };
 
-template <typename T, int kSp, int kRows, bool kVec>
+// kVec: states, maps and pairs of channels are aligned.
+template <typename T, int kSp, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_constant__ SsmStepParams p) {
+  using bw::f2_fma;
+  using bw::f2_hi;
+  using bw::f2_lo;
+  using bw::f2_mul;
+  using bw::f2_pack;
   constexpr int kQ = kSp / 4;
-  const int q = threadIdx.x % kQ, c = blockIdx.x * (kStepThreads / kQ) + threadIdx.x / kQ;
-  if (c >= p.C) return;  // whole channels leave
-  const unsigned team = ((kQ == 32 ? 0u : 1u << kQ) - 1u) << ((threadIdx.x & 31) / kQ * kQ);
-  const int g = c / (p.C / p.G), n = min(4, p.S - 4 * q);
-  const auto A = load_pack<float, 4, kVec>(p.a + (int64_t)c * p.S + 4 * q, n);
-  const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
-  const int b0 = blockIdx.y * kRows;
-  Pack<float, 4> h[kRows];
-  int entry[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    entry[r] = b0 + r < p.B ? p.state_idx[b0 + r] : -1;
-    if (entry[r] >= p.n_pool) entry[r] = -1;
-  }
-  // every load first
-  Pack<T, 4> bm[kRows], cm[kRows];
-  T x[kRows], dt[kRows], z[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int64_t b = b0 + r;
-    const bool live = entry[r] >= 0;
-    h[r] = load_pack<float, 4, kVec>(p.pool + ((int64_t)max(entry[r], 0) * p.C + c) * p.S + 4 * q, live ? n : 0);
-    x[r] = dt[r] = z[r] = from_float<T>(0.f);
-    if (live) {
-      x[r] = static_cast<const T*>(p.x)[b * p.sx + c];
-      dt[r] = static_cast<const T*>(p.dt)[b * p.sdt + c];
-      if (p.z) z[r] = static_cast<const T*>(p.z)[b * p.sz + c];
-    }
-    bm[r] = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + b * p.sb + g * p.S + 4 * q, live ? n : 0);
-    cm[r] = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + b * p.sc + g * p.S + 4 * q, live ? n : 0);
-  }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int64_t b = b0 + r;
-    if (b >= p.B) break;
-    T* out = static_cast<T*>(p.out) + b * p.C + c;
-    if (entry[r] < 0) {  // skipped, reported
-      if (q == 0) *out = from_float<T>(0.f);
-      if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
-      continue;
-    }
-    const float raw = to_float(dt[r]) + bias, delta = p.softplus ? softplus(raw) : raw, u = delta * to_float(x[r]);
-    float y = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < n) {
-        h[r].t[i] = fmaf(exp2_approx(delta * (kLog2e * A.t[i])), h[r].t[i], u * to_float(bm[r].t[i]));
-        y = fmaf(to_float(cm[r].t[i]), h[r].t[i], y);
-      }
-    }
-    store_pack<float, 4, kVec>(p.pool + ((int64_t)entry[r] * p.C + c) * p.S + 4 * q, h[r], n);
-#pragma unroll
-    for (int o = 1; o < kQ; o <<= 1) y += __shfl_xor_sync(team, y, o);
+  const int q = threadIdx.x % kQ, pair = blockIdx.x * (kStepThreads / kQ) + threadIdx.x / kQ;
+  const int Cg = p.C / p.G, per = (Cg + 1) / 2, g = pair / per, cg = 2 * (pair - g * per);
+  if (g >= p.G) return;  // whole teams leave
+  const unsigned team = ((1u << kQ) - 1u) << ((threadIdx.x & 31) / kQ * kQ);
+  const int c = g * Cg + cg, two = cg + 1 < Cg ? 1 : 0, n = min(4, p.S - 4 * q);
+  const int64_t b = blockIdx.y;
+  T* out = static_cast<T*>(p.out) + b * p.C + c;
+  const int entry = p.state_idx[b];
+  if (entry < 0 || entry >= p.n_pool) {  // skipped, reported
     if (q == 0) {
-      y = fmaf(skip, to_float(x[r]), y);
-      if (p.z) {
-        const float zv = to_float(z[r]);
-        y *= silu_of(zv, sigmoid(zv));
-      }
-      *out = from_float<T>(y);
+      out[0] = from_float<T>(0.f);
+      if (two) out[1] = from_float<T>(0.f);
     }
+    if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
+    return;
+  }
+  const int k = 1 + two;  // channels
+  float* state = p.pool + ((int64_t)entry * p.C + c) * p.S + 4 * q;
+  const float* a = p.a + (int64_t)c * p.S + 4 * q;
+  Pack<float, 4> h[2], A[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    h[d] = load_pack<float, 4, kVec>(state + d * p.S, d < k ? n : 0);
+    A[d] = load_pack<float, 4, kVec>(a + d * p.S, d < k ? n : 0);
+  }
+  const auto bm = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + b * p.sb + g * p.S + 4 * q, n);
+  const auto cm = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + b * p.sc + g * p.S + 4 * q, n);
+  const auto xr = load_pack<T, 2, kVec>(static_cast<const T*>(p.x) + b * p.sx + c, k);
+  const auto dr = load_pack<T, 2, kVec>(static_cast<const T*>(p.dt) + b * p.sdt + c, k);
+  Pack<T, 2> zr{};
+  if (p.z) zr = load_pack<T, 2, kVec>(static_cast<const T*>(p.z) + b * p.sz + c, k);
+  float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f};
+  if (p.dt_bias) bias[0] = p.dt_bias[c], bias[1] = p.dt_bias[c + two];
+  if (p.skip) skip[0] = p.skip[c], skip[1] = p.skip[c + two];
+  uint64_t delta = f2_pack(to_float(dr.t[0]) + bias[0], to_float(dr.t[1]) + bias[1]);
+  if (p.softplus) delta = softplus_pair(delta);
+  const uint64_t x = f2_pack(to_float(xr.t[0]), to_float(xr.t[1])), u = f2_mul(delta, x);
+  const uint64_t bv[2] = {f2_pack(to_float(bm.t[0]), to_float(bm.t[1])), f2_pack(to_float(bm.t[2]), to_float(bm.t[3]))};
+  const uint64_t cv[2] = {f2_pack(to_float(cm.t[0]), to_float(cm.t[1])), f2_pack(to_float(cm.t[2]), to_float(cm.t[3]))};
+  float y[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const uint64_t dd = f2_dup((d ? f2_hi(delta) : f2_lo(delta)) * kLog2e), uu = f2_dup(d ? f2_hi(u) : f2_lo(u));
+    uint64_t y2 = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t e = exp2_pair(f2_mul(dd, f2_pack(A[d].t[2 * i], A[d].t[2 * i + 1])));
+      const uint64_t v = f2_fma(e, f2_pack(h[d].t[2 * i], h[d].t[2 * i + 1]), f2_mul(uu, bv[i]));
+      y2 = f2_fma(cv[i], v, y2);
+      h[d].t[2 * i] = f2_lo(v), h[d].t[2 * i + 1] = f2_hi(v);
+    }
+    y[d] = bw::f2_sum(y2);
+    store_pack<float, 4, kVec>(state + d * p.S, h[d], d < k ? n : 0);
+  }
+#pragma unroll
+  for (int o = 1; o < kQ; o <<= 1) {
+    y[0] += __shfl_xor_sync(team, y[0], o);
+    y[1] += __shfl_xor_sync(team, y[1], o);
+  }
+  if (q == 0) {
+    uint64_t r = f2_fma(f2_pack(skip[0], skip[1]), x, f2_pack(y[0], y[1]));
+    if (p.z) r = f2_mul(r, silu_pair(f2_pack(to_float(zr.t[0]), to_float(zr.t[1]))));
+    Pack<T, 2> o;
+    o.t[0] = from_float<T>(f2_lo(r)), o.t[1] = from_float<T>(f2_hi(r));
+    store_pack<T, 2, kVec>(out, o, k);
   }
 }
 
 template <typename T, int kSp>
 void launch_step(const SsmStepParams& p, bool vec, cudaStream_t s) {
   constexpr int kPer = kStepThreads / (kSp / 4);
-  const unsigned gx = (unsigned)((p.C + kPer - 1) / kPer);
-  if (p.B == 1) {
-    if (vec)
-      ssm_step_kernel<T, kSp, 1, true><<<dim3(gx, 1), kStepThreads, 0, s>>>(p);
-    else
-      ssm_step_kernel<T, kSp, 1, false><<<dim3(gx, 1), kStepThreads, 0, s>>>(p);
-  } else {
-    const unsigned gy = (unsigned)((p.B + 3) / 4);
-    if (vec)
-      ssm_step_kernel<T, kSp, 4, true><<<dim3(gx, gy), kStepThreads, 0, s>>>(p);
-    else
-      ssm_step_kernel<T, kSp, 4, false><<<dim3(gx, gy), kStepThreads, 0, s>>>(p);
-  }
+  const int64_t pairs = (int64_t)p.G * ((p.C / p.G + 1) / 2);
+  const dim3 grid((unsigned)((pairs + kPer - 1) / kPer), (unsigned)p.B);
+  if (vec)
+    ssm_step_kernel<T, kSp, true><<<grid, kStepThreads, 0, s>>>(p);
+  else
+    ssm_step_kernel<T, kSp, false><<<grid, kStepThreads, 0, s>>>(p);
 }
 
 template <typename T>
@@ -138,7 +142,7 @@ extern "C" int gdn_ssm_decode_step(const void* x, const void* dt, const void* z,
   using namespace gdn;
   if (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_FP16 && dtype != GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED;
   if (B < 0 || C < 1 || S < 1 || S > kSsmMaxState || G < 1 || C % G != 0 || n_pool < 0) return GDN_ERR_INVALID_ARG;
-  if (B > 4 * 65535 || (int64_t)C * S > ((int64_t)1 << 28)) return GDN_ERR_INVALID_ARG;
+  if (B > 65535 || (int64_t)C * S > ((int64_t)1 << 28)) return GDN_ERR_INVALID_ARG;
   if (B == 0) return GDN_OK;
   if (!x || !dt || !a || !b || !c || !state_idx || !state_pool || !out || n_pool == 0) return GDN_ERR_INVALID_ARG;
   const int64_t rows[5] = {C, C, C, (int64_t)G * S, (int64_t)G * S};
@@ -166,7 +170,10 @@ extern "C" int gdn_ssm_decode_step(const void* x, const void* dt, const void* z,
   if (major != 10 || minor != 3) return GDN_ERR_UNSUPPORTED;
   const SsmStepParams p{x, dt, z, b, c, st[0], st[1], st[2], st[3], st[4], a, skip, dt_bias, state_idx, state_pool, out, status,
                         B, C, S, G, n_pool, dt_softplus != 0};
-  const bool vec = S % 4 == 0 && al(a, 16) && al(state_pool, 16) && al(b, 4 * es) && al(c, 4 * es) && st[3] % 4 == 0 && st[4] % 4 == 0;
+  bool vec = S % 4 == 0 && C / G % 2 == 0 && al(a, 16) && al(state_pool, 16) && al(b, 4 * es) && al(c, 4 * es) &&
+             st[3] % 4 == 0 && st[4] % 4 == 0;
+  for (const void* q : {x, dt, z, (const void*)out}) vec = vec && al(q, 2 * es);
+  for (int i = 0; i < 3; ++i) vec = vec && (st[i] % 2 == 0 || (i == 2 && !z));
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == GDN_DTYPE_BF16)
     launch_step_of<__nv_bfloat16>(p, vec, s);

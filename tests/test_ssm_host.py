@@ -70,7 +70,7 @@ def step(lib, **kw):
 
 
 def test_step_refusals(lib):
-    for kw in (dict(B=-1), dict(B=262141), dict(C=0), dict(S=65), dict(S=0), dict(G=3), dict(x=None), dict(idx=None),
+    for kw in (dict(B=-1), dict(B=65536), dict(C=0), dict(S=65), dict(S=0), dict(G=3), dict(x=None), dict(idx=None),
                dict(pool=None), dict(out=None), dict(n_pool=0), dict(pool=A + 2), dict(strides=[63, 0, 0, 0, 0]),
                dict(strides=[0, 0, 0, 15, 0]), dict(status=A + 2)):
         assert step(lib, **kw) == gdn.GDN_ERR_INVALID_ARG, kw
