@@ -40,6 +40,7 @@ using bw::f2_mul;
 using bw::f2_pack;
 using bw::f2_sum;
 
+constexpr int kGradSub = 4;  // tokens whose states the backward's walk holds at once
 constexpr int kPlanThreads = 1024;
 
 struct SsmParams {
@@ -189,7 +190,8 @@ enum { kWalkState = 0, kWalkOut = 1, kWalkGrad = 2 };
 // Rows of a [T, C] tensor on their way into shared memory: the kN channels from `first` on, of up to kRows tokens one
 // after the other, by asynchronous copies of 16 bytes from kThreads threads. kVec: everything is aligned to them, and a
 // thread keeps its place. Other rows bring the pieces that cover the channels, and each row's place within its first
-// piece is found again from its address; a piece that sticks out of the tensor is copied by elements.
+// piece is found again from its address; a piece that sticks out of the tensor is copied by elements. Rows behind the
+// last one are zero.
 template <typename T, int kN, int kRows, int kThreads, bool kVec>
 struct Rows {
   static constexpr int K = 16 / (int)sizeof(T);
@@ -215,14 +217,18 @@ struct Rows {
       const T* p = src + (t + r0) * stride + q * K;
 #pragma unroll
       for (int i = 0; i < (kRows + kAbreast - 1) / kAbreast; ++i) {
-        if (r0 + i * kAbreast < rows) cp_async16(dst + tid * 16 + i * kThreads * 16, p);
+        if (r0 + i * kAbreast < kRows) cp_async16_if(dst + tid * 16 + i * kThreads * 16, r0 + i * kAbreast < rows ? p : src, r0 + i * kAbreast < rows);
         p += kAbreast * stride;
       }
     } else {
-      for (int i = tid; i < rows * kPieces; i += kThreads) {
+      for (int i = tid; i < kRows * kPieces; i += kThreads) {
         const int r = i / kPieces, q = i - r * kPieces;
-        const T* p = src + (t + r) * stride;
         uint8_t* to = dst + r * kBytes + q * 16;
+        if (r >= rows) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const T* p = src + (t + r) * stride;
         const T* piece = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15) + q * K;
         if (piece >= p + n) continue;
         if (piece >= lo && piece + K <= hi) {
@@ -326,7 +332,8 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
       const float* from = p.maps + ((t + lane / kM) * p.G + g) * 2 * kSp + lane % kM * 4;
 #pragma unroll
       for (int i = 0; i < kTb * kM / 32; ++i) {
-        if (i * 32 + lane < rows * kM) cp_async16(mp + (i * 32 + lane) * 16, from);
+        const bool live = i * 32 + lane < rows * kM;
+        cp_async16_if(mp + (i * 32 + lane) * 16, live ? from : p.maps, live);
         from += (int64_t)(32 / kM) * p.G * 2 * kSp;
       }
       cp_async_commit();
@@ -386,8 +393,10 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
       __syncwarp();
       const int rows = min(kTb, sg.ntok - i0);
       const float* maps = reinterpret_cast<const float*>(st + W::kTensors * W::kRowsBytes) + nl * kNt;
+      // kBatch tokens at a time, without a branch, so that what belongs to different tokens can run side by side. Behind
+      // the last token the inputs are zero and the step is held at zero: the state stays.
+#pragma unroll 2
       for (int kb = 0; kb < rows; kb += kBatch) {
-        // steps and gates of kBatch tokens side by side (behind the last one of whatever lies there: not used)
         constexpr int kN = kBatch * kDt;
         float x[kN], delta[kN], gate[kN];
 #pragma unroll
@@ -402,22 +411,19 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
             gate[k * kDt + d] = 1.f;
           }
           if constexpr (kGate) {
-            if (has_z) {
-              const auto zv = rz.template get<kDt>(st + 2 * W::kRowsBytes, kb + k, t, dl * kDt);
+            const auto zv = rz.template get<kDt>(st + 2 * W::kRowsBytes, kb + k, t, dl * kDt);
 #pragma unroll
-              for (int d = 0; d < kDt; ++d) gate[k * kDt + d] = to_float(zv.t[d]);
-            }
+            for (int d = 0; d < kDt; ++d) gate[k * kDt + d] = to_float(zv.t[d]);
           }
         }
 #pragma unroll
         for (int i = 0; i < kN; i += 2) {
-          if (p.softplus) {
-            const uint64_t v = softplus_pair(f2_pack(delta[i], delta[i + 1]));
-            delta[i] = f2_lo(v), delta[i + 1] = f2_hi(v);
-          }
-          if (has_z) {
-            const uint64_t v = silu_pair(f2_pack(gate[i], gate[i + 1]));
-            gate[i] = f2_lo(v), gate[i + 1] = f2_hi(v);
+          const uint64_t v = softplus_pair(f2_pack(delta[i], delta[i + 1]));
+          delta[i] = kb + i / kDt >= rows ? 0.f : p.softplus ? f2_lo(v) : delta[i];
+          delta[i + 1] = kb + (i + 1) / kDt >= rows ? 0.f : p.softplus ? f2_hi(v) : delta[i + 1];
+          if constexpr (kGate) {
+            const uint64_t w = silu_pair(f2_pack(gate[i], gate[i + 1]));
+            gate[i] = has_z ? f2_lo(w) : 1.f, gate[i + 1] = has_z ? f2_hi(w) : 1.f;
           }
         }
         if constexpr (kMode == kWalkGrad) {
@@ -430,7 +436,6 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          if (kb + k >= rows) break;
           const float* mp = maps + (kb + k) * 2 * kSp;
           uint64_t dd[kDt], uu[kDt], gg[kDt], y2[kDt];
 #pragma unroll
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
               if constexpr (kNl == 2) y += __shfl_xor_sync(0xffffffffu, y, 1);
               r.t[d] = from_float<T>(fmaf(skip[d], x[k * kDt + d], y) * gate[k * kDt + d]);
             }
-            if (nl == 0 && nch > 0)
+            if (nl == 0 && nch > 0 && kb + k < rows)
               store_pack<T, kDt, kVec>(static_cast<T*>(p.out) + ((int64_t)sg.tok0 + i0 + kb + k) * p.C + c0, r, nch);
           }
         }
@@ -615,8 +620,9 @@ struct GradSmem {
   uint8_t raw[kStages][4][kSsmTile * R::kBytes];  // x, dt, z, dout
   float maps[kStages][kSsmTile][2 * kSp];
   float part[kSsmWarps][kSsmTile][2 * kSp];       // db and dc of each warp's channels
+  float bias[kSsmWarps][kCh];
   float delta[kSsmWarps][kSsmTile][kCh], u[kSsmWarps][kSsmTile][kCh], dy[kSsmWarps][kSsmTile][kCh];
-  float4 keep[kSsmWarps][kSsmTile / 4][4][32];
+  float4 keep[kSsmWarps][kSsmTile / kGradSub][4][32];
 };
 
 // v[0 .. kN - 1] of two lanes that differ in `mask` become the sums of the first half in the one without the bit, of
@@ -681,6 +687,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
       K[d][0] = f2_pack(kv.x, kv.y), K[d][1] = f2_pack(kv.z, kv.w);
       dA[d][0] = dA[d][1] = 0;
     }
+    for (int i = lane; i < kCh; i += 32) sm.bias[wid][i] = p.dt_bias ? p.dt_bias[g * Cg + min(cb + i, Cg - 1)] : 0.f;
     // for the steps a lane takes four channels of every kNl-th token
     const int lq = lane % kDl, lt = lane / kDl, lcg = cb + 4 * lq, ln = max(0, min(4, Cg - lcg));
     // and the gradients of channel ec[j], where it exists
@@ -722,33 +729,28 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
       cp_async_wait<0>();
       __syncthreads();  // this tile has landed, and every warp is done with the one before
       if (kStages == 2 && tile > 0) fetch(tile - 1);
-      for (int k = lt; k < kTb; k += kNl) {
-        float dv[4] = {0.f, 0.f, 0.f, 0.f}, uv[4] = {0.f, 0.f, 0.f, 0.f}, gv[4] = {0.f, 0.f, 0.f, 0.f};
-        if (k < nt) {
-          const int64_t t = t0 + k;
-          const int at = wid * kCh + 4 * lq;
-          const auto xr = rx.template get<4>(sm.raw[st][0], k, t, at);
-          const auto dr = rd.template get<4>(sm.raw[st][1], k, t, at);
-          const auto gr = ro.template get<4>(sm.raw[st][3], k, t, at);
-          Pack<T, 4> zr{};
-          if (has_z) zr = rz.template get<4>(sm.raw[st][2], k, t, at);
+      for (int k = lt; k < kTb; k += kNl) {  // behind the last token everything is zero
+        const int64_t t = t0 + k;
+        const int at = wid * kCh + 4 * lq;
+        const auto xr = rx.template get<4>(sm.raw[st][0], k, t, at);
+        const auto dr = rd.template get<4>(sm.raw[st][1], k, t, at);
+        const auto zr = rz.template get<4>(sm.raw[st][2], k, t, at);
+        const auto gr = ro.template get<4>(sm.raw[st][3], k, t, at);
+        const float4 bi = *reinterpret_cast<const float4*>(&sm.bias[wid][4 * lq]);
+        float dv[4] = {bi.x, bi.y, bi.z, bi.w}, uv[4], gv[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < ln) dv[j] = to_float(dr.t[j]) + (p.dt_bias ? p.dt_bias[g * Cg + lcg + j] : 0.f);
+        for (int j = 0; j < 4; ++j) dv[j] += to_float(dr.t[j]);
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            if (p.softplus) {
-              const uint64_t v = softplus_pair(f2_pack(dv[j], dv[j + 1]));
-              dv[j] = f2_lo(v), dv[j + 1] = f2_hi(v);
-            }
-            uint64_t gate = f2_dup(1.f);
-            if (has_z) gate = silu_pair(f2_pack(to_float(zr.t[j]), to_float(zr.t[j + 1])));
-            gv[j] = to_float(gr.t[j]) * f2_lo(gate), gv[j + 1] = to_float(gr.t[j + 1]) * f2_hi(gate);
-          }
+        for (int j = 0; j < 4; j += 2) {
+          const uint64_t v = softplus_pair(f2_pack(dv[j], dv[j + 1]));
+          const uint64_t w = silu_pair(f2_pack(to_float(zr.t[j]), to_float(zr.t[j + 1])));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uv[j] = dv[j] * to_float(xr.t[j]);
-            if (j >= ln) dv[j] = uv[j] = gv[j] = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            const bool live = k < nt && j + i < ln;
+            dv[j + i] = !live ? 0.f : p.softplus ? (i ? f2_hi(v) : f2_lo(v)) : dv[j + i];
+            uv[j + i] = live ? dv[j + i] * to_float(xr.t[j + i]) : 0.f;
+            gv[j + i] = to_float(gr.t[j + i]);
+            gv[j + i] = live ? (has_z ? gv[j + i] * (i ? f2_hi(w) : f2_lo(w)) : gv[j + i]) : 0.f;
           }
         }
         *reinterpret_cast<float4*>(&sm.delta[wid][k][4 * lq]) = make_float4(dv[0], dv[1], dv[2], dv[3]);
@@ -773,14 +775,14 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
           h[d][1] = f2_fma(exp2_pair(f2_mul(dd, A[d][1])), h[d][1], f2_mul(uu, bv.y));
         }
       };
-      const int subs = (nt + 3) / 4;
+      const int subs = (nt + kGradSub - 1) / kGradSub;
       for (int s = 0; s < subs; ++s) {
 #pragma unroll
         for (int d = 0; d < 4; ++d)
           *reinterpret_cast<ulonglong2*>(&sm.keep[wid][s][d][lane]) = make_ulonglong2(h[d][0], h[d][1]);
         if (s + 1 < subs) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) forward(4 * s + k);
+          for (int k = 0; k < kGradSub; ++k) forward(kGradSub * s + k);
         }
       }
       for (int s = subs - 1; s >= 0; --s) {
@@ -789,16 +791,16 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
           const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sm.keep[wid][s][d][lane]);
           h[d][0] = f.x, h[d][1] = f.y;
         }
-        uint64_t hb[4][4][2];  // states before each of the four tokens
+        uint64_t hb[kGradSub][4][2];  // states before each of these tokens
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kGradSub; ++k) {
 #pragma unroll
           for (int d = 0; d < 4; ++d) hb[k][d][0] = h[d][0], hb[k][d][1] = h[d][1];
-          forward(4 * s + k);  // behind the last token dt, u, b and c are 0: the state stays
+          forward(kGradSub * s + k);  // behind the last token dt, u, b and c are 0: the state stays
         }
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
-          const int tk = 4 * s + k;
+        for (int k = kGradSub - 1; k >= 0; --k) {
+          const int tk = kGradSub * s + k;
           float dv[4], uv[4], gv[4];
           row4(&sm.delta[wid][tk][4 * dl], dv);
           row4(&sm.u[wid][tk][4 * dl], uv);
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
             uint64_t du = 0, va = 0, yv = 0;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const uint64_t hn = k == 3 ? h[d][n] : hb[k == 3 ? 3 : k + 1][d][n], b = n ? bv.y : bv.x, c = n ? cv.y : cv.x;
+              const uint64_t hn = k == kGradSub - 1 ? h[d][n] : hb[k == kGradSub - 1 ? k : k + 1][d][n], b = n ? bv.y : bv.x, c = n ? cv.y : cv.x;
               K[d][n] = f2_fma(gg, c, K[d][n]);
               yv = f2_fma(c, hn, yv);
               dc[n] = f2_fma(gg, hn, dc[n]);
@@ -860,28 +862,26 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < kW; ++i) sm.part[wid][tk][(at + i) / 4 * kSp + 4 * nl + (at + i) % 4] = w[i];
           }
-          if (tk < nt) {
-            const int64_t t = t0 + tk;
 #pragma unroll
-            for (int j = 0; j < kCl; ++j) {
-              if (!ev[j]) continue;
-              const int rc = ec[j] - (int)first, wc = rc - wid * kCh;  // in the CTA's rows, in the warp's
-              const float x = to_float(rx.template get<1>(sm.raw[st][0], tk, t, rc).t[0]);
-              const float raw = to_float(rd.template get<1>(sm.raw[st][1], tk, t, rc).t[0]) + bias[j];
-              float dyv = to_float(ro.template get<1>(sm.raw[st][3], tk, t, rc).t[0]);
-              const float du = v[3 * j], va = v[3 * j + 1] * (1.f / kLog2e), yv = v[3 * j + 2];
-              const int64_t o = t * p.C + ec[j];
-              if (has_z) {
-                const float zv = to_float(rz.template get<1>(sm.raw[st][2], tk, t, rc).t[0]), sig = sigmoid(zv);
-                static_cast<T*>(p.dz)[o] = from_float<T>(dyv * fmaf(skip[j], x, yv) * silu_slope(zv, sig));
-                dyv = sm.dy[wid][tk][wc];
-              }
-              static_cast<T*>(p.dx)[o] = from_float<T>(fmaf(sm.delta[wid][tk][wc], du, skip[j] * dyv));
-              float dd = fmaf(x, du, va);
-              if (p.softplus) dd *= sigmoid(raw);
+          for (int j = 0; j < kCl; ++j) {
+            const int64_t t = t0 + tk, o = t * p.C + ec[j];
+            const int rc = ec[j] - (int)first, wc = rc - wid * kCh;  // in the CTA's rows, in the warp's
+            const bool live = tk < nt;
+            const float x = live ? to_float(rx.template get<1>(sm.raw[st][0], tk, t, rc).t[0]) : 0.f;
+            const float raw = to_float(rd.template get<1>(sm.raw[st][1], tk, t, rc).t[0]) + bias[j];
+            const float zv = to_float(rz.template get<1>(sm.raw[st][2], tk, t, rc).t[0]), sig = sigmoid(zv);
+            const float gout = to_float(ro.template get<1>(sm.raw[st][3], tk, t, rc).t[0]), dyv = sm.dy[wid][tk][wc];
+            const float du = v[3 * j], va = v[3 * j + 1] * (1.f / kLog2e), yv = v[3 * j + 2], sp = sigmoid(raw);
+            const float dx = fmaf(sm.delta[wid][tk][wc], du, skip[j] * dyv);
+            float dd = fmaf(x, du, va) * (p.softplus ? sp : 1.f);
+            dd = live ? dd : 0.f;
+            dbias[j] += dd;
+            dskip[j] = fmaf(dyv, x, dskip[j]);
+            const float dz = gout * fmaf(skip[j], x, yv) * silu_slope(zv, sig);
+            if (live && ev[j]) {
+              static_cast<T*>(p.dx)[o] = from_float<T>(dx);
               static_cast<T*>(p.ddt)[o] = from_float<T>(dd);
-              dbias[j] += dd;
-              dskip[j] = fmaf(dyv, x, dskip[j]);
+              if (has_z) static_cast<T*>(p.dz)[o] = from_float<T>(dz);
             }
           }
         }
@@ -1122,7 +1122,7 @@ bool launch_walk(const SsmParams& p, int sms, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const int Sp = ssm_padded(p.S), ch = ssm_walk_channels(Sp);
   const int64_t items = p.smax * p.G * ((p.C / p.G + ch - 1) / ch), ctas = (items + kSsmWarps - 1) / kSsmWarps;
-  const unsigned grid = (unsigned)(ctas < 8 * sms ? ctas : 8 * sms);
+  const unsigned grid = (unsigned)(ctas < 64 * sms ? ctas : 64 * sms);
   const bool vec = vectors_ok(p);
   bool ok = false;
   by_type(p.dtype, [&](auto t) {
@@ -1158,7 +1158,7 @@ bool launch_grad(const SsmParams& p, int sms, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const int64_t items = p.smax * p.G * p.parts;
-  const unsigned grid = (unsigned)(items < 4 * sms ? items : 4 * sms);
+  const unsigned grid = (unsigned)(items < 64 * sms ? items : 64 * sms);
   const bool vec = vectors_ok(p);
   bool ok = false;
   by_type(p.dtype, [&](auto t) {
