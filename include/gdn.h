@@ -429,7 +429,7 @@ int gdn_ssm_bwd(const void* x, const void* dt, const void* z, const float* a, co
  * One token per sequence of the selective scan, in place on a pool of states: the scan of a one-token
  * document that starts from state_pool[state_idx[b]] and leaves its state there.
  *   x, dt, z, out : [B, C];  b, c : [B, G, S];  state_pool : fp32 [n_pool, C, S];  strides : of x, dt, z, b, c;
- *   B <= 65535;  state_idx, status : as in gdn_decode_step (an index out of range is skipped, its out row
+ *   B and G <= 65535;  state_idx, status : as in gdn_decode_step (an index out of range is skipped, its out row
  *   zero, and reported)
  */
 int gdn_ssm_decode_step(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,

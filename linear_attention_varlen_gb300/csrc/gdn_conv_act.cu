@@ -394,30 +394,28 @@ __global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_const
   for (int m = 0; m < 5; ++m) write(p.part + ((int64_t)blockIdx.x * 5 + m) * p.C, dw[m]);
 }
 
-// dw and dbias over the blocks of tokens, in their order: 32 channels a CTA, each summed by eight threads.
+// dw[.][m], or dbias (m = 4), m = blockIdx.y, over the blocks of tokens in a fixed order: 32 channels a CTA, each summed
+// by eight threads.
 __global__ void __launch_bounds__(256) act_sum_kernel(const __grid_constant__ ActParams p) {
-  __shared__ float s[8][5][32];
+  __shared__ float s[8][32];
   bw::griddep_wait();
   bw::griddep_launch_dependents();
   if (p.hd->status != 0) return;
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float v[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-  if (c < p.C)
-#pragma unroll 4
-    for (int b = r; b < p.n_tb; b += 8)
-#pragma unroll
-      for (int m = 0; m < 5; ++m) v[m] += p.part[((int64_t)b * 5 + m) * p.C + c];
-#pragma unroll
-  for (int m = 0; m < 5; ++m) s[r][m][lane] = v[m];
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, m = blockIdx.y;
+  float v = 0.f;
+  if (c < p.C) {
+#pragma unroll 8
+    for (int b = r; b < p.n_tb; b += 8) v += p.part[((int64_t)b * 5 + m) * p.C + c];
+  }
+  s[r][lane] = v;
   __syncthreads();
-  if (r < 5 && c < p.C) {
-    float sum = 0.f;
+  if (r == 0 && c < p.C) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += s[k][r][lane];
-    if (r < 4)
-      p.dw[(int64_t)c * 4 + r] = sum;
+    for (int k = 1; k < 8; ++k) v += s[k][lane];
+    if (m < 4)
+      p.dw[(int64_t)c * 4 + m] = v;
     else if (p.dbias)
-      p.dbias[c] = sum;
+      p.dbias[c] = v;
   }
 }
 
@@ -638,7 +636,7 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
       const unsigned cb = (unsigned)((C / kCh + kActThreads - 1) / kActThreads);
       launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kActThreads, 0, s, p);
     });
-  launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32)), 256, 0, s, p);
+  launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32), 5), 256, 0, s, p);
   if (dfinal_tail || init_idx)
     launch_early(act_ends_kernel, dim3((unsigned)((C + 255) / 256), (unsigned)(N < 64 ? N : 64)), 256, 0, s, p);
   if (n_init > 0) {

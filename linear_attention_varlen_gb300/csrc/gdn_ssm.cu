@@ -61,7 +61,7 @@ struct SsmParams {
   int32_t *seg0, *is_src;
   float *maps, *slot, *sums, *slot_r, *ckpt, *csum, *dstart, *facc, *part_a, *part_c, *part_m;
   int64_t smax;
-  int parts, seg_tokens, bwd;
+  int parts, seg_tokens, bwd, whole;
 };
 
 // ------------------------------------------------------------------------------ planner, maps in fp32
@@ -256,22 +256,31 @@ struct Rows {
   }
 };
 
-// The state that document `src` (encoded as init_idx's pool entries) starts from, for four states of a channel.
-__device__ __forceinline__ float4 pool_quad(const float* pool, int64_t entry, int C, int S, int c, int q) {
+// Four states of channel c of an entry of [entries, C, S], zero behind the last one. `whole`: S is a multiple of four and
+// the array lies on 16 bytes.
+__device__ __forceinline__ float4 pool_quad(const float* pool, int64_t entry, int C, int S, int c, int q, int whole) {
   const float* h = pool + (entry * C + c) * S + 4 * q;
-  float4 v;
-  v.x = 4 * q < S ? h[0] : 0.f;
-  v.y = 4 * q + 1 < S ? h[1] : 0.f;
-  v.z = 4 * q + 2 < S ? h[2] : 0.f;
-  v.w = 4 * q + 3 < S ? h[3] : 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (whole) {
+    if (4 * q < S) v = *reinterpret_cast<const float4*>(h);
+  } else {
+    if (4 * q < S) v.x = h[0];
+    if (4 * q + 1 < S) v.y = h[1];
+    if (4 * q + 2 < S) v.z = h[2];
+    if (4 * q + 3 < S) v.w = h[3];
+  }
   return v;
 }
-__device__ __forceinline__ void store_quad(float* pool, int64_t entry, int C, int S, int c, int q, float4 v) {
+__device__ __forceinline__ void store_quad(float* pool, int64_t entry, int C, int S, int c, int q, float4 v, int whole) {
   float* h = pool + (entry * C + c) * S + 4 * q;
-  if (4 * q < S) h[0] = v.x;
-  if (4 * q + 1 < S) h[1] = v.y;
-  if (4 * q + 2 < S) h[2] = v.z;
-  if (4 * q + 3 < S) h[3] = v.w;
+  if (whole) {
+    if (4 * q < S) *reinterpret_cast<float4*>(h) = v;
+  } else {
+    if (4 * q < S) h[0] = v.x;
+    if (4 * q + 1 < S) h[1] = v.y;
+    if (4 * q + 2 < S) h[2] = v.z;
+    if (4 * q + 3 < S) h[3] = v.w;
+  }
 }
 
 // A warp walks one segment for 32 kDt / kNl channels: kNl lanes share a channel, each lane holds kNt states of kDt
@@ -350,13 +359,13 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
 #pragma unroll
       for (int q = 0; q < kQt; ++q) {
         const int qq = nl * kQt + q;
-        const float4 av = pool_quad(p.a, 0, p.C, p.S, c, qq);
+        const float4 av = pool_quad(p.a, 0, p.C, p.S, c, qq, p.whole);
         A[d][2 * q] = f2_pack(av.x * kLog2e, av.y * kLog2e);
         A[d][2 * q + 1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
         float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
         if (kMode == kWalkOut) {
           if (sg.src >= 0)
-            hv = pool_quad(p.init, sg.src, p.C, p.S, c, qq);
+            hv = pool_quad(p.init, sg.src, p.C, p.S, c, qq, p.whole);
           else if (sg.src == -2)
             hv = *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + qq) * p.C + c) * 4);
         }
@@ -493,7 +502,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
         const int qq = nl * kQt + q;
         const float4 hv = make_float4(f2_lo(h[d][2 * q]), f2_hi(h[d][2 * q]), f2_lo(h[d][2 * q + 1]), f2_hi(h[d][2 * q + 1]));
         if constexpr (kMode == kWalkOut) {
-          if (sg.last) store_quad(p.final_state, sg.doc, p.C, p.S, c0 + d, qq, hv);
+          if (sg.last) store_quad(p.final_state, sg.doc, p.C, p.S, c0 + d, qq, hv, p.whole);
         } else {
           *reinterpret_cast<float4*>(p.slot + (((int64_t)seg * kQ + qq) * p.C + c0 + d) * 4) = hv;
         }
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
 
 // ------------------------------------------------------------------------------ scan over segments
 
-constexpr int kScanAhead = 8;  // segments whose loads are in flight
+constexpr int kScanAhead = 16;  // segments whose loads are in flight
 
 __device__ __forceinline__ float4 carry(float4 a, float time, float4 h, float4 add) {
   return make_float4(fmaf(exp2_approx(a.x * time), h.x, add.x), fmaf(exp2_approx(a.y * time), h.y, add.y),
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
   if (forks && blockIdx.y > 0) return;
   const int step = forks ? 1 : gridDim.y, d0 = forks ? 0 : blockIdx.y;
   const int64_t state = (int64_t)Q * p.C * 4;
-  float4 a = pool_quad(p.a, 0, p.C, p.S, c, q);
+  float4 a = pool_quad(p.a, 0, p.C, p.S, c, q, p.whole);
   a = make_float4(a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e);
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   // final states of documents that others fork from: the output in the forward, the workspace in the backward
@@ -542,9 +551,9 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
     if (!p.bwd && s1 - s0 == 1 && !fork && !p.is_src[d]) continue;
     float4 h = zero;
     if (fork)
-      h = p.bwd ? *fin(src - p.n_init) : pool_quad(p.final_state, src - p.n_init, p.C, p.S, c, q);
+      h = p.bwd ? *fin(src - p.n_init) : pool_quad(p.final_state, src - p.n_init, p.C, p.S, c, q, p.whole);
     else if (src >= 0)
-      h = pool_quad(p.init, src, p.C, p.S, c, q);
+      h = pool_quad(p.init, src, p.C, p.S, c, q, p.whole);
     const int se = p.is_src[d] ? s1 : s1 - 1;  // the last segment's end state is wanted for forks only
     for (int sb = s0; sb < s1; sb += kScanAhead) {
       float4 e[kScanAhead];
@@ -564,7 +573,7 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
     if (p.bwd) {
       if (p.is_src[d]) *fin(d) = h;
     } else if (s1 == s0 || p.is_src[d]) {
-      store_quad(p.final_state, d, p.C, p.S, c, q, h);
+      store_quad(p.final_state, d, p.C, p.S, c, q, h, p.whole);
     }
   }
   if (!p.bwd) return;
@@ -575,7 +584,7 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
   for (int d = dn; d >= 0; d -= step) {
     const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
     const int src = p.init_idx ? p.init_idx[d] : -1;
-    float4 k = p.dfinal ? pool_quad(p.dfinal, d, p.C, p.S, c, q) : zero;
+    float4 k = p.dfinal ? pool_quad(p.dfinal, d, p.C, p.S, c, q, p.whole) : zero;
     if (forks) {
       const float4 f = *facc(d);
       k = make_float4(k.x + f.x, k.y + f.y, k.z + f.z, k.w + f.w);
@@ -681,7 +690,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const int c = min(c0 + d, cmax);
-      const float4 av = pool_quad(p.a, 0, p.C, p.S, c, nl);
+      const float4 av = pool_quad(p.a, 0, p.C, p.S, c, nl, p.whole);
       const float4 kv = *reinterpret_cast<const float4*>(p.slot_r + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
       A[d][0] = f2_pack(av.x * kLog2e, av.y * kLog2e), A[d][1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
       K[d][0] = f2_pack(kv.x, kv.y), K[d][1] = f2_pack(kv.z, kv.w);
@@ -716,7 +725,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
           const int c = min(c0 + d, cmax);
           float4 f = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
           if (sg.src != -1) {
-            const float4 s = sg.src >= 0 ? pool_quad(p.init, sg.src, p.C, p.S, c, nl)
+            const float4 s = sg.src >= 0 ? pool_quad(p.init, sg.src, p.C, p.S, c, nl, p.whole)
                                          : *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
             const float time = p.csum[tl * p.C + c];
             const float4 a = make_float4(f2_lo(A[d][0]), f2_hi(A[d][0]), f2_lo(A[d][1]), f2_hi(A[d][1]));
@@ -922,6 +931,7 @@ __device__ void maps_grad(const SsmParams& p, int64_t i) {  // i over [T][G][2][
   const int s = (int)(i % p.S), m = (int)(i / p.S % 2);
   const int64_t tg = i / (2 * p.S);
   float v = 0.f;
+#pragma unroll 8
   for (int k = 0; k < p.parts; ++k) v += p.part_m[((int64_t)k * p.T * p.G + tg) * 2 * Sp + m * Sp + s];
   static_cast<T*>(m ? p.dc : p.db)[tg * p.S + s] = from_float<T>(v);
 }
@@ -947,15 +957,17 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
   } else if (blockIdx.y == 1) {
     for (int64_t i = i0; i < (int64_t)Q * p.C; i += step) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
       for (int s = 0; s < segs; ++s) {
         const float4 f = *reinterpret_cast<const float4*>(p.part_a + s * state + i * 4);
         v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
       }
-      store_quad(p.da, 0, p.C, p.S, (int)(i % p.C), (int)(i / p.C), v);
+      store_quad(p.da, 0, p.C, p.S, (int)(i % p.C), (int)(i / p.C), v, p.whole);
     }
   } else if (blockIdx.y == 2) {
     for (int64_t i = i0; i < 2 * p.C; i += step) {
       float v = 0.f;
+#pragma unroll 8
       for (int s = 0; s < segs; ++s) v += p.part_c[(int64_t)s * 2 * p.C + i];
       float* out = i < p.C ? p.dskip : p.dbias;
       if (out) out[i % p.C] = v;
@@ -971,7 +983,7 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
             const float4 f = *reinterpret_cast<const float4*>(p.dstart + d * state + r * 4);
             v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
           }
-      store_quad(p.dinit, e, p.C, p.S, (int)(r % p.C), (int)(r / p.C), v);
+      store_quad(p.dinit, e, p.C, p.S, (int)(r % p.C), (int)(r / p.C), v, p.whole);
     }
   }
 }
@@ -1058,6 +1070,8 @@ int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p,
   p->smax = L->smax;
   p->parts = L->parts;
   p->bwd = c.bwd;
+  p->whole = c.S % 4 == 0 && al(c.a, 16) && al(c.init, 16);
+  for (int i = 0; i < n_outs; ++i) p->whole = p->whole && al(outs[i], 16);
   p->seg_tokens = L->seg_tokens;
   return GDN_OK;
 }

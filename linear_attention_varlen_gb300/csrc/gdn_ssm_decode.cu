@@ -44,12 +44,12 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
   using bw::f2_pack;
   constexpr int kQ = kSp / 4;
   const int q = threadIdx.x % kQ, pair = blockIdx.x * (kStepThreads / kQ) + threadIdx.x / kQ;
-  const int Cg = p.C / p.G, per = (Cg + 1) / 2, g = pair / per, cg = 2 * (pair - g * per);
-  if (g >= p.G) return;  // whole teams leave
+  const int Cg = p.C / p.G, g = blockIdx.z, cg = 2 * pair;
+  if (cg >= Cg) return;  // whole teams leave
   const unsigned team = ((1u << kQ) - 1u) << ((threadIdx.x & 31) / kQ * kQ);
   const int c = g * Cg + cg, two = cg + 1 < Cg ? 1 : 0, n = min(4, p.S - 4 * q);
   const int64_t b = blockIdx.y;
-  T* out = static_cast<T*>(p.out) + b * p.C + c;
+  T* out = static_cast<T*>(p.out) + (b * p.C + (int64_t)g * Cg) + cg;
   const int entry = p.state_idx[b];
   if (entry < 0 || entry >= p.n_pool) {  // skipped, reported
     if (q == 0) {
@@ -60,20 +60,20 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
     return;
   }
   const int k = 1 + two;  // channels
-  float* state = p.pool + ((int64_t)entry * p.C + c) * p.S + 4 * q;
-  const float* a = p.a + (int64_t)c * p.S + 4 * q;
+  float* state = p.pool + ((int64_t)entry * p.C + (int64_t)g * Cg) * p.S + (cg * p.S + 4 * q);
+  const float* a = p.a + (int64_t)g * Cg * p.S + (cg * p.S + 4 * q);
   Pack<float, 4> h[2], A[2];
 #pragma unroll
   for (int d = 0; d < 2; ++d) {
     h[d] = load_pack<float, 4, kVec>(state + d * p.S, d < k ? n : 0);
     A[d] = load_pack<float, 4, kVec>(a + d * p.S, d < k ? n : 0);
   }
-  const auto bm = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + b * p.sb + g * p.S + 4 * q, n);
-  const auto cm = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + b * p.sc + g * p.S + 4 * q, n);
-  const auto xr = load_pack<T, 2, kVec>(static_cast<const T*>(p.x) + b * p.sx + c, k);
-  const auto dr = load_pack<T, 2, kVec>(static_cast<const T*>(p.dt) + b * p.sdt + c, k);
+  const auto bm = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + (b * p.sb + (int64_t)g * p.S) + 4 * q, n);
+  const auto cm = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + (b * p.sc + (int64_t)g * p.S) + 4 * q, n);
+  const auto xr = load_pack<T, 2, kVec>(static_cast<const T*>(p.x) + (b * p.sx + (int64_t)g * Cg) + cg, k);
+  const auto dr = load_pack<T, 2, kVec>(static_cast<const T*>(p.dt) + (b * p.sdt + (int64_t)g * Cg) + cg, k);
   Pack<T, 2> zr{};
-  if (p.z) zr = load_pack<T, 2, kVec>(static_cast<const T*>(p.z) + b * p.sz + c, k);
+  if (p.z) zr = load_pack<T, 2, kVec>(static_cast<const T*>(p.z) + (b * p.sz + (int64_t)g * Cg) + cg, k);
   float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f};
   if (p.dt_bias) bias[0] = p.dt_bias[c], bias[1] = p.dt_bias[c + two];
   if (p.skip) skip[0] = p.skip[c], skip[1] = p.skip[c + two];
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
 template <typename T, int kSp>
 void launch_step(const SsmStepParams& p, bool vec, cudaStream_t s) {
   constexpr int kPer = kStepThreads / (kSp / 4);
-  const int64_t pairs = (int64_t)p.G * ((p.C / p.G + 1) / 2);
-  const dim3 grid((unsigned)((pairs + kPer - 1) / kPer), (unsigned)p.B);
+  const int pairs = (p.C / p.G + 1) / 2;
+  const dim3 grid((unsigned)((pairs + kPer - 1) / kPer), (unsigned)p.B, (unsigned)p.G);
   if (vec)
     ssm_step_kernel<T, kSp, true><<<grid, kStepThreads, 0, s>>>(p);
   else
@@ -142,7 +142,7 @@ extern "C" int gdn_ssm_decode_step(const void* x, const void* dt, const void* z,
   using namespace gdn;
   if (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_FP16 && dtype != GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED;
   if (B < 0 || C < 1 || S < 1 || S > kSsmMaxState || G < 1 || C % G != 0 || n_pool < 0) return GDN_ERR_INVALID_ARG;
-  if (B > 65535 || (int64_t)C * S > ((int64_t)1 << 28)) return GDN_ERR_INVALID_ARG;
+  if (B > 65535 || G > 65535 || (int64_t)C * S > ((int64_t)1 << 28)) return GDN_ERR_INVALID_ARG;
   if (B == 0) return GDN_OK;
   if (!x || !dt || !a || !b || !c || !state_idx || !state_pool || !out || n_pool == 0) return GDN_ERR_INVALID_ARG;
   const int64_t rows[5] = {C, C, C, (int64_t)G * S, (int64_t)G * S};
