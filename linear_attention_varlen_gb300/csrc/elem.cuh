@@ -132,6 +132,39 @@ __device__ __forceinline__ void set_pair(Words& r, int i, uint64_t v) {
   set_pair<T>(r.w, i, v);
 }
 template <typename T>
+__device__ __forceinline__ void set_element(uint32_t* w, int i, T v) {  // into zeros
+  if constexpr (sizeof(T) == 4)
+    w[i] = __float_as_uint(v);
+  else
+    w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(&v) << (i % 2 * 16);
+}
+// K consecutive elements as words, of which the first `n` exist (zero behind them). kVec: p is aligned to them, and n is
+// K or 0.
+template <typename T, int K>
+struct alignas(sizeof(T) * K > 16 ? 16 : sizeof(T) * K) Bits {
+  uint32_t w[sizeof(T) * K / 4];
+};
+template <typename T, int K, bool kVec>
+__device__ __forceinline__ Bits<T, K> load_bits(const T* p, int n) {
+  Bits<T, K> r{};
+  if constexpr (kVec) {
+    if (n > 0) r = *reinterpret_cast<const Bits<T, K>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (i < n) set_element<T>(r.w, i, p[i]);
+  }
+  return r;
+}
+// Nothing is made of the words before this point: loads that stand above are all under way when the first is waited for.
+template <typename T, int K>
+__device__ __forceinline__ void hold(Bits<T, K>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) * K / 4); ++i) asm volatile("" : "+r"(r.w[i]));
+}
+__device__ __forceinline__ void hold(float& v) { asm volatile("" : "+f"(v)); }
+__device__ __forceinline__ void hold(float4& v) { asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)); }
+template <typename T>
 __device__ __forceinline__ T element_of(const Words& r, int i) {
   if constexpr (sizeof(T) == 4) {
     return __uint_as_float(r.w[i]);
@@ -141,11 +174,8 @@ __device__ __forceinline__ T element_of(const Words& r, int i) {
   }
 }
 template <typename T>
-__device__ __forceinline__ void set_element(Words& r, int i, T v) {  // into zeros
-  if constexpr (sizeof(T) == 4)
-    r.w[i] = __float_as_uint(v);
-  else
-    r.w[i / 2] |= (uint32_t) * reinterpret_cast<const uint16_t*>(&v) << (i % 2 * 16);
+__device__ __forceinline__ void set_element(Words& r, int i, T v) {
+  set_element<T>(r.w, i, v);
 }
 
 // Pairs of the same in packed arithmetic.

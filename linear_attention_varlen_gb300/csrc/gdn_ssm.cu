@@ -271,6 +271,18 @@ __device__ __forceinline__ float4 pool_quad(const float* pool, int64_t entry, in
   }
   return v;
 }
+// The same for quads q0 .. q0 + kN - 1.
+template <int kN>
+__device__ __forceinline__ void pool_quads(float4* v, const float* pool, int64_t entry, int C, int S, int c, int q0, int whole) {
+  if (whole) {
+    const float4* h = reinterpret_cast<const float4*>(pool + (entry * C + c) * S) + q0;
+#pragma unroll
+    for (int q = 0; q < kN; ++q) v[q] = 4 * (q0 + q) < S ? h[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) v[q] = pool_quad(pool, entry, C, S, c, q0 + q, 0);
+  }
+}
 __device__ __forceinline__ void store_quad(float* pool, int64_t entry, int C, int S, int c, int q, float4 v, int whole) {
   float* h = pool + (entry * C + c) * S + 4 * q;
   if (whole) {
@@ -350,33 +362,42 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
     fetch(0, ring);
     uint64_t A[kDt][kP], h[kDt][kP], ga[kMode == kWalkGrad ? kDt : 1][kP], pr[kMode == kWalkGrad ? kDt : 1][kP];
     float bias[kDt], skip[kDt], total[kDt];
+    float4 av[kDt][kQt], hv[kDt][kQt];
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
       const int c = min(c0 + d, g * Cg + Cg - 1);
       bias[d] = p.dt_bias ? p.dt_bias[c] : 0.f;
       skip[d] = kMode == kWalkOut && p.skip ? p.skip[c] : 0.f;
       total[d] = 0.f;
+      pool_quads<kQt>(av[d], p.a, 0, p.C, p.S, c, nl * kQt, p.whole);
+      if constexpr (kMode == kWalkOut) {
+        if (sg.src >= 0) {
+          pool_quads<kQt>(hv[d], p.init, sg.src, p.C, p.S, c, nl * kQt, p.whole);
+        } else {
+#pragma unroll
+          for (int q = 0; q < kQt; ++q)
+            hv[d][q] = sg.src == -2 ? *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + nl * kQt + q) * p.C + c) * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kDt; ++d)
 #pragma unroll
       for (int q = 0; q < kQt; ++q) {
-        const int qq = nl * kQt + q;
-        const float4 av = pool_quad(p.a, 0, p.C, p.S, c, qq, p.whole);
-        A[d][2 * q] = f2_pack(av.x * kLog2e, av.y * kLog2e);
-        A[d][2 * q + 1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
-        float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (kMode == kWalkOut) {
-          if (sg.src >= 0)
-            hv = pool_quad(p.init, sg.src, p.C, p.S, c, qq, p.whole);
-          else if (sg.src == -2)
-            hv = *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + qq) * p.C + c) * 4);
-        }
-        h[d][2 * q] = f2_pack(hv.x, hv.y);
-        h[d][2 * q + 1] = f2_pack(hv.z, hv.w);
+        hold(av[d][q]);
+        if constexpr (kMode == kWalkOut)
+          hold(hv[d][q]);
+        else
+          hv[d][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = av[d][q], s = hv[d][q];
+        A[d][2 * q] = f2_pack(a.x * kLog2e, a.y * kLog2e), A[d][2 * q + 1] = f2_pack(a.z * kLog2e, a.w * kLog2e);
+        h[d][2 * q] = f2_pack(s.x, s.y), h[d][2 * q + 1] = f2_pack(s.z, s.w);
         if constexpr (kMode == kWalkGrad) {
           ga[d][2 * q] = ga[d][2 * q + 1] = 0;
           pr[d][2 * q] = pr[d][2 * q + 1] = f2_pack(1.f, 1.f);
         }
       }
-    }
     for (int i0 = 0, it = 0; i0 < sg.ntok; i0 += kTb, ++it) {
       if constexpr (kMode == kWalkGrad) {
         if (i0 % kSsmTile == 0 && nch > 0) {
@@ -687,14 +708,21 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
     const int tiles = (sg.ntok + kTb - 1) / kTb;
     if (tiles > 0) fetch(tiles - 1);
     uint64_t A[4][2], K[4][2], dA[4][2];  // A in units of log2 e
+    {
+      float4 av[4], kv[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const int c = min(c0 + d, cmax);
-      const float4 av = pool_quad(p.a, 0, p.C, p.S, c, nl, p.whole);
-      const float4 kv = *reinterpret_cast<const float4*>(p.slot_r + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
-      A[d][0] = f2_pack(av.x * kLog2e, av.y * kLog2e), A[d][1] = f2_pack(av.z * kLog2e, av.w * kLog2e);
-      K[d][0] = f2_pack(kv.x, kv.y), K[d][1] = f2_pack(kv.z, kv.w);
-      dA[d][0] = dA[d][1] = 0;
+      for (int d = 0; d < 4; ++d) {
+        const int c = min(c0 + d, cmax);
+        pool_quads<1>(&av[d], p.a, 0, p.C, p.S, c, nl, p.whole);
+        kv[d] = *reinterpret_cast<const float4*>(p.slot_r + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        hold(av[d]), hold(kv[d]);
+        A[d][0] = f2_pack(av[d].x * kLog2e, av[d].y * kLog2e), A[d][1] = f2_pack(av[d].z * kLog2e, av[d].w * kLog2e);
+        K[d][0] = f2_pack(kv[d].x, kv[d].y), K[d][1] = f2_pack(kv[d].z, kv[d].w);
+        dA[d][0] = dA[d][1] = 0;
+      }
     }
     for (int i = lane; i < kCh; i += 32) sm.bias[wid][i] = p.dt_bias ? p.dt_bias[g * Cg + min(cb + i, Cg - 1)] : 0.f;
     // for the steps a lane takes four channels of every kNl-th token
@@ -720,23 +748,29 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
       uint64_t h[4][2];
       {
         const int64_t tl = sg.tok0 / kSsmTile + seg + tile;
+        float4 kept[4], start[4];
+        float time[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const int c = min(c0 + d, cmax);
-          float4 f = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
-          if (sg.src != -1) {
-            const float4 s = sg.src >= 0 ? pool_quad(p.init, sg.src, p.C, p.S, c, nl, p.whole)
-                                         : *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + nl) * p.C + c) * 4);
-            const float time = p.csum[tl * p.C + c];
-            const float4 a = make_float4(f2_lo(A[d][0]), f2_hi(A[d][0]), f2_lo(A[d][1]), f2_hi(A[d][1]));
-            f = make_float4(fmaf(exp2_approx(a.x * time), s.x, f.x), fmaf(exp2_approx(a.y * time), s.y, f.y),
-                            fmaf(exp2_approx(a.z * time), s.z, f.z), fmaf(exp2_approx(a.w * time), s.w, f.w));
-          }
-          h[d][0] = f2_pack(f.x, f.y), h[d][1] = f2_pack(f.z, f.w);
+          kept[d] = *reinterpret_cast<const float4*>(p.ckpt + ((tl * kQ + nl) * p.C + c) * 4);
+          time[d] = p.csum[tl * p.C + c];
+          if (sg.src >= 0)
+            pool_quads<1>(&start[d], p.init, sg.src, p.C, p.S, c, nl, p.whole);
+          else
+            start[d] = sg.src == -2 ? *reinterpret_cast<const float4*>(p.slot + (((int64_t)seg * kQ + nl) * p.C + c) * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // this tile has landed, and every warp is done with the one before
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          hold(kept[d]), hold(start[d]), hold(time[d]);
+          const uint64_t t = f2_dup(time[d]);
+          h[d][0] = f2_fma(exp2_pair(f2_mul(A[d][0], t)), f2_pack(start[d].x, start[d].y), f2_pack(kept[d].x, kept[d].y));
+          h[d][1] = f2_fma(exp2_pair(f2_mul(A[d][1], t)), f2_pack(start[d].z, start[d].w), f2_pack(kept[d].z, kept[d].w));
         }
       }
-      cp_async_wait<0>();
-      __syncthreads();  // this tile has landed, and every warp is done with the one before
       if (kStages == 2 && tile > 0) fetch(tile - 1);
       for (int k = lt; k < kTb; k += kNl) {  // behind the last token everything is zero
         const int64_t t = t0 + k;
@@ -928,20 +962,47 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
 template <typename T>
 __device__ void maps_grad(const SsmParams& p, int64_t i) {  // i over [T][G][2][S]
   const int Sp = ssm_padded(p.S);
-  const int s = (int)(i % p.S), m = (int)(i / p.S % 2);
-  const int64_t tg = i / (2 * p.S);
+  const int64_t tg = i >> 31 ? i / (2 * p.S) : (int64_t)((uint32_t)i / (uint32_t)(2 * p.S));
+  const int r = (int)(i - tg * 2 * p.S), m = r >= p.S, s = m ? r - p.S : r;
   float v = 0.f;
 #pragma unroll 8
   for (int k = 0; k < p.parts; ++k) v += p.part_m[((int64_t)k * p.T * p.G + tg) * 2 * Sp + m * Sp + s];
   static_cast<T*>(m ? p.dc : p.db)[tg * p.S + s] = from_float<T>(v);
 }
 
+// The sum of term(0) .. term(n - 1), eight threads (threadIdx.x / 32) to a result, in a fixed order; valid in the first.
+template <typename V, typename F>
+__device__ V sum_by_eight(int n, V zero, V (*s)[32], F term) {
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  V v = zero;
+#pragma unroll 4
+  for (int k = r; k < n; k += 8) v = v + term(k);
+  __syncthreads();
+  s[r][lane] = v;
+  __syncthreads();
+  if (r == 0) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v = v + s[k][lane];
+  }
+  return v;
+}
+struct Quad {
+  float4 f;
+  __device__ __forceinline__ Quad operator+(const Quad& o) const {
+    return {make_float4(f.x + o.f.x, f.y + o.f.y, f.z + o.f.z, f.w + o.f.w)};
+  }
+};
+
 // blockIdx.y 0: db and dc over the CTAs of the channels; 1: da over the segments; 2: dskip and ddt_bias; 3: the start
 // states' gradients over the documents of each pool entry.
 __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ SsmParams p) {
+  __shared__ Quad s_quad[8][32];
+  __shared__ float s_one[8][32];
   bw::griddep_wait();
   if (p.hd->status != 0) return;
   const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  const int64_t j0 = (int64_t)blockIdx.x * 32, jstep = (int64_t)gridDim.x * 32;
+  const int lane = threadIdx.x & 31;
   const int Sp = ssm_padded(p.S), Q = Sp / 4, segs = p.hd->n_segs;
   const int64_t state = (int64_t)Q * p.C * 4;
   if (blockIdx.y == 0) {
@@ -955,22 +1016,20 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
         maps_grad<float>(p, i);
     }
   } else if (blockIdx.y == 1) {
-    for (int64_t i = i0; i < (int64_t)Q * p.C; i += step) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int s = 0; s < segs; ++s) {
-        const float4 f = *reinterpret_cast<const float4*>(p.part_a + s * state + i * 4);
-        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
-      }
-      store_quad(p.da, 0, p.C, p.S, (int)(i % p.C), (int)(i / p.C), v, p.whole);
+    const int64_t n = (int64_t)Q * p.C;
+    for (int64_t j = j0; j < n; j += jstep) {
+      const int64_t i = min(j + lane, n - 1);
+      const Quad v = sum_by_eight(segs, Quad{make_float4(0.f, 0.f, 0.f, 0.f)}, s_quad,
+                                  [&](int s) { return Quad{*reinterpret_cast<const float4*>(p.part_a + s * state + i * 4)}; });
+      if (threadIdx.x < 32 && j + lane < n) store_quad(p.da, 0, p.C, p.S, (int)(i % p.C), (int)(i / p.C), v.f, p.whole);
     }
   } else if (blockIdx.y == 2) {
-    for (int64_t i = i0; i < 2 * p.C; i += step) {
-      float v = 0.f;
-#pragma unroll 8
-      for (int s = 0; s < segs; ++s) v += p.part_c[(int64_t)s * 2 * p.C + i];
+    const int64_t n = 2 * (int64_t)p.C;
+    for (int64_t j = j0; j < n; j += jstep) {
+      const int64_t i = min(j + lane, n - 1);
+      const float v = sum_by_eight(segs, 0.f, s_one, [&](int s) { return p.part_c[s * n + i]; });
       float* out = i < p.C ? p.dskip : p.dbias;
-      if (out) out[i % p.C] = v;
+      if (threadIdx.x < 32 && j + lane < n && out) out[i % p.C] = v;
     }
   } else {
     for (int64_t i = i0; i < (int64_t)p.n_init * Q * p.C; i += step) {

@@ -21,7 +21,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128;
 
 struct SsmStepParams {
   const void *x, *dt, *z, *b, *c;
@@ -47,55 +47,49 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
   const int Cg = p.C / p.G, g = blockIdx.z, cg = 2 * pair;
   if (cg >= Cg) return;  // whole teams leave
   const unsigned team = ((1u << kQ) - 1u) << ((threadIdx.x & 31) / kQ * kQ);
-  const int c = g * Cg + cg, two = cg + 1 < Cg ? 1 : 0, n = min(4, p.S - 4 * q);
+  const int two = cg + 1 < Cg ? 1 : 0, n = min(4, p.S - 4 * q);
   const int64_t b = blockIdx.y;
-  T* out = static_cast<T*>(p.out) + (b * p.C + (int64_t)g * Cg) + cg;
-  const int entry = p.state_idx[b];
+  const int k = 1 + two;  // channels
+  const int64_t c0 = (int64_t)g * Cg;
+  int entry = p.state_idx[b];
+  Bits<float, 4> h[2], A[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) A[d] = load_bits<float, 4, kVec>(p.a + c0 * p.S + (cg * p.S + 4 * q) + d * p.S, d < k ? n : 0);
+  auto bm = load_bits<T, 4, kVec>(static_cast<const T*>(p.b) + (b * p.sb + (int64_t)g * p.S) + 4 * q, n);
+  auto cm = load_bits<T, 4, kVec>(static_cast<const T*>(p.c) + (b * p.sc + (int64_t)g * p.S) + 4 * q, n);
+  auto xr = load_bits<T, 2, kVec>(static_cast<const T*>(p.x) + (b * p.sx + c0) + cg, k);
+  auto dr = load_bits<T, 2, kVec>(static_cast<const T*>(p.dt) + (b * p.sdt + c0) + cg, k);
+  auto zr = load_bits<T, 2, kVec>(static_cast<const T*>(p.z) + (b * p.sz + c0) + cg, p.z ? k : 0);
+  Bits<float, 2> bias = load_bits<float, 2, false>(p.dt_bias + c0 + cg, p.dt_bias ? k : 0);
+  Bits<float, 2> skip = load_bits<float, 2, false>(p.skip + c0 + cg, p.skip ? k : 0);
+  T* out = static_cast<T*>(p.out) + (b * p.C + c0) + cg;
   if (entry < 0 || entry >= p.n_pool) {  // skipped, reported
-    if (q == 0) {
-      out[0] = from_float<T>(0.f);
-      if (two) out[1] = from_float<T>(0.f);
-    }
+    if (q == 0) store_pack<T, 2, kVec>(out, Pack<T, 2>{}, k);
     if (threadIdx.x == 0 && p.status) atomicCAS(p.status, 0, kErrInvalid);
     return;
   }
-  const int k = 1 + two;  // channels
-  float* state = p.pool + ((int64_t)entry * p.C + (int64_t)g * Cg) * p.S + (cg * p.S + 4 * q);
-  const float* a = p.a + (int64_t)g * Cg * p.S + (cg * p.S + 4 * q);
-  Pack<float, 4> h[2], A[2];
+  float* state = p.pool + ((int64_t)entry * p.C + c0) * p.S + (cg * p.S + 4 * q);
 #pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    h[d] = load_pack<float, 4, kVec>(state + d * p.S, d < k ? n : 0);
-    A[d] = load_pack<float, 4, kVec>(a + d * p.S, d < k ? n : 0);
-  }
-  const auto bm = load_pack<T, 4, kVec>(static_cast<const T*>(p.b) + (b * p.sb + (int64_t)g * p.S) + 4 * q, n);
-  const auto cm = load_pack<T, 4, kVec>(static_cast<const T*>(p.c) + (b * p.sc + (int64_t)g * p.S) + 4 * q, n);
-  const auto xr = load_pack<T, 2, kVec>(static_cast<const T*>(p.x) + (b * p.sx + (int64_t)g * Cg) + cg, k);
-  const auto dr = load_pack<T, 2, kVec>(static_cast<const T*>(p.dt) + (b * p.sdt + (int64_t)g * Cg) + cg, k);
-  Pack<T, 2> zr{};
-  if (p.z) zr = load_pack<T, 2, kVec>(static_cast<const T*>(p.z) + (b * p.sz + (int64_t)g * Cg) + cg, k);
-  float bias[2] = {0.f, 0.f}, skip[2] = {0.f, 0.f};
-  if (p.dt_bias) bias[0] = p.dt_bias[c], bias[1] = p.dt_bias[c + two];
-  if (p.skip) skip[0] = p.skip[c], skip[1] = p.skip[c + two];
-  uint64_t delta = f2_pack(to_float(dr.t[0]) + bias[0], to_float(dr.t[1]) + bias[1]);
+  for (int d = 0; d < 2; ++d) h[d] = load_bits<float, 4, kVec>(state + d * p.S, d < k ? n : 0);
+  hold(h[0]), hold(h[1]), hold(A[0]), hold(A[1]), hold(bm), hold(cm), hold(xr), hold(dr), hold(zr), hold(bias), hold(skip);
+  uint64_t delta = bw::f2_add(pair_of<T>(dr.w, 0), pair_of<float>(bias.w, 0));
   if (p.softplus) delta = softplus_pair(delta);
-  const uint64_t x = f2_pack(to_float(xr.t[0]), to_float(xr.t[1])), u = f2_mul(delta, x);
-  const uint64_t bv[2] = {f2_pack(to_float(bm.t[0]), to_float(bm.t[1])), f2_pack(to_float(bm.t[2]), to_float(bm.t[3]))};
-  const uint64_t cv[2] = {f2_pack(to_float(cm.t[0]), to_float(cm.t[1])), f2_pack(to_float(cm.t[2]), to_float(cm.t[3]))};
+  const uint64_t x = pair_of<T>(xr.w, 0), u = f2_mul(delta, x);
   float y[2];
 #pragma unroll
   for (int d = 0; d < 2; ++d) {
     const uint64_t dd = f2_dup((d ? f2_hi(delta) : f2_lo(delta)) * kLog2e), uu = f2_dup(d ? f2_hi(u) : f2_lo(u));
     uint64_t y2 = 0;
+    Pack<float, 4> r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint64_t e = exp2_pair(f2_mul(dd, f2_pack(A[d].t[2 * i], A[d].t[2 * i + 1])));
-      const uint64_t v = f2_fma(e, f2_pack(h[d].t[2 * i], h[d].t[2 * i + 1]), f2_mul(uu, bv[i]));
-      y2 = f2_fma(cv[i], v, y2);
-      h[d].t[2 * i] = f2_lo(v), h[d].t[2 * i + 1] = f2_hi(v);
+      const uint64_t e = exp2_pair(f2_mul(dd, pair_of<float>(A[d].w, i)));
+      const uint64_t v = f2_fma(e, pair_of<float>(h[d].w, i), f2_mul(uu, pair_of<T>(bm.w, i)));
+      y2 = f2_fma(pair_of<T>(cm.w, i), v, y2);
+      r.t[2 * i] = f2_lo(v), r.t[2 * i + 1] = f2_hi(v);
     }
     y[d] = bw::f2_sum(y2);
-    store_pack<float, 4, kVec>(state + d * p.S, h[d], d < k ? n : 0);
+    store_pack<float, 4, kVec>(state + d * p.S, r, d < k ? n : 0);
   }
 #pragma unroll
   for (int o = 1; o < kQ; o <<= 1) {
@@ -103,8 +97,8 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const __grid_con
     y[1] += __shfl_xor_sync(team, y[1], o);
   }
   if (q == 0) {
-    uint64_t r = f2_fma(f2_pack(skip[0], skip[1]), x, f2_pack(y[0], y[1]));
-    if (p.z) r = f2_mul(r, silu_pair(f2_pack(to_float(zr.t[0]), to_float(zr.t[1]))));
+    uint64_t r = f2_fma(pair_of<float>(skip.w, 0), x, f2_pack(y[0], y[1]));
+    if (p.z) r = f2_mul(r, silu_pair(pair_of<T>(zr.w, 0)));
     Pack<T, 2> o;
     o.t[0] = from_float<T>(f2_lo(r)), o.t[1] = from_float<T>(f2_hi(r));
     store_pack<T, 2, kVec>(out, o, k);
