@@ -447,12 +447,12 @@ def _tokens(t, name, dtype, shape, align=1):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return 0
-    need = 1
-    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and st != need:
+    strides, need = t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != need and shape[i] > 1:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
-        need *= n
-    st = t.stride(0)
+        need *= shape[i]
+    st = strides[0]
     if st < need or st % align != 0:
         raise ValueError(f"{name}: tokens must be a multiple of {align} elements apart, at least {need}")
     return st
