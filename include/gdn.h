@@ -448,7 +448,8 @@ enum gdn_gate { GDN_GATE_AFTER_NORM = 0, GDN_GATE_BEFORE_NORM = 1 };
  *   x, z, y, dy, dx, dz : [T, D] of `dtype`; the strides are the elements between rows of x, z and dy (0 =
  *   contiguous), y, dx and dz are contiguous; y may be x or z itself, dx and dz any of x, z and dy (not the same)
  *   w : of `w_dtype`, [group] (shared_w) or [D];  dw : fp32, as w, summed in a fixed order
- * Sums are fp32; each output is rounded once. T = 0 is a no-op (dw is then zero). workspace:
+ * Sums are fp32 (squares of magnitudes above 2^63 overflow); each output is rounded once. T = 0 is a no-op (dw
+ * is then zero). workspace:
  * gdn_gated_rmsnorm_workspace_size(T, D, group, dtype) bytes, 256-byte aligned; its status word
  * (gdn_workspace_status) is GDN_OK.
  */

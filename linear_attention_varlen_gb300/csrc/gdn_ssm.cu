@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
 // ------------------------------------------------------------------------------ host
 
 bool sizes_ok(int N, int T, int C, int S, int G) {
-  return N >= 1 && T >= 0 && T <= INT32_MAX - 4096 && C >= 1 && S >= 1 && S <= kSsmMaxState && G >= 1 && C % G == 0 &&
+  return N >= 1 && N <= (1 << 30) && T >= 0 && T <= INT32_MAX - 4096 && C >= 1 && S >= 1 && S <= kSsmMaxState && G >= 1 && C % G == 0 &&
          (int64_t)T * C <= ((int64_t)1 << 40) && (int64_t)C * S <= ((int64_t)1 << 28) &&
          (int64_t)N * C <= ((int64_t)1 << 36);
 }

@@ -98,6 +98,10 @@ def test_pools_and_forks(idx, lens):
     check(inputs(8, lens, 16, "bf16", n_pool=2), idx)
 
 
+def test_forks_without_a_pool():
+    check(inputs(19, [40, 0, 2, 70, 1], 16, "fp32"), [-1, 0, 1, 2, 0])
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_views_into_wider_rows(dtype):
     check(inputs(5, [50, 0, 20], 40, dtype, n_pool=1, apart=16), [0, -1, 1 + 0])

@@ -138,6 +138,10 @@ def test_pools_and_forks(idx, S, dfin):
     check(ssm_ref.problem(17, [150, 70, 0, 9, 1, 33], 40, S, 2, n_pool=3, dfin=dfin), "fp32", idx)
 
 
+def test_forks_without_a_pool():
+    check(ssm_ref.problem(18, [40, 0, 25, 90, 1], 24, 16, dfin=True), "fp32", [-1, 0, 1, 2, 0])
+
+
 def test_pool_without_indices():
     p = ssm_ref.problem(4, [20, 5], 16, 8, n_pool=2, dfin=True)
     check(p, "fp32")  # every document starts from zero, dinit is zero

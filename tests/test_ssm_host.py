@@ -36,7 +36,7 @@ def ssm(lib, bwd=False, **kw):
 @pytest.mark.parametrize("bwd", [False, True])
 def test_scan_refusals(lib, bwd):
     bad = gdn.GDN_ERR_INVALID_ARG
-    for kw in (dict(N=0), dict(T=-1), dict(C=0), dict(S=0), dict(S=65), dict(G=0), dict(G=3), dict(x=None), dict(dt=None),
+    for kw in (dict(N=0), dict(N=(1 << 30) + 1), dict(T=-1), dict(T=2 ** 31 - 1), dict(C=0), dict(S=0), dict(S=65), dict(G=0), dict(G=3), dict(x=None), dict(dt=None),
                dict(a=None), dict(b=None), dict(c=None), dict(cu=None), dict(ws=None), dict(n_init=1), dict(n_init=-1),
                dict(x=A + 1), dict(a=A + 2), dict(cu=A + 1), dict(ws=A + 128), dict(strides=[8, 0, 0, 0, 0, 0]),
                dict(strides=[0, 0, 0, -16, 0, 0]), dict(strides=[0, 0, 0, 0, 1 << 41, 0])):
