@@ -291,14 +291,6 @@ def _empty_on(stream):
     return empty
 
 
-def _new(like, stream):
-    """like.new_empty, or its counterpart for a call on `stream`."""
-    if stream is None:
-        return like.new_empty
-    empty = _empty_on(stream)
-    return lambda shape, dtype=like.dtype: empty(shape, dtype=dtype, device=like.device)
-
-
 def _check(t, name, dtype, shape=None):
     if t is None:
         raise ValueError(f"{name} is required")
@@ -502,11 +494,13 @@ def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None,
     empty = torch.empty if stream is None else _empty_on(stream)
     if activation is not None:
         T, C, N, n_init, code, act, xs = _conv_act_inputs(x, w, cu_seqlens, bias, init_idx, conv_init, activation)
-        new = _new(x, stream)
-        y = new((T, C)) if y is None else _check(y, "y", x.dtype, (T, C))
-        final_tail = new((N, 3, C)) if final_tail is None else _check(final_tail, "final_tail", x.dtype, (N, 3, C))
+        y = empty((T, C), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (T, C))
+        if final_tail is None:
+            final_tail = empty((N, 3, C), dtype=x.dtype, device=x.device)
+        else:
+            _check(final_tail, "final_tail", x.dtype, (N, 3, C))
         if workspace is None:
-            workspace = new(conv_workspace_size(N, T, C, False, activation), dtype=torch.uint8)
+            workspace = empty(conv_workspace_size(N, T, C, False, activation), dtype=torch.uint8, device=x.device)
         rc = load().gdn_conv_act_fwd(_ptr(x), xs, _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, code, act,
                                      _ptr(init_idx), _ptr(conv_init), n_init, _ptr(y), _ptr(final_tail),
                                      _ptr(workspace), workspace.numel(), _stream_handle(stream))
@@ -554,12 +548,12 @@ def conv_bwd(x, w, cu_seqlens, dy, bias=None, init_idx=None, conv_init=None, dfi
         gs = _tokens(dy, "dy", x.dtype, (T, C), 16 // x.element_size())
         if dfinal_tail is not None:
             _check(dfinal_tail, "dfinal_tail", torch.float32, (N, 3, C))
-        new = _new(w, stream)  # fp32
-        dx, dw = new((T, C)), new((C, 4))
-        dbias = new((C,)) if bias is not None else None
-        dci = new((n_init, 3, C)) if n_init > 0 else None
+        f32 = dict(dtype=torch.float32, device=x.device)
+        dx, dw = empty((T, C), **f32), empty((C, 4), **f32)
+        dbias = empty((C,), **f32) if bias is not None else None
+        dci = empty((n_init, 3, C), **f32) if n_init > 0 else None
         if workspace is None:
-            workspace = new(conv_workspace_size(N, T, C, True, activation), dtype=torch.uint8)
+            workspace = empty(conv_workspace_size(N, T, C, True, activation), dtype=torch.uint8, device=x.device)
         rc = load().gdn_conv_act_bwd(_ptr(x), xs, _ptr(w), _ptr(bias), _ptr(cu_seqlens), N, T, C, code, act,
                                      _ptr(init_idx), _ptr(conv_init), n_init, _ptr(dy), gs, _ptr(dfinal_tail), _ptr(dx),
                                      _ptr(dw), _ptr(dbias), _ptr(dci), _ptr(workspace), workspace.numel(),
@@ -591,6 +585,7 @@ def conv_decode_step(x, w, tail_pool, state_idx, bias=None, activation="none", y
     x [B, C] (bf16, fp16 or fp32; sequences may be strided); w [C, 4], bias [C] fp32; tail_pool [n_pool, 3, C] of x's
     type (updated); state_idx [B] int32 (distinct entries); status as in decode_step. Returns y [B, C]."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     B, C, code, act, xs = _conv_act_inputs(x, w, None, bias, None, None, activation, step=True)
     _check(state_idx, "state_idx", torch.int32, (B,))
     if tail_pool is None:
@@ -598,7 +593,7 @@ def conv_decode_step(x, w, tail_pool, state_idx, bias=None, activation="none", y
     _check(tail_pool, "tail_pool", x.dtype, (tail_pool.shape[0], 3, C))
     if status is not None:
         _check(status, "status", torch.int32, (1,))
-    y = _new(x, stream)((B, C)) if y is None else _check(y, "y", x.dtype, (B, C))
+    y = empty((B, C), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (B, C))
     rc = load().gdn_conv_decode_step(_ptr(x), xs, _ptr(w), _ptr(bias), B, C, code, act, _ptr(state_idx),
                                      _ptr(tail_pool), tail_pool.shape[0], _ptr(y), _ptr(status), _stream_handle(stream))
     if rc != GDN_OK:
@@ -887,16 +882,17 @@ def ssm_scan_fwd(x, dt, a, b, c, cu_seqlens, skip=None, z=None, dt_bias=None, in
     initial_state [n_init, C, S] fp32; cu_seqlens and init_idx as in chunk_fwd. Returns (out [T, C], final_state
     [N, C, S] fp32)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     code, T, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias)
     N, n_init = _ssm_packed(cu_seqlens, init_idx, initial_state, C, S)
-    new = _new(x, stream)
-    out = new((T, C)) if out is None else _check(out, "out", x.dtype, (T, C))
+    dev = x.device
+    out = empty((T, C), dtype=x.dtype, device=dev) if out is None else _check(out, "out", x.dtype, (T, C))
     if final_state is None:
-        final_state = new((N, C, S), dtype=torch.float32)
+        final_state = empty((N, C, S), dtype=torch.float32, device=dev)
     else:
         _check(final_state, "final_state", torch.float32, (N, C, S))
     if workspace is None:
-        workspace = new(ssm_workspace_size(N, T, C, S, G), dtype=torch.uint8)
+        workspace = empty(ssm_workspace_size(N, T, C, S, G), dtype=torch.uint8, device=dev)
     rc = load().gdn_ssm_fwd(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias),
                             _ptr(cu_seqlens), N, T, C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(init_idx),
                             _ptr(initial_state), n_init, _ptr(out), _ptr(final_state), _ptr(workspace),
@@ -912,27 +908,28 @@ def ssm_scan_bwd(x, dt, a, b, c, cu_seqlens, dout, dfinal_state=None, skip=None,
     ddt_bias and dinit in fp32 (None without skip, dt_bias or a pool). `grads` may hold preallocated outputs under
     those keys."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if dout is None:
         raise ValueError("dout is required")
     code, T, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias, dout)
     N, n_init = _ssm_packed(cu_seqlens, init_idx, initial_state, C, S)
     if dfinal_state is not None:
         _check(dfinal_state, "dfinal_state", torch.float32, (N, C, S))
-    new, h, f32 = _new(x, stream), x.dtype, torch.float32
+    dev, h, f32 = x.device, x.dtype, torch.float32
     grads = grads or {}
 
     def out_buf(key, shape, dtype, wanted=True):
         if not wanted:
             return None
         t = grads.get(key)
-        return new(shape, dtype=dtype) if t is None else _check(t, key, dtype, shape)
+        return empty(shape, dtype=dtype, device=dev) if t is None else _check(t, key, dtype, shape)
     g = dict(dx=out_buf("dx", (T, C), h), ddt=out_buf("ddt", (T, C), h), dz=out_buf("dz", (T, C), h, z is not None),
              da=out_buf("da", (C, S), f32), db=out_buf("db", (T, G, S), h), dc=out_buf("dc", (T, G, S), h),
              dskip=out_buf("dskip", (C,), f32, skip is not None),
              ddt_bias=out_buf("ddt_bias", (C,), f32, dt_bias is not None),
              dinit=out_buf("dinit", (n_init, C, S), f32, n_init > 0))
     if workspace is None:
-        workspace = new(ssm_workspace_size(N, T, C, S, G, True), dtype=torch.uint8)
+        workspace = empty(ssm_workspace_size(N, T, C, S, G, True), dtype=torch.uint8, device=dev)
     rc = load().gdn_ssm_bwd(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias),
                             _ptr(cu_seqlens), N, T, C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(init_idx),
                             _ptr(initial_state), n_init, _ptr(dout), _ptr(dfinal_state), _ptr(g["dx"]), _ptr(g["ddt"]),
@@ -950,6 +947,7 @@ def ssm_decode_step(x, dt, a, b, c, state_pool, state_idx, skip=None, z=None, dt
     (sequences may be strided); state_pool [n_pool, C, S] fp32 (updated); state_idx [B] int32 (distinct entries);
     status as in decode_step. Returns out [B, C] of x's type."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     code, B, C, S, G, strides = _ssm_inputs(x, dt, a, b, c, skip, z, dt_bias)
     _check(state_idx, "state_idx", torch.int32, (B,))
     if state_pool is None:
@@ -957,7 +955,7 @@ def ssm_decode_step(x, dt, a, b, c, state_pool, state_idx, skip=None, z=None, dt
     _check(state_pool, "state_pool", torch.float32, (state_pool.shape[0], C, S))
     if status is not None:
         _check(status, "status", torch.int32, (1,))
-    out = _new(x, stream)((B, C)) if out is None else _check(out, "out", x.dtype, (B, C))
+    out = empty((B, C), dtype=x.dtype, device=x.device) if out is None else _check(out, "out", x.dtype, (B, C))
     rc = load().gdn_ssm_decode_step(_ptr(x), _ptr(dt), _ptr(z), _ptr(a), _ptr(b), _ptr(c), _ptr(skip), _ptr(dt_bias), B,
                                     C, S, G, code, strides, 1 if dt_softplus else 0, _ptr(state_idx), _ptr(state_pool),
                                     state_pool.shape[0], _ptr(out), _ptr(status), _stream_handle(stream))
@@ -996,8 +994,9 @@ def gated_rmsnorm_fwd(x, z, w, group=None, eps: float = 1e-6, first: str = "norm
     fp16 or fp32; rows may be strided); w [group] (the same for every group) or [D], of any of the types; group <=
     16384. Returns y [T, D] of x's type; it may be x or z itself, when contiguous."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     T, D, group, shared, order, code, wcode, (xs, zs) = _gnorm_inputs(x, z, w, group, first)
-    y = _new(x, stream)((T, D)) if y is None else _check(y, "y", x.dtype, (T, D))
+    y = empty((T, D), dtype=x.dtype, device=x.device) if y is None else _check(y, "y", x.dtype, (T, D))
     rc = load().gdn_gated_rmsnorm_fwd(_ptr(x), xs, _ptr(z), zs, _ptr(w), T, D, group, shared, order, code, wcode,
                                       float(eps), _ptr(y), _stream_handle(stream))
     if rc != GDN_OK:
@@ -1009,18 +1008,19 @@ def gated_rmsnorm_bwd(x, z, w, dy, group=None, eps: float = 1e-6, first: str = "
                       workspace=None, stream=None):
     """Backward of gated_rmsnorm_fwd. Returns (dx, dz [T, D] of x's type, dw fp32 of w's shape)."""
     torch = _torch()
+    empty = torch.empty if stream is None else _empty_on(stream)
     if dy is None:
         raise ValueError("dy is required")
     T, D, group, shared, order, code, wcode, (xs, zs, gs) = _gnorm_inputs(x, z, w, group, first, dy)
-    new = _new(x, stream)
-    dx = new((T, D)) if dx is None else _check(dx, "dx", x.dtype, (T, D))
-    dz = new((T, D)) if dz is None else _check(dz, "dz", x.dtype, (T, D))
+    dx = empty((T, D), dtype=x.dtype, device=x.device) if dx is None else _check(dx, "dx", x.dtype, (T, D))
+    dz = empty((T, D), dtype=x.dtype, device=x.device) if dz is None else _check(dz, "dz", x.dtype, (T, D))
     if dw is None:
-        dw = new(w.shape, dtype=torch.float32)
+        dw = empty(tuple(w.shape), dtype=torch.float32, device=x.device)
     else:
         _check(dw, "dw", torch.float32, tuple(w.shape))
     if workspace is None:
-        workspace = new(int(load().gdn_gated_rmsnorm_workspace_size(T, D, group, code)), dtype=torch.uint8)
+        workspace = empty(int(load().gdn_gated_rmsnorm_workspace_size(T, D, group, code)), dtype=torch.uint8,
+                          device=x.device)
     rc = load().gdn_gated_rmsnorm_bwd(_ptr(x), xs, _ptr(z), zs, _ptr(w), _ptr(dy), gs, T, D, group, shared, order, code,
                                       wcode, float(eps), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(workspace),
                                       workspace.numel(), _stream_handle(stream))
