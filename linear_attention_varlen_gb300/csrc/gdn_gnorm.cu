@@ -93,11 +93,16 @@ struct Share {
 template <int kN, int kNv, int kStages>
 struct Ring {
   static constexpr int bytes(int threads) { return kN * kNv * kStages * 16 * threads; }
-  static __device__ __forceinline__ Words* at(int slot, int tensor, int v) {
-    extern __shared__ Words ring[];
-    return ring + ((slot * kN + tensor) * kNv + v) * (int)blockDim.x + threadIdx.x;
+  int pitch, row, put, take;  // bytes between a thread's vectors, and between rows; places of the next rows
+  __device__ __forceinline__ Ring() : pitch(16 * (int)blockDim.x), row(kN * kNv * pitch), put(16 * (int)threadIdx.x), take(put) {}
+  __device__ __forceinline__ Words* at(int place, int tensor, int v) const {
+    extern __shared__ __align__(16) uint8_t ring[];
+    return reinterpret_cast<Words*>(ring + place + (tensor * kNv + v) * pitch);
   }
-  static __device__ __forceinline__ void step(int& slot) { slot = slot + 1 == kStages ? 0 : slot + 1; }
+  __device__ __forceinline__ void step(int& place) const {
+    place += row;
+    if (place >= kStages * row) place -= kStages * row;
+  }
 };
 
 // Sums over the team; every thread of it gets them, added up in the same order. `buf` has room for two rows of a CTA's
@@ -150,7 +155,7 @@ __host__ __device__ constexpr int bwd_stages() {
 template <typename T, int kNv, bool kVec, bool kGateFirst>
 __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_constant__ GnormParams p, int L) {
   constexpr int P = kPairs<T>, kStages = fwd_stages<T, kNv, kVec>();
-  using R = Ring<2, kNv, kStages>;
+  Ring<2, kNv, kStages> ring;
   __shared__ Sums<1> buf[2][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
@@ -176,19 +181,22 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
   const int64_t dx = p.rows * p.sx, dz = p.rows * p.sz, dy = p.rows * p.D;
   // rows behind the last one (and those of threads behind the last team) are left out
   const int mine = row0 < p.rows && row0 < p.T ? (int)((p.T - row0 + p.rows - 1) / p.rows) : 0;
-  int put = 0, take = 0;  // places in the ring; x and z: the row that comes next
+  bool in[kNv];
+#pragma unroll
+  for (int v = 0; v < kNv; ++v) in[v] = sh.col(v, 0) < p.group;
+  // x and z: the row that comes next
   auto issue = [&](int k) {
     if (k < mine) {
 #pragma unroll
       for (int v = 0; v < kNv; ++v)
-        if (sh.col(v, 0) < p.group) {
-          cp_async16(R::at(put, 0, v), x + sh.col(v, 0));
-          cp_async16(R::at(put, 1, v), z + sh.col(v, 0));
+        if (in[v]) {
+          cp_async16(ring.at(ring.put, 0, v), x + sh.col(v, 0));
+          cp_async16(ring.at(ring.put, 1, v), z + sh.col(v, 0));
         }
     }
     cp_async_commit();
     x += dx, z += dz;
-    R::step(put);
+    ring.step(ring.put);
   };
   if constexpr (kStages > 0) {
 #pragma unroll
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
     for (int v = 0; v < kNv; ++v) {
       Words xr{}, zr{};
       if constexpr (kStages > 0) {
-        if (k < mine && sh.col(v, 0) < p.group) xr = *R::at(take, 0, v), zr = *R::at(take, 1, v);
+        if (k < mine && in[v]) xr = *ring.at(ring.take, 0, v), zr = *ring.at(ring.take, 1, v);
       } else {
         xr = sh.load(x, v, k < mine);
         zr = sh.load(z, v, k < mine);
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
       }
     }
     if constexpr (kStages > 0)
-      R::step(take);
+      ring.step(ring.take);
     else
       x += dx, z += dz;
     float sum[1] = {f2_sum(sum2)};
@@ -244,7 +252,7 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(con
   constexpr int K = kElems<T>, P = kPairs<T>;
   constexpr bool kKeep = kNv * K <= 8;
   constexpr int kStages = bwd_stages<T, kNv, kVec>();
-  using R = Ring<3, kNv, kStages>;
+  Ring<3, kNv, kStages> ring;
   __shared__ Sums<2> buf[2][kMaxTeam / 32];
   int turn = 0;
   const int64_t team = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
@@ -280,21 +288,24 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(con
   const int64_t ex = p.rows * p.sx, ez = p.rows * p.sz, eg = p.rows * p.sdy, eo = p.rows * p.D;
   T *dxp = static_cast<T*>(p.dx) + row0 * p.D + at, *dzp = static_cast<T*>(p.dz) + row0 * p.D + at;
   const int mine = row0 < p.rows && row0 < p.T ? (int)((p.T - row0 + p.rows - 1) / p.rows) : 0;
-  int put = 0, take = 0;  // places in the ring; x, z and g: the row that comes next
+  bool in[kNv];
+#pragma unroll
+  for (int v = 0; v < kNv; ++v) in[v] = sh.col(v, 0) < p.group;
+  // x, z and g: the row that comes next
   constexpr int kHold = kKeep ? kNv : 1;
   auto issue = [&](int k) {
     if (k < mine) {
 #pragma unroll
       for (int v = 0; v < kNv; ++v)
-        if (sh.col(v, 0) < p.group) {
-          cp_async16(R::at(put, 0, v), x + sh.col(v, 0));
-          cp_async16(R::at(put, 1, v), z + sh.col(v, 0));
-          cp_async16(R::at(put, 2, v), g + sh.col(v, 0));
+        if (in[v]) {
+          cp_async16(ring.at(ring.put, 0, v), x + sh.col(v, 0));
+          cp_async16(ring.at(ring.put, 1, v), z + sh.col(v, 0));
+          cp_async16(ring.at(ring.put, 2, v), g + sh.col(v, 0));
         }
     }
     cp_async_commit();
     x += ex, z += ez, g += eg;
-    R::step(put);
+    ring.step(ring.put);
   };
   if constexpr (kStages > 0) {
 #pragma unroll
@@ -321,7 +332,7 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(con
     auto fetch = [&](int v, int hold, bool live) {
       if constexpr (kStages > 0) {
         xr[hold] = zr[hold] = gr[hold] = Words{};
-        if (live && sh.col(v, 0) < p.group) xr[hold] = *R::at(take, 0, v), zr[hold] = *R::at(take, 1, v), gr[hold] = *R::at(take, 2, v);
+        if (live && in[v]) xr[hold] = *ring.at(ring.take, 0, v), zr[hold] = *ring.at(ring.take, 1, v), gr[hold] = *ring.at(ring.take, 2, v);
       } else {
         xr[hold] = sh.load(x, v, live);
         zr[hold] = sh.load(z, v, live);
@@ -368,7 +379,7 @@ __global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(con
     }
     dxp += eo, dzp += eo;
     if constexpr (kStages > 0)
-      R::step(take);
+      ring.step(ring.take);
     else
       x += ex, z += ez, g += eg;
   }
