@@ -9,6 +9,9 @@ workspaces that are not given are allocated for it. Inputs of another stream are
     import linear_attention_varlen_gb300 as gdn
     out, final_state = gdn.chunk_fwd(q, k, v, g, beta, cu_seqlens)
     grads = gdn.chunk_bwd(q, k, v, g, beta, cu_seqlens, dout)
+
+Beside the delta rule: decayed linear attention (la_*), the norm (rmsnorm_*), and a state-space block's short convolution
+with its activation (conv_*), selective scan (ssm_*) and norm with its gate (gated_rmsnorm_*).
 """
 from __future__ import annotations
 

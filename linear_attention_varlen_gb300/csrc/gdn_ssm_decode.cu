@@ -4,8 +4,10 @@
 // It is the scan on a document of one token that starts from the pool entry.
 //
 // The step reads and writes each state once and does seven operations an element: it is bound by HBM traffic as long as
-// what is done for each channel stays small beside it. A thread takes four states of two channels of one sequence, in
-// packed pairs.
+// what is done for each channel stays small beside it, and that all loads are under way before the first is waited for
+// (67 us without that). A thread takes four states of two channels of one sequence, in packed pairs.
+// Measured: 200 sequences of 8192 channels of 16 states 42 us (223 MB, 5.3 TB/s); one sequence of 2048 channels 2 us.
+// Several sequences to a CTA, one after the other or the next one's loads ahead, took 70 to 115 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
