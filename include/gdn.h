@@ -399,7 +399,8 @@ int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const 
  * empty document is its start state). All tensor pointers are device pointers:
  *   x, dt, z, out, dout, dx, ddt, dz : [T, C] of `dtype`;  z NULL: no gate (dz is then not written)
  *   b, c, db, dc : [T, G, S] of `dtype`;  1 <= S <= 64, C a multiple of G
- *   a : fp32 [C, S], expected <= 0;  skip, dt_bias : fp32 [C] or NULL (zero)
+ *   a : fp32 [C, S], expected <= 0 (where a dt is positive, exp(a sum of dt) has to stay finite over a document, or
+ *   even states of zero become NaN);  skip, dt_bias : fp32 [C] or NULL (zero)
  *   strides : host array or NULL. Elements from one token to the next of x, dt, z, b, c (and dout in the
  *   backward), for views into a projection; 0 or NULL = contiguous. Channels (and the G S entries of a map) are
  *   contiguous within a token, as are out and the gradients throughout.

@@ -71,6 +71,25 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
 
+// Documents that start from the same entry of a pool, as chains in their order: link[d] = {the next one or -1, whether d
+// is the first}. One warp a document, warp `warp` of `warps`; what the pool's entries gather is set to zero on the way.
+__device__ __forceinline__ void link_pool_starts(const int32_t* init_idx, int N, int n_init, int2* link, int64_t warp, int64_t warps) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t d = warp; d < N; d += warps) {
+    const int e = init_idx ? init_idx[d] : -1;
+    int next = -1, first = e >= 0 && e < n_init;
+    if (first) {
+      for (int64_t i = d - 32; first && i > -32; i -= 32)  // earlier documents, the nearest first
+        first = !__any_sync(0xffffffffu, i + lane >= 0 && init_idx[max(i + lane, (int64_t)0)] == e);
+      for (int64_t i = d + 1; next < 0 && i < N; i += 32) {
+        const unsigned m = __ballot_sync(0xffffffffu, i + lane < N && init_idx[min(i + lane, (int64_t)N - 1)] == e);
+        if (m) next = (int)i + __ffs(m) - 1;
+      }
+    }
+    if (lane == 0) link[d] = make_int2(next, first);
+  }
+}
+
 // 2^x, relative error about 2^-22
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;

@@ -56,10 +56,11 @@ struct ActParams {
   float *dx, *dw, *dbias, *dinit;
   ActHeader* hd;
   float *dstart, *dend, *part;
+  int2* link;
 };
 
 struct ActLayout {
-  size_t header, dstart, dend, part, total;
+  size_t header, dstart, dend, part, link, total;
   int n_tb;
 };
 inline ActLayout act_layout(int N, int T, int C, bool bwd) {
@@ -77,6 +78,7 @@ inline ActLayout act_layout(int N, int T, int C, bool bwd) {
     L.dstart = take((size_t)N * 3 * C * 4);     // gradient at each document's start
     L.dend = take((size_t)N * 3 * C * 4);       // gradient at its tail from forks
     L.part = take((size_t)L.n_tb * C * 5 * 4);  // dw, dbias of each block of tokens: [block][5][C]
+    L.link = take(sizeof(int2) * N);            // documents of the same pool entry
   }
   L.total = o;
   return L;
@@ -125,9 +127,18 @@ __device__ __forceinline__ void unpack(const Raw4<T>& r, uint64_t* f) {
   for (int i = 0; i < kPr; ++i) f[i] = pair_of<T>(r.w, i);
 }
 
+// Block 0 checks cu_seqlens and init_idx. The others (backward with a pool): which documents share an entry, and the
+// entries' gradients set to zero.
 __global__ void __launch_bounds__(256) act_check_kernel(const __grid_constant__ ActParams p) {
   bw::griddep_wait();
   bw::griddep_launch_dependents();
+  if (blockIdx.x > 0) {
+    const int64_t n = (int64_t)p.n_init * 3 * p.C, step = (int64_t)(gridDim.x - 1) * 256;
+    const int64_t i0 = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x;
+    link_pool_starts(p.init_idx, p.N, p.n_init, p.link, i0 / 32, step / 32);
+    for (int64_t i = i0; i < n; i += step) p.dinit[i] = 0.f;
+    return;
+  }
   __shared__ int s_bad, s_forks;
   if (threadIdx.x == 0) s_bad = s_forks = 0;
   __syncthreads();
@@ -462,18 +473,19 @@ __global__ void __launch_bounds__(256) act_ends_kernel(const __grid_constant__ A
   }
 }
 
-// The pool entries' gradients: the start gradients of their documents, in order.
+// The gradients of the pool entries that some document starts from: their documents' start gradients, in order.
 __global__ void __launch_bounds__(256) act_pool_kernel(const __grid_constant__ ActParams p) {
   bw::griddep_wait();
   if (p.hd->status != 0) return;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = 3 * (int64_t)p.C;
-  if (i >= p.n_init * row) return;
-  const int e = (int)(i / row);
-  float v = 0.f;
-  if (p.init_idx)
-    for (int d = 0; d < p.N; ++d)
-      if (p.init_idx[d] == e) v += p.dstart[d * row + i % row];
-  p.dinit[i] = v;
+  const int64_t row = 3 * (int64_t)p.C;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.N * row; i += (int64_t)gridDim.x * 256) {
+    int d = (int)(i / row);
+    if (!p.link[d].y) continue;
+    const int64_t r = i - d * row, e = p.init_idx[d];
+    float v = 0.f;
+    for (; d >= 0; d = p.link[d].x) v += p.dstart[d * row + r];
+    p.dinit[e * row + r] = v;
+  }
 }
 
 struct StepParams {
@@ -630,9 +642,11 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   p.dstart = reinterpret_cast<float*>(ws + L.dstart);
   p.dend = reinterpret_cast<float*>(ws + L.dend);
   p.part = reinterpret_cast<float*>(ws + L.part);
+  p.link = reinterpret_cast<int2*>(ws + L.link);
   p.n_tb = L.n_tb;
   cudaStream_t s = (cudaStream_t)stream;
-  launch_early(act_check_kernel, dim3(1), 256, 0, s, p);
+  const int64_t zeros = n_init > 0 ? ((int64_t)n_init * 3 * C + 32 * (int64_t)N + 1023) / 1024 : 0;  // blocks
+  launch_early(act_check_kernel, dim3((unsigned)(1 + (zeros < 1024 ? zeros : 1024))), 256, 0, s, p);
   if (T > 0)
     by_type(dtype, [&](auto t) {
       using T_ = decltype(t);
@@ -642,10 +656,9 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32), 5), 256, 0, s, p);
   if (dfinal_tail || init_idx)
     launch_early(act_ends_kernel, dim3((unsigned)((C + 255) / 256), (unsigned)(N < 64 ? N : 64)), 256, 0, s, p);
-  if (n_init > 0) {
-    const int64_t n = (int64_t)n_init * 3 * C;
-    if (n > (int64_t)256 * INT32_MAX) return GDN_ERR_INVALID_ARG;
-    launch_early(act_pool_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, s, p);
+  if (n_init > 0 && init_idx) {
+    const int64_t blocks = ((int64_t)N * 3 * C + 255) / 256;
+    launch_early(act_pool_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, s, p);
   }
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

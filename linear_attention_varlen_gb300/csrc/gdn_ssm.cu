@@ -68,6 +68,7 @@ struct SsmParams {
   SsmHeader* hd;
   SsmSeg* segs;
   int32_t *seg0, *is_src;
+  int2* link;
   float *maps, *slot, *sums, *slot_r, *ckpt, *csum, *dstart, *facc, *part_a, *part_c, *part_m;
   int64_t smax;
   int parts, seg_tokens, bwd, whole;
@@ -94,11 +95,18 @@ __device__ void maps_to_float(const SsmParams& p, int block, int blocks) {
 }
 
 // Block 0: checks cu_seqlens and init_idx and cuts the documents into segments of at most seg_tokens. The others:
-// the maps b and c in fp32, [T][G][2][Sp], zero behind the last state.
+// the maps b and c in fp32, [T][G][2][Sp], zero behind the last state; in the backward which documents share a pool entry,
+// and the entries' gradients set to zero.
 __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_constant__ SsmParams p) {
   bw::griddep_wait();  // the call before on this stream may still read the workspace
   bw::griddep_launch_dependents();
   if (blockIdx.x > 0) {
+    if (p.bwd && p.n_init > 0) {
+      const int64_t n = (int64_t)p.n_init * p.C * p.S, step = (int64_t)(gridDim.x - 1) * blockDim.x;
+      const int64_t i0 = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+      link_pool_starts(p.init_idx, p.N, p.n_init, p.link, i0 / 32, step / 32);
+      for (int64_t i = i0; i < n; i += step) p.dinit[i] = 0.f;
+    }
     if (p.dtype == GDN_DTYPE_BF16)
       maps_to_float<__nv_bfloat16>(p, blockIdx.x - 1, gridDim.x - 1);
     else if (p.dtype == GDN_DTYPE_FP16)
@@ -1035,7 +1043,7 @@ struct Quad {
 };
 
 // blockIdx.y 0: db and dc over the CTAs of the channels; 1: da over the segments; 2: dskip and ddt_bias; 3: the start
-// states' gradients over the documents of each pool entry.
+// states' gradients over the documents of each pool entry that some document starts from.
 __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ SsmParams p) {
   __shared__ Quad s_quad[8][32];
   __shared__ float s_one[8][32];
@@ -1073,16 +1081,16 @@ __global__ void __launch_bounds__(256) ssm_sum_kernel(const __grid_constant__ Ss
       if (threadIdx.x < 32 && j + lane < n && out) out[i % p.C] = v;
     }
   } else {
-    for (int64_t i = i0; i < (int64_t)p.n_init * Q * p.C; i += step) {
-      const int e = (int)(i / ((int64_t)Q * p.C));
-      const int64_t r = i % ((int64_t)Q * p.C);
+    const int64_t per = (int64_t)Q * p.C;
+    for (int64_t i = i0; i < p.N * per; i += step) {
+      int d = (int)(i / per);
+      if (!p.link[d].y) continue;
+      const int64_t e = p.init_idx[d], r = i - d * per;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.init_idx)
-        for (int d = 0; d < p.N; ++d)
-          if (p.init_idx[d] == e) {
-            const float4 f = *reinterpret_cast<const float4*>(p.dstart + d * state + r * 4);
-            v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
-          }
+      for (; d >= 0; d = p.link[d].x) {
+        const float4 f = *reinterpret_cast<const float4*>(p.dstart + d * state + r * 4);
+        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+      }
       store_quad(p.dinit, e, p.C, p.S, (int)(r % p.C), (int)(r / p.C), v, p.whole);
     }
   }
@@ -1164,6 +1172,7 @@ int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p,
   p->is_src = reinterpret_cast<int32_t*>(ws + L->is_src);
   p->maps = f(L->maps), p->slot = f(L->slot), p->sums = f(L->sums);
   if (c.bwd) {
+    p->link = reinterpret_cast<int2*>(ws + L->link);
     p->slot_r = f(L->slot_r), p->ckpt = f(L->ckpt), p->csum = f(L->csum), p->dstart = f(L->dstart);
     p->facc = f(L->facc), p->part_a = f(L->part_a), p->part_c = f(L->part_c), p->part_m = f(L->part_m);
   }
@@ -1250,7 +1259,9 @@ bool launch_walk(const SsmParams& p, int sms, cudaStream_t s) {
 }
 
 void launch_plan(const SsmParams& p, int sms, cudaStream_t s) {
-  const int64_t n = (int64_t)p.T * p.G * 2 * ssm_padded(p.S), blocks = (n + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  int64_t n = (int64_t)p.T * p.G * 2 * ssm_padded(p.S);
+  if (p.bwd && p.n_init > 0) n += (int64_t)p.n_init * p.C * p.S + 32 * (int64_t)p.N;
+  const int64_t blocks = (n + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   launch_early(ssm_plan_kernel, dim3((unsigned)(1 + (blocks < 2 * sms ? blocks : 2 * sms))), kPlanThreads, 0, s, p);
 }
 

@@ -44,7 +44,7 @@ constexpr int kSsmWarps = 4;  // warps to a CTA
 // Workspace (byte offsets). State-sized arrays hold [Sp / 4][C][4] floats: four states of one channel together,
 // channels beside one another.
 struct SsmLayout {
-  size_t header, segs, seg0, is_src, maps, slot, sums, slot_r, ckpt, csum, dstart, facc, part_a, part_c, part_m, total;
+  size_t header, segs, seg0, is_src, link, maps, slot, sums, slot_r, ckpt, csum, dstart, facc, part_a, part_c, part_m, total;
   int64_t smax, tiles;
   int seg_tokens;  // most tokens to a segment
   int parts;  // CTAs of the backward's walk to a group of channels
@@ -76,6 +76,7 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   L.slot = take(state * L.smax);                          // end states from zero, then start states
   L.sums = take(sizeof(float) * C * L.smax);              // time of each segment
   if (bwd) {
+    L.link = take(sizeof(int2) * N);                      // documents of the same pool entry
     L.slot_r = take(state * L.smax);                      // the same for the state's gradient, in reverse
     L.ckpt = take(state * L.tiles);                       // states from zero at each tile of a segment
     L.csum = take(sizeof(float) * C * L.tiles);           // time from the segment's start to each tile

@@ -192,3 +192,26 @@ def test_rows_beyond_32_bit_offsets():
     near = dict(rtol=2.0 ** -7, atol=float(os_.abs().max()) * 2.0 ** -14)  # other segments: a rounding to bf16 may turn
     torch.testing.assert_close(out[-40:], os_, **near)
     torch.testing.assert_close(fin[1], fs[0], rtol=2.0 ** -14, atol=2.0 ** -14)
+
+
+def test_pools_of_many_entries():
+    """Thousands of documents, each from an entry of its own or from one that many share: gradients against those of the
+    documents by themselves, and the time stays that of the sizes."""
+    N, C, S = 6000, 24, 8
+    rng = torch.Generator().manual_seed(5)
+    own = torch.randperm(N, generator=rng)
+    own[::3] = 7
+    lens = [1] * N
+    d, _ = on_gpu(ssm_ref.problem(8, lens, C, S, n_pool=1, dfin=True), "fp32")
+    d["pool"] = torch.randn(N, C, S, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))
+    g = run_bwd(d, own.tolist())
+    alone = run_bwd(d | {"pool": d["pool"][own.to("cuda")].contiguous()}, list(range(N)))
+    want = torch.zeros(N, C, S, dtype=torch.float64, device="cuda").index_add_(0, own.to("cuda"), alone["dinit"].double())
+    torch.testing.assert_close(g["dinit"].double(), want, rtol=2.0 ** -20, atol=2000 * 2.0 ** -24 * float(want.abs().max()))
+    e = conv_inputs(9, lens, C, "fp32")
+    pool = torch.randn(N, 3, C, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+    run = lambda p, i: gdn.conv_bwd(e["x"], e["w"], e["cu"], e["dy"], bias=e["bias"], init_idx=int32(i), conv_init=p,  # noqa: E731
+                                    dfinal_tail=e["dtail"], activation="silu")["dconv_init"]
+    got, alone = run(pool, own.tolist()), run(pool[own.to("cuda")].contiguous(), list(range(N)))
+    want = torch.zeros(N, 3, C, dtype=torch.float64, device="cuda").index_add_(0, own.to("cuda"), alone.double())
+    torch.testing.assert_close(got.double(), want, rtol=2.0 ** -20, atol=2000 * 2.0 ** -24 * float(want.abs().max()))
