@@ -71,6 +71,33 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
 
+// How documents hang together. A fork starts where an earlier document ends, its source. Forks of documents that are no
+// forks (and, in reverse, sources whose forks have none) need but one step behind the rest; deeper ones go in order.
+enum { kDocFork = 1, kDocSource = 2, kDocDeepFork = 4, kDocDeepSource = 8 };
+// Where a document comes in three steps over all of them: 0, 1, or 2 (one after the other).
+__device__ __forceinline__ int fork_step(int kind) { return kind & kDocDeepFork ? 2 : kind & kDocFork ? 1 : 0; }
+__device__ __forceinline__ int source_step(int kind) { return kind & kDocDeepSource ? 2 : kind & kDocSource ? 1 : 0; }
+// kind[0 .. N - 1] by one CTA, from an init_idx that has been checked; returns (to every thread) whether some are deep.
+__device__ __forceinline__ bool fork_kinds(const int32_t* init_idx, int N, int n_init, int32_t* kind) {
+  for (int i = threadIdx.x; i < N; i += blockDim.x) kind[i] = 0;
+  __syncthreads();
+  if (!init_idx) return false;
+  for (int i = threadIdx.x; i < N; i += blockDim.x)
+    if (init_idx[i] >= n_init) {
+      atomicOr(&kind[i], kDocFork);
+      atomicOr(&kind[init_idx[i] - n_init], kDocSource);
+    }
+  __syncthreads();
+  int deep = 0;
+  for (int i = threadIdx.x; i < N; i += blockDim.x)
+    if (init_idx[i] >= n_init) {
+      const int j = init_idx[i] - n_init;
+      if (__ldcg(&kind[j]) & kDocFork) atomicOr(&kind[i], kDocDeepFork), deep = 1;
+      if (__ldcg(&kind[i]) & kDocSource) atomicOr(&kind[j], kDocDeepSource), deep = 1;
+    }
+  return __syncthreads_or(deep);
+}
+
 // Documents that start from the same entry of a pool, as chains in their order: link[d] = {the next one or -1, whether d
 // is the first}. One warp a document, warp `warp` of `warps`; what the pool's entries gather is set to zero on the way.
 __device__ __forceinline__ void link_pool_starts(const int32_t* init_idx, int N, int n_init, int2* link, int64_t warp, int64_t warps) {

@@ -40,7 +40,7 @@ using bw::f2_mul;
 using bw::f2_pack;
 
 struct ActHeader {
-  int32_t status, forks;
+  int32_t status, deep;
   int32_t pad[62];
 };
 
@@ -55,12 +55,13 @@ struct ActParams {
   const float* dtail;  // given gradient of the tails
   float *dx, *dw, *dbias, *dinit;
   ActHeader* hd;
-  float *dstart, *dend, *part;
+  float *dstart, *part;
+  int32_t* kind;
   int2* link;
 };
 
 struct ActLayout {
-  size_t header, dstart, dend, part, link, total;
+  size_t header, kind, dstart, part, link, total;
   int n_tb;
 };
 inline ActLayout act_layout(int N, int T, int C, bool bwd) {
@@ -76,7 +77,7 @@ inline ActLayout act_layout(int N, int T, int C, bool bwd) {
   L.header = take(sizeof(ActHeader));
   if (bwd) {
     L.dstart = take((size_t)N * 3 * C * 4);     // gradient at each document's start
-    L.dend = take((size_t)N * 3 * C * 4);       // gradient at its tail from forks
+    L.kind = take(sizeof(int32_t) * N);
     L.part = take((size_t)L.n_tb * C * 5 * 4);  // dw, dbias of each block of tokens: [block][5][C]
     L.link = take(sizeof(int2) * N);            // documents of the same pool entry
   }
@@ -139,24 +140,18 @@ __global__ void __launch_bounds__(256) act_check_kernel(const __grid_constant__ 
     for (int64_t i = i0; i < n; i += step) p.dinit[i] = 0.f;
     return;
   }
-  __shared__ int s_bad, s_forks;
-  if (threadIdx.x == 0) s_bad = s_forks = 0;
+  __shared__ int s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < p.N; i += 256) {
-    const int b = p.cu[i], e = p.cu[i + 1];
-    bool bad = b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T);
-    if (p.init_idx) {
-      const int s = p.init_idx[i];
-      if (s < -1 || (s >= p.n_init && s - p.n_init >= i))
-        bad = true;
-      else if (s >= p.n_init)
-        s_forks = 1;
-    }
-    if (bad) s_bad = 1;
+    const int b = p.cu[i], e = p.cu[i + 1], x = p.init_idx ? p.init_idx[i] : -1;
+    if (b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T) || x < -1 || (x >= p.n_init && x - p.n_init >= i))
+      s_bad = 1;
   }
   __syncthreads();
+  const bool deep = !s_bad && p.kind && fork_kinds(p.init_idx, p.N, p.n_init, p.kind);
   if (threadIdx.x == 0) {
-    p.hd->forks = s_forks;
+    p.hd->deep = deep;
     p.hd->status = s_bad ? kErrInvalid : 0;
   }
 }
@@ -433,43 +428,54 @@ __global__ void __launch_bounds__(256) act_sum_kernel(const __grid_constant__ Ac
   }
 }
 
-// The tails' gradients, given ones and those of forks, into the inputs they copy or on into the document's start;
-// each document's start gradient where it belongs. One thread to a channel; all documents from the last on where some
-// fork, else those of blockIdx.y.
+// The tails' gradients, given ones and those of forks, into the inputs they copy or on into the document's start. One
+// thread to a channel and the documents of blockIdx.y, in three steps as the scan's (kStep).
+template <int kStep>
 __global__ void __launch_bounds__(256) act_ends_kernel(const __grid_constant__ ActParams p) {
   bw::griddep_wait();
   bw::griddep_launch_dependents();
-  if (p.hd->status != 0) return;
+  if (p.hd->status != 0 || (kStep == 2 && !p.hd->deep)) return;
   const int c = blockIdx.x * 256 + threadIdx.x;
-  const bool forks = p.hd->forks != 0;
-  if (c >= p.C || (forks && blockIdx.y > 0)) return;
-  const int step = forks ? 1 : gridDim.y, d0 = forks ? 0 : blockIdx.y;
-  if (forks)
-    for (int64_t i = 0; i < 3 * (int64_t)p.N; ++i) p.dend[i * p.C + c] = 0.f;
+  if (c >= p.C) return;
+  const int step = gridDim.y, d0 = blockIdx.y;
   for (int d = d0 + (p.N - 1 - d0) / step * step; d >= 0; d -= step) {
+    if (source_step(p.kind[d]) != kStep) continue;
     const int t0 = p.cu[d], n = p.cu[d + 1] - t0;
     float* start = p.dstart + (int64_t)d * 3 * p.C + c;
-    float g[3];
+    float g[3], v[3];
 #pragma unroll
-    for (int e = 0; e < 3; ++e) g[e] = n > 0 ? start[(int64_t)e * p.C] : 0.f;
+    for (int e = 0; e < 3; ++e) {
+      g[e] = n > 0 ? start[(int64_t)e * p.C] : 0.f;
+      v[e] = p.dtail ? p.dtail[((int64_t)d * 3 + e) * p.C + c] : 0.f;
+    }
+    if (kStep > 0) {
+      constexpr int kAhead = 8;
+      for (int f0 = d + 1; f0 < p.N; f0 += kAhead) {
+        float f[kAhead][3];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const bool mine = f0 + j < p.N && p.init_idx[f0 + j] == p.n_init + d;
+#pragma unroll
+          for (int e = 0; e < 3; ++e) f[j][e] = mine ? p.dstart[((int64_t)(f0 + j) * 3 + e) * p.C + c] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int e = 0; e < 3; ++e) v[e] += f[j][e];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      float v = p.dtail ? p.dtail[((int64_t)d * 3 + k) * p.C + c] : 0.f;
-      if (forks) v += p.dend[((int64_t)d * 3 + k) * p.C + c];
       if (n + k >= 3) {
-        if (p.dtail || forks) p.dx[((int64_t)t0 + n + k - 3) * p.C + c] += v;
+        if (p.dtail || kStep > 0) p.dx[((int64_t)t0 + n + k - 3) * p.C + c] += v[k];
       } else {
 #pragma unroll
         for (int e = 0; e < 3; ++e)
-          if (e == n + k) g[e] += v;
+          if (e == n + k) g[e] += v[k];
       }
     }
-    const int s = p.init_idx ? p.init_idx[d] : -1;
 #pragma unroll
-    for (int e = 0; e < 3; ++e) {
-      start[(int64_t)e * p.C] = g[e];
-      if (s >= p.n_init && p.init_idx) p.dend[((int64_t)(s - p.n_init) * 3 + e) * p.C + c] += g[e];
-    }
+    for (int e = 0; e < 3; ++e) start[(int64_t)e * p.C] = g[e];
   }
 }
 
@@ -640,7 +646,7 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.hd = reinterpret_cast<ActHeader*>(ws + L.header);
   p.dstart = reinterpret_cast<float*>(ws + L.dstart);
-  p.dend = reinterpret_cast<float*>(ws + L.dend);
+  p.kind = reinterpret_cast<int32_t*>(ws + L.kind);
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.link = reinterpret_cast<int2*>(ws + L.link);
   p.n_tb = L.n_tb;
@@ -654,8 +660,12 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
       launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kActThreads, 0, s, p);
     });
   launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32), 5), 256, 0, s, p);
-  if (dfinal_tail || init_idx)
-    launch_early(act_ends_kernel, dim3((unsigned)((C + 255) / 256), (unsigned)(N < 64 ? N : 64)), 256, 0, s, p);
+  const unsigned cb = (unsigned)((C + 255) / 256), db = (unsigned)(N < 64 ? N : 64);
+  if (dfinal_tail || init_idx) launch_early(act_ends_kernel<0>, dim3(cb, db), 256, 0, s, p);
+  if (init_idx) {
+    launch_early(act_ends_kernel<1>, dim3(cb, db), 256, 0, s, p);
+    launch_early(act_ends_kernel<2>, dim3(cb, 1), 256, 0, s, p);
+  }
   if (n_init > 0 && init_idx) {
     const int64_t blocks = ((int64_t)N * 3 * C + 255) / 256;
     launch_early(act_pool_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, s, p);

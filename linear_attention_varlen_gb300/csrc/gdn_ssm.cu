@@ -67,9 +67,9 @@ struct SsmParams {
   // workspace
   SsmHeader* hd;
   SsmSeg* segs;
-  int32_t *seg0, *is_src;
+  int32_t *seg0, *kind;
   int2* link;
-  float *maps, *slot, *sums, *slot_r, *ckpt, *csum, *dstart, *facc, *part_a, *part_c, *part_m;
+  float *maps, *slot, *sums, *slot_r, *ckpt, *csum, *dstart, *fin, *part_a, *part_c, *part_m;
   int64_t smax;
   int parts, seg_tokens, bwd, whole;
 };
@@ -115,24 +115,14 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
       maps_to_float<float>(p, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
-  __shared__ int s_warp[32], s_base, s_bad, s_forks;
+  __shared__ int s_warp[32], s_base, s_bad;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (tid == 0) s_base = s_bad = s_forks = 0;
-  for (int i = tid; i < p.N; i += kPlanThreads) p.is_src[i] = 0;
+  if (tid == 0) s_base = s_bad = 0;
   __syncthreads();
   for (int i = tid; i < p.N; i += kPlanThreads) {
-    const int b = p.cu[i], e = p.cu[i + 1];
-    bool bad = b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T);
-    if (p.init_idx) {
-      const int x = p.init_idx[i];
-      if (x < -1 || (x >= p.n_init && x - p.n_init >= i)) {
-        bad = true;
-      } else if (x >= p.n_init) {
-        p.is_src[x - p.n_init] = 1;
-        s_forks = 1;
-      }
-    }
-    if (bad) s_bad = 1;
+    const int b = p.cu[i], e = p.cu[i + 1], x = p.init_idx ? p.init_idx[i] : -1;
+    if (b < 0 || e < b || e > p.T || (i == 0 && b != 0) || (i == p.N - 1 && e != p.T) || x < -1 || (x >= p.n_init && x - p.n_init >= i))
+      s_bad = 1;
   }
   __syncthreads();
   if (s_bad) {
@@ -142,6 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
     }
     return;
   }
+  const bool deep = fork_kinds(p.init_idx, p.N, p.n_init, p.kind);
   const int L = p.seg_tokens;
   for (int i0 = 0; i0 < p.N; i0 += kPlanThreads) {
     const int i = i0 + tid;
@@ -183,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
         s.first = j == 0;
         s.last = j == k - 1;
         s.src = j > 0 || src >= p.n_init ? -2 : src;
-        s.need = p.bwd || j < k - 1 || p.is_src[i];
+        s.need = p.bwd || j < k - 1 || (__ldcg(&p.kind[i]) & kDocSource);
         s.pad = 0;
         p.segs[at + j] = s;
       }
@@ -195,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
   if (tid == 0) {
     p.seg0[p.N] = s_base;
     p.hd->n_segs = s_base;
-    p.hd->forks = s_forks;
+    p.hd->deep = deep;
     p.hd->status = 0;
   }
 }
@@ -556,7 +547,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
 
 // ------------------------------------------------------------------------------ scan over segments
 
-constexpr int kScanAhead = 16;  // segments whose loads are in flight
+constexpr int kScanThreads = 128, kScanAhead = 16;  // segments whose loads are in flight
 
 __device__ __forceinline__ float4 carry(float4 a, float time, float4 h, float4 add) {
   return make_float4(fmaf(exp2_approx(a.x * time), h.x, add.x), fmaf(exp2_approx(a.y * time), h.y, add.y),
@@ -565,36 +556,36 @@ __device__ __forceinline__ float4 carry(float4 a, float time, float4 h, float4 a
 
 // Start states of the segments from their end states, in place; final states of empty documents and of those that
 // others fork from; in the backward the gradients behind the segments from those before them, and each document's
-// start-state gradient. A thread takes four states of a channel through the documents: all of them in order where
-// some fork, else the ones of blockIdx.y.
-__global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
+// start-state gradient. A thread takes four states of a channel through the documents of blockIdx.y. Three launches where
+// documents may fork: kStep 0 for documents that need no other, 1 for those that need what 0 left, 2 for the rest in order.
+template <int kStep>
+__global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const __grid_constant__ SsmParams p) {
   bw::griddep_wait();
   bw::griddep_launch_dependents();
-  if (p.hd->status != 0) return;
+  if (p.hd->status != 0 || (kStep == 2 && !p.hd->deep)) return;
   const int Sp = ssm_padded(p.S), Q = Sp / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * kScanThreads + threadIdx.x;
   if (i >= (int64_t)Q * p.C) return;
-  const int q = (int)(i / p.C), c = (int)(i % p.C);
-  const bool forks = p.hd->forks != 0;
-  if (forks && blockIdx.y > 0) return;
-  const int step = forks ? 1 : gridDim.y, d0 = forks ? 0 : blockIdx.y;
+  const int q = (int)(i / p.C), c = (int)(i % p.C), step = gridDim.y, d0 = blockIdx.y;
   const int64_t state = (int64_t)Q * p.C * 4;
   float4 a = pool_quad(p.a, 0, p.C, p.S, c, q, p.whole);
   a = make_float4(a.x * kLog2e, a.y * kLog2e, a.z * kLog2e, a.w * kLog2e);
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  // final states of documents that others fork from: the output in the forward, the workspace in the backward
-  auto fin = [&](int d) { return reinterpret_cast<float4*>(p.dstart + d * state + i * 4); };
+  auto fin = [&](int64_t d) { return reinterpret_cast<float4*>(p.fin + d * state + i * 4); };        // backward only
+  auto dstart = [&](int64_t d) { return reinterpret_cast<float4*>(p.dstart + d * state + i * 4); };
   for (int d = d0; d < p.N; d += step) {
+    const int kind = p.kind[d];
+    if (fork_step(kind) != kStep) continue;
     const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
     const int src = p.init_idx ? p.init_idx[d] : -1;
-    const bool fork = src >= p.n_init && p.init_idx;
-    if (!p.bwd && s1 - s0 == 1 && !fork && !p.is_src[d]) continue;
+    const bool fork = kind & kDocFork, source = kind & kDocSource;
+    if (!p.bwd && s1 - s0 == 1 && !fork && !source) continue;
     float4 h = zero;
     if (fork)
       h = p.bwd ? *fin(src - p.n_init) : pool_quad(p.final_state, src - p.n_init, p.C, p.S, c, q, p.whole);
     else if (src >= 0)
       h = pool_quad(p.init, src, p.C, p.S, c, q, p.whole);
-    const int se = p.is_src[d] ? s1 : s1 - 1;  // the last segment's end state is wanted for forks only
+    const int se = source ? s1 : s1 - 1;  // the last segment's end state is wanted for forks only
     for (int sb = s0; sb < s1; sb += kScanAhead) {
       float4 e[kScanAhead];
       float time[kScanAhead];
@@ -611,24 +602,26 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
       }
     }
     if (p.bwd) {
-      if (p.is_src[d]) *fin(d) = h;
-    } else if (s1 == s0 || p.is_src[d]) {
+      if (source) *fin(d) = h;
+    } else if (s1 == s0 || source) {
       store_quad(p.final_state, d, p.C, p.S, c, q, h, p.whole);
     }
   }
   if (!p.bwd) return;
-  auto facc = [&](int d) { return reinterpret_cast<float4*>(p.facc + d * state + i * 4); };
-  if (forks)
-    for (int d = 0; d < p.N; ++d) *facc(d) = zero;
-  const int dn = forks ? p.N - 1 : d0 + (p.N - 1 - d0) / step * step;
-  for (int d = dn; d >= 0; d -= step) {
+  for (int d = d0 + (p.N - 1 - d0) / step * step; d >= 0; d -= step) {
+    const int kind = p.kind[d];
+    if (source_step(kind) != kStep) continue;
     const int s0 = p.seg0[d], s1 = p.seg0[d + 1];
-    const int src = p.init_idx ? p.init_idx[d] : -1;
     float4 k = p.dfinal ? pool_quad(p.dfinal, d, p.C, p.S, c, q, p.whole) : zero;
-    if (forks) {
-      const float4 f = *facc(d);
-      k = make_float4(k.x + f.x, k.y + f.y, k.z + f.z, k.w + f.w);
-    }
+    if (kStep > 0)  // what its forks send back, in their order
+      for (int f0 = d + 1; f0 < p.N; f0 += kScanAhead) {
+        float4 e[kScanAhead];
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j)
+          e[j] = f0 + j < p.N && p.init_idx[f0 + j] == p.n_init + d ? *dstart(f0 + j) : zero;
+#pragma unroll
+        for (int j = 0; j < kScanAhead; ++j) k = make_float4(k.x + e[j].x, k.y + e[j].y, k.z + e[j].z, k.w + e[j].w);
+      }
     for (int sb = s1 - 1; sb >= s0; sb -= kScanAhead) {
       float4 e[kScanAhead];
       float time[kScanAhead];
@@ -645,11 +638,7 @@ __global__ void __launch_bounds__(256) ssm_scan_kernel(const __grid_constant__ S
           k = carry(a, time[j], k, e[j]);
         }
     }
-    *fin(d) = k;  // its final state has been read by every fork
-    if (src >= p.n_init && p.init_idx) {
-      float4* f = facc(src - p.n_init);
-      *f = make_float4(f->x + k.x, f->y + k.y, f->z + k.z, f->w + k.w);
-    }
+    *dstart(d) = k;
   }
 }
 
@@ -1169,12 +1158,12 @@ int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p,
   p->hd = reinterpret_cast<SsmHeader*>(ws + L->header);
   p->segs = reinterpret_cast<SsmSeg*>(ws + L->segs);
   p->seg0 = reinterpret_cast<int32_t*>(ws + L->seg0);
-  p->is_src = reinterpret_cast<int32_t*>(ws + L->is_src);
+  p->kind = reinterpret_cast<int32_t*>(ws + L->kind);
   p->maps = f(L->maps), p->slot = f(L->slot), p->sums = f(L->sums);
   if (c.bwd) {
     p->link = reinterpret_cast<int2*>(ws + L->link);
     p->slot_r = f(L->slot_r), p->ckpt = f(L->ckpt), p->csum = f(L->csum), p->dstart = f(L->dstart);
-    p->facc = f(L->facc), p->part_a = f(L->part_a), p->part_c = f(L->part_c), p->part_m = f(L->part_m);
+    p->fin = f(L->fin), p->part_a = f(L->part_a), p->part_c = f(L->part_c), p->part_m = f(L->part_m);
   }
   p->smax = L->smax;
   p->parts = L->parts;
@@ -1266,8 +1255,11 @@ void launch_plan(const SsmParams& p, int sms, cudaStream_t s) {
 }
 
 void launch_scan(const SsmParams& p, cudaStream_t s) {
-  const int64_t n = (int64_t)ssm_padded(p.S) / 4 * p.C;
-  launch_early(ssm_scan_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)(p.N < 16 ? p.N : 16)), 256, 0, s, p);
+  const unsigned gx = (unsigned)(((int64_t)ssm_padded(p.S) / 4 * p.C + kScanThreads - 1) / kScanThreads), gy = (unsigned)(p.N < 64 ? p.N : 64);
+  launch_early(ssm_scan_kernel<0>, dim3(gx, gy), kScanThreads, 0, s, p);
+  if (!p.init_idx) return;
+  launch_early(ssm_scan_kernel<1>, dim3(gx, gy), kScanThreads, 0, s, p);
+  launch_early(ssm_scan_kernel<2>, dim3(gx, 1), kScanThreads, 0, s, p);
 }
 
 template <typename T, int kSp, bool kVec>

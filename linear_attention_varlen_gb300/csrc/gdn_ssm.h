@@ -30,7 +30,7 @@ struct SsmSeg {
 struct SsmHeader {
   int32_t status;
   int32_t n_segs;
-  int32_t forks;     // some document starts from another one
+  int32_t deep;      // some fork's source is a fork
   int32_t pad[61];
 };
 static_assert(sizeof(SsmHeader) == 256, "header is 256 bytes");
@@ -44,7 +44,7 @@ constexpr int kSsmWarps = 4;  // warps to a CTA
 // Workspace (byte offsets). State-sized arrays hold [Sp / 4][C][4] floats: four states of one channel together,
 // channels beside one another.
 struct SsmLayout {
-  size_t header, segs, seg0, is_src, link, maps, slot, sums, slot_r, ckpt, csum, dstart, facc, part_a, part_c, part_m, total;
+  size_t header, segs, seg0, kind, link, maps, slot, sums, slot_r, ckpt, csum, dstart, fin, part_a, part_c, part_m, total;
   int64_t smax, tiles;
   int seg_tokens;  // most tokens to a segment
   int parts;  // CTAs of the backward's walk to a group of channels
@@ -71,7 +71,7 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   L.header = take(sizeof(SsmHeader));
   L.segs = take(sizeof(SsmSeg) * L.smax);
   L.seg0 = take(sizeof(int32_t) * (N + 1));
-  L.is_src = take(sizeof(int32_t) * N);
+  L.kind = take(sizeof(int32_t) * N);
   L.maps = take((size_t)T * G * 2 * Sp * sizeof(float));  // b and c in fp32, token by token
   L.slot = take(state * L.smax);                          // end states from zero, then start states
   L.sums = take(sizeof(float) * C * L.smax);              // time of each segment
@@ -81,7 +81,7 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
     L.ckpt = take(state * L.tiles);                       // states from zero at each tile of a segment
     L.csum = take(sizeof(float) * C * L.tiles);           // time from the segment's start to each tile
     L.dstart = take(state * N);
-    L.facc = take(state * N);                             // gradients that forks send back
+    L.fin = take(state * N);                              // final states of documents that others start from
     L.part_a = take(state * L.smax);                      // sums of each segment: da,
     L.part_c = take(sizeof(float) * 2 * C * L.smax);      //   dskip and ddt_bias
     L.part_m = take((size_t)L.parts * T * G * 2 * Sp * sizeof(float));  // db and dc of each CTA's channels
