@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
       maps_to_float<float>(p, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
-  __shared__ int s_warp[32], s_base, s_bad;
+  __shared__ int s_warp[32], s_base, s_bad, s_long, s_doc[kPlanThreads], s_at[kPlanThreads], s_k[kPlanThreads];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) s_base = s_bad = 0;
   __syncthreads();
@@ -136,12 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
   const int L = p.seg_tokens;
   for (int i0 = 0; i0 < p.N; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    int n = 0, k = 0, t0 = 0;
-    if (i < p.N) {
-      t0 = p.cu[i];
-      n = p.cu[i + 1] - t0;
-      k = (n + L - 1) / L;
-    }
+    const int k = i < p.N ? (p.cu[i + 1] - p.cu[i] + L - 1) / L : 0;
     int upto = k;  // inclusive sum over the warp, then over the block
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -161,24 +156,35 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
     }
     __syncthreads();
     const int at = s_base + upto - k + (wid ? s_warp[wid - 1] : 0);
+    // a document's segment j of k, equal ones in whole tiles
+    auto cut = [&](int doc, int first, int j, int k) {
+      const int t0 = p.cu[doc], n = p.cu[doc + 1] - t0, src = p.init_idx ? p.init_idx[doc] : -1;
+      const int len = ((n + k - 1) / k + kSsmTile - 1) / kSsmTile * kSsmTile;
+      SsmSeg s;
+      s.doc = doc;
+      s.tok0 = t0 + min(n, j * len);
+      s.ntok = min(n, (j + 1) * len) - min(n, j * len);
+      s.first = j == 0;
+      s.last = j == k - 1;
+      s.src = j > 0 || src >= p.n_init ? -2 : src;
+      s.need = p.bwd || j < k - 1 || (__ldcg(&p.kind[doc]) & kDocSource);
+      s.pad = 0;
+      p.segs[first + j] = s;
+    };
+    if (tid == 0) s_long = 0;
+    __syncthreads();
     if (i < p.N) {
       p.seg0[i] = at;
-      const int src = p.init_idx ? p.init_idx[i] : -1;
-      // equal segments, in whole tiles
-      const int len = k ? ((n + k - 1) / k + kSsmTile - 1) / kSsmTile * kSsmTile : 0;
-      for (int j = 0; j < k; ++j) {
-        SsmSeg s;
-        s.doc = i;
-        s.tok0 = t0 + min(n, j * len);
-        s.ntok = min(n, (j + 1) * len) - min(n, j * len);
-        s.first = j == 0;
-        s.last = j == k - 1;
-        s.src = j > 0 || src >= p.n_init ? -2 : src;
-        s.need = p.bwd || j < k - 1 || (__ldcg(&p.kind[i]) & kDocSource);
-        s.pad = 0;
-        p.segs[at + j] = s;
+      if (k <= 8) {
+        for (int j = 0; j < k; ++j) cut(i, at, j, k);
+      } else {
+        const int l = atomicAdd(&s_long, 1);  // in any order: their places are fixed
+        s_doc[l] = i, s_at[l] = at, s_k[l] = k;
       }
     }
+    __syncthreads();
+    for (int l = 0; l < s_long; ++l)  // long ones by all threads
+      for (int j = tid; j < s_k[l]; j += kPlanThreads) cut(s_doc[l], s_at[l], j, s_k[l]);
     __syncthreads();
     if (tid == 0) s_base += s_warp[31];
     __syncthreads();

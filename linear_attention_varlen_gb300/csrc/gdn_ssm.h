@@ -55,7 +55,12 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   const int Sp = ssm_padded(S);
   const int ch = ssm_walk_channels(Sp);
   const int64_t blocks = (int64_t)G * ((C / G + ch - 1) / ch), each = ((int64_t)T * blocks + kSsmFill - 1) / kSsmFill;
-  const int64_t most = each < T ? each : T, len = (most + kSsmTile - 1) / kSsmTile * kSsmTile;
+  // With few channels segments could be shorter than they are worth: a walk takes about 0.3 us a token, the scan over a
+  // document's segments 1 us for sixteen. Documents are taken to be up to four times as long as the mean.
+  const int64_t doc = 4 * (int64_t)T / N < T ? 4 * (int64_t)T / N : T;
+  int64_t worth = kSsmMinSeg;
+  while (5 * worth * worth < doc) worth += kSsmTile;
+  const int64_t most = each > worth ? each : worth, len = ((most < T ? most : T) + kSsmTile - 1) / kSsmTile * kSsmTile;
   L.seg_tokens = (int)(len < kSsmMinSeg ? kSsmMinSeg : len);
   L.smax = N + (int64_t)T / L.seg_tokens;
   L.tiles = L.smax + T / kSsmTile + 1;
