@@ -662,10 +662,8 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32), 5), 256, 0, s, p);
   const unsigned cb = (unsigned)((C + 255) / 256), db = (unsigned)(N < 64 ? N : 64);
   if (dfinal_tail || init_idx) launch_early(act_ends_kernel<0>, dim3(cb, db), 256, 0, s, p);
-  if (init_idx) {
-    launch_early(act_ends_kernel<1>, dim3(cb, db), 256, 0, s, p);
-    launch_early(act_ends_kernel<2>, dim3(cb, 1), 256, 0, s, p);
-  }
+  if (init_idx && N > 1) launch_early(act_ends_kernel<1>, dim3(cb, db), 256, 0, s, p);
+  if (init_idx && N > 2) launch_early(act_ends_kernel<2>, dim3(cb, 1), 256, 0, s, p);  // a fork of a fork is a third
   if (n_init > 0 && init_idx) {
     const int64_t blocks = ((int64_t)N * 3 * C + 255) / 256;
     launch_early(act_pool_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, s, p);

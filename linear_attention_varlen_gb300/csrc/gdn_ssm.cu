@@ -13,7 +13,7 @@
 //     k_t = c_t dy_t + exp(dt_{t+1} a) k_{t+1},  dc = dy h,  db = dt x k,  du = sum_s k b  (u = dt x),
 //     d dt = x du + sum_s a k exp(dt a) h_{t-1},  da = sum_t dt k exp(dt a) h_{t-1}
 // the first walk also leaves the gradient of each segment's start state for a zero gradient behind it
-// (sum_t exp(a (dt_1 + .. + dt_t)) c_t dy_t, formed forward in time) and the state at every 16th token, so that the
+// (sum_t exp(a (dt_1 + .. + dt_t)) c_t dy_t, formed forward in time) and the state at every 16th (8th) token, so that the
 // walk in reverse needs no state but a tile's.
 //
 // What bounds it is the rate of instructions: the recurrence alone, 32 exponentials and 48 packed products for a token of
@@ -23,7 +23,7 @@
 //     32768 x 2048, one document      walks 203 + 298 us, planner and scan 21; its bytes once would take 81
 //     9001 x 2048, 12 documents       walks 64 + 94 us
 //     backward, 16384 x 2048          first walk 179 us, walk in reverse 594, planner, scan and sums 33; bytes once 71
-//     backward, 1501 x 768 x 8 fp32   10 + 36 us, planner, scan and sums 24
+//     backward, 1501 x 768 x 8 fp32   10 + 31 us, planner, scan and sums 30
 //
 // Every sum has a fixed order.
 #include <cuda_bf16.h>
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
     // a document's segment j of k, equal ones in whole tiles
     auto cut = [&](int doc, int first, int j, int k) {
       const int t0 = p.cu[doc], n = p.cu[doc + 1] - t0, src = p.init_idx ? p.init_idx[doc] : -1;
-      const int len = ((n + k - 1) / k + kSsmTile - 1) / kSsmTile * kSsmTile;
+      const int len = ((n + k - 1) / k + kSsmSegStep - 1) / kSsmSegStep * kSsmSegStep;
       SsmSeg s;
       s.doc = doc;
       s.tok0 = t0 + min(n, j * len);
@@ -416,8 +416,9 @@ __global__ void __launch_bounds__(32 * kSsmWarps, kMode == kWalkGrad ? 2 : 4)
       }
     for (int i0 = 0, it = 0; i0 < sg.ntok; i0 += kTb, ++it) {
       if constexpr (kMode == kWalkGrad) {
-        if (i0 % kSsmTile == 0 && nch > 0) {
-          const int64_t tile = sg.tok0 / kSsmTile + seg + i0 / kSsmTile;
+        constexpr int kTile = ssm_tile(kSp);
+        if (i0 % kTile == 0 && nch > 0) {
+          const int64_t tile = sg.tok0 / kTile + seg + i0 / kTile;
 #pragma unroll
           for (int d = 0; d < kDt; ++d) {
             if (d >= nch) break;
@@ -660,17 +661,18 @@ __global__ void __launch_bounds__(kScanThreads) ssm_scan_kernel(const __grid_con
 template <typename T, int kSp, bool kVec>
 struct GradSmem {
   static constexpr int kNl = kSp / 4, kDl = 32 / kNl, kCh = 4 * kDl, kCtaCh = kSsmWarps * kCh;
+  static constexpr int kTile = ssm_tile(kSp);
   static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;  // two CTAs to an SM either way
-  using R = Rows<T, kCtaCh, kSsmTile, 32 * kSsmWarps, kVec>;
-  uint8_t raw[kStages][4][kSsmTile * R::kBytes];  // x, dt, z, dout
-  float maps[kStages][kSsmTile][2 * kSp];
-  float part[kSsmWarps][kSsmTile][2 * kSp];       // db and dc of each warp's channels
+  using R = Rows<T, kCtaCh, kTile, 32 * kSsmWarps, kVec>;
+  uint8_t raw[kStages][4][kTile * R::kBytes];  // x, dt, z, dout
+  float maps[kStages][kTile][2 * kSp];
+  float part[kSsmWarps][kTile][2 * kSp];       // db and dc of each warp's channels
   float bias[kSsmWarps][kCh], skip[kSsmWarps][kCh];
-  float delta[kSsmWarps][kSsmTile][kCh];
-  float u[kSsmWarps][kSsmTile][kCh];   // then sum_s b k
-  float dy[kSsmWarps][kSsmTile][kCh];  // then sum_s a k exp(dt a) h_{t-1}
-  float y[kSsmWarps][kSsmTile][kCh];
-  float4 keep[kSsmWarps][kSsmTile / kGradSub][4][32];
+  float delta[kSsmWarps][kTile][kCh];
+  float u[kSsmWarps][kTile][kCh];   // then sum_s b k
+  float dy[kSsmWarps][kTile][kCh];  // then sum_s a k exp(dt a) h_{t-1}
+  float y[kSsmWarps][kTile][kCh];
+  float4 keep[kSsmWarps][kTile / kGradSub][4][32];
 };
 
 // v[0 .. kN - 1] of two lanes that differ in `mask` become the sums of the first half in the one without the bit, of
@@ -688,7 +690,7 @@ template <typename T, int kSp, bool kVec>
 __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __grid_constant__ SsmParams p) {
   using Smem = GradSmem<T, kSp, kVec>;
   using R = typename Smem::R;
-  constexpr int kNl = Smem::kNl, kDl = Smem::kDl, kCh = Smem::kCh, kQ = kSp / 4, kTb = kSsmTile, kStages = Smem::kStages;
+  constexpr int kNl = Smem::kNl, kDl = Smem::kDl, kCh = Smem::kCh, kQ = kSp / 4, kTb = Smem::kTile, kStages = Smem::kStages;
   constexpr int kCl = kNl >= 4 ? 1 : 2;  // channels whose sums a lane ends up with
   extern __shared__ __align__(16) uint8_t raw_smem[];
   Smem& sm = *reinterpret_cast<Smem*>(raw_smem);
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(32 * kSsmWarps, 2) ssm_grad_kernel(const __gri
       // the state before the tile: kept from zero, and what is left of the segment's start state
       uint64_t h[4][2];
       {
-        const int64_t tl = sg.tok0 / kSsmTile + seg + tile;
+        const int64_t tl = sg.tok0 / kTb + seg + tile;
         float4 kept[4], start[4];
         float time[4];
 #pragma unroll
@@ -1264,8 +1266,8 @@ void launch_scan(const SsmParams& p, cudaStream_t s) {
   const unsigned gx = (unsigned)(((int64_t)ssm_padded(p.S) / 4 * p.C + kScanThreads - 1) / kScanThreads), gy = (unsigned)(p.N < 64 ? p.N : 64);
   launch_early(ssm_scan_kernel<0>, dim3(gx, gy), kScanThreads, 0, s, p);
   if (!p.init_idx) return;
-  launch_early(ssm_scan_kernel<1>, dim3(gx, gy), kScanThreads, 0, s, p);
-  launch_early(ssm_scan_kernel<2>, dim3(gx, 1), kScanThreads, 0, s, p);
+  if (p.N > 1) launch_early(ssm_scan_kernel<1>, dim3(gx, gy), kScanThreads, 0, s, p);
+  if (p.N > 2) launch_early(ssm_scan_kernel<2>, dim3(gx, 1), kScanThreads, 0, s, p);  // a fork of a fork is a third
 }
 
 template <typename T, int kSp, bool kVec>

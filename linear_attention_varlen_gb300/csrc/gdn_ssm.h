@@ -10,8 +10,11 @@
 
 namespace gdn {
 
-constexpr int kSsmTile = 16;     // tokens between two states that the backward keeps
-constexpr int kSsmMinSeg = 16;   // shortest segment, a multiple of the tile
+constexpr int kSsmSegStep = 16;  // segments are multiples of it, of one at least
+// Tokens between two states that the backward keeps, and a tile of its walk in reverse. Eight states or fewer go with twice
+// the channels to a warp, and half the tile lets two CTAs share an SM.
+__host__ __device__ constexpr int ssm_tile(int Sp) { return Sp <= 8 ? 8 : 16; }
+static_assert(kSsmSegStep % ssm_tile(8) == 0 && kSsmSegStep % ssm_tile(16) == 0, "segments are whole tiles");
 // Warps of a walk that segments are cut for, sixteen to each SM (that is what an SM holds forward; the arithmetic's
 // rate bounds the walks, so that a few more than fit cost nothing, and long segments of ragged documents leave SMs idle:
 // at most as many as fit took 203 instead of 187 us for 9001 tokens of 12 documents).
@@ -58,12 +61,12 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   // With few channels segments could be shorter than they are worth: a walk takes about 0.3 us a token, the scan over a
   // document's segments 1 us for sixteen. Documents are taken to be up to four times as long as the mean.
   const int64_t doc = 4 * (int64_t)T / N < T ? 4 * (int64_t)T / N : T;
-  int64_t worth = kSsmMinSeg;
-  while (5 * worth * worth < doc) worth += kSsmTile;
-  const int64_t most = each > worth ? each : worth, len = ((most < T ? most : T) + kSsmTile - 1) / kSsmTile * kSsmTile;
-  L.seg_tokens = (int)(len < kSsmMinSeg ? kSsmMinSeg : len);
+  int64_t worth = kSsmSegStep;
+  while (5 * worth * worth < doc) worth += kSsmSegStep;
+  const int64_t most = each > worth ? each : worth, len = ((most < T ? most : T) + kSsmSegStep - 1) / kSsmSegStep * kSsmSegStep;
+  L.seg_tokens = (int)(len < kSsmSegStep ? kSsmSegStep : len);
   L.smax = N + (int64_t)T / L.seg_tokens;
-  L.tiles = L.smax + T / kSsmTile + 1;
+  L.tiles = L.smax + T / ssm_tile(Sp) + 1;
   const int per = kSsmWarps * ssm_grad_channels(Sp);
   L.parts = (C / G + per - 1) / per;
   const size_t state = (size_t)C * Sp * sizeof(float);
