@@ -1,4 +1,5 @@
-// Elements in memory (bf16, fp16, fp32) and the fp32 values they stand for; the activation SiLU and its slope.
+// What the state-space block's kernels share: elements in memory (bf16, fp16, fp32) and the fp32 values they stand for,
+// asynchronous copies, SiLU, its slope and softplus in packed pairs, how documents fork and share pool entries.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,19 +34,7 @@ template <typename T, int K>
 struct alignas(sizeof(T) * K > 16 ? 16 : sizeof(T) * K) Pack {
   T t[K];
 };
-// Elements p[0 .. K - 1], of which the first `n` exist (zero behind them). kVec: p is aligned to the pack, and n is
-// K or 0.
-template <typename T, int K, bool kVec>
-__device__ __forceinline__ Pack<T, K> load_pack(const T* p, int n) {
-  Pack<T, K> r;
-  if (kVec && n >= K) {
-    r = *reinterpret_cast<const Pack<T, K>*>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < K; ++i) r.t[i] = i < n ? p[i] : from_float<T>(0.f);
-  }
-  return r;
-}
+// Its elements to p[0 .. n - 1]. kVec: p is aligned to the pack, and n is K or 0.
 template <typename T, int K, bool kVec>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, K>& r, int n) {
   if (kVec && n >= K) {
@@ -99,7 +88,7 @@ __device__ __forceinline__ bool fork_kinds(const int32_t* init_idx, int N, int n
 }
 
 // Documents that start from the same entry of a pool, as chains in their order: link[d] = {the next one or -1, whether d
-// is the first}. One warp a document, warp `warp` of `warps`; what the pool's entries gather is set to zero on the way.
+// is the first}. One warp a document, warp `warp` of `warps`.
 __device__ __forceinline__ void link_pool_starts(const int32_t* init_idx, int N, int n_init, int2* link, int64_t warp, int64_t warps) {
   const int lane = threadIdx.x & 31;
   for (int64_t d = warp; d < N; d += warps) {
@@ -131,15 +120,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 1 / (1 + e^-x): exact at the ends (0, 1), NaN stays NaN
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + exp2_approx(-kLog2e * x)); }
-// x sigmoid(x); its limit 0 for x = -inf
-__device__ __forceinline__ float silu_of(float x, float sig) { return sig == 0.f ? 0.f : x * sig; }
-// d silu / dx = sig (1 + x (1 - sig)); its limits 0 and 1 at the infinities
-__device__ __forceinline__ float silu_slope(float x, float sig) {
-  return sig == 0.f || sig == 1.f ? sig : sig * fmaf(x, 1.f - sig, 1.f);
-}
-
 // 16 bytes of elements, kept as words until they are used: pair i of them, and its place taken by two values rounded.
 struct alignas(16) Words {
   uint32_t w[4];
@@ -228,6 +208,7 @@ __device__ __forceinline__ void set_element(Words& r, int i, T v) {
 __device__ __forceinline__ uint64_t f2_dup(float v) { return bw::f2_pack(v, v); }
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) { return bw::f2_pack(exp2_approx(bw::f2_lo(x)), exp2_approx(bw::f2_hi(x))); }
 __device__ __forceinline__ uint64_t rcp_pair(uint64_t x) { return bw::f2_pack(rcp_approx(bw::f2_lo(x)), rcp_approx(bw::f2_hi(x))); }
+// 1 / (1 + e^-x): exact at the ends (0, 1), NaN stays NaN
 __device__ __forceinline__ uint64_t sigmoid_pair(uint64_t x) {
   return rcp_pair(bw::f2_add(exp2_pair(bw::f2_mul(x, f2_dup(-kLog2e))), f2_dup(1.f)));
 }
@@ -261,6 +242,5 @@ __device__ __forceinline__ uint64_t softplus_pair(uint64_t r) {
   p = bw::f2_fma(p, q, f2_dup(0.333332121f));
   return bw::f2_add(bw::f2_pack(fmaxf(lo, 0.f), fmaxf(hi, 0.f)), bw::f2_fma(bw::f2_mul(t, q), p, t));
 }
-__device__ __forceinline__ float softplus(float r) { return bw::f2_lo(softplus_pair(bw::f2_pack(r, 0.f))); }
 
 }  // namespace gdn

@@ -164,11 +164,10 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
       s.doc = doc;
       s.tok0 = t0 + min(n, j * len);
       s.ntok = min(n, (j + 1) * len) - min(n, j * len);
-      s.first = j == 0;
       s.last = j == k - 1;
       s.src = j > 0 || src >= p.n_init ? -2 : src;
       s.need = p.bwd || j < k - 1 || (__ldcg(&p.kind[doc]) & kDocSource);
-      s.pad = 0;
+      s.pad[0] = s.pad[1] = 0;
       p.segs[first + j] = s;
     };
     if (tid == 0) s_long = 0;

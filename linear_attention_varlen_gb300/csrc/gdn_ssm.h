@@ -24,10 +24,10 @@ constexpr int kSsmMaxState = 64;
 // A segment: consecutive tokens of one document that one warp walks for its channels.
 struct SsmSeg {
   int32_t doc, tok0, ntok;
-  int32_t first, last;  // of its document
+  int32_t last;         // of its document
   int32_t src;          // state before it: -1 zero, >= 0 pool entry, -2 its slot
   int32_t need;         // the end state from zero is needed
-  int32_t pad;
+  int32_t pad[2];
 };
 
 struct SsmHeader {
