@@ -368,7 +368,8 @@ enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* u / (1 + e^-u) */ };
  *   y and dx are contiguous
  *   w : fp32 [C, 4] on a 16-byte boundary; everything else as for gdn_conv_fwd / gdn_conv_bwd, dx in fp32
  * u is formed in fp32, y rounded once; the backward forms u again. Sums have a fixed order. Rows of the
- * outputs that no document holds do not exist: cu_seqlens ends at T.
+ * outputs that no document holds do not exist: cu_seqlens ends at T. No output overlaps an input (final_tail
+ * not conv_init either).
  */
 size_t gdn_conv_act_workspace_size(int N, int T, int C, int backward);
 int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w, const float* bias, const int32_t* cu_seqlens,
@@ -412,7 +413,8 @@ int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const 
  * document (and its forks), within it in its channel, but for db and dc, which sum over channels, and in the
  * backward the sums over documents.
  * workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned; bad cu_seqlens / init_idx are reported in its
- * status word (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd.
+ * status word (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd. No output overlaps
+ * an input (final_state not initial_state either).
  */
 size_t gdn_ssm_workspace_size(int N, int T, int C, int S, int G, int backward);
 int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,
