@@ -11,7 +11,7 @@
 // gradient, in registers, the next rows' vectors on their way into each thread's own places in shared memory. The gate is
 // formed once, in packed pairs. Measured (device time, bf16):
 //     forward, 16384 x 64 groups of 128     126 us (805 MB, 6.4 TB/s; 179 us with loads at their use)
-//     backward, 32768 x 2048                129 us (671 MB, 5.2 TB/s; 207 us), the sum over the teams 8
+//     backward, 32768 x 2048                112 us (671 MB, 6.0 TB/s; 207 us), the sum over the teams 8
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -249,9 +249,11 @@ __global__ void __launch_bounds__(kMaxTeam) gnorm_fwd_kernel(const __grid_consta
 
 // Either order: the sum of u w dn and dw are those of x gate w dy and x gate dy rs. Up to eight elements a thread, the
 // weights and the row stay in registers; longer shares take both again. Rows ahead are on their way into shared memory
-// where that holds enough of them, else a row's second reading comes from L2.
-template <typename T, int kNv, bool kVec, bool kGateFirst>
-__global__ void __maxnreg__(kNv* kElems<T> <= 8 ? 96 : 128) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
+// where that holds enough of them, else a row's second reading comes from L2. kRegs: teams of less than a warp have more
+// rows under way with fewer registers (8192 x 64 groups of 128: 5.1 against 4.7 TB/s with 128), the others rather not
+// (32768 x 2048: 4.9 against 5.6).
+template <typename T, int kNv, bool kVec, bool kGateFirst, int kRegs>
+__global__ void __maxnreg__(kRegs) gnorm_bwd_kernel(const __grid_constant__ GnormParams p, int L) {
   constexpr int K = kElems<T>, P = kPairs<T>;
   constexpr bool kKeep = kNv * K <= 8;
   constexpr int kStages = bwd_stages<T, kNv, kVec>();
@@ -510,7 +512,7 @@ void by_share(int nv, F f) {
 // Shared memory beyond the default limit.
 template <typename K>
 bool allow_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ||
+  return bytes <= 40 * 1024 ||
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
@@ -590,8 +592,16 @@ extern "C" int gdn_gated_rmsnorm_bwd(const void* x, int64_t x_stride, const void
       using T_ = decltype(t);
       by_share<T_>(s.nv, [&](auto n) {
         constexpr int kNv = decltype(n)::value;
-        auto* kernel = p.gate_first ? (vec ? gnorm_bwd_kernel<T_, kNv, true, true> : gnorm_bwd_kernel<T_, kNv, false, true>)
-                                    : (vec ? gnorm_bwd_kernel<T_, kNv, true, false> : gnorm_bwd_kernel<T_, kNv, false, false>);
+        auto pick = [&](auto regs) {
+          constexpr int kRegs = decltype(regs)::value;
+          return p.gate_first
+                     ? (vec ? gnorm_bwd_kernel<T_, kNv, true, true, kRegs> : gnorm_bwd_kernel<T_, kNv, false, true, kRegs>)
+                     : (vec ? gnorm_bwd_kernel<T_, kNv, true, false, kRegs> : gnorm_bwd_kernel<T_, kNv, false, false, kRegs>);
+        };
+        auto* kernel = pick(Int<128>{});
+        if constexpr (kNv == 1) {
+          if (s.L < 32) kernel = pick(Int<96>{});
+        }
         const size_t ring = vec ? Ring<3, kNv, bwd_stages<T_, kNv, true>()>::bytes(s.threads) : 0;
         ok = allow_smem(kernel, ring);
         if (ok) kernel<<<(unsigned)s.ctas, s.threads, ring, (cudaStream_t)stream>>>(p, s.L);
