@@ -10,7 +10,7 @@
 // of a warp, a warp or a CTA) takes one group of columns down the rows with its weights, and in the backward their
 // gradient, in registers, the next rows' vectors on their way into each thread's own places in shared memory. The gate is
 // formed once, in packed pairs. Measured (device time, bf16):
-//     forward, 16384 x 64 groups of 128     126 us (805 MB, 6.4 TB/s; 179 us with loads at their use)
+//     forward, 16384 x 64 groups of 128     120 us (805 MB, 6.7 TB/s; 179 us with loads at their use)
 //     backward, 32768 x 2048                112 us (671 MB, 6.0 TB/s; 207 us), the sum over the teams 8
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -142,10 +142,11 @@ __device__ __forceinline__ void team_sum(float (&v)[kN], int L, Sums<kN> (*buf)[
   turn ^= 1;
 }
 
-// Rows in flight for a thread, this one's included (0: read when they are needed).
+// Rows in flight for a thread, this one's included (0: read when they are needed). With four in the forward the same
+// bytes came at 5.5 TB/s instead of 6.2: the reads and writes under way lie further apart.
 template <typename T, int kNv, bool kVec>
 __host__ __device__ constexpr int fwd_stages() {
-  return !kVec ? 0 : kNv == 1 ? 4 : kNv == 2 ? 2 : 0;
+  return !kVec || kNv > 2 ? 0 : 2;
 }
 template <typename T, int kNv, bool kVec>
 __host__ __device__ constexpr int bwd_stages() {
@@ -444,7 +445,7 @@ Shape shape_of(int n, int64_t T, int ng, int es, bool vec, int sms, int threads_
   s.nv = next_pow2((nvec + L - 1) / L);
   s.threads = L > 32 ? L : kWarpTeamThreads;
   const int64_t teams = (int64_t)sms * threads_per_sm / L;  // resident
-  int64_t rows = (teams + ng - 1) / ng;
+  const int64_t rows = teams / ng;  // no more than are resident: a few more would take a second turn
   s.rows = rows < 1 ? 1 : rows > T ? T : rows;
   s.ctas = (s.rows * ng * L + s.threads - 1) / s.threads;
   return s;
