@@ -363,7 +363,7 @@ enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* u / (1 + e^-u) */ };
 /*
  * The short convolution of gdn_conv_fwd with its activation, in three types and with rows apart:
  *     u[p] = bias[c] + sum_m w[c][m] E[p + m],  y[p] = act(u[p]),  E and final_tail as there.
- *   x, dy, y, conv_init, final_tail : of `dtype`; C a multiple of 8, up to 2^24
+ *   x, dy, y, conv_init, final_tail : of `dtype`; C a multiple of 8, up to 2^23
  *   x_stride, dy_stride : elements from one token to the next (0 = contiguous), rows on 16-byte boundaries;
  *   y and dx are contiguous
  *   w : fp32 [C, 4] on a 16-byte boundary; everything else as for gdn_conv_fwd / gdn_conv_bwd, dx in fp32

@@ -491,7 +491,7 @@ def conv_fwd(x, w, cu_seqlens, bias=None, init_idx=None, conv_init=None, y=None,
     Returns (y [T, C] bf16, final_tail [N, 3, C] bf16).
 
     With activation "silu" (or "none") x may be fp16 or fp32 too and its tokens apart (a view into a
-    projection), C is at most 2^24, and y, conv_init and final_tail are of x's type; the workspace is then
+    projection), C is at most 2^23, and y, conv_init and final_tail are of x's type; the workspace is then
     conv_workspace_size(..., activation=activation) bytes."""
     torch = _torch()
     empty = torch.empty if stream is None else _empty_on(stream)

@@ -9,8 +9,8 @@
 // before a block of tokens (and the three behind it in the backward). A thread takes four channels, in packed pairs, down
 // the tokens of a block, the window of three inputs in registers; four rows at a time are worked on while the next four
 // are on their way. Four rows of one document go without a look at its bounds.
-// Measured (device time, bf16): 32768 x 2048 51 us (269 MB, 5.2 TB/s); backward of 16384 x 4096 109 us (537 MB, 4.9 TB/s;
-// four CTAs an SM, five spill: 200 us), sum over its blocks 7, tails 9; step of 200 x 8192 in fp16 9 us. Eight channels
+// Measured (device time, bf16): 32768 x 2048 51 us (269 MB, 5.2 TB/s); backward of 16384 x 4096 101 us (537 MB, 5.3 TB/s; sixteen
+// warps an SM, twenty spill: 200 us), sum over its blocks 6, tails 12; step of 200 x 8192 in fp16 9 us. Eight channels
 // to a thread without packed pairs took 79 and 227 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +28,13 @@ namespace gdn {
 namespace {
 
 constexpr int kActThreads = 128;
-constexpr int kFwdTokens = 32, kBwdTokens = 64;  // tokens to a block
+constexpr int kFwdTokens = 32;                   // tokens to a block
+constexpr int kBwdThreads = 64;
+// Tokens to a block of the backward: few enough for small calls to spread, else 124. Blocks a power of two of rows
+// apart meet in memory: 64 took 128, 96 took 126 and 124 took 116 us at 16384 x 4096.
+inline int bwd_tokens(int T, int C) {
+  return (int64_t)(T / 124) * ((C / 4 + kBwdThreads - 1) / kBwdThreads) >= 8 * 152 ? 124 : 60;
+}
 constexpr int kRows = 4;                         // rows at a time
 constexpr int kCh = 4, kPr = kCh / 2;             // channels of a thread, and their pairs
 
@@ -50,7 +56,7 @@ struct ActParams {
   const float *w, *bias;
   const int32_t *cu, *init_idx;
   const void* conv_init;
-  int N, T, C, n_init, silu, n_tb;
+  int N, T, C, n_init, silu, n_tb, tokens;
   void *y, *tail;
   const float* dtail;  // given gradient of the tails
   float *dx, *dw, *dbias, *dinit;
@@ -62,7 +68,7 @@ struct ActParams {
 
 struct ActLayout {
   size_t header, kind, dstart, part, link, total;
-  int n_tb;
+  int n_tb, tokens;
 };
 inline ActLayout act_layout(int N, int T, int C, bool bwd) {
   ActLayout L{};
@@ -72,8 +78,8 @@ inline ActLayout act_layout(int N, int T, int C, bool bwd) {
     o = align_up(o + b, 256);
     return at;
   };
-  const int per = bwd ? kBwdTokens : kFwdTokens;
-  L.n_tb = (T + per - 1) / per;
+  L.tokens = bwd ? bwd_tokens(T, C) : kFwdTokens;
+  L.n_tb = (T + L.tokens - 1) / L.tokens;
   L.header = take(sizeof(ActHeader));
   if (bwd) {
     L.dstart = take((size_t)N * 3 * C * 4);     // gradient at each document's start
@@ -269,17 +275,17 @@ __global__ void __launch_bounds__(kActThreads) act_fwd_kernel(const __grid_const
   }
 }
 
-// Blocks of kBwdTokens tokens. du runs up the tokens once; the gradient of an input is complete three tokens later, so a
+// Blocks of p.tokens tokens. du runs up the tokens once; the gradient of an input is complete three tokens later, so a
 // block goes three tokens beyond its own (as far as its last document) and leaves dw and dbias of those to the next.
 template <typename T>
-__global__ void __launch_bounds__(kActThreads) act_bwd_kernel(const __grid_constant__ ActParams p) {
+__global__ void __launch_bounds__(kBwdThreads) act_bwd_kernel(const __grid_constant__ ActParams p) {
   using P = Raw4<T>;
   bw::griddep_wait();
   bw::griddep_launch_dependents();
   if (p.hd->status != 0) return;
-  const int c = (blockIdx.y * kActThreads + threadIdx.x) * kCh;
+  const int c = (blockIdx.y * kBwdThreads + threadIdx.x) * kCh;
   if (c >= p.C) return;
-  const int t0 = blockIdx.x * kBwdTokens, t1 = min(t0 + kBwdTokens, p.T), stop = min(p.T, t1 + 3);
+  const int t0 = blockIdx.x * p.tokens, t1 = min(t0 + p.tokens, p.T), stop = min(p.T, t1 + 3);
   const T *x = static_cast<const T*>(p.x) + c, *dy = static_cast<const T*>(p.dy) + c;
   P xn[kRows], gn[kRows];
   auto fetch = [&](int t) {
@@ -556,7 +562,7 @@ int check_kind(int dtype, int activation) {
 
 // Block counts and the token loops' bounds stay within 31 bits.
 bool sizes_ok(int N, int T, int C) {
-  return N >= 1 && N <= (1 << 30) && T >= 0 && T <= INT32_MAX - 4096 && C >= 8 && C <= (1 << 24) && C % 8 == 0 &&
+  return N >= 1 && N <= (1 << 30) && T >= 0 && T <= INT32_MAX - 4096 && C >= 8 && C <= (1 << 23) && C % 8 == 0 &&
          (int64_t)T * C <= ((int64_t)1 << 40);
 }
 
@@ -613,6 +619,7 @@ extern "C" int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w,
   if ((rc = check_device(workspace, ptrs, (int)(sizeof(ptrs) / sizeof(ptrs[0])), guard)) != GDN_OK) return rc;
   p.hd = static_cast<ActHeader*>(workspace);
   p.n_tb = L.n_tb;
+  p.tokens = L.tokens;
   cudaStream_t s = (cudaStream_t)stream;
   launch_early(act_check_kernel, dim3(1), 256, 0, s, p);
   by_type(dtype, [&](auto t) {
@@ -650,14 +657,15 @@ extern "C" int gdn_conv_act_bwd(const void* x, int64_t x_stride, const float* w,
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.link = reinterpret_cast<int2*>(ws + L.link);
   p.n_tb = L.n_tb;
+  p.tokens = L.tokens;
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t zeros = n_init > 0 ? ((int64_t)n_init * 3 * C + 32 * (int64_t)N + 1023) / 1024 : 0;  // blocks
   launch_early(act_check_kernel, dim3((unsigned)(1 + (zeros < 1024 ? zeros : 1024))), 256, 0, s, p);
   if (T > 0)
     by_type(dtype, [&](auto t) {
       using T_ = decltype(t);
-      const unsigned cb = (unsigned)((C / kCh + kActThreads - 1) / kActThreads);
-      launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kActThreads, 0, s, p);
+      const unsigned cb = (unsigned)((C / kCh + kBwdThreads - 1) / kBwdThreads);
+      launch_early(act_bwd_kernel<T_>, dim3((unsigned)L.n_tb, cb), kBwdThreads, 0, s, p);
     });
   launch_early(act_sum_kernel, dim3((unsigned)((C + 31) / 32), 5), 256, 0, s, p);
   const unsigned cb = (unsigned)((C + 255) / 256), db = (unsigned)(N < 64 ? N : 64);
@@ -677,7 +685,7 @@ extern "C" int gdn_conv_decode_step(const void* x, int64_t x_stride, const float
   using namespace gdn;
   int rc = check_kind(dtype, activation);
   if (rc != GDN_OK) return rc;
-  if (B < 0 || B > 65535 || C < 8 || C > (1 << 24) || C % 8 != 0 || n_pool < 0) return GDN_ERR_INVALID_ARG;
+  if (B < 0 || B > 65535 || C < 8 || C > (1 << 23) || C % 8 != 0 || n_pool < 0) return GDN_ERR_INVALID_ARG;
   if (!stride_ok(&x_stride, C, dtype)) return GDN_ERR_INVALID_ARG;
   if (B == 0) return GDN_OK;
   if (!x || !w || !state_idx || !tail_pool || !y || n_pool == 0) return GDN_ERR_INVALID_ARG;

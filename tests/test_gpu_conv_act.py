@@ -203,3 +203,22 @@ def test_the_same_bits_every_time():
     for _ in range(3):
         again = gdn.conv_bwd(d["x"], d["w"], d["cu"], d["dy"], dfinal_tail=d["dtail"], **kw)
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_backward_of_a_large_batch_as_of_its_documents():
+    """Enough rows for the backward's longer blocks: dx has the bits of calls on one document each (their blocks are
+    shorter), dw and dbias differ by the order of their sums, 12000 roundings of 2^-24 of the terms."""
+    lens, C = [5000, 1, 3499, 0, 3500], 4096
+    d = inputs(21, lens, C, "bf16")
+    g = gdn.conv_bwd(d["x"], d["w"], d["cu"], d["dy"], bias=d["bias"], dfinal_tail=d["dtail"], activation="silu")
+    dw, db, size, t = 0.0, 0.0, 0.0, 0
+    for i, n in enumerate(lens):
+        if n == 0:
+            continue
+        a = gdn.conv_bwd(d["x"][t:t + n], d["w"], int32([0, n]), d["dy"][t:t + n], bias=d["bias"],
+                         dfinal_tail=d["dtail"][i:i + 1], activation="silu")
+        assert torch.equal(g["dx"][t:t + n], a["dx"])
+        dw, db, t = dw + a["dw"].double(), db + a["dbias"].double(), t + n
+    size = 12000 ** 0.5 * 12  # of sums of 12000 products of normal values, none of them above this by far
+    assert float((g["dw"].double() - dw).abs().max()) <= 12000 * 2.0 ** -24 * size
+    assert float((g["dbias"].double() - db).abs().max()) <= 12000 * 2.0 ** -24 * size

@@ -92,7 +92,7 @@ def conv(lib, bwd=False, **kw):
 
 @pytest.mark.parametrize("bwd", [False, True])
 def test_convolution_refusals(lib, bwd):
-    for kw in (dict(N=0), dict(T=-1), dict(C=4), dict(C=12), dict(C=(1 << 24) + 8), dict(x=None), dict(w=None), dict(cu=None),
+    for kw in (dict(N=0), dict(T=-1), dict(C=4), dict(C=12), dict(C=(1 << 23) + 8), dict(x=None), dict(w=None), dict(cu=None),
                dict(ws=None), dict(n_init=1), dict(n_init=-1), dict(x=A + 8), dict(w=A + 4), dict(ws=A + 16), dict(xs=56),
                dict(xs=68), dict(xs=-64), dict(T=2 ** 31 - 1, C=8)):
         assert conv(lib, bwd, **kw) == gdn.GDN_ERR_INVALID_ARG, kw
