@@ -446,7 +446,8 @@ Shape shape_of(int n, int64_t T, int ng, int es, bool vec, int sms, int threads_
   s.threads = L > 32 ? L : kWarpTeamThreads;
   const int64_t teams = (int64_t)sms * threads_per_sm / L;  // resident
   const int64_t rows = teams / ng;  // no more than are resident: a few more would take a second turn
-  s.rows = rows < 1 ? 1 : rows > T ? T : rows;
+  s.rows = rows < 1 ? 1 : rows;
+  if (s.rows > T) s.rows = T;  // none for no rows: the sum of dw takes what the teams wrote
   s.ctas = (s.rows * ng * L + s.threads - 1) / s.threads;
   return s;
 }

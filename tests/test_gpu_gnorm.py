@@ -123,3 +123,14 @@ def test_no_rows():
     assert gdn.gated_rmsnorm_fwd(x, z, w, group=32).shape == (0, 64)
     dx, dz, dw = gdn.gated_rmsnorm_bwd(x, z, w, dy, group=32)
     assert dx.shape == (0, 64) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("group", [1, 128])
+def test_no_rows_of_more_groups_than_teams(shared, group):
+    D = 80000 if group == 1 else 128 * 5000  # 77824 threads to teams of one and of sixteen
+    x, z, w, dy = inputs(2, 0, D, group, "bf16", shared)
+    ws = torch.full((256 + 4 * D,), 63, dtype=torch.uint8, device="cuda")  # an earlier call's
+    dw = torch.full(w.shape, 5.0, device="cuda")
+    gdn.gated_rmsnorm_bwd(x, z, w, dy, group=group, workspace=ws, dw=dw)
+    assert (dw == 0).all() and gdn.workspace_status(ws) == gdn.GDN_OK
