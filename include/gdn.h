@@ -412,6 +412,7 @@ int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const 
  * NULL where skip and dt_bias are. Every sum has a fixed order (deterministic). A NaN or infinity stays in its
  * document (and its forks), within it in its channel, but for db and dc, which sum over channels, and in the
  * backward the sums over documents.
+ * Every array lies on a multiple of its elements' size: fp32 ones on 4 bytes beside 16-bit ones on 2.
  * workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned; bad cu_seqlens / init_idx are reported in its
  * status word (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd. No output overlaps
  * an input (final_state not initial_state either).

@@ -1118,7 +1118,8 @@ struct SsmCall {
   bool bwd;
 };
 
-int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p, SsmLayout* L, DeviceGuard& guard, int* sms) {
+// outs: the first n_typed of the call's type, the others fp32 (dfinal_state, an input, among them).
+int prepare(const SsmCall& c, const void* const* outs, int n_outs, int n_typed, SsmParams* p, SsmLayout* L, DeviceGuard& guard, int* sms) {
   if (c.dtype != GDN_DTYPE_BF16 && c.dtype != GDN_DTYPE_FP16 && c.dtype != GDN_DTYPE_FP32) return GDN_ERR_UNSUPPORTED;
   if (!sizes_ok(c.N, c.T, c.C, c.S, c.G) || c.n_init < 0) return GDN_ERR_INVALID_ARG;
   if (!c.a || !c.cu || !c.ws || (c.n_init > 0 && !c.init)) return GDN_ERR_INVALID_ARG;
@@ -1136,15 +1137,14 @@ int prepare(const SsmCall& c, const void* const* outs, int n_outs, SsmParams* p,
   for (const void* q : {(const void*)c.a, (const void*)c.skip, (const void*)c.dt_bias, (const void*)c.init, (const void*)c.cu,
                         (const void*)c.init_idx})
     if (!al(q, 4)) return GDN_ERR_INVALID_ARG;
+  for (int i = 0; i < n_outs; ++i)
+    if (!al(outs[i], i < n_typed ? es : 4)) return GDN_ERR_INVALID_ARG;
   if (!al(c.ws, 256)) return GDN_ERR_INVALID_ARG;
   *L = ssm_layout(c.N, c.T, c.C, c.S, c.G, c.bwd);
   if (c.ws_bytes < L->total) return GDN_ERR_WORKSPACE;
   const void* ptrs[24] = {c.x, c.dt, c.z, c.a, c.b, c.c, c.skip, c.dt_bias, c.cu, c.init_idx, c.init, c.dout};
   int n = 12;
-  for (int i = 0; i < n_outs; ++i) {
-    if (!al(outs[i], 4) && !al(outs[i], es)) return GDN_ERR_INVALID_ARG;
-    ptrs[n++] = outs[i];
-  }
+  for (int i = 0; i < n_outs; ++i) ptrs[n++] = outs[i];
   int dev = 0;
   if (device_of(c.ws, ptrs, n, &dev) != kOk) return GDN_ERR_INVALID_ARG;
   if (!guard.set(dev)) return GDN_ERR_CUDA;
@@ -1317,7 +1317,7 @@ extern "C" int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const f
   SsmLayout L;
   DeviceGuard guard;
   int sms = 0;
-  const int rc = prepare(call, outs, 2, &p, &L, guard, &sms);
+  const int rc = prepare(call, outs, 2, 1, &p, &L, guard, &sms);
   if (rc != GDN_OK) return rc;
   p.out = out;
   p.final_state = final_state;
@@ -1341,12 +1341,12 @@ extern "C" int gdn_ssm_bwd(const void* x, const void* dt, const void* z, const f
     return GDN_ERR_INVALID_ARG;
   const SsmCall call{x,       dt,          z,        a,             b,      c,    skip,      dt_bias,  cu_seqlens, N, T, C, S, G, dtype,
                      strides, dt_softplus, init_idx, initial_state, n_init, dout, workspace, ws_bytes, true};
-  const void* outs[] = {dx, ddt, dz, da, db, dc, dskip, ddt_bias, dinitial_state, dfinal_state};
+  const void* outs[] = {dx, ddt, dz, db, dc, da, dskip, ddt_bias, dinitial_state, dfinal_state};
   SsmParams p;
   SsmLayout L;
   DeviceGuard guard;
   int sms = 0;
-  const int rc = prepare(call, outs, 10, &p, &L, guard, &sms);
+  const int rc = prepare(call, outs, 10, 5, &p, &L, guard, &sms);
   if (rc != GDN_OK) return rc;
   p.dfinal = dfinal_state;
   p.dx = dx, p.ddt = ddt, p.dz = dz, p.db = db, p.dc = dc;

@@ -54,6 +54,25 @@ def test_scan_refusals(lib, bwd):
     assert gdn.ssm_workspace_size(1, 64, 64, 65) == 0 and gdn.ssm_workspace_size(1, 64, 65, 16, 2) == 0
 
 
+@pytest.mark.parametrize("dtype", [gdn.DTYPE_BF16, gdn.DTYPE_FP16, gdn.DTYPE_FP32])
+def test_scan_outputs_are_aligned_to_their_types(lib, dtype):
+    """Two bytes are enough for an output in 16 bits, not for one in fp32, whatever the inputs' type. The check comes before
+    the workspace's, which tells a call that passed it from one that did not."""
+    kw = dict(dtype=dtype, n_init=1, pool=A, idx=A, dinit=A, dfin=A, ws_bytes=0)
+    typed = {False: ("out",), True: ("dx", "ddt", "dz", "db", "dc")}
+    fp32 = {False: ("fin",), True: ("da", "dskip", "dbias", "dinit", "dfin")}
+    by_two = gdn.GDN_ERR_INVALID_ARG if dtype == gdn.DTYPE_FP32 else gdn.GDN_ERR_WORKSPACE
+    for bwd in (False, True):
+        assert ssm(lib, bwd, **kw) == gdn.GDN_ERR_WORKSPACE
+        for name in typed[bwd]:
+            assert ssm(lib, bwd, **(kw | {name: A + 1})) == gdn.GDN_ERR_INVALID_ARG, name
+            assert ssm(lib, bwd, **(kw | {name: A + 2})) == by_two, name
+        for name in fp32[bwd]:
+            for off in (1, 2, 3):
+                assert ssm(lib, bwd, **(kw | {name: A + off})) == gdn.GDN_ERR_INVALID_ARG, (name, off)
+            assert ssm(lib, bwd, **(kw | {name: A + 4})) == gdn.GDN_ERR_WORKSPACE, name
+
+
 def test_scan_workspace_holds_the_largest_call(lib):
     sizes = [gdn.ssm_workspace_size(n, t, 2048, 16, 1, True) for n, t in ((1, 1), (1, 16384), (4, 16384), (4, 32768))]
     assert sizes == sorted(sizes) and gdn.ssm_workspace_size(1, 0, 1, 1) > 0
