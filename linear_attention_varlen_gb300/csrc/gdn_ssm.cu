@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
     return;
   }
   const bool deep = fork_kinds(p.init_idx, p.N, p.n_init, p.kind);
-  const int L = p.seg_tokens;
+  const uint32_t L = p.seg_tokens;  // a document's tokens and a segment's more can pass 31 bits, not 32
   for (int i0 = 0; i0 < p.N; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const int k = i < p.N ? (p.cu[i + 1] - p.cu[i] + L - 1) / L : 0;
+    const int k = i < p.N ? ((uint32_t)(p.cu[i + 1] - p.cu[i]) + L - 1) / L : 0;
     int upto = k;  // inclusive sum over the warp, then over the block
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -158,12 +158,13 @@ __global__ void __launch_bounds__(kPlanThreads) ssm_plan_kernel(const __grid_con
     const int at = s_base + upto - k + (wid ? s_warp[wid - 1] : 0);
     // a document's segment j of k, equal ones in whole tiles
     auto cut = [&](int doc, int first, int j, int k) {
-      const int t0 = p.cu[doc], n = p.cu[doc + 1] - t0, src = p.init_idx ? p.init_idx[doc] : -1;
-      const int len = ((n + k - 1) / k + kSsmSegStep - 1) / kSsmSegStep * kSsmSegStep;
+      const int t0 = p.cu[doc], src = p.init_idx ? p.init_idx[doc] : -1;
+      const uint32_t n = p.cu[doc + 1] - t0, len = ((n + k - 1) / k + kSsmSegStep - 1) / kSsmSegStep * kSsmSegStep;
+      const uint32_t from = min(n, j * len), to = min(n, (j + 1) * len);
       SsmSeg s;
       s.doc = doc;
-      s.tok0 = t0 + min(n, j * len);
-      s.ntok = min(n, (j + 1) * len) - min(n, j * len);
+      s.tok0 = t0 + (int)from;
+      s.ntok = (int)(to - from);
       s.last = j == k - 1;
       s.src = j > 0 || src >= p.n_init ? -2 : src;
       s.need = p.bwd || j < k - 1 || (__ldcg(&p.kind[doc]) & kDocSource);

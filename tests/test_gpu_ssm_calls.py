@@ -215,3 +215,34 @@ def test_pools_of_many_entries():
     got, alone = run(pool, own.tolist()), run(pool[own.to("cuda")].contiguous(), list(range(N)))
     want = torch.zeros(N, 3, C, dtype=torch.float64, device="cuda").index_add_(0, own.to("cuda"), alone.double())
     torch.testing.assert_close(got.double(), want, rtol=2.0 ** -20, atol=2000 * 2.0 ** -24 * float(want.abs().max()))
+
+
+def test_a_document_of_almost_the_most_tokens():
+    """One channel and a document so long that its last segment's end, in whole tiles, lies beyond 31 bits. Tokens of zeros
+    have a step of zero, so they leave the state: what the others make of it, from the first segment to the last, is the
+    same as in a document of those alone."""
+    torch.cuda.empty_cache()
+    T = 2 ** 31 - 5000
+    if torch.cuda.mem_get_info()[0] < gdn.ssm_workspace_size(1, T, 1, 1) + (12 << 30):
+        pytest.skip("needs 160 GB of free memory")
+    marks = torch.tensor([0, 1, 20, 883023, 883024, T // 2, T - 900000, T - 883024, T - 3, T - 2, T - 1], device="cuda")
+    values = torch.linspace(0.2, 1.0, len(marks), device="cuda").bfloat16().unsqueeze(1)
+    v = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    v[marks] = values
+    a = torch.tensor([[-0.5]], device="cuda")
+    run = lambda x, **kw: gdn.ssm_scan_fwd(x, x, a, x.unsqueeze(2), x.unsqueeze(2), int32([0, x.shape[0]]),  # noqa: E731
+                                           dt_softplus=False, **kw)
+    want, wfin = run(values)
+    out = torch.full((T, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(gdn.ssm_workspace_size(1, T, 1, 1), dtype=torch.uint8, device="cuda")
+    _, fin = run(v, out=out, workspace=ws)
+    assert gdn.workspace_status(ws) == gdn.GDN_OK
+    got = out[marks].clone()
+    # each token's step rounds as often as in the short document (2^-21 a token); a state that is carried over a segment
+    # of zeros alone is multiplied by exp(0) = 1; an output rounded to bf16 may turn (2^-8 of it on either side)
+    torch.testing.assert_close(fin, wfin, rtol=len(marks) * 2.0 ** -20, atol=0)
+    torch.testing.assert_close(got.float(), want.float(), rtol=2.0 ** -7, atol=0)
+    out[marks] = 0
+    assert not out.any()
+    del v, out, ws
+    torch.cuda.empty_cache()
