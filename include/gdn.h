@@ -413,9 +413,10 @@ int gdn_conv_decode_step(const void* x, int64_t x_stride, const float* w, const 
  * document (and its forks), within it in its channel, but for db and dc, which sum over channels, and in the
  * backward the sums over documents.
  * Every array lies on a multiple of its elements' size: fp32 ones on 4 bytes beside 16-bit ones on 2.
- * workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned; bad cu_seqlens / init_idx are reported in its
- * status word (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd. No output overlaps
- * an input (final_state not initial_state either).
+ * workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned; the size grows with N and T, so the largest call's
+ * serves the smaller ones of a layer. Bad cu_seqlens / init_idx are reported in its status word
+ * (gdn_workspace_status). Ownership, stream and device rules as for gdn_chunk_fwd. No output overlaps an input
+ * (final_state not initial_state either).
  */
 size_t gdn_ssm_workspace_size(int N, int T, int C, int S, int G, int backward);
 int gdn_ssm_fwd(const void* x, const void* dt, const void* z, const float* a, const void* b, const void* c,

@@ -3,6 +3,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 
@@ -48,7 +50,8 @@ constexpr int kSsmWarps = 4;  // warps to a CTA
 // channels beside one another.
 struct SsmLayout {
   size_t header, segs, seg0, kind, link, maps, slot, sums, slot_r, ckpt, csum, dstart, fin, part_a, part_c, part_m, total;
-  int64_t smax, tiles;
+  int64_t smax;  // segments at most
+  int64_t room, tiles;  // segments and tiles that there is room for
   int seg_tokens;  // most tokens to a segment
   int parts;  // CTAs of the backward's walk to a group of channels
 };
@@ -66,7 +69,14 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
   const int64_t most = each > worth ? each : worth, len = ((most < T ? most : T) + kSsmSegStep - 1) / kSsmSegStep * kSsmSegStep;
   L.seg_tokens = (int)(len < kSsmSegStep ? kSsmSegStep : len);
   L.smax = N + (int64_t)T / L.seg_tokens;
-  L.tiles = L.smax + T / ssm_tile(Sp) + 1;
+  // Segments grow in steps, so fewer tokens can have more of them. The room is that of any call of no more documents and
+  // tokens, which makes the size monotonic: one workspace serves the largest call and all below it. A segment that is not
+  // its whole batch has at least kSsmSegStep tokens, T blocks / kSsmFill and sqrt(doc / 5), where doc is T up to four
+  // documents and else 4 T / N rounded down, at least 2 T / N once it is two; so T over it is at most the least of these.
+  const int64_t by_worth = (int64_t)std::sqrt(2.5 * T * (N > 2 ? N : 2)) + 1, by_fill = kSsmFill / blocks;
+  const int64_t more = std::max<int64_t>(1, std::min(by_fill, by_worth));
+  L.room = N + std::min<int64_t>(more, T / kSsmSegStep);
+  L.tiles = L.room + T / ssm_tile(Sp) + 1;
   const int per = kSsmWarps * ssm_grad_channels(Sp);
   L.parts = (C / G + per - 1) / per;
   const size_t state = (size_t)C * Sp * sizeof(float);
@@ -77,21 +87,21 @@ inline SsmLayout ssm_layout(int N, int T, int C, int S, int G, bool bwd) {
     return at;
   };
   L.header = take(sizeof(SsmHeader));
-  L.segs = take(sizeof(SsmSeg) * L.smax);
+  L.segs = take(sizeof(SsmSeg) * L.room);
   L.seg0 = take(sizeof(int32_t) * (N + 1));
   L.kind = take(sizeof(int32_t) * N);
   L.maps = take((size_t)T * G * 2 * Sp * sizeof(float));  // b and c in fp32, token by token
-  L.slot = take(state * L.smax);                          // end states from zero, then start states
-  L.sums = take(sizeof(float) * C * L.smax);              // time of each segment
+  L.slot = take(state * L.room);                          // end states from zero, then start states
+  L.sums = take(sizeof(float) * C * L.room);              // time of each segment
   if (bwd) {
     L.link = take(sizeof(int2) * N);                      // documents of the same pool entry
-    L.slot_r = take(state * L.smax);                      // the same for the state's gradient, in reverse
+    L.slot_r = take(state * L.room);                      // the same for the state's gradient, in reverse
     L.ckpt = take(state * L.tiles);                       // states from zero at each tile of a segment
     L.csum = take(sizeof(float) * C * L.tiles);           // time from the segment's start to each tile
     L.dstart = take(state * N);
     L.fin = take(state * N);                              // final states of documents that others start from
-    L.part_a = take(state * L.smax);                      // sums of each segment: da,
-    L.part_c = take(sizeof(float) * 2 * C * L.smax);      //   dskip and ddt_bias
+    L.part_a = take(state * L.room);                      // sums of each segment: da,
+    L.part_c = take(sizeof(float) * 2 * C * L.room);      //   dskip and ddt_bias
     L.part_m = take((size_t)L.parts * T * G * 2 * Sp * sizeof(float));  // db and dc of each CTA's channels
   }
   L.total = o;

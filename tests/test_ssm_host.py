@@ -78,6 +78,23 @@ def test_scan_workspace_holds_the_largest_call(lib):
     assert sizes == sorted(sizes) and gdn.ssm_workspace_size(1, 0, 1, 1) > 0
 
 
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("C,S,G", [(2048, 16, 1), (64, 16, 1), (1, 1, 1), (768, 8, 3), (8192, 64, 8), (200000, 8, 1)])
+def test_scan_workspace_grows_with_tokens_and_documents(lib, C, S, G, bwd):
+    """A workspace of the largest call holds every call of no more documents and tokens, on either side of each step of the
+    segments' length."""
+    size = lib.gdn_ssm_workspace_size
+    tokens = sorted(set(range(0, 3000)) | {t + d for t in (int(1.07 ** k) for k in range(120, 300)) for d in (-1, 0, 1) if t < 2 ** 22}
+                    | {16 * k + d for k in range(180, 20000, 97) for d in (0, 1)})
+    for N in (1, 2, 5, 64, 1500):
+        sizes = [size(N, t, C, S, G, bwd) for t in tokens]
+        assert sizes[0] > 0 and sizes == sorted(sizes), N
+    documents = [*range(1, 300), *range(300, 9000, 61)]
+    for t in (0, 7, 16, 500, 1217, 9001, 32768, 300001):
+        sizes = [size(n, t, C, S, G, bwd) for n in documents]
+        assert sizes == sorted(sizes), t
+
+
 def step(lib, **kw):
     a = dict(x=A, dt=A, z=A, a=A, b=A, c=A, skip=A, bias=A, B=2, C=64, S=16, G=1, dtype=0, strides=None, idx=A, pool=A,
              n_pool=4, out=A, status=None)
