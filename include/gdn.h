@@ -369,7 +369,7 @@ enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 /* u / (1 + e^-u) */ };
  *   w : fp32 [C, 4] on a 16-byte boundary; everything else as for gdn_conv_fwd / gdn_conv_bwd, dx in fp32
  * u is formed in fp32, y rounded once; the backward forms u again. Sums have a fixed order. Rows of the
  * outputs that no document holds do not exist: cu_seqlens ends at T. No output overlaps an input (final_tail
- * not conv_init either).
+ * not conv_init either). The workspace's size grows with N and T.
  */
 size_t gdn_conv_act_workspace_size(int N, int T, int C, int backward);
 int gdn_conv_act_fwd(const void* x, int64_t x_stride, const float* w, const float* bias, const int32_t* cu_seqlens,

@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/gdn.h"
@@ -32,8 +33,11 @@ constexpr int kFwdTokens = 32;                   // tokens to a block
 constexpr int kBwdThreads = 64;
 // Tokens to a block of the backward: few enough for small calls to spread, else 124. Blocks a power of two of rows
 // apart meet in memory: 64 took 128, 96 took 126 and 124 took 116 us at 16384 x 4096.
-inline int bwd_tokens(int T, int C) {
-  return (int64_t)(T / 124) * ((C / 4 + kBwdThreads - 1) / kBwdThreads) >= 8 * 152 ? 124 : 60;
+constexpr int kBwdShort = 60, kBwdLong = 124;
+// the fewest tokens that go in long blocks: eight CTAs of them to each SM
+inline int64_t bwd_long_from(int C) {
+  const int64_t cb = (C / 4 + kBwdThreads - 1) / kBwdThreads;
+  return kBwdLong * ((8 * 152 + cb - 1) / cb);
 }
 constexpr int kRows = 4;                         // rows at a time
 constexpr int kCh = 4, kPr = kCh / 2;             // channels of a thread, and their pairs
@@ -78,13 +82,16 @@ inline ActLayout act_layout(int N, int T, int C, bool bwd) {
     o = align_up(o + b, 256);
     return at;
   };
-  L.tokens = bwd ? bwd_tokens(T, C) : kFwdTokens;
+  L.tokens = !bwd ? kFwdTokens : T >= bwd_long_from(C) ? kBwdLong : kBwdShort;
   L.n_tb = (T + L.tokens - 1) / L.tokens;
   L.header = take(sizeof(ActHeader));
   if (bwd) {
     L.dstart = take((size_t)N * 3 * C * 4);     // gradient at each document's start
     L.kind = take(sizeof(int32_t) * N);
-    L.part = take((size_t)L.n_tb * C * 5 * 4);  // dw, dbias of each block of tokens: [block][5][C]
+    // dw, dbias of each block of tokens: [block][5][C]. Room for those of any call of no more tokens, which may have more
+    // (short) blocks, so that the size grows with T.
+    const int64_t room = std::max<int64_t>(L.n_tb, (std::min<int64_t>(T, bwd_long_from(C) - 1) + kBwdShort - 1) / kBwdShort);
+    L.part = take((size_t)room * C * 5 * 4);
     L.link = take(sizeof(int2) * N);            // documents of the same pool entry
   }
   L.total = o;

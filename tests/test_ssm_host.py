@@ -141,6 +141,20 @@ def test_convolution_refusals(lib, bwd):
     assert gdn.conv_workspace_size(1, 10, 12, activation="silu") == 0
 
 
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("C", [8, 264, 4096, 65536, 1 << 23])
+def test_convolution_workspace_grows_with_tokens_and_documents(lib, C, bwd):
+    """As the scan's: the backward's blocks get longer from some length on, and fewer."""
+    size = lib.gdn_conv_act_workspace_size
+    tokens = sorted(set(range(0, 20000)) | set(range(20000, 400000, 61)) | {124 * 1216 + d for d in range(-130, 130)})
+    tokens = [t for t in tokens if t * C <= 1 << 40]
+    for N in (1, 33, 4000):
+        sizes = [size(N, t, C, bwd) for t in tokens]
+        assert sizes[0] > 0 and sizes == sorted(sizes), N
+    sizes = [size(n, 9001, C, bwd) for n in range(1, 3000)]
+    assert sizes == sorted(sizes)
+
+
 def test_convolution_step_refusals(lib):
     def call(x=A, xs=0, w=A, B=2, C=64, dtype=0, act=1, idx=A, pool=A, n_pool=3, y=A, status=None):
         return lib.gdn_conv_decode_step(P(x), xs, P(w), None, B, C, dtype, act, P(idx), P(pool), n_pool, P(y), P(status), None)
