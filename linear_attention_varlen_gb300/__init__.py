@@ -464,7 +464,7 @@ def _tokens(t, name, dtype, shape, align=1):
 def _conv_act_inputs(x, w, cu_seqlens, bias, init_idx, conv_init, activation, step=False):
     torch = _torch()
     if activation not in ACTIVATIONS:
-        raise ValueError('activation: expected None, "none" or "silu"')
+        raise ValueError(f'activation: expected {"" if step else "None, "}"none" or "silu"')
     code = _dtype_code(x, "x", (DTYPE_BF16, DTYPE_FP16, DTYPE_FP32))
     T, C = x.shape
     xs = _tokens(x, "x", x.dtype, (T, C), 16 // x.element_size())

@@ -213,3 +213,15 @@ def test_binding_refusals():
                  lambda: gdn.ssm_scan_fwd(x.int(), x, x, x[:, None], x[:, None], cu)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_refused_activations_name_the_allowed_ones():
+    """The step has no call without an activation, whose default is None."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match='^activation: expected None, "none" or "silu"$'):
+        gdn.conv_fwd(x, x, cu, activation="relu")
+    for activation in (None, "relu"):
+        with pytest.raises(ValueError, match='^activation: expected "none" or "silu"$'):
+            gdn.conv_decode_step(x, x, x, cu, activation=activation)
