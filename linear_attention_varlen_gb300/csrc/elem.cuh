@@ -208,7 +208,7 @@ __device__ __forceinline__ void set_element(Words& r, int i, T v) {
 __device__ __forceinline__ uint64_t f2_dup(float v) { return bw::f2_pack(v, v); }
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) { return bw::f2_pack(exp2_approx(bw::f2_lo(x)), exp2_approx(bw::f2_hi(x))); }
 __device__ __forceinline__ uint64_t rcp_pair(uint64_t x) { return bw::f2_pack(rcp_approx(bw::f2_lo(x)), rcp_approx(bw::f2_hi(x))); }
-// 1 / (1 + e^-x): exact at the ends (0, 1), NaN stays NaN
+// 1 / (1 + e^-x), as close as the softplus below: exact at the ends (0, 1), NaN stays NaN
 __device__ __forceinline__ uint64_t sigmoid_pair(uint64_t x) {
   return rcp_pair(bw::f2_add(exp2_pair(bw::f2_mul(x, f2_dup(-kLog2e))), f2_dup(1.f)));
 }
@@ -232,7 +232,8 @@ __device__ __forceinline__ uint64_t silu_slope_pair(uint64_t x, uint64_t sig) {
 }
 // log(1 + e^r) = max(r, 0) + log1p(e^-|r|), with log1p(e) = 2 artanh(s), s = e / (2 + e) <= 1/3, and the rest of
 // artanh(s) / s = 1 + s^2 p(s^2) by the cubic p nearest to 1/3 + q / 5 + q^2 / 7 + ... on [0, 1/9] (relative error of the
-// sum 6e-9). About 2^-21 in all (the exponential's error, and its argument's rounding); NaN stays NaN.
+// sum 6e-9). About 2^-21 in all from r = -5 on (the exponential's 2^-22, and its argument's rounding); further down, where
+// the sum is e^r, that rounding alone is |r| 2^-24 (2^-19 at -30). NaN stays NaN.
 __device__ __forceinline__ uint64_t softplus_pair(uint64_t r) {
   const float lo = bw::f2_lo(r), hi = bw::f2_hi(r);
   const uint64_t e = bw::f2_pack(exp2_approx(-kLog2e * fabsf(lo)), exp2_approx(-kLog2e * fabsf(hi)));

@@ -10,8 +10,8 @@
 // the tokens of a block, the window of three inputs in registers; four rows at a time are worked on while the next four
 // are on their way. Four rows of one document go without a look at its bounds.
 // Measured (device time, bf16): 32768 x 2048 51 us (269 MB, 5.2 TB/s); backward of 16384 x 4096 101 us (537 MB, 5.3 TB/s; sixteen
-// warps an SM, twenty spill: 200 us), sum over its blocks 6, tails 12; step of 200 x 8192 in fp16 9 us. Eight channels
-// to a thread without packed pairs took 79 and 227 us.
+// warps an SM, twenty spill: 200 us), sum over its blocks 6, tails 12; step of 200 x 8192 in fp16 7.5 us
+// one after the other, 9.5 with cold caches. Eight channels to a thread without packed pairs took 79 and 227 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -16,10 +16,13 @@
 // (sum_t exp(a (dt_1 + .. + dt_t)) c_t dy_t, formed forward in time) and the state at every 16th (8th) token, so that the
 // walk in reverse needs no state but a tile's.
 //
-// What bounds it is the rate of instructions: the recurrence alone, 32 exponentials and 48 packed products for a token of
-// a warp's 64 channels and 16 states, takes 168 clocks of a scheduler (an exponential 4.4, a packed product with three
-// operands 2.6), and what is done once for a token and channel takes as many instructions again. So that part is in packed
-// pairs too and without branches, and the inputs come by asynchronous copies. Measured (device time, bf16, 16 states):
+// What bounds it is its instructions, not memory: the recurrence alone, 32 exponentials and 48 packed products for a token
+// of a warp's 64 channels and 16 states, takes 168 clocks of a scheduler (an exponential 4.4, a packed product with three
+// operands 2.6) of the 243 and 356 that the two walks take, and what is done once for a token and channel takes as many
+// instructions again. So that part is in packed pairs too and without branches, and the inputs come by asynchronous
+// copies. No pipe is full, though: forward 61 to 64 % of the issue slots and 46 to 60 % of the FMA and exponential pipes are
+// in use, in reverse 53, 46 and 29 %. With three warps to a scheduler (two in reverse, whose registers allow no more)
+// instructions wait for the ones before. Measured (device time, bf16, 16 states):
 //     32768 x 2048, one document      walks 203 + 298 us, planner and scan 21; its bytes once would take 81
 //     9001 x 2048, 12 documents       walks 64 + 94 us
 //     backward, 16384 x 2048          first walk 179 us, walk in reverse 594, planner, scan and sums 33; bytes once 71

@@ -17,9 +17,9 @@ constexpr int kSsmSegStep = 16;  // segments are multiples of it, of one at leas
 // the channels to a warp, and half the tile lets two CTAs share an SM.
 __host__ __device__ constexpr int ssm_tile(int Sp) { return Sp <= 8 ? 8 : 16; }
 static_assert(kSsmSegStep % ssm_tile(8) == 0 && kSsmSegStep % ssm_tile(16) == 0, "segments are whole tiles");
-// Warps of a walk that segments are cut for, sixteen to each SM (that is what an SM holds forward; the arithmetic's
-// rate bounds the walks, so that a few more than fit cost nothing, and long segments of ragged documents leave SMs idle:
-// at most as many as fit took 203 instead of 187 us for 9001 tokens of 12 documents).
+// Warps of a walk that segments are cut for, sixteen to each SM (that is what an SM holds forward; a few more than fit
+// cost nothing, and long segments of ragged documents leave SMs idle: at most as many as fit took 203 instead of 187 us
+// for 9001 tokens of 12 documents).
 constexpr int kSsmFill = 16 * 152;
 constexpr int kSsmMaxState = 64;
 
