@@ -222,3 +222,35 @@ def test_backward_of_a_large_batch_as_of_its_documents():
     size = 12000 ** 0.5 * 12  # of sums of 12000 products of normal values, none of them above this by far
     assert float((g["dw"].double() - dw).abs().max()) <= 12000 * 2.0 ** -24 * size
     assert float((g["dbias"].double() - db).abs().max()) <= 12000 * 2.0 ** -24 * size
+
+
+def test_backward_in_long_blocks():
+    """Enough tokens and channels for the longer blocks of the backward, documents that end at their borders and around
+    them. The reference is the definition in fp64 on the GPU; bounds as in `check`."""
+    C = 4096
+    lens = [124 * 30, 1, 0, 122, 3, 124 * 20 - 2, 2, 124 * 26]
+    T = sum(lens)
+    assert T >= 124 * 76  # eight CTAs to each SM: 16 blocks of channels, 152 SMs
+    d = inputs(77, lens, C, "bf16")
+    g = gdn.conv_bwd(d["x"], d["w"], d["cu"], d["dy"], bias=d["bias"], activation="silu")
+    x, dy, w, b = (d[k].double() for k in ("x", "dy", "w", "bias"))
+    ref = {k: torch.zeros_like(v, dtype=torch.float64) for k, v in g.items() if v is not None}
+    mag = {k: torch.zeros_like(v) for k, v in ref.items()}
+    t = 0
+    for n in lens:
+        e = torch.cat([torch.zeros_like(x[:3]), x[t:t + n]])
+        u = b + sum(w[:, m] * e[m:m + n] for m in range(4))
+        mu = b.abs() + sum((w[:, m] * e[m:m + n]).abs() for m in range(4))
+        s = torch.sigmoid(u)
+        du = dy[t:t + n] * s * (1 + u * (1 - s))
+        mdu = dy[t:t + n].abs() * (s * (1 + u.abs() * (1 - s)) + mu)
+        for out, v, wv, ev in ((ref, du, w, e), (mag, mdu, w.abs(), e.abs())):
+            de = torch.zeros_like(e)
+            for m in range(4):
+                de[m:m + n] += wv[:, m] * v
+                out["dw"][:, m] += (v * ev[m:m + n]).sum(0)
+            out["dx"][t:t + n] = de[3:]
+            out["dbias"] += v.sum(0)
+        t += n
+    for k, roundings in (("dx", 16 + len(lens)), ("dw", T + 16 + len(lens)), ("dbias", T + 16 + len(lens))):
+        assert ((g[k].double() - ref[k]).abs() <= 2.0 ** -21 * roundings * mag[k] + 2.0 ** -115).all(), k
